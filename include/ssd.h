@@ -383,6 +383,162 @@ ssd_status_t ssd_carry_in(const float *seg_states, const float *seg_decays,
                           ssd_dims_t dims, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Layer operators around the scan.  Shared conventions:
+ *   Inputs named x, u, dt, z, Bm, Cm and dy / dout of a scan or convolution
+ *   may be slices of wider projection outputs: their last dimension is
+ *   contiguous, consecutive tokens are `row` elements apart (at least the
+ *   row's own length) and consecutive sequences seqlen * row.  Everything
+ *   else is contiguous.  Pointers need element alignment only; rows that
+ *   start on vector boundaries take vector accesses.
+ *   Outputs may not overlap inputs or one another (SSD_ERR_INVALID_ARG)
+ *   except where an entry point says so.  Parameters (weights, A, D, biases,
+ *   gates) and their gradients are f32; sums over tokens are formed in a
+ *   fixed order without atomics, so results repeat bit for bit.
+ *   workspace: 256-byte aligned, at least the named size; contents on entry
+ *   do not matter.  It may be NULL where the size is 0.
+ */
+
+/*
+ * Short causal depthwise convolution, the step between a layer's input
+ * projection and its scan.  With x_t = initial_state for t < 0 (row
+ * width - 1 + t of [batch, width - 1, dim]; NULL: zeros):
+ *     pre[t,c] = bias[c] + sum_k weight[c,k] x[t - (width - 1) + k, c]
+ *     y = silu != 0 ? pre / (1 + exp(-pre)) : pre
+ * x [B, L, dim] rows `row` apart, y [B, L, dim], weight [dim, width], bias
+ * [dim] or NULL.  final_state (may be NULL) [B, width - 1, dim] receives the
+ * last width - 1 tokens of (initial_state | x).  width 2, 3 or 4 (others
+ * SSD_ERR_UNSUPPORTED); batch <= 65535; L == 0 only carries the state.
+ */
+typedef struct {
+    int64_t batch, seqlen, dim, width;
+} ssd_conv_dims_t;
+ssd_status_t ssd_causal_conv(const void *x, int64_t row, const float *weight, const float *bias,
+                             const void *initial_state, void *y, void *final_state,
+                             ssd_conv_dims_t dims, int silu, ssd_dtype_t dtype, void *stream);
+
+/*
+ * Gradients of ssd_causal_conv for dy [B, L, dim] (rows row_dy apart) and
+ * dfinal [B, width - 1, dim] (NULL: zero): dx [B, L, dim], dweight [dim,
+ * width], dbias [dim] (NULL: not wanted), dinit [B, width - 1, dim] (NULL:
+ * not wanted).  pre is recomputed from x.
+ */
+size_t ssd_causal_conv_bwd_workspace_size(ssd_conv_dims_t dims);
+ssd_status_t ssd_causal_conv_bwd(const void *x, int64_t row, const float *weight, const float *bias,
+                                 const void *initial_state, const void *dy, int64_t row_dy,
+                                 const void *dfinal, void *dx, float *dweight, float *dbias,
+                                 void *dinit, ssd_conv_dims_t dims, int silu, ssd_dtype_t dtype,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of ssd_causal_conv (dims.seqlen == 1): x [B, dim] rows `row`
+ * apart, y [B, dim]; state [B, width - 1, dim] holds the tokens before it,
+ * oldest first, and state_out receives them with x appended and the oldest
+ * dropped.  state_out may be state (in place).
+ */
+ssd_status_t ssd_causal_conv_step(const void *x, int64_t row, const float *weight,
+                                  const float *bias, const void *state, void *state_out, void *y,
+                                  ssd_conv_dims_t dims, int silu, ssd_dtype_t dtype, void *stream);
+
+/*
+ * Selective scan: the recurrence with a decay of its own for every channel d
+ * and state n (ssd_fwd has one per head), g = d / (dim / ngroups):
+ *     delta = dt + dt_bias[d], through softplus when dt_softplus != 0
+ *     h[d,n] <- exp(delta A[d,n]) h[d,n] + delta u[d] Bm[g,n]
+ *     y[d]   = (sum_n Cm[g,n] h[d,n] + D[d] u[d]) * silu(z[d])
+ * u, dt, z [B, L, dim], Bm, Cm [B, L, ngroups * dstate] in the call's dtype
+ * with rows as in ssd_scan_rows_t; y [B, L, dim].  A [dim, dstate]; D and
+ * dt_bias [dim], z and initial_state [B, dim, dstate] f32 may be NULL (no
+ * skip, no bias, no gate, zeros).  Optional outputs: final_state [B, dim,
+ * dstate] f32, which may be initial_state itself; chunk_states [B, nc, dim,
+ * dstate] f32, nc = ceil(L / ssd_selective_scan_chunk()), the state before
+ * each chunk, which the backward starts from.  1 <= dstate <= 64, dim %
+ * ngroups == 0, batch <= 65535.  Arithmetic is f32; the decay is exp2 of
+ * delta A log2(e) with the hardware's approximation (relative error 2^-22).
+ */
+typedef struct {
+    int64_t batch, seqlen, dim, dstate, ngroups;
+} ssd_scan_dims_t;
+typedef struct {
+    int64_t u, dt, z, b, c, dy; /* elements between consecutive tokens */
+} ssd_scan_rows_t;
+int ssd_selective_scan_chunk(void);
+size_t ssd_selective_scan_workspace_size(ssd_scan_dims_t dims);
+ssd_status_t ssd_selective_scan(const void *u, const void *dt, const float *A, const void *Bm,
+                                const void *Cm, const float *D, const void *z,
+                                const float *dt_bias, const float *initial_state, void *y,
+                                float *final_state, float *chunk_states, ssd_scan_dims_t dims,
+                                ssd_scan_rows_t rows, int dt_softplus, ssd_dtype_t dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of ssd_selective_scan for dy [B, L, dim] and dfinal [B, dim,
+ * dstate] f32 (NULL: zero).  chunk_states: the forward's (NULL: recomputed
+ * here, in the workspace; have_chunk_states tells the size function which).
+ * Outputs: du, ddt (of dt as given, through the softplus), dz (with z) [B, L,
+ * dim], dB, dC [B, L, ngroups * dstate] in the call's dtype, dA [dim,
+ * dstate], dD (with D; NULL: not wanted), ddt_bias [dim] (NULL: not wanted),
+ * dinit [B, dim, dstate] f32 (NULL: not wanted).
+ */
+size_t ssd_selective_scan_bwd_workspace_size(ssd_scan_dims_t dims, int have_chunk_states);
+ssd_status_t ssd_selective_scan_bwd(const void *u, const void *dt, const float *A, const void *Bm,
+                                    const void *Cm, const float *D, const void *z,
+                                    const float *dt_bias, const float *initial_state,
+                                    const void *dy, const float *dfinal,
+                                    const float *chunk_states, void *du, void *ddt, float *dA,
+                                    void *dB, void *dC, float *dD, void *dz, float *ddt_bias,
+                                    float *dinit, ssd_scan_dims_t dims, ssd_scan_rows_t rows,
+                                    int dt_softplus, ssd_dtype_t dtype, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * One token of ssd_selective_scan (dims.seqlen == 1; rows are then the
+ * elements between sequences): state_out [B, dim, dstate] f32 receives the
+ * updated state and may be state itself; y [B, dim].
+ */
+ssd_status_t ssd_selective_scan_step(const void *u, const void *dt, const float *A,
+                                     const void *Bm, const void *Cm, const float *D,
+                                     const void *z, const float *dt_bias, const float *state,
+                                     float *state_out, void *y, ssd_scan_dims_t dims,
+                                     ssd_scan_rows_t rows, int dt_softplus, ssd_dtype_t dtype,
+                                     void *stream);
+
+/*
+ * The norms between two blocks with the block's gate and the scaled residual
+ * add.  Row t of dim channels (contiguous), gate row j = t / (ntokens /
+ * gate_rows), rmsnorm(v) = v / sqrt(mean(v^2) + eps):
+ *     p = post_weight ? rmsnorm(y) * post_weight : y
+ *     residual_out = residual + scale * gate[j] * p
+ *     out          = rmsnorm(residual_out) * weight
+ * y, out in `dtype`; residual (NULL: zeros), residual_out in residual_dtype
+ * (`dtype` or SSD_F32); weight, post_weight (NULL: no norm after the block)
+ * [dim]; gate [gate_rows, dim] (NULL with gate_rows 0: no gate), ntokens %
+ * gate_rows == 0, so one gate row for all tokens, one per sequence or one
+ * per token.  out is formed from residual_out before its rounding.
+ * residual_out may be residual itself.  dim <= 32768.
+ */
+ssd_status_t ssd_block_norm(const void *y, const void *residual, const float *weight,
+                            const float *post_weight, const float *gate, void *out,
+                            void *residual_out, int64_t ntokens, int64_t dim, int64_t gate_rows,
+                            float scale, float eps, ssd_dtype_t dtype,
+                            ssd_dtype_t residual_dtype, void *stream);
+
+/*
+ * Gradients of ssd_block_norm, from its y and residual_out: dout of out,
+ * dresidual_out of residual_out (NULL: zero).  Outputs: dy, dresidual (in
+ * residual_dtype; may be dresidual_out itself), dweight [dim], dpost_weight
+ * [dim] (with post_weight), dgate [gate_rows, dim] (with gate).
+ */
+size_t ssd_block_norm_bwd_workspace_size(int64_t ntokens, int64_t dim, int64_t gate_rows);
+ssd_status_t ssd_block_norm_bwd(const void *y, const void *residual_out, const float *weight,
+                                const float *post_weight, const float *gate, const void *dout,
+                                const void *dresidual_out, void *dy, void *dresidual,
+                                float *dweight, float *dpost_weight, float *dgate,
+                                int64_t ntokens, int64_t dim, int64_t gate_rows, float scale,
+                                float eps, ssd_dtype_t dtype, ssd_dtype_t residual_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Number of kernel launches this library has issued in this process (all
  * devices, all threads).  Diagnostic: a call rejected by validation leaves it
  * unchanged; the benchmark reports launches per step from it.

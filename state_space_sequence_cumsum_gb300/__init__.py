@@ -11,4 +11,8 @@ from .ssd import (SsdError, SsdFunction, Workspace, ssd_bwd, ssd_chunk_cumsum,  
                   ssd_fwd_plan, ssd_fwd_staged, ssd_fwd_workspace_size, ssd_state_out,
                   ssd_state_pass, ssd_status_string, ssd_stream_status, ssd_segment_summary,
                   ssd_carry_in, ssd_fwd_context_parallel)
+from .layer import (BlockNormFunction, CausalConvFunction, SelectiveScanFunction,  # noqa: F401
+                    ssd_block_norm, ssd_block_norm_bwd, ssd_causal_conv, ssd_causal_conv_bwd,
+                    ssd_causal_conv_step, ssd_selective_scan, ssd_selective_scan_bwd,
+                    ssd_selective_scan_chunk, ssd_selective_scan_step)
 from ._build import build  # noqa: F401

@@ -31,6 +31,11 @@ EXPORTS = ("ssd_chunk_cumsum", "ssd_state_pass", "ssd_chunk_out", "ssd_state_out
            "ssd_bwd", "ssd_bwd_workspace_size",
            "ssd_gated_rmsnorm", "ssd_segment_summary", "ssd_segment_summary_workspace_size",
            "ssd_carry_in",
+           "ssd_causal_conv", "ssd_causal_conv_bwd", "ssd_causal_conv_bwd_workspace_size",
+           "ssd_causal_conv_step", "ssd_selective_scan", "ssd_selective_scan_workspace_size",
+           "ssd_selective_scan_chunk", "ssd_selective_scan_bwd",
+           "ssd_selective_scan_bwd_workspace_size", "ssd_selective_scan_step", "ssd_block_norm",
+           "ssd_block_norm_bwd", "ssd_block_norm_bwd_workspace_size",
            "ssd_launch_count", "ssd_status_string", "ssd_stream_status")
 PATH_NAMES = {0: "staged-cuda-cores", 1: "staged-tensor-cores", 2: "fused-tensor-cores",
               3: "fused-pair-tensor-cores"}
@@ -40,6 +45,21 @@ class ssd_dims_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
                 ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
+
+
+class ssd_conv_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("width", ctypes.c_int64)]
+
+
+class ssd_scan_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
+
+
+class ssd_scan_rows_t(ctypes.Structure):
+    _fields_ = [("u", ctypes.c_int64), ("dt", ctypes.c_int64), ("z", ctypes.c_int64),
+                ("b", ctypes.c_int64), ("c", ctypes.c_int64), ("dy", ctypes.c_int64)]
 
 
 class SsdError(RuntimeError):
@@ -68,7 +88,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             raise RuntimeError(f"CUDA library {_build.LIB} is missing; run __graft_entry__.build()")
         lib = ctypes.CDLL(_build.LIB)
         vp, fp, i32, st = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int
-        D = ssd_dims_t
+        D, CD, SD, SR = ssd_dims_t, ssd_conv_dims_t, ssd_scan_dims_t, ssd_scan_rows_t
+        i64, f32 = ctypes.c_int64, ctypes.c_float
         sig = {
             "ssd_chunk_cumsum": ([fp, fp, fp, fp, D, i32, vp], st),
             "ssd_state_pass": ([vp, vp, fp, fp, fp, fp, fp, D, i32, i32, vp], st),
@@ -96,6 +117,25 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "ssd_segment_summary": ([vp, fp, fp, vp, fp, fp, D, i32, i32, vp, ctypes.c_size_t,
                                      vp], st),
             "ssd_carry_in": ([fp, fp, fp, i32, i32, fp, D, vp], st),
+            "ssd_causal_conv": ([vp, i64, fp, fp, vp, vp, vp, CD, i32, i32, vp], st),
+            "ssd_causal_conv_bwd_workspace_size": ([CD], ctypes.c_size_t),
+            "ssd_causal_conv_bwd": ([vp, i64, fp, fp, vp, vp, i64, vp, vp, fp, fp, vp, CD, i32, i32,
+                                     vp, ctypes.c_size_t, vp], st),
+            "ssd_causal_conv_step": ([vp, i64, fp, fp, vp, vp, vp, CD, i32, i32, vp], st),
+            "ssd_selective_scan_chunk": ([], ctypes.c_int),
+            "ssd_selective_scan_workspace_size": ([SD], ctypes.c_size_t),
+            "ssd_selective_scan": ([vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, fp, fp, SD, SR, i32, i32,
+                                    vp, ctypes.c_size_t, vp], st),
+            "ssd_selective_scan_bwd_workspace_size": ([SD, i32], ctypes.c_size_t),
+            "ssd_selective_scan_bwd": ([vp, vp, fp, vp, vp, fp, vp, fp, fp, vp, fp, fp, vp, vp, fp,
+                                        vp, vp, fp, vp, fp, fp, SD, SR, i32, i32, vp,
+                                        ctypes.c_size_t, vp], st),
+            "ssd_selective_scan_step": ([vp, vp, fp, vp, vp, fp, vp, fp, fp, fp, vp, SD, SR, i32,
+                                         i32, vp], st),
+            "ssd_block_norm": ([vp, vp, fp, fp, fp, vp, vp, i64, i64, i64, f32, f32, i32, i32, vp], st),
+            "ssd_block_norm_bwd_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
+            "ssd_block_norm_bwd": ([vp, vp, fp, fp, fp, vp, vp, vp, vp, fp, fp, fp, i64, i64, i64,
+                                    f32, f32, i32, i32, vp, ctypes.c_size_t, vp], st),
             "ssd_launch_count": ([], ctypes.c_uint64),
             "ssd_status_string": ([st], ctypes.c_char_p),
             "ssd_stream_status": ([vp], st),

@@ -1,0 +1,86 @@
+// Pieces the selective scan's forward, reverse and gradient kernels share.
+#pragma once
+#include "ssd_internal.h"
+#include "vec.cuh"
+
+namespace ssd {
+
+// A block has kScanThreads threads.  A thread holds four of a channel's
+// states, LN = 1, 2, 4, 8 or 16 lanes hold the channel (up to 4 LN states;
+// the ones past dstate stay zero).
+constexpr int kScanThreads = 128;
+// Tokens of one chunk: a state is kept at each chunk's start for the backward.
+constexpr int kScanChunk = 16;
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Four consecutive elements as loaded; elements past n are zero.
+template <typename TI> using Raw4 = typename Pack<TI, 4>::T;
+
+template <typename TI> __device__ __forceinline__ Raw4<TI> load_raw4(const TI *p, int n, bool vec)
+{
+    Raw4<TI> r{};
+    if (vec && n >= 4)
+        return *reinterpret_cast<const Raw4<TI> *>(p);
+    TI *e = reinterpret_cast<TI *>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n)
+            e[i] = p[i];
+    return r;
+}
+template <typename TI> __device__ __forceinline__ void store4(TI *p, const float (&v)[4], int n, bool vec)
+{
+    if (vec && n >= 4) {
+        store_vec<TI, 4>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n)
+            p[i] = from_f32<TI>(v[i]);
+}
+
+// The four states of one lane in an f32 [.., N] array.
+__device__ __forceinline__ void load_states(const float *p, int n, float (&v)[4])
+{
+    if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        load_vec<float, 4>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = i < n ? p[i] : 0.f;
+}
+__device__ __forceinline__ void store_states(float *p, int n, const float (&v)[4])
+{
+    if (n >= 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        store_vec<float, 4>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n)
+            p[i] = v[i];
+}
+
+template <int LN> __device__ __forceinline__ float lane_sum(float v)
+{
+#pragma unroll
+    for (int o = LN / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The rows of B or C of a tile, as f32 [kScanChunk][4 LN], zero past N and
+// past the last token.
+template <typename TI, int LN>
+__device__ __forceinline__ void load_rows(const TI *m, int64_t row, int nt, int N, float *s)
+{
+    for (int i = threadIdx.x; i < kScanChunk * 4 * LN; i += kScanThreads) {
+        const int t = i / (4 * LN), n = i % (4 * LN);
+        s[i] = (t < nt && n < N) ? to_f32(m[t * row + n]) : 0.f;
+    }
+}
+
+}  // namespace ssd

@@ -150,4 +150,68 @@ cudaError_t launch_fused_pair_tc(const void *x, const void *Bm, const void *Cm, 
                                  float *final_state, void *y, const Geom &g, void *scratch,
                                  size_t scratch_bytes, cudaStream_t st, bool allow_prefill = true);
 
+// SMs of the current device.
+int device_sm_count();
+
+// Short causal convolution (k_conv.cu): rows are elements between the tokens
+// of x and dy.
+struct ConvGeom {
+    int64_t batch, seqlen, dim, row, row_dy;
+    int width;
+    bool silu;
+};
+cudaError_t launch_conv(const void *x, const float *w, const float *bias, const void *init, void *y,
+                        void *fin, const ConvGeom &g, bool bf16, cudaStream_t st);
+cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, const void *state,
+                             void *state_out, void *y, const ConvGeom &g, bool bf16, cudaStream_t st);
+size_t conv_bwd_workspace(const ConvGeom &g);
+cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, const void *init,
+                            const void *dy, const void *dfinal, void *dx, float *dw, float *dbias,
+                            void *dinit, float *part, const ConvGeom &g, bool bf16, cudaStream_t st);
+
+// Selective scan (k_scan.cu, k_scan_bwd.cu): kpg = channels per group, rows
+// are elements between tokens.
+struct ScanGeom {
+    int64_t batch, seqlen, dim, N, G, kpg;
+    int64_t row_u, row_dt, row_z, row_b, row_c, row_dy;
+    bool softplus;
+};
+struct ScanSegs {
+    int64_t n_seg, chunks_per_seg;
+};
+int scan_lanes(int64_t N);  // lanes that hold a channel's states, four each
+int scan_chunk();           // tokens between kept states
+ScanSegs scan_segments(const ScanGeom &g);
+size_t scan_pass_workspace(const ScanGeom &g);
+cudaError_t launch_selective_scan(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                                  const float *D, const void *z, const float *bias, const float *init, void *y,
+                                  float *fin, float *kept, void *ws, const ScanGeom &g, bool bf16,
+                                  cudaStream_t st);
+cudaError_t launch_scan_reverse(const void *dy, const void *dt, const float *A, const void *Cm, const void *z,
+                                const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws,
+                                const ScanGeom &g, bool bf16, cudaStream_t st);
+cudaError_t launch_scan_step(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                             const float *D, const void *z, const float *bias, const float *state,
+                             float *state_out, void *y, const ScanGeom &g, bool bf16, cudaStream_t st);
+size_t scan_grad_workspace(const ScanGeom &g);
+cudaError_t launch_scan_grad(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
+                             const float *D, const void *z, const float *bias, const void *dy, const float *h0,
+                             const float *g1, void *du, void *ddt, float *dA, void *dB, void *dC, float *dD,
+                             void *dz, float *dbias, void *ws, const ScanGeom &g, bool bf16, cudaStream_t st);
+
+// Norms around a block (k_block_norm.cu).
+struct NormGeom {
+    int64_t ntokens, dim, tokens_per_gate;
+    float scale, eps, inv_dim;
+};
+cudaError_t launch_block_norm(const void *y, const void *residual, const float *weight,
+                              const float *post_weight, const float *gate, void *out, void *residual_out,
+                              const NormGeom &g, bool bf16, bool res_bf16, cudaStream_t st);
+size_t block_norm_bwd_workspace(const NormGeom &g, bool gate);
+cudaError_t launch_block_norm_bwd(const void *y, const void *r, const float *weight, const float *post_weight,
+                                  const float *gate, const void *dout, const void *dr, void *dy,
+                                  void *dresidual, float *dweight, float *dpost_weight, float *dgate,
+                                  float *workspace, const NormGeom &g, bool bf16, bool res_bf16,
+                                  cudaStream_t st);
+
 }  // namespace ssd

@@ -148,6 +148,21 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         return lib
 
 
+_native = None
+
+
+def native():
+    """The compiled binding of the layer operators (``_native.so``)."""
+    global _native
+    if _native is None:
+        load()
+        import importlib
+        mod = importlib.import_module("." + os.path.splitext(os.path.basename(_build.NATIVE))[0], __package__)
+        mod.set_error(SsdError)
+        _native = mod
+    return _native
+
+
 def status_string(status: int) -> str:
     return load().ssd_status_string(int(status)).decode()
 

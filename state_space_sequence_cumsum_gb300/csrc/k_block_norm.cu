@@ -23,8 +23,12 @@ namespace {
 constexpr int kMaxTeam = 512;  // threads of a row's team
 
 // Adds K values over the team (blockDim.x threads, a multiple of 32); every
-// thread of the block must call it.
-template <int K> __device__ __forceinline__ void team_sum(float (&v)[K], float *smem)
+// thread of the block must call it.  One barrier: `buf` (one Sum<K> per warp
+// of the block) may be used again once another barrier has passed.
+template <int K> struct alignas(K > 2 ? 16 : 4 * K) Sum {
+    float v[K];
+};
+template <int K> __device__ __forceinline__ void team_sum(float (&v)[K], Sum<K> *buf)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -34,21 +38,21 @@ template <int K> __device__ __forceinline__ void team_sum(float (&v)[K], float *
     const int warps = blockDim.x >> 5;
     if (warps == 1)
         return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float *s = smem + threadIdx.y * warps * K;
-    if (lane == 0)
+    Sum<K> *s = buf + threadIdx.y * warps;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            s[warp * K + k] = v[k];
+            s[threadIdx.x >> 5].v[k] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float t = 0.f;
-        for (int q = 0; q < warps; ++q)
-            t += s[q * K + k];
-        v[k] = t;
+    for (int k = 0; k < K; ++k)
+        v[k] = 0.f;
+    for (int q = 0; q < warps; ++q) {
+        const Sum<K> t = s[q];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            v[k] += t.v[k];
     }
-    __syncthreads();
 }
 
 template <int VEC> __device__ __forceinline__ void scale_by(const float *p, float (&v)[VEC])
@@ -68,7 +72,7 @@ block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__r
                   const float *__restrict__ post_weight, const float *__restrict__ gate, TI *__restrict__ out,
                   TR *residual_out, NormGeom g)
 {
-    __shared__ float smem[32];
+    __shared__ Sum<1> sum_y[16], sum_r[16];
     const int team = blockDim.x;
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < g.ntokens;
@@ -97,7 +101,7 @@ block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__r
     }
     float f = g.scale;
     if (post_weight) {
-        team_sum<1>(s, smem);
+        team_sum<1>(s, sum_y);
         f *= rsqrtf(s[0] * g.inv_dim + g.eps);
     }
     const float *gr = gate ? gate + (live ? row / g.tokens_per_gate : 0) * g.dim : nullptr;
@@ -122,7 +126,7 @@ block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__r
             store_vec<TR, VEC>(residual_out + row * g.dim + v * VEC, rv[q]);
         }
     }
-    team_sum<1>(s, smem);
+    team_sum<1>(s, sum_r);
     const float rs = rsqrtf(s[0] * g.inv_dim + g.eps);
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
@@ -159,7 +163,9 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                       float *__restrict__ part, float *__restrict__ dgate_part, NormGeom g, int64_t groups,
                       int64_t spans)
 {
-    __shared__ float smem[3 * 32];
+    __shared__ Sum<3> sum_row[2][16];
+    __shared__ Sum<1> sum_p[16];
+    int flip = 0;
     const int team = blockDim.x;
     const int nv = (int)(g.dim / VEC);
     float dw[VPT][VEC], dpw[VPT][VEC], dg[VPT][VEC];
@@ -177,27 +183,43 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
                 dg[q][i] = 0.f;
+        using VI = typename Pack<TI, VEC>::T;
+        using VR = typename Pack<TR, VEC>::T;
+        VI y_raw[VPT], n_raw[VPT];
+        VR r_raw[VPT], d_raw[VPT];
+        auto fetch = [&](int64_t row) {
+#pragma unroll
+            for (int q = 0; q < VPT; ++q) {
+                const int v = threadIdx.x + q * team;
+                y_raw[q] = n_raw[q] = VI{};
+                r_raw[q] = d_raw[q] = VR{};
+                if (v < nv) {
+                    const int64_t at = row * g.dim + v * VEC;
+                    y_raw[q] = *reinterpret_cast<const VI *>(y + at);
+                    r_raw[q] = *reinterpret_cast<const VR *>(r + at);
+                    n_raw[q] = *reinterpret_cast<const VI *>(dout + at);
+                    if (dr)
+                        d_raw[q] = *reinterpret_cast<const VR *>(dr + at);
+                }
+            }
+        };
+        if (t0 < t1)
+            fetch(t0);
         for (int64_t row = t0; row < t1; ++row) {
             float yv[VPT][VEC], rv[VPT][VEC], gn[VPT][VEC], gr[VPT][VEC];
             float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
+                unpack<TI, VEC>(y_raw[q], yv[q]);
+                unpack<TR, VEC>(r_raw[q], rv[q]);
+                unpack<TI, VEC>(n_raw[q], gn[q]);
+                unpack<TR, VEC>(d_raw[q], gr[q]);
+            }
+            if (row + 1 < t1)  // in flight while this row is reduced
+                fetch(row + 1);
+#pragma unroll
+            for (int q = 0; q < VPT; ++q) {
                 const int v = threadIdx.x + q * team;
-                if (v < nv) {
-                    load_vec<TI, VEC>(y + row * g.dim + v * VEC, yv[q]);
-                    load_vec<TR, VEC>(r + row * g.dim + v * VEC, rv[q]);
-                    load_vec<TI, VEC>(dout + row * g.dim + v * VEC, gn[q]);
-                    if (dr)
-                        load_vec<TR, VEC>(dr + row * g.dim + v * VEC, gr[q]);
-                    else
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            gr[q][i] = 0.f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        yv[q][i] = rv[q][i] = gn[q][i] = gr[q][i] = 0.f;
-                }
                 float w[VEC] = {};
                 if (v < nv)
                     load_vec<float, VEC>(weight + v * VEC, w);
@@ -208,7 +230,8 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                     s[2] = fmaf(gn[q][i] * w[i], rv[q][i], s[2]);
                 }
             }
-            team_sum<3>(s, smem);
+            team_sum<3>(s, sum_row[flip]);
+            flip ^= 1;
             const float rs_y = post_weight ? rsqrtf(s[0] * g.inv_dim + g.eps) : 1.f;
             const float rs_r = rsqrtf(s[1] * g.inv_dim + g.eps);
             const float c = s[2] * g.inv_dim * rs_r * rs_r;  // mean(gn rh) rs_r
@@ -245,7 +268,7 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
             }
             float m = 0.f;
             if (post_weight) {
-                team_sum<1>(u, smem);
+                team_sum<1>(u, sum_p);
                 m = u[0] * g.inv_dim;
             }
 #pragma unroll

@@ -17,18 +17,26 @@ namespace ssd {
 namespace {
 
 constexpr int kConvThreads = 256;
+constexpr int kGroup = 4;  // tokens whose loads a thread has in flight
 
+// A thread's VEC x W weights are one run of floats: four at a time where VEC > 1
+// (rows then start on 16-byte boundaries).
 template <int VEC, int W>
 __device__ __forceinline__ void load_weights(const float *__restrict__ w, const float *__restrict__ bias,
                                              int64_t c, float (&wv)[W][VEC], float (&bv)[VEC])
 {
+    constexpr int NL = VEC > 1 ? 4 : 1;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
+    for (int q = 0; q < VEC * W; q += NL) {
+        float v[NL];
+        load_vec<float, NL>(w + c * W + q, v);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-            wv[k][i] = w[(c + i) * W + k];
-        bv[i] = bias ? bias[c + i] : 0.f;
+        for (int e = 0; e < NL; ++e)
+            wv[(q + e) % W][(q + e) / W] = v[e];
     }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        bv[i] = bias ? bias[c + i] : 0.f;
 }
 
 // One thread: VEC channels of `run` consecutive tokens of one sequence.
@@ -62,21 +70,32 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
                 win[k][i] = 0.f;
     }
     const int64_t t1 = min64(t0 + run, g.seqlen);
-    for (int64_t t = t0; t < t1; ++t) {
-        load_vec<TI, VEC>(xb + t * g.row, win[W - 1]);
-        float o[VEC];
+    // kGroup tokens' loads are issued before the first is used
+    for (int64_t tg = t0; tg < t1; tg += kGroup) {
+        typename Pack<TI, VEC>::T raw[kGroup];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            float s = bv[i];
+        for (int j = 0; j < kGroup; ++j)
+            if (tg + j < t1)
+                raw[j] = *reinterpret_cast<const typename Pack<TI, VEC>::T *>(xb + (tg + j) * g.row);
 #pragma unroll
-            for (int k = 0; k < W; ++k)
-                s = fmaf(wv[k][i], win[k][i], s);
-            o[i] = g.silu ? fast_silu(s) : s;
+        for (int j = 0; j < kGroup; ++j) {
+            if (tg + j >= t1)
+                break;
+            unpack<TI, VEC>(raw[j], win[W - 1]);
+            float o[VEC];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                win[k][i] = win[k + 1][i];
+            for (int i = 0; i < VEC; ++i) {
+                float s = bv[i];
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    s = fmaf(wv[k][i], win[k][i], s);
+                o[i] = g.silu ? fast_silu(s) : s;
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+                    win[k][i] = win[k + 1][i];
+            }
+            store_vec<TI, VEC>(yb + (tg + j) * g.dim, o);
         }
-        store_vec<TI, VEC>(yb + t * g.dim, o);
     }
     if (fin && t1 == g.seqlen)
 #pragma unroll
@@ -170,12 +189,32 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 load_xf(e0 - (W - 1) + k, win[k]);
         }
         const int64_t e1 = min64(e0 + run, L + W - 1);
-        for (int64_t e = e0 - (W - 1); e < e1; ++e) {
-            load_xf(e + W - 1, win[W - 1]);
-            // dp[0] is dpre[e], dp[k] = dpre[e - k]
-            float d[VEC];
-            if (e >= 0 && e < L) {
-                load_vec<TI, VEC>(dyb + e * g.row_dy, d);
+        for (int64_t eg = e0 - (W - 1); eg < e1; eg += kGroup) {
+            using V = typename Pack<TI, VEC>::T;
+            V xr[kGroup], yr[kGroup];
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const int64_t e = eg + j;
+                xr[j] = yr[j] = V{};
+                if (e < e1) {
+                    if (e >= 0 && e < L) {  // xf[e + W - 1] is x[e]
+                        xr[j] = *reinterpret_cast<const V *>(xb + e * g.row);
+                        yr[j] = *reinterpret_cast<const V *>(dyb + e * g.row_dy);
+                    } else if (e < 0 && e + W - 1 >= 0 && init) {
+                        xr[j] = *reinterpret_cast<const V *>(init + (b * (W - 1) + e + W - 1) * g.dim + c);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const int64_t e = eg + j;
+                if (e >= e1)
+                    break;
+                unpack<TI, VEC>(xr[j], win[W - 1]);
+                // dp[0] is dpre[e], dp[k] = dpre[e - k]; zero outside [0, L)
+                float d[VEC];
+                unpack<TI, VEC>(yr[j], d);
+                const bool in = e >= 0 && e < L;
                 if (g.silu) {
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
@@ -183,53 +222,49 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
 #pragma unroll
                         for (int k = 0; k < W; ++k)
                             s = fmaf(wv[k][i], win[k][i], s);
-                        d[i] *= silu_grad(s, fast_sigmoid(s));
+                        d[i] = in ? d[i] * silu_grad(s, fast_sigmoid(s)) : 0.f;
                     }
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    d[i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-                for (int k = W - 1; k > 0; --k)
-                    dp[k][i] = dp[k - 1][i];
-                dp[0][i] = d[i];
-            }
-            if (e >= e0) {
-                float o[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    float s = 0.f;
 #pragma unroll
-                    for (int k = 0; k < W; ++k) {
-                        s = fmaf(wv[k][i], dp[k][i], s);
-                        if (e < L)
-                            dw[k][i] = fmaf(d[i], win[k][i], dw[k][i]);
+                    for (int k = W - 1; k > 0; --k)
+                        dp[k][i] = dp[k - 1][i];
+                    dp[0][i] = d[i];
+                }
+                if (e >= e0) {
+                    float o[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        float s = 0.f;
+#pragma unroll
+                        for (int k = 0; k < W; ++k) {
+                            s = fmaf(wv[k][i], dp[k][i], s);
+                            if (in)
+                                dw[k][i] = fmaf(d[i], win[k][i], dw[k][i]);
+                        }
+                        dw[W][i] += d[i];
+                        o[i] = s;
                     }
-                    dw[W][i] += d[i];
-                    o[i] = s;
-                }
-                const int64_t t = e - (W - 1);
-                if (dfinal && e >= L) {  // the carried rows are the last W - 1 of xf
-                    float f[VEC];
-                    load_vec<TI, VEC>(dfinal + (b * (W - 1) + e - L) * g.dim + c, f);
+                    const int64_t t = e - (W - 1);
+                    if (dfinal && e >= L) {  // the carried rows are the last W - 1 of xf
+                        float f[VEC];
+                        load_vec<TI, VEC>(dfinal + (b * (W - 1) + e - L) * g.dim + c, f);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        o[i] += f[i];
+                        for (int i = 0; i < VEC; ++i)
+                            o[i] += f[i];
+                    }
+                    if (t >= 0)
+                        store_vec<TI, VEC>(dxb + t * g.dim, o);
+                    else if (dinit)
+                        store_vec<TI, VEC>(dinit + (b * (W - 1) + e) * g.dim + c, o);
                 }
-                if (t >= 0)
-                    store_vec<TI, VEC>(dxb + t * g.dim, o);
-                else if (dinit)
-                    store_vec<TI, VEC>(dinit + (b * (W - 1) + e) * g.dim + c, o);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k)
+                        win[k][i] = win[k + 1][i];
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-                    win[k][i] = win[k + 1][i];
         }
     }
 #pragma unroll
@@ -364,7 +399,7 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
 cudaError_t launch_conv(const void *x, const float *w, const float *bias, const void *init, void *y,
                         void *fin, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
-    const bool al = aligned(x, 16) && aligned(init, 16) && aligned(y, 16) && aligned(fin, 16);
+    const bool al = aligned(x, 16) && aligned(init, 16) && aligned(y, 16) && aligned(fin, 16) && aligned(w, 16);
     if (bf16) {
         if (al && g.dim % 8 == 0 && g.row % 8 == 0)
             return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 8, x, w, bias, init, y, fin, g, st);
@@ -380,7 +415,7 @@ cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, c
 {
     const size_t a = bf16 ? 8 : 16;
     const bool al = aligned(x, a) && aligned(state, a) && aligned(state_out, a) && aligned(y, a) &&
-                    g.dim % 4 == 0 && g.row % 4 == 0;
+                    aligned(w, 16) && g.dim % 4 == 0 && g.row % 4 == 0;
     if (bf16) {
         if (al)
             return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 4, x, w, bias, state, state_out, y, g, st);
@@ -407,7 +442,7 @@ cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, co
                             void *dinit, float *part, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
     const size_t a = bf16 ? 8 : 16;
-    bool al = g.dim % 4 == 0 && g.row % 4 == 0 && g.row_dy % 4 == 0;
+    bool al = g.dim % 4 == 0 && g.row % 4 == 0 && g.row_dy % 4 == 0 && aligned(w, 16);
     for (const void *p : {x, init, dy, dfinal, static_cast<const void *>(dx), static_cast<const void *>(dinit)})
         al = al && aligned(p, a);
     const int run = conv_bwd_run(g, al ? 4 : 1);

@@ -15,150 +15,250 @@ namespace ssd {
 namespace {
 
 // One pass over a run of chunks of one sequence and one block of channels.
-// Forward (REV = false): m = B, x = u, z gates the output.  Reverse: m = C,
-// x = dout gated by z, tokens from the last to the first.
+//   kOut      forward with the output: m = B, c = C, x = u, z gates the output
+//   kStates   forward, states only
+//   kReverse  m = C, x = dout gated by z, tokens from the last to the first
+// The block's threads first turn a tile of kScanChunk tokens into (delta,
+// delta u) pairs and f32 matrix rows in shared memory, then walk it with the
+// states in registers.  Tiles are double buffered: the next tile's loads are
+// issued before the walk and converted after it, one barrier a tile.
+enum PassMode { kOut, kStates, kReverse };
+
 template <typename TI> struct PassArgs {
     const TI *x, *dt, *z, *m, *cm;
     const float *A, *D, *bias;
     const float *start;  // [B][segments][dim][N], nullptr: zeros
-    TI *y;               // forward output, or nullptr: states only
+    TI *y;               // forward output
     float *last;         // final state (forward), initial state's gradient (reverse), or nullptr
     float *kept;         // [B][nc][dim][N] state entering each chunk, or nullptr
     float *seg_end;      // [B][segments][dim][N] end state of each segment, or nullptr
     float *seg_dsum;     // [B][segments][dim] sum of delta of each segment
-    int64_t row_x;
+    int64_t row_x, row_m;
     int64_t chunks_per_seg, first_seg, n_seg;
-    bool vec;
+    bool vec, vec_bc;
 };
 
-template <typename TI, int LN, bool REV>
-__global__ void __launch_bounds__(kScanThreads) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
+template <int LN, int MODE, int NT> struct PassTile {
+    static constexpr int CB = NT / LN, NP = 4 * LN;
+    // row pitch of y: the LN tokens that a batch stores together start in different banks
+    static constexpr int YP = (CB + 31) / 32 * 32 + (32 / LN > 4 ? 32 / LN : 4);
+    struct Buf {
+        float4 dx[kScanChunk][CB];  // delta twice, then twice what multiplies the matrix row
+        float m[kScanChunk * NP];
+        float c[MODE == kOut ? kScanChunk * NP : 4];
+        float y[MODE == kOut ? kScanChunk * YP : 4];
+    } buf[2];
+};
+
+template <typename TI, int LN, int MODE, int NT>
+__global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
 {
-    constexpr int CB = kScanThreads / LN, T = kScanChunk, NP = 4 * LN;
-    constexpr int QUADS = T * CB / 4, QPT = (QUADS + kScanThreads - 1) / kScanThreads;
-    __shared__ float2 s_dx[T][CB];  // delta, and what multiplies the matrix row
-    __shared__ __align__(16) float s_m[T * NP], s_c[T * NP];
-    __shared__ float s_y[REV ? 1 : T][CB];
+    constexpr int CB = NT / LN, T = kScanChunk, NP = 4 * LN;
+    constexpr int QUADS = T * CB / 4, QPT = (QUADS + NT - 1) / NT, COLS = CB / 4;
+    constexpr int MATS = MODE == kOut ? 2 : 1, BQ = (MATS * T * LN + NT - 1) / NT;
+    constexpr bool REV = MODE == kReverse;
+    using Tile = PassTile<LN, MODE, NT>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Tile &sm = *reinterpret_cast<Tile *>(smem_raw);
     const int tid = threadIdx.x;
     const int64_t nblk = (g.kpg + CB - 1) / CB;
     const int grp = (int)(blockIdx.x / nblk);
-    const int64_t c0 = (blockIdx.x - grp * nblk) * CB;       // first channel, within the group
+    const int64_t c0 = (blockIdx.x - grp * nblk) * CB;  // first channel, within the group
     const int nch = (int)min64(CB, g.kpg - c0);
     const int64_t ch0 = grp * g.kpg + c0;
     const int64_t b = blockIdx.z, seg = a.first_seg + blockIdx.y;
     const int64_t nc = (g.seqlen + T - 1) / T;
     const int64_t cbeg = seg * a.chunks_per_seg, cend = min64(cbeg + a.chunks_per_seg, nc);
+    const int N = (int)g.N;
     // this thread's states
     const int c = tid / LN, n0 = 4 * (tid % LN);
-    const int nn = c < nch ? (int)g.N - n0 : 0;  // live states (may exceed 4)
-    const int64_t st = (ch0 + c) * g.N + n0;     // its place in a [dim][N] array
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, A2[4] = {0.f, 0.f, 0.f, 0.f}, dsum = 0.f;
+    const int nn = c < nch ? N - n0 : 0;      // live states (may exceed 4)
+    const int64_t st = (ch0 + c) * g.N + n0;  // its place in a [dim][N] array
+    f32x2 h0 = 0, h1 = 0, A0 = 0, A1 = 0;
+    float dsum = 0.f;
     if (nn > 0) {
-        load_states(a.A + st, nn, A2);
-        if (a.start)
-            load_states(a.start + (b * a.n_seg + seg) * g.dim * g.N + st, nn, h);
+        float v[4];
+        load_states(a.A + st, nn, v);
+        A0 = pk2(decay_rate(v[0]), decay_rate(v[1]));
+        A1 = pk2(decay_rate(v[2]), decay_rate(v[3]));
+        if (a.start) {
+            load_states(a.start + (b * a.n_seg + seg) * g.dim * g.N + st, nn, v);
+            h0 = pk2(v[0], v[1]);
+            h1 = pk2(v[2], v[3]);
+        }
     }
+    // this thread's elementwise work: one column of four channels
+    const int cq = 4 * (tid % COLS), nq = nch - cq;
+    float bias[4] = {}, Dv[4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        A2[i] *= kLog2e;
+    for (int e = 0; e < 4; ++e)
+        if (e < nq) {
+            bias[e] = a.bias ? a.bias[ch0 + cq + e] : 0.f;
+            Dv[e] = MODE == kOut && a.D ? a.D[ch0 + cq + e] : 0.f;
+        }
 
-    for (int64_t k = 0; k < cend - cbeg; ++k) {
-        const int64_t chunk = REV ? cend - 1 - k : cbeg + k;
-        const int64_t t0 = chunk * T;
-        const int nt = (int)min64(T, g.seqlen - t0);
-        Raw4<TI> xr[QPT], zr[QPT];
+    Raw4<TI> xr[QPT], dr[QPT], zr[QPT], br[BQ], xk[QPT], zk[QPT];
+    auto fetch = [&](int64_t chunk) {
+        const int64_t tok0 = b * g.seqlen + chunk * T;
+        const int nt = (int)min64(T, g.seqlen - chunk * T);
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
-            const int q = tid + i * kScanThreads;
-            const int t = q / (CB / 4), cq = 4 * (q % (CB / 4));
+            const int q = tid + i * NT, t = q / COLS;
+            xr[i] = dr[i] = zr[i] = Raw4<TI>{};
+            if (q < QUADS && t < nt && nq > 0) {
+                const int64_t tok = tok0 + t;
+                xr[i] = load_raw4(a.x + tok * a.row_x + ch0 + cq, nq, a.vec);
+                dr[i] = load_raw4(a.dt + tok * g.row_dt + ch0 + cq, nq, a.vec);
+                if (a.z)
+                    zr[i] = load_raw4(a.z + tok * g.row_z + ch0 + cq, nq, a.vec);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BQ; ++i) {
+            const int q = tid + i * NT, w = q / (T * LN), t = q / LN % T, n = 4 * (q % LN);
+            br[i] = Raw4<TI>{};
+            if (q < MATS * T * LN && t < nt && n < N)
+                br[i] = load_raw4((w ? a.cm + (tok0 + t) * g.row_c : a.m + (tok0 + t) * a.row_m) + grp * g.N + n,
+                                  N - n, a.vec_bc);
+        }
+    };
+    auto put = [&](int64_t chunk, typename Tile::Buf &s) {
+        const int nt = (int)min64(T, g.seqlen - chunk * T);
+#pragma unroll
+        for (int i = 0; i < QPT; ++i) {
+            const int q = tid + i * NT, t = q / COLS;
             if (q >= QUADS)
                 break;
-            const int n = t < nt ? nch - cq : 0;
-            const int64_t tok = b * g.seqlen + t0 + t;
-            Raw4<TI> dr{};
-            xr[i] = zr[i] = dr;
-            if (n > 0) {
-                xr[i] = load_raw4(a.x + tok * a.row_x + ch0 + cq, n, a.vec);
-                dr = load_raw4(a.dt + tok * g.row_dt + ch0 + cq, n, a.vec);
-                if (a.z)
-                    zr[i] = load_raw4(a.z + tok * g.row_z + ch0 + cq, n, a.vec);
-            }
             float xv[4], dv[4], zv[4];
             unpack<TI, 4>(xr[i], xv);
-            unpack<TI, 4>(dr, dv);
-            unpack<TI, 4>(zr[i], zv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float d = 0.f, v = 0.f;
-                if (e < n) {
-                    d = dv[e] + (a.bias ? a.bias[ch0 + cq + e] : 0.f);
-                    d = g.softplus ? softplus(d) : d;
-                    v = REV ? (a.z ? xv[e] * fast_silu(zv[e]) : xv[e]) : d * xv[e];
-                }
-                s_dx[t][cq + e] = make_float2(d, v);
-            }
-        }
-        const int64_t tok0 = b * g.seqlen + t0;
-        load_rows<TI, LN>(a.m + tok0 * (REV ? g.row_c : g.row_b) + grp * g.N, REV ? g.row_c : g.row_b, nt,
-                          (int)g.N, s_m);
-        if (!REV && a.y)
-            load_rows<TI, LN>(a.cm + tok0 * g.row_c + grp * g.N, g.row_c, nt, (int)g.N, s_c);
-        __syncthreads();
-        if (a.kept && nn > 0)
-            store_states(a.kept + (b * nc + chunk) * g.dim * g.N + st, nn, h);
-        for (int i = 0; i < nt; ++i) {
-            const int t = REV ? nt - 1 - i : i;
-            const float2 dx = s_dx[t][c];
-            const float4 m = *reinterpret_cast<const float4 *>(&s_m[t * NP + n0]);
-            const float mv[4] = {m.x, m.y, m.z, m.w};
-            dsum += dx.x;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float d = ex2(dx.x * A2[e]);
-                h[e] = REV ? d * fmaf(dx.y, mv[e], h[e]) : fmaf(d, h[e], dx.y * mv[e]);
-            }
-            if (!REV && a.y) {
-                const float4 cv = *reinterpret_cast<const float4 *>(&s_c[t * NP + n0]);
-                float s = h[0] * cv.x;
-                s = fmaf(h[1], cv.y, s);
-                s = fmaf(h[2], cv.z, s);
-                s = fmaf(h[3], cv.w, s);
-                s = lane_sum<LN>(s);
-                if (n0 == 0)
-                    s_y[REV ? 0 : t][c] = s;
-            }
-        }
-        __syncthreads();
-        if (!REV && a.y) {
-#pragma unroll
-            for (int i = 0; i < QPT; ++i) {
-                const int q = tid + i * kScanThreads;
-                const int t = q / (CB / 4), cq = 4 * (q % (CB / 4));
-                if (q >= QUADS)
-                    break;
-                const int n = t < nt ? nch - cq : 0;
-                if (n <= 0)
-                    continue;
-                float xv[4], zv[4], o[4];
-                unpack<TI, 4>(xr[i], xv);
+            unpack<TI, 4>(dr[i], dv);
+            if (REV)
                 unpack<TI, 4>(zr[i], zv);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[e] = s_y[REV ? 0 : t][cq + e];
-                    if (a.D && e < n)
-                        o[e] = fmaf(a.D[ch0 + cq + e], xv[e], o[e]);
-                    if (a.z)
-                        o[e] *= fast_silu(zv[e]);
+            for (int e = 0; e < 4; e += 2) {
+                float d0 = dv[e] + bias[e], d1 = dv[e + 1] + bias[e + 1];
+                if (g.softplus)
+                    softplus2(d0, d1, d0, d1);
+                const bool on = t < nt;
+                d0 = on && e < nq ? d0 : 0.f;
+                d1 = on && e + 1 < nq ? d1 : 0.f;
+                float v0, v1;
+                if (REV) {
+                    v0 = a.z ? xv[e] * fast_silu(zv[e]) : xv[e];
+                    v1 = a.z ? xv[e + 1] * fast_silu(zv[e + 1]) : xv[e + 1];
+                } else {
+                    un2(mul2(pk2(d0, d1), pk2(xv[e], xv[e + 1])), v0, v1);
                 }
-                store4(a.y + (b * g.seqlen + t0 + t) * g.dim + ch0 + cq, o, n, a.vec);
+                s.dx[t][cq + e] = make_float4(d0, d0, v0, v0);
+                s.dx[t][cq + e + 1] = make_float4(d1, d1, v1, v1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BQ; ++i) {
+            const int q = tid + i * NT, w = q / (T * LN), r = q % (T * LN);
+            float v[4];
+            if (q >= MATS * T * LN)
+                break;
+            unpack<TI, 4>(br[i], v);
+            store_vec<float, 4>((w ? s.c : s.m) + 4 * r, v);
+        }
+    };
+    auto at = [&](int64_t k) { return REV ? cend - 1 - k : cbeg + k; };
+
+    const int64_t n_tiles = cend - cbeg;
+    fetch(at(0));
+    put(at(0), sm.buf[0]);
+#pragma unroll
+    for (int i = 0; i < QPT; ++i) {
+        xk[i] = xr[i];
+        zk[i] = zr[i];
+    }
+    __syncthreads();
+    for (int64_t k = 0; k < n_tiles; ++k) {
+        const int64_t chunk = at(k);
+        const int nt = (int)min64(T, g.seqlen - chunk * T);
+        typename Tile::Buf &s = sm.buf[k & 1];
+        if (k + 1 < n_tiles)
+            fetch(at(k + 1));
+        if (a.kept && nn > 0) {
+            float v[4];
+            un2(h0, v[0], v[1]);
+            un2(h1, v[2], v[3]);
+            store_states(a.kept + (b * nc + chunk) * g.dim * g.N + st, nn, v);
+        }
+        // LN tokens at a time, whose outputs are summed over the lanes together;
+        // tokens past the end have delta = x = 0 and change nothing
+        constexpr int BT = LN < 4 ? 4 : LN;
+#pragma unroll 1
+        for (int i0 = 0; i0 < T; i0 += BT) {
+            const int tb = REV ? T - BT - i0 : i0;
+            if (tb >= nt)
+                continue;
+            float v[BT];
+#pragma unroll
+            for (int i = 0; i < BT; ++i) {
+                const int t = tb + (REV ? BT - 1 - i : i);
+                const ulonglong2 dx = *reinterpret_cast<const ulonglong2 *>(&s.dx[t][c]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                const f32x2 d0 = ex2_2(mul2(dx.x, A0)), d1 = ex2_2(mul2(dx.x, A1));
+                if (MODE != kOut)
+                    dsum += __uint_as_float((unsigned)dx.x);
+                if (REV) {
+                    h0 = mul2(d0, fma2(dx.y, m.x, h0));
+                    h1 = mul2(d1, fma2(dx.y, m.y, h1));
+                } else {
+                    h0 = fma2(d0, h0, mul2(dx.y, m.x));
+                    h1 = fma2(d1, h1, mul2(dx.y, m.y));
+                }
+                if (MODE == kOut) {
+                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
+                    v[i] = hsum(fma2(h1, cv.y, mul2(h0, cv.x)));
+                }
+            }
+            if (MODE == kOut) {
+#pragma unroll
+                for (int i = 0; i < BT; i += LN) {
+                    float w[LN];
+#pragma unroll
+                    for (int e = 0; e < LN; ++e)
+                        w[e] = v[i + e];
+                    s.y[(tb + i + tid % LN) * Tile::YP + c] = lane_transpose_sum<LN>(w);
+                }
+            }
+        }
+        if (k + 1 < n_tiles)
+            put(at(k + 1), sm.buf[(k + 1) & 1]);
+        __syncthreads();
+        if (MODE == kOut) {
+#pragma unroll
+            for (int i = 0; i < QPT; ++i) {
+                const int q = tid + i * NT, t = q / COLS;
+                if (q < QUADS && t < nt && nq > 0) {
+                    float xv[4], zv[4], o[4];
+                    unpack<TI, 4>(xk[i], xv);
+                    unpack<TI, 4>(zk[i], zv);
+                    load_vec<float, 4>(&s.y[t * Tile::YP + cq], o);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = fmaf(Dv[e], xv[e], o[e]);
+                        if (a.z)
+                            o[e] *= fast_silu(zv[e]);
+                    }
+                    store4(a.y + (b * g.seqlen + chunk * T + t) * g.dim + ch0 + cq, o, nq, a.vec);
+                }
+                xk[i] = xr[i];
+                zk[i] = zr[i];
             }
         }
     }
     if (nn > 0) {
+        float v[4];
+        un2(h0, v[0], v[1]);
+        un2(h1, v[2], v[3]);
         if (a.last && (REV ? cbeg == 0 : cend == nc))
-            store_states(a.last + b * g.dim * g.N + st, nn, h);
+            store_states(a.last + b * g.dim * g.N + st, nn, v);
         if (a.seg_end) {
-            store_states(a.seg_end + (b * a.n_seg + seg) * g.dim * g.N + st, nn, h);
+            store_states(a.seg_end + (b * a.n_seg + seg) * g.dim * g.N + st, nn, v);
             if (n0 == 0)
                 a.seg_dsum[(b * a.n_seg + seg) * g.dim + ch0 + c] = dsum;
         }
@@ -177,7 +277,7 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
     if (i >= batch * DN)
         return;
     const int64_t b = i / DN, r = i - b * DN, d = r / N;
-    const float A2 = A[r] * kLog2e;
+    const float A2 = decay_rate(A[r]);
     float h = start ? start[i] : 0.f;
     for (int64_t k = 0; k < n_seg; ++k) {
         const int64_t s = b * n_seg + (REV ? n_seg - 1 - k : k);
@@ -223,7 +323,7 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
         const float du = dl * uv;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            h[e] = fmaf(ex2(dl * (av[e] * kLog2e)), h[e], du * bv[e]);
+            h[e] = fmaf(ex2(dl * decay_rate(av[e])), h[e], du * bv[e]);
             s = fmaf(h[e], cv[e], s);
         }
         store_states(state_out + bd * g.N + n0, nn, h);
@@ -240,21 +340,33 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <typename TI, bool REV>
-cudaError_t launch_pass(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, cudaStream_t st)
+template <typename TI, int LN, int MODE>
+cudaError_t launch_pass_ln(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, cudaStream_t st)
 {
-    const int LN = scan_lanes(g.N);
-    const int64_t CB = kScanThreads / LN;
+    constexpr int NT = kScanThreads;
+    constexpr int64_t CB = NT / LN;
     const dim3 grid((unsigned)(g.G * ((g.kpg + CB - 1) / CB)), (unsigned)segs, (unsigned)g.batch);
-    switch (LN) {
-    case 1: scan_pass_kernel<TI, 1, REV><<<grid, kScanThreads, 0, st>>>(a, g); break;
-    case 2: scan_pass_kernel<TI, 2, REV><<<grid, kScanThreads, 0, st>>>(a, g); break;
-    case 4: scan_pass_kernel<TI, 4, REV><<<grid, kScanThreads, 0, st>>>(a, g); break;
-    case 8: scan_pass_kernel<TI, 8, REV><<<grid, kScanThreads, 0, st>>>(a, g); break;
-    default: scan_pass_kernel<TI, 16, REV><<<grid, kScanThreads, 0, st>>>(a, g); break;
+    constexpr size_t smem = sizeof(PassTile<LN, MODE, NT>);
+    auto k = scan_pass_kernel<TI, LN, MODE, NT>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
     }
+    k<<<grid, NT, smem, st>>>(a, g);
     note_launch(1);
     return cudaGetLastError();
+}
+template <typename TI, int MODE>
+cudaError_t launch_pass(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, cudaStream_t st)
+{
+    switch (scan_lanes(g.N)) {
+    case 1: return launch_pass_ln<TI, 1, MODE>(a, g, segs, st);
+    case 2: return launch_pass_ln<TI, 2, MODE>(a, g, segs, st);
+    case 4: return launch_pass_ln<TI, 4, MODE>(a, g, segs, st);
+    case 8: return launch_pass_ln<TI, 8, MODE>(a, g, segs, st);
+    default: return launch_pass_ln<TI, 16, MODE>(a, g, segs, st);
+    }
 }
 
 // Runs a pass, in segments where the channels alone cannot fill the GPU: the
@@ -262,23 +374,29 @@ cudaError_t launch_pass(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, 
 template <typename TI, bool REV>
 cudaError_t run_pass(PassArgs<TI> a, const float *start, void *ws, const ScanGeom &g, cudaStream_t st)
 {
+    constexpr int ENDS = REV ? kReverse : kStates;
     const ScanSegs sp = scan_segments(g);
     a.chunks_per_seg = sp.chunks_per_seg;
     a.n_seg = sp.n_seg;
     a.first_seg = 0;
     a.seg_end = a.seg_dsum = nullptr;
     a.start = start;
+    a.row_m = REV ? g.row_c : g.row_b;
+    const size_t al = 4 * sizeof(TI);
+    a.vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(a.m, al) && aligned(a.cm, al);
     if (sp.n_seg > 1) {
         float *seg = static_cast<float *>(ws);
         float *dsum = seg + g.batch * sp.n_seg * g.dim * g.N;
         PassArgs<TI> e = a;
         e.start = nullptr;
         e.y = nullptr;
+        if (!REV)
+            e.z = nullptr;
         e.last = e.kept = nullptr;
         e.seg_end = seg;
         e.seg_dsum = dsum;
         e.first_seg = REV ? 1 : 0;
-        cudaError_t err = launch_pass<TI, REV>(e, g, sp.n_seg - 1, st);
+        cudaError_t err = launch_pass<TI, ENDS>(e, g, sp.n_seg - 1, st);
         if (err != cudaSuccess)
             return err;
         const int64_t n = g.batch * g.dim * g.N;
@@ -290,7 +408,9 @@ cudaError_t run_pass(PassArgs<TI> a, const float *start, void *ws, const ScanGeo
             return err;
         a.start = seg;
     }
-    return launch_pass<TI, REV>(a, g, sp.n_seg, st);
+    if (REV || !a.y)
+        return launch_pass<TI, ENDS>(a, g, sp.n_seg, st);
+    return launch_pass<TI, kOut>(a, g, sp.n_seg, st);
 }
 
 bool quads_ok(const ScanGeom &g, const void *x, int64_t row_x, const void *dt, const void *z, const void *y,

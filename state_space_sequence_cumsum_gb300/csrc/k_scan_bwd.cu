@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_grad_kernel(GradArgs<TI> a,
                 to4(*reinterpret_cast<const float4 *>(&s.m[t * NP + n0]), m);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    h[e] = fmaf(ex2(dd.x * (A2[e] * kLog2e)), h[e], dd.y * m[e]);
+                    h[e] = fmaf(ex2(dd.x * decay_rate(A2[e])), h[e], dd.y * m[e]);
             }
             s.h[k][tid] = make_float4(h[0], h[1], h[2], h[3]);
             s.e[k][tid] = make_float4(e0[0], e0[1], e0[2], e0[3]);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_grad_kernel(GradArgs<TI> a,
                     load_states(a.A + (ch0 + c) * g.N + n0, nn, A2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    A2[e] *= kLog2e;
+                    A2[e] = decay_rate(A2[e]);
                 if (sub)
                     to4(s.h[k][tid], h);
                 else if (c < nch && nn > 0)

@@ -72,6 +72,32 @@ template <int LN> __device__ __forceinline__ float lane_sum(float v)
     return v;
 }
 
+// Sums LN values over a channel's LN lanes at once; lane j returns the sum of
+// every lane's v[j].  Each step sends one half and keeps the other, so LN
+// sums take LN - 1 shuffles where one at a time they take LN log2 LN.
+template <int LN> __device__ __forceinline__ float lane_transpose_sum(float (&v)[LN])
+{
+#pragma unroll
+    for (int o = 1, n = LN; o < LN; o *= 2, n /= 2) {
+        const bool up = threadIdx.x & o;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = up ? v[2 * i + 1] : v[2 * i];
+            const float send = up ? v[2 * i] : v[2 * i + 1];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    return v[0];
+}
+
+// A decay rate in log2 units.  -inf becomes the lowest float, so that a token
+// without a step (delta = 0, as past a sequence's end) still keeps the state.
+__device__ __forceinline__ float decay_rate(float a)
+{
+    const float r = a * kLog2e;
+    return r == -INFINITY ? -3.402823466e38f : r;
+}
+
 // The rows of B or C of a tile, as f32 [kScanChunk][4 LN], zero past N and
 // past the last token.
 template <typename TI, int LN>

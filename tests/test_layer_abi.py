@@ -194,32 +194,33 @@ def test_binding_refusals():
     torch = pytest.importorskip("torch")
     import state_space_sequence_cumsum_gb300 as ssd
     x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
-    with pytest.raises(ValueError):
-        ssd.ssd_causal_conv(x, w)                              # a CPU tensor
-    with pytest.raises(ValueError):
-        ssd.ssd_causal_conv(x, torch.zeros(7, 4))
-    with pytest.raises(ValueError):
-        ssd.ssd_causal_conv(x, w, activation="relu")
-    with pytest.raises(TypeError):
-        ssd.ssd_causal_conv(x.half(), w)
-    with pytest.raises(TypeError):
-        ssd.ssd_causal_conv(x, w.double())
-    with pytest.raises(ValueError):
-        ssd.ssd_causal_conv(x.transpose(1, 2).contiguous().transpose(1, 2), w)
-    with pytest.raises(ValueError):
-        ssd.ssd_causal_conv(torch.zeros(2, 8, 8)[:, ::3].expand(2, 3, 8)[:, :2], w)  # uneven rows
     A, m = torch.zeros(8, 4), torch.zeros(1, 4, 4)
-    with pytest.raises(ValueError):
-        ssd.ssd_selective_scan(x, x, A, m, torch.zeros(1, 4, 5))
-    with pytest.raises(ValueError):
-        ssd.ssd_selective_scan(x, x, A, torch.zeros(1, 4, 3, 4), torch.zeros(1, 4, 3, 4))
-    with pytest.raises(ValueError):
-        ssd.ssd_selective_scan(x, x[:, :2], A, m, m)
-    with pytest.raises(TypeError):
-        ssd.ssd_selective_scan(x, x, A, m, m, initial_state=torch.zeros(1, 8, 4, dtype=torch.bfloat16))
-    with pytest.raises(ValueError):
-        ssd.ssd_block_norm(x, x, torch.zeros(7))
-    with pytest.raises(ValueError):
-        ssd.ssd_block_norm(x, x, torch.zeros(8), gate=torch.zeros(3, 8))
-    with pytest.raises(ValueError):
-        ssd.ssd_block_norm(x, torch.zeros(1, 4, 9), torch.zeros(8))
+
+    def refused(error, match, call, *args, **kw):
+        with pytest.raises(error, match=match):
+            call(*args, **kw)
+    refused(ValueError, "CUDA tensors", ssd.ssd_causal_conv, x, w)
+    refused(ValueError, "weight must be", ssd.ssd_causal_conv, x, torch.zeros(7, 4))
+    refused(ValueError, "activation", ssd.ssd_causal_conv, x, w, activation="relu")
+    refused(TypeError, "bfloat16 or float32", ssd.ssd_causal_conv, x.half(), w)
+    refused(TypeError, "weight must be", ssd.ssd_causal_conv, x, w.double())
+    refused(TypeError, "x must be a tensor", ssd.ssd_causal_conv, None, w)
+    refused(ValueError, "last dimension", ssd.ssd_causal_conv,
+            x.transpose(1, 2).contiguous().transpose(1, 2), w)
+    refused(ValueError, "evenly spaced", ssd.ssd_causal_conv, torch.zeros(2, 8, 8)[:, ::3], w)
+    refused(ValueError, "rows overlap", ssd.ssd_causal_conv, torch.zeros(1, 1, 8).expand(1, 4, 8), w)
+    refused(ValueError, "initial_state must be", ssd.ssd_causal_conv, x, w, initial_state=torch.zeros(1, 2, 8))
+    refused(ValueError, "C must be", ssd.ssd_selective_scan, x, x, A, m, torch.zeros(1, 4, 5))
+    refused(ValueError, "multiple of the groups", ssd.ssd_selective_scan, x, x, A, torch.zeros(1, 4, 3, 4),
+            torch.zeros(1, 4, 3, 4))
+    refused(ValueError, "dt must be", ssd.ssd_selective_scan, x, x[:, :2], A, m, m)
+    refused(TypeError, "initial_state must be", ssd.ssd_selective_scan, x, x, A, m, m,
+            initial_state=torch.zeros(1, 8, 4, dtype=torch.bfloat16))
+    refused(ValueError, "state must be", ssd.ssd_selective_scan_step, x[:, 0], x[:, 0], A, m[:, 0], m[:, 0], None,
+            torch.zeros(1, 8, 5))
+    refused(ValueError, "weight must be", ssd.ssd_block_norm, x, x, torch.zeros(7))
+    refused(ValueError, "gate's rows", ssd.ssd_block_norm, x, x, torch.zeros(8), gate=torch.zeros(3, 8))
+    refused(ValueError, "residual must be", ssd.ssd_block_norm, x, torch.zeros(1, 4, 9), torch.zeros(8))
+    refused(ValueError, "y must be contiguous", ssd.ssd_block_norm, x[:, ::2], x, torch.zeros(8))
+    refused(TypeError, "residual must be", ssd.ssd_block_norm, x, None, torch.zeros(8),
+            residual_dtype=torch.bfloat16)

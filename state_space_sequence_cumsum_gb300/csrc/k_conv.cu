@@ -17,35 +17,91 @@ namespace ssd {
 namespace {
 
 constexpr int kConvThreads = 256;
-constexpr int kGroup = 4;  // tokens whose loads a thread has in flight
 
-// A thread's VEC x W weights are one run of floats: four at a time where VEC > 1
-// (rows then start on 16-byte boundaries).
+// A thread's VEC channels (VEC even, or one) as f32 pairs; with one channel
+// the second of the pair is unused.
+template <int VEC> constexpr int kPairs = (VEC + 1) / 2;
+template <typename TI, int VEC> using RawV = typename Pack<TI, VEC>::T;
+
+template <typename TI, int VEC> __device__ __forceinline__ void to_pairs(const RawV<TI, VEC> &r, f32x2 (&p)[kPairs<VEC>])
+{
+    float v[VEC];
+    unpack<TI, VEC>(r, v);
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i)
+        p[i] = pk2(v[2 * i], 2 * i + 1 < VEC ? v[(2 * i + 1) % VEC] : 0.f);
+}
+template <typename TI, int VEC> __device__ __forceinline__ void store_pairs(TI *p, const f32x2 (&o)[kPairs<VEC>])
+{
+    float v[VEC];
+#pragma unroll
+    for (int i = 0; i < kPairs<VEC>; ++i) {
+        float x, y;
+        un2(o[i], x, y);
+        v[2 * i] = x;
+        if (2 * i + 1 < VEC)
+            v[(2 * i + 1) % VEC] = y;
+    }
+    store_vec<TI, VEC>(p, v);
+}
+template <typename TI, int VEC> __device__ __forceinline__ RawV<TI, VEC> load_raw(const TI *p)
+{
+    return *reinterpret_cast<const RawV<TI, VEC> *>(p);
+}
+
+// A thread's VEC x W weights are one run of floats: two at a time where
+// VEC > 1 (rows then start on 8-byte boundaries).
 template <int VEC, int W>
 __device__ __forceinline__ void load_weights(const float *__restrict__ w, const float *__restrict__ bias,
-                                             int64_t c, float (&wv)[W][VEC], float (&bv)[VEC])
+                                             int64_t c, f32x2 (&wv)[W][kPairs<VEC>], f32x2 (&bv)[kPairs<VEC>])
 {
-    constexpr int NL = VEC > 1 ? 4 : 1;
+    constexpr int NL = VEC > 1 ? 2 : 1;
+    float t[kPairs<VEC> * 2 * W] = {};
 #pragma unroll
     for (int q = 0; q < VEC * W; q += NL) {
         float v[NL];
         load_vec<float, NL>(w + c * W + q, v);
 #pragma unroll
         for (int e = 0; e < NL; ++e)
-            wv[(q + e) % W][(q + e) / W] = v[e];
+            t[q + e] = v[e];
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        bv[i] = bias ? bias[c + i] : 0.f;
+    for (int i = 0; i < kPairs<VEC>; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            wv[k][i] = pk2(t[2 * i * W + k], t[(2 * i + 1) * W + k]);
+        bv[i] = bias ? pk2(bias[c + 2 * i], 2 * i + 1 < VEC ? bias[c + 2 * i + 1] : 0.f) : 0;
+    }
 }
 
-// One thread: VEC channels of `run` consecutive tokens of one sequence.
+// The convolution of one window.
+template <int P, int W>
+__device__ __forceinline__ f32x2 window_sum(const f32x2 (&wv)[W][P], const f32x2 (&bv)[P], const f32x2 (&win)[W][P], int i)
+{
+    f32x2 s = bv[i];
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+        s = fma2(wv[k][i], win[k][i], s);
+    return s;
+}
+template <int P, int W> __device__ __forceinline__ void shift(f32x2 (&win)[W][P])
+{
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            win[k][i] = win[k + 1][i];
+}
+
+// One thread: VEC channels of `run` consecutive tokens of one sequence, in
+// groups of kGroup tokens whose loads are issued together.
 template <typename TI, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const TI *__restrict__ init, TI *__restrict__ y, TI *__restrict__ fin, ConvGeom g, int run,
             int64_t n_runs)
 {
+    constexpr int P = kPairs<VEC>, kGroup = 8;
     const int64_t nv = g.dim / VEC;
     const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
     const int64_t r = idx / nv;
@@ -53,86 +109,87 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
         return;
     const int64_t c = (idx - r * nv) * VEC;
     const int64_t b = r / n_runs, t0 = (r - b * n_runs) * run;
-    float wv[W][VEC], bv[VEC], win[W][VEC];
+    f32x2 wv[W][P], bv[P], win[W][P];
     load_weights<VEC, W>(w, bias, c, wv, bv);
-    const TI *xb = x + b * g.seqlen * g.row + c;
-    TI *yb = y + b * g.seqlen * g.dim + c;
+    const TI *xp = x + (b * g.seqlen + t0) * g.row + c;
+    TI *yp = y + (b * g.seqlen + t0) * g.dim + c;
     // the W - 1 tokens before the run
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int64_t t = t0 - (W - 1) + k;
+        RawV<TI, VEC> v{};
         if (t >= 0)
-            load_vec<TI, VEC>(xb + t * g.row, win[k]);
+            v = load_raw<TI, VEC>(xp + (k - (W - 1)) * g.row);
         else if (init)
-            load_vec<TI, VEC>(init + (b * (W - 1) + (W - 1) + t) * g.dim + c, win[k]);
-        else
-            for (int i = 0; i < VEC; ++i)
-                win[k][i] = 0.f;
+            v = load_raw<TI, VEC>(init + (b * (W - 1) + (W - 1) + t) * g.dim + c);
+        to_pairs<TI, VEC>(v, win[k]);
     }
-    const int64_t t1 = min64(t0 + run, g.seqlen);
-    // kGroup tokens' loads are issued before the first is used
-    for (int64_t tg = t0; tg < t1; tg += kGroup) {
-        typename Pack<TI, VEC>::T raw[kGroup];
+    const int n = (int)min64(run, g.seqlen - t0);
+    auto token = [&](const RawV<TI, VEC> &raw) {
+        to_pairs<TI, VEC>(raw, win[W - 1]);
+        f32x2 o[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            o[i] = window_sum<P, W>(wv, bv, win, i);
+            if (g.silu)
+                o[i] = mul2(o[i], sigmoid2(o[i]));
+        }
+        shift<P, W>(win);
+        store_pairs<TI, VEC>(yp, o);
+        yp += g.dim;
+    };
+    int t = 0;
+    for (; t + kGroup <= n; t += kGroup) {
+        RawV<TI, VEC> raw[kGroup];
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
-            if (tg + j < t1)
-                raw[j] = *reinterpret_cast<const typename Pack<TI, VEC>::T *>(xb + (tg + j) * g.row);
+            raw[j] = load_raw<TI, VEC>(xp + j * g.row);
+        xp += kGroup * g.row;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-            if (tg + j >= t1)
-                break;
-            unpack<TI, VEC>(raw[j], win[W - 1]);
-            float o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float s = bv[i];
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    s = fmaf(wv[k][i], win[k][i], s);
-                o[i] = g.silu ? fast_silu(s) : s;
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-                    win[k][i] = win[k + 1][i];
-            }
-            store_vec<TI, VEC>(yb + (tg + j) * g.dim, o);
-        }
+        for (int j = 0; j < kGroup; ++j)
+            token(raw[j]);
     }
-    if (fin && t1 == g.seqlen)
+    for (; t < n; ++t) {
+        token(load_raw<TI, VEC>(xp));
+        xp += g.row;
+    }
+    if (fin && t0 + n == g.seqlen)
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            store_vec<TI, VEC>(fin + (b * (W - 1) + k) * g.dim + c, win[k]);
+            store_pairs<TI, VEC>(fin + (b * (W - 1) + k) * g.dim + c, win[k]);
 }
 
-// One token of every sequence; state and state_out may be one buffer.
+// One token of every sequence (blockIdx.y); state and state_out may be one buffer.
 template <typename TI, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
                  const TI *state, TI *state_out, TI *__restrict__ y, ConvGeom g)
 {
-    const int64_t nv = g.dim / VEC;
-    const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t b = idx / nv;
-    if (b >= g.batch)
+    constexpr int P = kPairs<VEC>;
+    const int64_t c = ((int64_t)blockIdx.x * kConvThreads + threadIdx.x) * VEC;
+    const int64_t b = blockIdx.y;
+    if (c >= g.dim)
         return;
-    const int64_t c = (idx - b * nv) * VEC;
-    float wv[W][VEC], bv[VEC], win[W][VEC], o[VEC];
+    f32x2 wv[W][P], bv[P], win[W][P], o[P];
+    RawV<TI, VEC> raw[W];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-        load_vec<TI, VEC>(state + (b * (W - 1) + k) * g.dim + c, win[k]);
-    load_vec<TI, VEC>(x + b * g.row + c, win[W - 1]);
+        raw[k] = load_raw<TI, VEC>(state + (b * (W - 1) + k) * g.dim + c);
+    raw[W - 1] = load_raw<TI, VEC>(x + b * g.row + c);
     load_weights<VEC, W>(w, bias, c, wv, bv);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        float s = bv[i];
+    for (int k = 0; k < W; ++k)
+        to_pairs<TI, VEC>(raw[k], win[k]);
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-            s = fmaf(wv[k][i], win[k][i], s);
-        o[i] = g.silu ? fast_silu(s) : s;
+    for (int i = 0; i < P; ++i) {
+        o[i] = window_sum<P, W>(wv, bv, win, i);
+        if (g.silu)
+            o[i] = mul2(o[i], sigmoid2(o[i]));
     }
-    store_vec<TI, VEC>(y + b * g.dim + c, o);
+    store_pairs<TI, VEC>(y + b * g.dim + c, o);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k)
-        store_vec<TI, VEC>(state_out + (b * (W - 1) + k) * g.dim + c, win[k + 1]);
+        *reinterpret_cast<RawV<TI, VEC> *>(state_out + (b * (W - 1) + k) * g.dim + c) = raw[k + 1];
 }
 
 // Backward.  With xf = (initial state | x), L + W - 1 rows, pre[i] reads
@@ -151,138 +208,163 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 TI *__restrict__ dx, TI *__restrict__ dinit, float *__restrict__ part, ConvGeom g, int run,
                 int64_t parts_per_seq)
 {
-    __shared__ float red[kBwdRuns][kBwdCols][VEC];
+    constexpr int P = kPairs<VEC>, kGroup = 4;
+    using V = RawV<TI, VEC>;
+    __shared__ f32x2 red[kBwdRuns][P][kBwdCols];
     const int64_t c = ((int64_t)blockIdx.x * kBwdCols + threadIdx.x) * VEC;
     const int64_t b = blockIdx.y / parts_per_seq;
     const int64_t e0 = ((blockIdx.y - b * parts_per_seq) * kBwdRuns + threadIdx.y) * run;
     const int64_t L = g.seqlen;
     const bool live = c < g.dim;
-    float dw[W + 1][VEC];
+    f32x2 dw[W + 1][P];
 #pragma unroll
     for (int k = 0; k <= W; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            dw[k][i] = 0.f;
+        for (int i = 0; i < P; ++i)
+            dw[k][i] = 0;
     if (live && e0 < L + W - 1) {
-        float wv[W][VEC], bv[VEC], win[W][VEC], dp[W][VEC];
+        f32x2 wv[W][P], bv[P], win[W][P], dp[W][P];
         load_weights<VEC, W>(w, bias, c, wv, bv);
         const TI *xb = x + b * L * g.row + c;
         const TI *dyb = dy + b * L * g.row_dy + c;
         TI *dxb = dx + b * L * g.dim + c;
-        auto load_xf = [&](int64_t e, float (&v)[VEC]) {
+        auto load_xf = [&](int64_t e) {
             const int64_t t = e - (W - 1);
+            V v{};
             if (t >= 0 && t < L)
-                load_vec<TI, VEC>(xb + t * g.row, v);
+                v = load_raw<TI, VEC>(xb + t * g.row);
             else if (t < 0 && e >= 0 && init)
-                load_vec<TI, VEC>(init + (b * (W - 1) + e) * g.dim + c, v);
-            else
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    v[i] = 0.f;
+                v = load_raw<TI, VEC>(init + (b * (W - 1) + e) * g.dim + c);
+            return v;
         };
 #pragma unroll
         for (int k = 0; k < W; ++k) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                dp[k][i] = 0.f;
+            for (int i = 0; i < P; ++i)
+                dp[k][i] = 0;
             if (k < W - 1)
-                load_xf(e0 - (W - 1) + k, win[k]);
+                to_pairs<TI, VEC>(load_xf(e0 - (W - 1) + k), win[k]);
         }
         const int64_t e1 = min64(e0 + run, L + W - 1);
-        for (int64_t eg = e0 - (W - 1); eg < e1; eg += kGroup) {
-            using V = typename Pack<TI, VEC>::T;
-            V xr[kGroup], yr[kGroup];
+        // dp[0] = dpre[e] from xf[e + W - 1] = x[e] and dy[e]; dp[k] = dpre[e - k]
+        auto step_in = [&](const V &xr, const V &yr) {
+            to_pairs<TI, VEC>(xr, win[W - 1]);
+            f32x2 d[P];
+            to_pairs<TI, VEC>(yr, d);
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const int64_t e = eg + j;
-                xr[j] = yr[j] = V{};
-                if (e < e1) {
-                    if (e >= 0 && e < L) {  // xf[e + W - 1] is x[e]
-                        xr[j] = *reinterpret_cast<const V *>(xb + e * g.row);
-                        yr[j] = *reinterpret_cast<const V *>(dyb + e * g.row_dy);
-                    } else if (e < 0 && e + W - 1 >= 0 && init) {
-                        xr[j] = *reinterpret_cast<const V *>(init + (b * (W - 1) + e + W - 1) * g.dim + c);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const int64_t e = eg + j;
-                if (e >= e1)
-                    break;
-                unpack<TI, VEC>(xr[j], win[W - 1]);
-                // dp[0] is dpre[e], dp[k] = dpre[e - k]; zero outside [0, L)
-                float d[VEC];
-                unpack<TI, VEC>(yr[j], d);
-                const bool in = e >= 0 && e < L;
+            for (int i = 0; i < P; ++i) {
                 if (g.silu) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        float s = bv[i];
-#pragma unroll
-                        for (int k = 0; k < W; ++k)
-                            s = fmaf(wv[k][i], win[k][i], s);
-                        d[i] = in ? d[i] * silu_grad(s, fast_sigmoid(s)) : 0.f;
-                    }
+                    const f32x2 s = window_sum<P, W>(wv, bv, win, i);
+                    d[i] = mul2(d[i], silu_grad2(s, sigmoid2(s)));
                 }
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
+                for (int k = W - 1; k > 0; --k)
+                    dp[k][i] = dp[k - 1][i];
+                dp[0][i] = d[i];
+            }
+        };
+        auto sums = [&]() {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    dw[k][i] = fma2(dp[0][i], win[k][i], dw[k][i]);
+                dw[W][i] = add2(dw[W][i], dp[0][i]);
+            }
+        };
+        auto grad = [&](f32x2 (&o)[P]) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                o[i] = mul2(wv[0][i], dp[0][i]);
+#pragma unroll
+                for (int k = 1; k < W; ++k)
+                    o[i] = fma2(wv[k][i], dp[k][i], o[i]);
+            }
+        };
+        // any row: before the sequence, past its end, or not yet this thread's own
+        auto edge = [&](int64_t e) {
+            V xr = load_xf(e + W - 1), yr{};
+            const bool in = e >= 0 && e < L;
+            if (in) {
+                yr = load_raw<TI, VEC>(dyb + e * g.row_dy);
+                step_in(xr, yr);
+            } else {
+                to_pairs<TI, VEC>(xr, win[W - 1]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
 #pragma unroll
                     for (int k = W - 1; k > 0; --k)
                         dp[k][i] = dp[k - 1][i];
-                    dp[0][i] = d[i];
+                    dp[0][i] = 0;
                 }
-                if (e >= e0) {
-                    float o[VEC];
+            }
+            if (e >= e0) {
+                if (in)
+                    sums();
+                f32x2 o[P];
+                grad(o);
+                if (dfinal && e >= L) {  // the carried rows are the last W - 1 of xf
+                    f32x2 f[P];
+                    to_pairs<TI, VEC>(load_raw<TI, VEC>(dfinal + (b * (W - 1) + e - L) * g.dim + c), f);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        float s = 0.f;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) {
-                            s = fmaf(wv[k][i], dp[k][i], s);
-                            if (in)
-                                dw[k][i] = fmaf(d[i], win[k][i], dw[k][i]);
-                        }
-                        dw[W][i] += d[i];
-                        o[i] = s;
-                    }
-                    const int64_t t = e - (W - 1);
-                    if (dfinal && e >= L) {  // the carried rows are the last W - 1 of xf
-                        float f[VEC];
-                        load_vec<TI, VEC>(dfinal + (b * (W - 1) + e - L) * g.dim + c, f);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i)
-                            o[i] += f[i];
-                    }
-                    if (t >= 0)
-                        store_vec<TI, VEC>(dxb + t * g.dim, o);
-                    else if (dinit)
-                        store_vec<TI, VEC>(dinit + (b * (W - 1) + e) * g.dim + c, o);
+                    for (int i = 0; i < P; ++i)
+                        o[i] = add2(o[i], f[i]);
                 }
+                if (e >= W - 1)
+                    store_pairs<TI, VEC>(dxb + (e - (W - 1)) * g.dim, o);
+                else if (dinit)
+                    store_pairs<TI, VEC>(dinit + (b * (W - 1) + e) * g.dim + c, o);
+            }
+            shift<P, W>(win);
+        };
+        int64_t e = e0 - (W - 1);
+        for (const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0; e < own; ++e)
+            edge(e);
+        // rows inside the sequence, kGroup tokens' loads at a time
+        const int64_t inner = min64(e1, L);
+        const TI *xp = xb + e * g.row, *yp = dyb + e * g.row_dy;
+        TI *op = dxb + (e - (W - 1)) * g.dim;
+        for (; e + kGroup <= inner; e += kGroup) {
+            V xr[kGroup], yr[kGroup];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i)
+            for (int j = 0; j < kGroup; ++j) {
+                xr[j] = load_raw<TI, VEC>(xp + j * g.row);
+                yr[j] = load_raw<TI, VEC>(yp + j * g.row_dy);
+            }
+            xp += kGroup * g.row;
+            yp += kGroup * g.row_dy;
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-                        win[k][i] = win[k + 1][i];
+            for (int j = 0; j < kGroup; ++j) {
+                step_in(xr[j], yr[j]);
+                sums();
+                f32x2 o[P];
+                grad(o);
+                store_pairs<TI, VEC>(op, o);
+                op += g.dim;
+                shift<P, W>(win);
             }
         }
+        for (; e < e1; ++e)
+            edge(e);
     }
 #pragma unroll
     for (int k = 0; k <= W; ++k) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            red[threadIdx.y][threadIdx.x][i] = dw[k][i];
+        for (int i = 0; i < P; ++i)
+            red[threadIdx.y][i][threadIdx.x] = dw[k][i];
         __syncthreads();
-        if (threadIdx.y == 0 && live)
+        if (threadIdx.y == 0 && live) {
+            f32x2 s[P];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float s = 0.f;
+            for (int i = 0; i < P; ++i) {
+                s[i] = red[0][i][threadIdx.x];
 #pragma unroll
-                for (int q = 0; q < kBwdRuns; ++q)
-                    s += red[q][threadIdx.x][i];
-                part[((int64_t)blockIdx.y * (W + 1) + k) * g.dim + c + i] = s;
+                for (int q = 1; q < kBwdRuns; ++q)
+                    s[i] = add2(s[i], red[q][i][threadIdx.x]);
             }
+            store_pairs<float, VEC>(part + ((int64_t)blockIdx.y * (W + 1) + k) * g.dim + c, s);
+        }
     }
 }
 
@@ -361,9 +443,8 @@ template <typename TI, int VEC, int W>
 cudaError_t step_w(const void *x, const float *w, const float *bias, const void *state, void *state_out,
                    void *y, const ConvGeom &g, cudaStream_t st)
 {
-    const int64_t threads = g.batch * (g.dim / VEC);
-    conv_step_kernel<TI, VEC, W>
-        <<<(unsigned)((threads + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(
+    const dim3 grid((unsigned)((g.dim / VEC + kConvThreads - 1) / kConvThreads), (unsigned)g.batch);
+    conv_step_kernel<TI, VEC, W><<<grid, kConvThreads, 0, st>>>(
             static_cast<const TI *>(x), w, bias, static_cast<const TI *>(state), static_cast<TI *>(state_out),
             static_cast<TI *>(y), g);
     note_launch(1);
@@ -396,16 +477,20 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
 
 }  // namespace
 
+// Four channels a thread where every row starts on a boundary of four (8
+// bytes of bf16, 16 of f32), else one.
 cudaError_t launch_conv(const void *x, const float *w, const float *bias, const void *init, void *y,
                         void *fin, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
-    const bool al = aligned(x, 16) && aligned(init, 16) && aligned(y, 16) && aligned(fin, 16) && aligned(w, 16);
+    const size_t a = bf16 ? 8 : 16;
+    const bool al = aligned(x, a) && aligned(init, a) && aligned(y, a) && aligned(fin, a) && aligned(w, 8) &&
+                    g.dim % 4 == 0 && g.row % 4 == 0;
     if (bf16) {
-        if (al && g.dim % 8 == 0 && g.row % 8 == 0)
-            return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 8, x, w, bias, init, y, fin, g, st);
+        if (al)
+            return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 4, x, w, bias, init, y, fin, g, st);
         return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 1, x, w, bias, init, y, fin, g, st);
     }
-    if (al && g.dim % 4 == 0 && g.row % 4 == 0)
+    if (al)
         return SSD_CONV_WIDTHS(fwd_w, float, 4, x, w, bias, init, y, fin, g, st);
     return SSD_CONV_WIDTHS(fwd_w, float, 1, x, w, bias, init, y, fin, g, st);
 }
@@ -415,7 +500,7 @@ cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, c
 {
     const size_t a = bf16 ? 8 : 16;
     const bool al = aligned(x, a) && aligned(state, a) && aligned(state_out, a) && aligned(y, a) &&
-                    aligned(w, 16) && g.dim % 4 == 0 && g.row % 4 == 0;
+                    aligned(w, 8) && g.dim % 4 == 0 && g.row % 4 == 0;
     if (bf16) {
         if (al)
             return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 4, x, w, bias, state, state_out, y, g, st);
@@ -430,31 +515,33 @@ cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, c
 size_t conv_bwd_workspace(const ConvGeom &g)
 {
     int64_t parts = 0;
-    for (int vec : {4, 1}) {
+    for (int vec : {2, 1}) {
         const int64_t p = conv_bwd_parts_per_seq(g, conv_bwd_run(g, vec)) * g.batch;
         parts = p > parts ? p : parts;
     }
     return (size_t)(parts * (g.width + 1) * g.dim) * sizeof(float);
 }
 
+// Two channels a thread (the window, the gradients behind it and the weight
+// sums of four would not leave registers for two blocks an SM), or one.
 cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, const void *init,
                             const void *dy, const void *dfinal, void *dx, float *dw, float *dbias,
                             void *dinit, float *part, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
-    const size_t a = bf16 ? 8 : 16;
-    bool al = g.dim % 4 == 0 && g.row % 4 == 0 && g.row_dy % 4 == 0 && aligned(w, 16);
+    const size_t a = bf16 ? 4 : 8;
+    bool al = g.dim % 2 == 0 && g.row % 2 == 0 && g.row_dy % 2 == 0 && aligned(w, 8);
     for (const void *p : {x, init, dy, dfinal, static_cast<const void *>(dx), static_cast<const void *>(dinit)})
         al = al && aligned(p, a);
-    const int run = conv_bwd_run(g, al ? 4 : 1);
+    const int run = conv_bwd_run(g, al ? 2 : 1);
     if (bf16) {
         if (al)
-            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias,
+            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 2, x, w, bias, init, dy, dfinal, dx, dw, dbias,
                                    dinit, part, g, run, st);
         return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit,
                                part, g, run, st);
     }
     if (al)
-        return SSD_CONV_WIDTHS(bwd_w, float, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g,
+        return SSD_CONV_WIDTHS(bwd_w, float, 2, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g,
                                run, st);
     return SSD_CONV_WIDTHS(bwd_w, float, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, run,
                            st);

@@ -97,58 +97,87 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
             Dv[e] = MODE == kOut && a.D ? a.D[ch0 + cq + e] : 0.f;
         }
 
+    // where this thread's elements of the next tile to fetch are: its column of
+    // the token t_first (then every NT / COLS-th), and its matrix quads
     Raw4<TI> xr[QPT], dr[QPT], zr[QPT], br[BQ], xk[QPT], zk[QPT];
-    auto fetch = [&](int64_t chunk) {
-        const int64_t tok0 = b * g.seqlen + chunk * T;
-        const int nt = (int)min64(T, g.seqlen - chunk * T);
+    const int t_first = tid / COLS;
+    const int64_t tile0 = REV ? cend - 1 : cbeg;
+    const int64_t tok0 = b * g.seqlen + tile0 * T, tok = tok0 + t_first;
+    const TI *px = a.x + tok * a.row_x + ch0 + cq, *pd = a.dt + tok * g.row_dt + ch0 + cq;
+    const TI *pz = a.z ? a.z + tok * g.row_z + ch0 + cq : nullptr;
+    const TI *pm[BQ];
+#pragma unroll
+    for (int i = 0; i < BQ; ++i) {
+        const int q = tid + i * NT, w = q / (T * LN), t = q / LN % T, n = 4 * (q % LN);
+        pm[i] = (w ? a.cm + (tok0 + t) * g.row_c : a.m + (tok0 + t) * a.row_m) + grp * g.N + n;
+    }
+    const bool whole = a.vec && nq >= 4, whole_bc = a.vec_bc && N == NP;
+    auto fetch = [&](int nt) {
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
-            const int q = tid + i * NT, t = q / COLS;
-            xr[i] = dr[i] = zr[i] = Raw4<TI>{};
-            if (q < QUADS && t < nt && nq > 0) {
-                const int64_t tok = tok0 + t;
-                xr[i] = load_raw4(a.x + tok * a.row_x + ch0 + cq, nq, a.vec);
-                dr[i] = load_raw4(a.dt + tok * g.row_dt + ch0 + cq, nq, a.vec);
-                if (a.z)
-                    zr[i] = load_raw4(a.z + tok * g.row_z + ch0 + cq, nq, a.vec);
+            const int t = t_first + i * (NT / COLS);
+            if (QUADS % NT != 0 && t >= T)
+                break;
+            const TI *qx = px + i * (NT / COLS) * a.row_x, *qd = pd + i * (NT / COLS) * g.row_dt;
+            const TI *qz = pz + i * (NT / COLS) * g.row_z;
+            if (whole && nt == T) {
+                xr[i] = *reinterpret_cast<const Raw4<TI> *>(qx);
+                dr[i] = *reinterpret_cast<const Raw4<TI> *>(qd);
+                if (pz)
+                    zr[i] = *reinterpret_cast<const Raw4<TI> *>(qz);
+            } else {
+                const int n = t < nt ? nq : 0;
+                xr[i] = load_raw4(qx, n, a.vec);
+                dr[i] = load_raw4(qd, n, a.vec);
+                if (pz)
+                    zr[i] = load_raw4(qz, n, a.vec);
             }
         }
+        px += (REV ? -T : T) * a.row_x;
+        pd += (REV ? -T : T) * g.row_dt;
+        if (pz)
+            pz += (REV ? -T : T) * g.row_z;
 #pragma unroll
         for (int i = 0; i < BQ; ++i) {
             const int q = tid + i * NT, w = q / (T * LN), t = q / LN % T, n = 4 * (q % LN);
-            br[i] = Raw4<TI>{};
-            if (q < MATS * T * LN && t < nt && n < N)
-                br[i] = load_raw4((w ? a.cm + (tok0 + t) * g.row_c : a.m + (tok0 + t) * a.row_m) + grp * g.N + n,
-                                  N - n, a.vec_bc);
+            if (MATS * T * LN % NT != 0 && q >= MATS * T * LN)
+                break;
+            if (whole_bc && nt == T)
+                br[i] = *reinterpret_cast<const Raw4<TI> *>(pm[i]);
+            else
+                br[i] = load_raw4(pm[i], t < nt ? N - n : 0, a.vec_bc);
+            pm[i] += (REV ? -T : T) * (w ? g.row_c : a.row_m);
         }
     };
-    auto put = [&](int64_t chunk, typename Tile::Buf &s) {
-        const int nt = (int)min64(T, g.seqlen - chunk * T);
+    auto put = [&](int nt, typename Tile::Buf &s) {
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
-            const int q = tid + i * NT, t = q / COLS;
-            if (q >= QUADS)
+            const int t = t_first + i * (NT / COLS);
+            if (QUADS % NT != 0 && t >= T)
                 break;
             float xv[4], dv[4], zv[4];
             unpack<TI, 4>(xr[i], xv);
             unpack<TI, 4>(dr[i], dv);
-            if (REV)
+            if (REV && pz)
                 unpack<TI, 4>(zr[i], zv);
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
                 float d0 = dv[e] + bias[e], d1 = dv[e + 1] + bias[e + 1];
                 if (g.softplus)
                     softplus2(d0, d1, d0, d1);
-                const bool on = t < nt;
-                d0 = on && e < nq ? d0 : 0.f;
-                d1 = on && e + 1 < nq ? d1 : 0.f;
-                float v0, v1;
-                if (REV) {
-                    v0 = a.z ? xv[e] * fast_silu(zv[e]) : xv[e];
-                    v1 = a.z ? xv[e + 1] * fast_silu(zv[e + 1]) : xv[e + 1];
-                } else {
-                    un2(mul2(pk2(d0, d1), pk2(xv[e], xv[e + 1])), v0, v1);
+                if (nt < T || nq < 4) {
+                    d0 = t < nt && e < nq ? d0 : 0.f;
+                    d1 = t < nt && e + 1 < nq ? d1 : 0.f;
                 }
+                f32x2 v = pk2(xv[e], xv[e + 1]);
+                if (!REV) {
+                    v = mul2(v, pk2(d0, d1));
+                } else if (pz) {
+                    const f32x2 z = pk2(zv[e], zv[e + 1]);
+                    v = mul2(v, mul2(z, sigmoid2(z)));
+                }
+                float v0, v1;
+                un2(v, v0, v1);
                 s.dx[t][cq + e] = make_float4(d0, d0, v0, v0);
                 s.dx[t][cq + e + 1] = make_float4(d1, d1, v1, v1);
             }
@@ -157,7 +186,7 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
         for (int i = 0; i < BQ; ++i) {
             const int q = tid + i * NT, w = q / (T * LN), r = q % (T * LN);
             float v[4];
-            if (q >= MATS * T * LN)
+            if (MATS * T * LN % NT != 0 && q >= MATS * T * LN)
                 break;
             unpack<TI, 4>(br[i], v);
             store_vec<float, 4>((w ? s.c : s.m) + 4 * r, v);
@@ -165,21 +194,24 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
     };
     auto at = [&](int64_t k) { return REV ? cend - 1 - k : cbeg + k; };
 
+    auto tokens = [&](int64_t k) { return (int)min64(T, g.seqlen - at(k) * T); };
+
     const int64_t n_tiles = cend - cbeg;
-    fetch(at(0));
-    put(at(0), sm.buf[0]);
+    fetch(tokens(0));
+    put(tokens(0), sm.buf[0]);
 #pragma unroll
     for (int i = 0; i < QPT; ++i) {
         xk[i] = xr[i];
         zk[i] = zr[i];
     }
+    TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
     __syncthreads();
     for (int64_t k = 0; k < n_tiles; ++k) {
         const int64_t chunk = at(k);
-        const int nt = (int)min64(T, g.seqlen - chunk * T);
+        const int nt = tokens(k);
         typename Tile::Buf &s = sm.buf[k & 1];
         if (k + 1 < n_tiles)
-            fetch(at(k + 1));
+            fetch(tokens(k + 1));
         if (a.kept && nn > 0) {
             float v[4];
             un2(h0, v[0], v[1]);
@@ -189,11 +221,9 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
         // LN tokens at a time, whose outputs are summed over the lanes together;
         // tokens past the end have delta = x = 0 and change nothing
         constexpr int BT = LN < 4 ? 4 : LN;
-#pragma unroll 1
+#pragma unroll
         for (int i0 = 0; i0 < T; i0 += BT) {
             const int tb = REV ? T - BT - i0 : i0;
-            if (tb >= nt)
-                continue;
             float v[BT];
 #pragma unroll
             for (int i = 0; i < BT; ++i) {
@@ -227,28 +257,32 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
             }
         }
         if (k + 1 < n_tiles)
-            put(at(k + 1), sm.buf[(k + 1) & 1]);
+            put(tokens(k + 1), sm.buf[(k + 1) & 1]);
         __syncthreads();
         if (MODE == kOut) {
 #pragma unroll
             for (int i = 0; i < QPT; ++i) {
-                const int q = tid + i * NT, t = q / COLS;
-                if (q < QUADS && t < nt && nq > 0) {
+                const int t = t_first + i * (NT / COLS);
+                if (t < nt && nq > 0) {
                     float xv[4], zv[4], o[4];
                     unpack<TI, 4>(xk[i], xv);
                     unpack<TI, 4>(zk[i], zv);
                     load_vec<float, 4>(&s.y[t * Tile::YP + cq], o);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = fmaf(Dv[e], xv[e], o[e]);
-                        if (a.z)
-                            o[e] *= fast_silu(zv[e]);
+                    for (int e = 0; e < 4; e += 2) {
+                        f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
+                        if (pz) {
+                            const f32x2 z = pk2(zv[e], zv[e + 1]);
+                            v = mul2(v, mul2(z, sigmoid2(z)));
+                        }
+                        un2(v, o[e], o[e + 1]);
                     }
-                    store4(a.y + (b * g.seqlen + chunk * T + t) * g.dim + ch0 + cq, o, nq, a.vec);
+                    store4(py + i * (NT / COLS) * g.dim, o, nq, a.vec);
                 }
                 xk[i] = xr[i];
                 zk[i] = zr[i];
             }
+            py += T * g.dim;
         }
     }
     if (nn > 0) {
@@ -291,50 +325,52 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
     }
 }
 
-// One token: four states of a channel per thread, LN lanes per channel.
+// One token: four states of a channel per thread, LN lanes per channel;
+// blockIdx.y is the sequence.
 template <typename TI, int LN>
 __global__ void __launch_bounds__(256)
 scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const float *__restrict__ A,
                  const TI *__restrict__ Bm, const TI *__restrict__ Cm, const float *__restrict__ D,
                  const TI *__restrict__ z, const float *__restrict__ bias, const float *state,
-                 float *state_out, TI *__restrict__ y, ScanGeom g)
+                 float *state_out, TI *__restrict__ y, ScanGeom g, bool vec_bc)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t bd = i / LN;
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;
+    const unsigned d = i / LN;
     const int n0 = 4 * (int)(i % LN);
-    const bool live = bd < g.batch * g.dim;
-    const int64_t b = live ? bd / g.dim : 0, d = live ? bd - b * g.dim : 0;
+    const bool live = d < (unsigned)g.dim;
+    const int64_t b = blockIdx.y;
     const int nn = live ? (int)g.N - n0 : 0;
-    const int64_t grp = d / g.kpg;
-    float s = 0.f, uv = 0.f;
+    float s = 0.f, uv = 0.f, zv = 0.f;
     if (nn > 0) {
+        const unsigned grp = g.G == 1 ? 0 : d / (unsigned)g.kpg;
+        const int64_t st = (b * g.dim + d) * g.N + n0;
         float h[4], av[4], bv[4], cv[4];
-        load_states(state + bd * g.N + n0, nn, h);
-        load_states(A + d * g.N + n0, nn, av);
+        load_states(state + st, nn, h);
+        load_states(A + (int64_t)d * g.N + n0, nn, av);
         uv = to_f32(u[b * g.row_u + d]);
-        float dl = to_f32(dt[b * g.row_dt + d]) + (bias ? bias[d] : 0.f);
+        float dl = to_f32(dt[b * g.row_dt + d]);
+        if (z)
+            zv = to_f32(z[b * g.row_z + d]);
+        unpack<TI, 4>(load_raw4(Bm + b * g.row_b + grp * g.N + n0, nn, vec_bc), bv);
+        unpack<TI, 4>(load_raw4(Cm + b * g.row_c + grp * g.N + n0, nn, vec_bc), cv);
+        if (bias)
+            dl += bias[d];
         dl = g.softplus ? softplus(dl) : dl;
-        const TI *bp = Bm + b * g.row_b + grp * g.N + n0, *cp = Cm + b * g.row_c + grp * g.N + n0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            bv[e] = e < nn ? to_f32(bp[e]) : 0.f;
-            cv[e] = e < nn ? to_f32(cp[e]) : 0.f;
-        }
         const float du = dl * uv;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             h[e] = fmaf(ex2(dl * decay_rate(av[e])), h[e], du * bv[e]);
             s = fmaf(h[e], cv[e], s);
         }
-        store_states(state_out + bd * g.N + n0, nn, h);
+        store_states(state_out + st, nn, h);
     }
     s = lane_sum<LN>(s);
     if (live && n0 == 0) {
         if (D)
             s = fmaf(D[d], uv, s);
         if (z)
-            s *= fast_silu(to_f32(z[b * g.row_z + d]));
-        y[bd] = from_f32<TI>(s);
+            s *= fast_silu(zv);
+        y[b * g.dim + d] = from_f32<TI>(s);
     }
 }
 
@@ -468,12 +504,14 @@ cudaError_t step_t(const void *u, const void *dt, const float *A, const void *Bm
                    const ScanGeom &g, cudaStream_t st)
 {
     const int LN = scan_lanes(g.N);
-    const unsigned blocks = (unsigned)((g.batch * g.dim * LN + 255) / 256);
+    const dim3 blocks((unsigned)((g.dim * LN + 255) / 256), (unsigned)g.batch);
+    const size_t al = 4 * sizeof(TI);
+    const bool vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al);
 #define SSD_STEP(LANES)                                                                              \
     scan_step_kernel<TI, LANES><<<blocks, 256, 0, st>>>(                                             \
         static_cast<const TI *>(u), static_cast<const TI *>(dt), A, static_cast<const TI *>(Bm),     \
         static_cast<const TI *>(Cm), D, static_cast<const TI *>(z), bias, state, state_out,          \
-        static_cast<TI *>(y), g)
+        static_cast<TI *>(y), g, vec_bc)
     switch (LN) {
     case 1: SSD_STEP(1); break;
     case 2: SSD_STEP(2); break;

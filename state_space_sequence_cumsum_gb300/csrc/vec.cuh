@@ -43,24 +43,26 @@ template <typename TI, int NV> __device__ __forceinline__ void load_vec(const TI
     unpack<TI, NV>(u, v);
 }
 
+__device__ __forceinline__ void round_pair(float a, float b, __nv_bfloat16 *e)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(e) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void round_pair(float a, float b, float *e)
+{
+    e[0] = a;
+    e[1] = b;
+}
 template <typename TI, int NV> __device__ __forceinline__ void store_vec(TI *p, const float (&v)[NV])
 {
     using T = typename Pack<TI, NV>::T;
-    T u;
-    TI *e = reinterpret_cast<TI *>(&u);
+    alignas(16) TI e[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        e[i] = from_f32<TI>(v[i]);
-    *reinterpret_cast<T *>(p) = u;
+    for (int i = 0; i + 1 < NV; i += 2)
+        round_pair(v[i], v[i + 1], e + i);
+    if (NV % 2)
+        e[NV - 1] = from_f32<TI>(v[NV - 1]);
+    *reinterpret_cast<T *>(p) = *reinterpret_cast<const T *>(e);
 }
-
-// 1 / (1 + e^-z) with the fast exponential and division (a few ulp each);
-// e^-z overflows to inf for z < -88 and the quotient is then 0.
-__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-
-// silu(z) = z sigmoid(z) and its derivative s (1 + z (1 - s)).
-__device__ __forceinline__ float fast_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-__device__ __forceinline__ float silu_grad(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -75,6 +77,14 @@ __device__ __forceinline__ float rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// 1 / (1 + e^-z) with the hardware's exponential and reciprocal (a few ulp);
+// e^-z overflows to inf for z < -88 and the result is then 0.
+__device__ __forceinline__ float fast_sigmoid(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
+
+// silu(z) = z sigmoid(z) and its derivative s (1 + z (1 - s)).
+__device__ __forceinline__ float fast_silu(float z) { return z * fast_sigmoid(z); }
+__device__ __forceinline__ float silu_grad(float z, float s) { return s * fmaf(z, 1.f - s, 1.f); }
 
 // Two f32 lanes in one instruction (half the issue slots of two scalar ones).
 typedef unsigned long long f32x2;
@@ -117,6 +127,19 @@ __device__ __forceinline__ float hsum(f32x2 p)
     float a, b;
     un2(p, a, b);
     return a + b;
+}
+
+__device__ __forceinline__ f32x2 dup2(float a) { return pk2(a, a); }
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 z)
+{
+    float a, b;
+    un2(add2(ex2_2(mul2(z, dup2(-kLog2e))), dup2(1.f)), a, b);
+    return pk2(rcp(a), rcp(b));
+}
+// s (1 + z (1 - s)) = s + s z (1 - s)
+__device__ __forceinline__ f32x2 silu_grad2(f32x2 z, f32x2 s)
+{
+    return fma2(mul2(s, z), fma2(s, dup2(-1.f), dup2(1.f)), s);
 }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1].  With

@@ -38,29 +38,62 @@ template <typename TI> struct PassArgs {
     bool vec, vec_bc;
 };
 
-template <int LN, int MODE, int NT> struct PassTile {
-    static constexpr int CB = NT / LN, NP = 4 * LN;
-    // row pitch of y: the LN tokens that a batch stores together start in different banks
-    static constexpr int YP = (CB + 31) / 32 * 32 + (32 / LN > 4 ? 32 / LN : 4);
+// A thread holds four states of two adjacent channels: what a token costs in
+// shared memory reads (16 bytes of delta and input, 16 of B, 16 of C a thread)
+// then serves eight states.  With one channel a thread those reads, not the
+// arithmetic, bounded the walk.
+template <int LN> struct PassShape {
+    // threads of a block: one warp where that gives rows of 16 channels or more
+    static constexpr int NT = LN <= 4 ? 32 : 8 * LN;
+    static constexpr int CB = 2 * NT / LN;  // channels
+    // blocks an SM holds (2 NT threads each); nine of two warps leave 112
+    // registers a thread, and take the 8.4 blocks an SM of four sequences of
+    // 5120 channels in one wave
+    static constexpr int BLOCKS = LN == 1 ? 3 : LN == 2 ? 5 : (LN == 4 ? 9 : 72 / (2 * LN));
+};
+
+template <int LN, int MODE> struct PassTile {
+    static constexpr int CB = PassShape<LN>::CB, NP = 4 * LN;
+    // y: one plane per lane of a channel, the planes 8 (or 4) banks apart
+    static constexpr int YP = kScanChunk * CB + (LN > 4 ? 4 : 8);
     struct Buf {
-        float4 dx[kScanChunk][CB];  // delta twice, then twice what multiplies the matrix row
+        float2 dx[kScanChunk][CB];  // delta, and what multiplies the matrix row
         float m[kScanChunk * NP];
         float c[MODE == kOut ? kScanChunk * NP : 4];
-        float y[MODE == kOut ? kScanChunk * YP : 4];
+        float y[MODE == kOut ? LN * YP : 4];
     } buf[2];
 };
 
-template <typename TI, int LN, int MODE, int NT>
-__global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
+// Half of a block's warps walk tiles (the states live in their registers), the
+// other half make them: per step the walkers go through tile k while the
+// makers convert tile k + 1, fetch tile k + 2 and finish the output of tile
+// k - 1.  One barrier a step.  A walker alone has too few independent
+// instructions to fill its scheduler; the makers fill the gaps.
+template <typename TI, int LN, int MODE>
+__global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
 {
-    constexpr int CB = NT / LN, T = kScanChunk, NP = 4 * LN;
-    constexpr int QUADS = T * CB / 4, QPT = (QUADS + NT - 1) / NT, COLS = CB / 4;
-    constexpr int MATS = MODE == kOut ? 2 : 1, BQ = (MATS * T * LN + NT - 1) / NT;
+    constexpr int NT = PassShape<LN>::NT, CB = PassShape<LN>::CB, T = kScanChunk, NP = 4 * LN;
+    // a thread's quads of a tile: QPT of one column of channels, TROWS tokens
+    // apart, and PER of a matrix, BT tokens apart (in the widest and narrowest
+    // shapes half the threads have none)
+    constexpr int COLS = CB / 4, TROWS = NT / COLS, QPT = TROWS < T ? T / TROWS : 1;
+    constexpr int MATS = MODE == kOut ? 2 : 1, BT = NT / LN, PER = BT < T ? T / BT : 1, BQ = MATS * PER;
     constexpr bool REV = MODE == kReverse;
-    using Tile = PassTile<LN, MODE, NT>;
+    using Tile = PassTile<LN, MODE>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Tile &sm = *reinterpret_cast<Tile *>(smem_raw);
-    const int tid = threadIdx.x;
+    // A block's warps go to the SM's schedulers in turn, so with fixed roles all
+    // walkers of two-warp blocks would share two of the four: blocks in the
+    // upper half of every eight warp slots swap theirs.
+    __shared__ int s_swap;
+    if (threadIdx.x == 0) {
+        unsigned slot;
+        asm("mov.u32 %0, %%warpid;" : "=r"(slot));
+        s_swap = slot >> 2 & 1;
+    }
+    __syncthreads();
+    const bool walker = (threadIdx.x < NT) != (s_swap != 0);
+    const int tid = threadIdx.x % NT;
     const int64_t nblk = (g.kpg + CB - 1) / CB;
     const int grp = (int)(blockIdx.x / nblk);
     const int64_t c0 = (blockIdx.x - grp * nblk) * CB;  // first channel, within the group
@@ -69,24 +102,119 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
     const int64_t b = blockIdx.z, seg = a.first_seg + blockIdx.y;
     const int64_t nc = (g.seqlen + T - 1) / T;
     const int64_t cbeg = seg * a.chunks_per_seg, cend = min64(cbeg + a.chunks_per_seg, nc);
-    const int N = (int)g.N;
-    // this thread's states
-    const int c = tid / LN, n0 = 4 * (tid % LN);
-    const int nn = c < nch ? N - n0 : 0;      // live states (may exceed 4)
+    const int64_t n_tiles = cend - cbeg;
+    const int N = (int)g.N, n0 = 4 * (tid % LN);
+    auto at = [&](int64_t k) { return REV ? cend - 1 - k : cbeg + k; };
+    auto tokens = [&](int64_t k) { return (int)min64(T, g.seqlen - at(k) * T); };
+
+    if (walker) {
+    // ---- walkers
+    // this thread's states: h[channel][pair of states]
+    const int c = 2 * (tid / LN);
+    int nn[2];                                // live states of each channel (may exceed 4)
     const int64_t st = (ch0 + c) * g.N + n0;  // its place in a [dim][N] array
-    f32x2 h0 = 0, h1 = 0, A0 = 0, A1 = 0;
-    float dsum = 0.f;
-    if (nn > 0) {
-        float v[4];
-        load_states(a.A + st, nn, v);
-        A0 = pk2(decay_rate(v[0]), decay_rate(v[1]));
-        A1 = pk2(decay_rate(v[2]), decay_rate(v[3]));
-        if (a.start) {
-            load_states(a.start + (b * a.n_seg + seg) * g.dim * g.N + st, nn, v);
-            h0 = pk2(v[0], v[1]);
-            h1 = pk2(v[2], v[3]);
+    f32x2 h[2][2] = {}, A[2][2] = {};
+    float dsum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        nn[i] = c + i < nch ? N - n0 : 0;
+        if (nn[i] > 0) {
+            float v[4];
+            load_states(a.A + st + i * g.N, nn[i], v);
+            A[i][0] = pk2(decay_rate(v[0]), decay_rate(v[1]));
+            A[i][1] = pk2(decay_rate(v[2]), decay_rate(v[3]));
+            if (a.start) {
+                load_states(a.start + (b * a.n_seg + seg) * g.dim * g.N + st + i * g.N, nn[i], v);
+                h[i][0] = pk2(v[0], v[1]);
+                h[i][1] = pk2(v[2], v[3]);
+            }
         }
     }
+    auto save = [&](float *p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (nn[i] > 0) {
+                float v[4];
+                un2(h[i][0], v[0], v[1]);
+                un2(h[i][1], v[2], v[3]);
+                store_states(p + st + i * g.N, nn[i], v);
+            }
+    };
+    __syncthreads();  // tile 0
+    for (int64_t k = 0; k < n_tiles; ++k) {
+        typename Tile::Buf &s = sm.buf[k & 1];
+        if (a.kept)
+            save(a.kept + (b * nc + at(k)) * g.dim * g.N);
+        // Tokens past the end have delta = x = 0 and change nothing.  A group's
+        // decays and inputs do not depend on the states: the next group's are
+        // formed before this one's recurrence, which hides their latencies.
+        // Each lane stores its part of the output, which the tile's last step
+        // adds up.
+        constexpr int GROUP = 2;
+        f32x2 d[2][GROUP][2][2], x[2][GROUP][2][2];
+        auto prepare = [&](int i0, int w) {
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) {
+                const int t = REV ? T - 1 - i0 - i : i0 + i;
+                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    d[w][i][j][0] = ex2_2(mul2(dl[j], A[j][0]));
+                    d[w][i][j][1] = ex2_2(mul2(dl[j], A[j][1]));
+                    x[w][i][j][0] = mul2(xv[j], m.x);
+                    x[w][i][j][1] = mul2(xv[j], m.y);
+                }
+                if (MODE != kOut) {
+                    dsum[0] += dx.x;
+                    dsum[1] += dx.z;
+                }
+            }
+        };
+        prepare(0, 0);
+#pragma unroll
+        for (int i0 = 0; i0 < T; i0 += GROUP) {
+            const int w = i0 / GROUP & 1;
+            ulonglong2 cv[GROUP];
+            if (MODE == kOut)
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i)
+                    cv[i] = *reinterpret_cast<const ulonglong2 *>(&s.c[(i0 + i) * NP + n0]);
+            if (i0 + GROUP < T)
+                prepare(i0 + GROUP, w ^ 1);
+            float part[GROUP][2];
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        h[j][e] = REV ? mul2(d[w][i][j][e], add2(x[w][i][j][e], h[j][e]))
+                                      : fma2(d[w][i][j][e], h[j][e], x[w][i][j][e]);
+                    if (MODE == kOut)
+                        part[i][j] = hsum(fma2(h[j][1], cv[i].y, mul2(h[j][0], cv[i].x)));
+                }
+            if (MODE == kOut)
+#pragma unroll
+                for (int i = 0; i < GROUP; ++i)
+                    *reinterpret_cast<float2 *>(&s.y[(tid % LN) * Tile::YP + (i0 + i) * CB + c]) =
+                        make_float2(part[i][0], part[i][1]);
+        }
+        __syncthreads();
+    }
+    if (a.last && (REV ? cbeg == 0 : cend == nc))
+        save(a.last + b * g.dim * g.N);
+    if (a.seg_end) {
+        save(a.seg_end + (b * a.n_seg + seg) * g.dim * g.N);
+        if (n0 == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (nn[i] > 0)
+                    a.seg_dsum[(b * a.n_seg + seg) * g.dim + ch0 + c + i] = dsum[i];
+    }
+    } else {
+    // ---- makers
     // this thread's elementwise work: one column of four channels
     const int cq = 4 * (tid % COLS), nq = nch - cq;
     float bias[4] = {}, Dv[4] = {};
@@ -98,33 +226,29 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
         }
 
     // where this thread's elements of the next tile to fetch are: its column of
-    // the token t_first (then every NT / COLS-th), and its matrix quads
-    Raw4<TI> xr[QPT], dr[QPT], zr[QPT], br[BQ], xk[QPT], zk[QPT];
+    // the token t_first (then every TROWS-th), and its matrix quads
+    Raw4<TI> xr[QPT], dr[QPT], zr[QPT], br[BQ];
+    Raw4<TI> xk[3][QPT], zk[3][QPT];  // x and z of tiles k - 1, k, k + 1, for the output
     const int t_first = tid / COLS;
     const int64_t tile0 = REV ? cend - 1 : cbeg;
     const int64_t tok0 = b * g.seqlen + tile0 * T, tok = tok0 + t_first;
     const TI *px = a.x + tok * a.row_x + ch0 + cq, *pd = a.dt + tok * g.row_dt + ch0 + cq;
     const TI *pz = a.z ? a.z + tok * g.row_z + ch0 + cq : nullptr;
-    const TI *pm[BQ];
-#pragma unroll
-    for (int i = 0; i < BQ; ++i) {
-        const int q = tid + i * NT, w = q / (T * LN), t = q / LN % T, n = 4 * (q % LN);
-        pm[i] = (w ? a.cm + (tok0 + t) * g.row_c : a.m + (tok0 + t) * a.row_m) + grp * g.N + n;
-    }
+    const TI *pm = a.m + (tok0 + tid / LN) * a.row_m + grp * g.N + n0;
+    const TI *pc = MODE == kOut ? a.cm + (tok0 + tid / LN) * g.row_c + grp * g.N + n0 : nullptr;
     const bool whole = a.vec && nq >= 4, whole_bc = a.vec_bc && N == NP;
     auto fetch = [&](int nt) {
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
-            const int t = t_first + i * (NT / COLS);
-            if (QUADS % NT != 0 && t >= T)
+            const int t = t_first + i * TROWS;
+            if (TROWS > T && t >= T)
                 break;
-            const TI *qx = px + i * (NT / COLS) * a.row_x, *qd = pd + i * (NT / COLS) * g.row_dt;
-            const TI *qz = pz + i * (NT / COLS) * g.row_z;
+            const TI *qx = px + i * TROWS * a.row_x, *qd = pd + i * TROWS * g.row_dt, *qz = pz + i * TROWS * g.row_z;
             if (whole && nt == T) {
-                xr[i] = *reinterpret_cast<const Raw4<TI> *>(qx);
-                dr[i] = *reinterpret_cast<const Raw4<TI> *>(qd);
+                xr[i] = load_ahead(qx);
+                dr[i] = load_ahead(qd);
                 if (pz)
-                    zr[i] = *reinterpret_cast<const Raw4<TI> *>(qz);
+                    zr[i] = load_ahead(qz);
             } else {
                 const int n = t < nt ? nq : 0;
                 xr[i] = load_raw4(qx, n, a.vec);
@@ -139,23 +263,26 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
             pz += (REV ? -T : T) * g.row_z;
 #pragma unroll
         for (int i = 0; i < BQ; ++i) {
-            const int q = tid + i * NT, w = q / (T * LN), t = q / LN % T, n = 4 * (q % LN);
-            if (MATS * T * LN % NT != 0 && q >= MATS * T * LN)
+            const int t = tid / LN + i % PER * BT;
+            if (BT > T && t >= T)
                 break;
+            const TI *q = i < PER ? pm + i % PER * BT * a.row_m : pc + i % PER * BT * g.row_c;
             if (whole_bc && nt == T)
-                br[i] = *reinterpret_cast<const Raw4<TI> *>(pm[i]);
+                br[i] = load_ahead(q);
             else
-                br[i] = load_raw4(pm[i], t < nt ? N - n : 0, a.vec_bc);
-            pm[i] += (REV ? -T : T) * (w ? g.row_c : a.row_m);
+                br[i] = load_raw4(q, t < nt ? N - n0 : 0, a.vec_bc);
         }
+        pm += (REV ? -T : T) * a.row_m;
+        if (MODE == kOut)
+            pc += T * g.row_c;
     };
     auto put = [&](int nt, typename Tile::Buf &s) {
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
-            const int t = t_first + i * (NT / COLS);
-            if (QUADS % NT != 0 && t >= T)
+            const int t = t_first + i * TROWS;
+            if (TROWS > T && t >= T)
                 break;
-            float xv[4], dv[4], zv[4];
+            float xv[4], dv[4], zv[4], o[8];
             unpack<TI, 4>(xr[i], xv);
             unpack<TI, 4>(dr[i], dv);
             if (REV && pz)
@@ -176,136 +303,100 @@ __global__ void __launch_bounds__(NT) scan_pass_kernel(PassArgs<TI> a, ScanGeom 
                     const f32x2 z = pk2(zv[e], zv[e + 1]);
                     v = mul2(v, mul2(z, sigmoid2(z)));
                 }
-                float v0, v1;
-                un2(v, v0, v1);
-                s.dx[t][cq + e] = make_float4(d0, d0, v0, v0);
-                s.dx[t][cq + e + 1] = make_float4(d1, d1, v1, v1);
+                o[2 * e] = d0;
+                o[2 * e + 2] = d1;
+                un2(v, o[2 * e + 1], o[2 * e + 3]);
             }
+            *reinterpret_cast<float4 *>(&s.dx[t][cq]) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(&s.dx[t][cq + 2]) = make_float4(o[4], o[5], o[6], o[7]);
         }
 #pragma unroll
         for (int i = 0; i < BQ; ++i) {
-            const int q = tid + i * NT, w = q / (T * LN), r = q % (T * LN);
             float v[4];
-            if (MATS * T * LN % NT != 0 && q >= MATS * T * LN)
+            if (BT > T && tid / LN >= T)
                 break;
             unpack<TI, 4>(br[i], v);
-            store_vec<float, 4>((w ? s.c : s.m) + 4 * r, v);
+            store_vec<float, 4>((i < PER ? s.m : s.c) + 4 * (tid + i % PER * NT), v);
         }
     };
-    auto at = [&](int64_t k) { return REV ? cend - 1 - k : cbeg + k; };
-
-    auto tokens = [&](int64_t k) { return (int)min64(T, g.seqlen - at(k) * T); };
-
-    const int64_t n_tiles = cend - cbeg;
+    TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
+            auto finish = [&](int nt, const typename Tile::Buf &s, const Raw4<TI> (&xq)[QPT], const Raw4<TI> (&zq)[QPT]) {
+#pragma unroll
+                for (int i = 0; i < QPT; ++i) {
+                    const int t = t_first + i * TROWS;
+                    if (t < nt && nq > 0) {
+                        float xv[4], zv[4], o[4];
+                        unpack<TI, 4>(xq[i], xv);
+                        unpack<TI, 4>(zq[i], zv);
+                        ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&s.y[t * CB + cq]);
+#pragma unroll
+                        for (int j = 1; j < LN; ++j) {
+                            const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(&s.y[j * Tile::YP + t * CB + cq]);
+                            y.x = add2(y.x, p.x);
+                            y.y = add2(y.y, p.y);
+                        }
+                        un2(y.x, o[0], o[1]);
+                        un2(y.y, o[2], o[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
+                            if (pz) {
+                                const f32x2 z = pk2(zv[e], zv[e + 1]);
+                                v = mul2(v, mul2(z, sigmoid2(z)));
+                            }
+                            un2(v, o[e], o[e + 1]);
+                        }
+                        store4(py + i * TROWS * g.dim, o, nq, a.vec);
+                    }
+                }
+                py += T * g.dim;
+            };
+    // x and z of the tile in the fetch registers, kept for its output
+    auto keep = [&](Raw4<TI> (&xq)[QPT], Raw4<TI> (&zq)[QPT]) {
+#pragma unroll
+        for (int i = 0; i < QPT; ++i) {
+            xq[i] = xr[i];
+            zq[i] = zr[i];
+        }
+    };
     fetch(tokens(0));
     put(tokens(0), sm.buf[0]);
-#pragma unroll
-    for (int i = 0; i < QPT; ++i) {
-        xk[i] = xr[i];
-        zk[i] = zr[i];
-    }
-    TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
-    __syncthreads();
+    keep(xk[1], zk[1]);
+    if (n_tiles > 1)
+        fetch(tokens(1));
+    __syncthreads();  // tile 0
     for (int64_t k = 0; k < n_tiles; ++k) {
-        const int64_t chunk = at(k);
-        const int nt = tokens(k);
-        typename Tile::Buf &s = sm.buf[k & 1];
-        if (k + 1 < n_tiles)
-            fetch(tokens(k + 1));
-        if (a.kept && nn > 0) {
-            float v[4];
-            un2(h0, v[0], v[1]);
-            un2(h1, v[2], v[3]);
-            store_states(a.kept + (b * nc + chunk) * g.dim * g.N + st, nn, v);
-        }
-        // LN tokens at a time, whose outputs are summed over the lanes together;
-        // tokens past the end have delta = x = 0 and change nothing
-        constexpr int BT = LN < 4 ? 4 : LN;
-#pragma unroll
-        for (int i0 = 0; i0 < T; i0 += BT) {
-            const int tb = REV ? T - BT - i0 : i0;
-            float v[BT];
-#pragma unroll
-            for (int i = 0; i < BT; ++i) {
-                const int t = tb + (REV ? BT - 1 - i : i);
-                const ulonglong2 dx = *reinterpret_cast<const ulonglong2 *>(&s.dx[t][c]);
-                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
-                const f32x2 d0 = ex2_2(mul2(dx.x, A0)), d1 = ex2_2(mul2(dx.x, A1));
-                if (MODE != kOut)
-                    dsum += __uint_as_float((unsigned)dx.x);
-                if (REV) {
-                    h0 = mul2(d0, fma2(dx.y, m.x, h0));
-                    h1 = mul2(d1, fma2(dx.y, m.y, h1));
-                } else {
-                    h0 = fma2(d0, h0, mul2(dx.y, m.x));
-                    h1 = fma2(d1, h1, mul2(dx.y, m.y));
-                }
-                if (MODE == kOut) {
-                    const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
-                    v[i] = hsum(fma2(h1, cv.y, mul2(h0, cv.x)));
-                }
-            }
-            if (MODE == kOut) {
-#pragma unroll
-                for (int i = 0; i < BT; i += LN) {
-                    float w[LN];
-#pragma unroll
-                    for (int e = 0; e < LN; ++e)
-                        w[e] = v[i + e];
-                    s.y[(tb + i + tid % LN) * Tile::YP + c] = lane_transpose_sum<LN>(w);
-                }
-            }
-        }
-        if (k + 1 < n_tiles)
+        if (k + 1 < n_tiles) {
             put(tokens(k + 1), sm.buf[(k + 1) & 1]);
+            keep(xk[2], zk[2]);
+            if (k + 2 < n_tiles)
+                fetch(tokens(k + 2));
+        }
+        if (MODE == kOut && k > 0)
+            finish(tokens(k - 1), sm.buf[(k - 1) & 1], xk[0], zk[0]);
+#pragma unroll
+        for (int i = 0; i < QPT; ++i) {
+            xk[0][i] = xk[1][i];
+            zk[0][i] = zk[1][i];
+            xk[1][i] = xk[2][i];
+            zk[1][i] = zk[2][i];
+        }
         __syncthreads();
-        if (MODE == kOut) {
-#pragma unroll
-            for (int i = 0; i < QPT; ++i) {
-                const int t = t_first + i * (NT / COLS);
-                if (t < nt && nq > 0) {
-                    float xv[4], zv[4], o[4];
-                    unpack<TI, 4>(xk[i], xv);
-                    unpack<TI, 4>(zk[i], zv);
-                    load_vec<float, 4>(&s.y[t * Tile::YP + cq], o);
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
-                        if (pz) {
-                            const f32x2 z = pk2(zv[e], zv[e + 1]);
-                            v = mul2(v, mul2(z, sigmoid2(z)));
-                        }
-                        un2(v, o[e], o[e + 1]);
-                    }
-                    store4(py + i * (NT / COLS) * g.dim, o, nq, a.vec);
-                }
-                xk[i] = xr[i];
-                zk[i] = zr[i];
-            }
-            py += T * g.dim;
-        }
     }
-    if (nn > 0) {
-        float v[4];
-        un2(h0, v[0], v[1]);
-        un2(h1, v[2], v[3]);
-        if (a.last && (REV ? cbeg == 0 : cend == nc))
-            store_states(a.last + b * g.dim * g.N + st, nn, v);
-        if (a.seg_end) {
-            store_states(a.seg_end + (b * a.n_seg + seg) * g.dim * g.N + st, nn, v);
-            if (n0 == 0)
-                a.seg_dsum[(b * a.n_seg + seg) * g.dim + ch0 + c] = dsum;
-        }
+    if (MODE == kOut)
+        finish(tokens(n_tiles - 1), sm.buf[(n_tiles - 1) & 1], xk[0], zk[0]);
     }
 }
 
 // Segment end states -> segment start states, in place, in the order of the
-// pass: start' = exp(A dsum) start + end.
+// pass: start' = exp(A dsum) start + end.  kJoin segments' values are read
+// before the first is replaced.
 template <bool REV>
 __global__ void __launch_bounds__(256)
 scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const float *__restrict__ A,
                  const float *start, int64_t batch, int64_t dim, int64_t N, int64_t n_seg)
 {
+    constexpr int kJoin = 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t DN = dim * N;
     if (i >= batch * DN)
@@ -313,15 +404,22 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
     const int64_t b = i / DN, r = i - b * DN, d = r / N;
     const float A2 = decay_rate(A[r]);
     float h = start ? start[i] : 0.f;
-    for (int64_t k = 0; k < n_seg; ++k) {
-        const int64_t s = b * n_seg + (REV ? n_seg - 1 - k : k);
-        float end = 0.f, q = 0.f;
-        if (k < n_seg - 1) {  // the last segment's end is not needed (nor computed)
-            end = seg[s * DN + r];
-            q = dsum[s * dim + d];
+    for (int64_t k0 = 0; k0 < n_seg; k0 += kJoin) {
+        float end[kJoin], q[kJoin];
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
+            // the last segment's end is not needed (nor computed)
+            end[j] = k < n_seg - 1 ? seg[s * DN + r] : 0.f;
+            q[j] = k < n_seg - 1 ? dsum[s * dim + d] : 0.f;
         }
-        seg[s * DN + r] = h;
-        h = fmaf(ex2(A2 * q), h, end);
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+            const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
+            if (k < n_seg)
+                seg[s * DN + r] = h;
+            h = fmaf(ex2(A2 * q[j]), h, end[j]);
+        }
     }
 }
 
@@ -379,17 +477,16 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 template <typename TI, int LN, int MODE>
 cudaError_t launch_pass_ln(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, cudaStream_t st)
 {
-    constexpr int NT = kScanThreads;
-    constexpr int64_t CB = NT / LN;
+    constexpr int64_t CB = PassShape<LN>::CB;
     const dim3 grid((unsigned)(g.G * ((g.kpg + CB - 1) / CB)), (unsigned)segs, (unsigned)g.batch);
-    constexpr size_t smem = sizeof(PassTile<LN, MODE, NT>);
-    auto k = scan_pass_kernel<TI, LN, MODE, NT>;
+    constexpr size_t smem = sizeof(PassTile<LN, MODE>);
+    auto k = scan_pass_kernel<TI, LN, MODE>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess)
             return e;
     }
-    k<<<grid, NT, smem, st>>>(a, g);
+    k<<<grid, 2 * PassShape<LN>::NT, smem, st>>>(a, g);
     note_launch(1);
     return cudaGetLastError();
 }
@@ -536,18 +633,21 @@ int scan_lanes(int64_t N)
 
 int scan_chunk() { return kScanChunk; }
 
-// Segments of a pass: one where the channel blocks give every SM several
-// blocks; else enough segments (of at least four chunks) to do so.
+// Segments of a pass: one where the channels alone give an SM three walking
+// warps or more, or the sequence is short; else as many as one wave of blocks
+// holds.  Measured on 4096 tokens of 5120 channels: one sequence (2.1 warps an
+// SM) 283 us whole, 246 us in four segments; two sequences 342 us whole, 389
+// us in two.
 ScanSegs scan_segments(const ScanGeom &g)
 {
-    const int64_t CB = kScanThreads / scan_lanes(g.N);
-    const int64_t blocks = g.G * ((g.kpg + CB - 1) / CB) * g.batch;
+    const int LN = scan_lanes(g.N);
+    const int64_t per_warp = 2 * 32 / LN;  // channels
+    const int64_t warps = g.G * ((g.kpg + per_warp - 1) / per_warp) * g.batch;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    const int64_t want = (int64_t)device_sm_count() * 3;
+    const int64_t sms = device_sm_count();
     ScanSegs s{1, nc};
-    if (blocks < want) {
-        int64_t n = (2 * want + blocks - 1) / blocks;
-        n = min64(n, nc / 4);
+    if (warps < 3 * sms && nc >= 32) {
+        const int64_t n = min64(9 * sms / warps, nc / 8);
         if (n > 1) {
             s.chunks_per_seg = (nc + n - 1) / n;
             s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;

@@ -17,6 +17,23 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Four consecutive elements as loaded; elements past n are zero.
 template <typename TI> using Raw4 = typename Pack<TI, 4>::T;
 
+// An aligned quad.  Volatile, so that a load issued ahead of a tile stays
+// there: the compiler would otherwise sink it to its use a tile later.
+__device__ __forceinline__ uint2 load_ahead(const __nv_bfloat16 *p)
+{
+    uint2 r;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ float4 load_ahead(const float *p)
+{
+    float4 r;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "l"(p));
+    return r;
+}
+
 template <typename TI> __device__ __forceinline__ Raw4<TI> load_raw4(const TI *p, int n, bool vec)
 {
     Raw4<TI> r{};
@@ -70,24 +87,6 @@ template <int LN> __device__ __forceinline__ float lane_sum(float v)
     for (int o = LN / 2; o > 0; o >>= 1)
         v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-
-// Sums LN values over a channel's LN lanes at once; lane j returns the sum of
-// every lane's v[j].  Each step sends one half and keeps the other, so LN
-// sums take LN - 1 shuffles where one at a time they take LN log2 LN.
-template <int LN> __device__ __forceinline__ float lane_transpose_sum(float (&v)[LN])
-{
-#pragma unroll
-    for (int o = 1, n = LN; o < LN; o *= 2, n /= 2) {
-        const bool up = threadIdx.x & o;
-#pragma unroll
-        for (int i = 0; i < n / 2; ++i) {
-            const float keep = up ? v[2 * i + 1] : v[2 * i];
-            const float send = up ? v[2 * i] : v[2 * i + 1];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-    }
-    return v[0];
 }
 
 // A decay rate in log2 units.  -inf becomes the lowest float, so that a token

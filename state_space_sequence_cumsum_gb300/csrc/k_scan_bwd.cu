@@ -8,19 +8,23 @@
 //     g <- a e
 //     du = delta sB + D dyy,  ddelta = u sB + sA,  ddt = ddelta softplus'(dt + bias)
 //     dz = dout (sum_n C h + D u) silu'(z),        dD += dyy u,  dbias += ddt
-// dB and dC are sums over the group's channels: a thread owns four states of
-// one channel and goes through four channels for the same eight tokens with
-// the sums in registers; a block adds its threads' sums once per eight tokens
-// and writes one partial per channel block, and a last kernel adds those in a
-// fixed order (no atomics, so results do not depend on scheduling).
-// Arithmetic on about 12 issue slots per (token, channel, state) bounds it.
+// dB and dC are sums over the group's channels.  A thread owns four states of
+// two adjacent channels and walks a chunk in pieces of kPiece tokens, last to
+// first: forward through the piece from its start state (kept in registers by
+// a first walk over the chunk) holding each token's a and a h, then back.  Its
+// parts of dB and dC are added over the block's threads in shared memory once
+// a piece and written as one partial per channel block; a last kernel adds
+// those in a fixed order (no atomics, so results do not depend on scheduling).
+// About 18 issue slots and 27 bytes of shared memory traffic per (token,
+// channel, state) bound it.
 #include "scan.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kIters = 4;  // channels a thread goes through
-constexpr int kSub = 8;    // tokens whose a and a h a thread holds
+constexpr int kPiece = 4;      // tokens whose a and a h a thread holds
+constexpr int kRound = 8;      // tokens between two elementwise rounds
+constexpr int kGradThreads = 128;
 
 template <typename TI> struct GradArgs {
     const TI *u, *dt, *bm, *cm, *z, *dy;
@@ -30,283 +34,391 @@ template <typename TI> struct GradArgs {
     float *dA;             // [B * chunk groups][dim][N]
     float *dD;             // [B * chunk groups][2][dim]: dD, dbias
     int64_t chunks_per_group;
-    bool vec;
+    bool vec, vec_bc;
 };
 
-template <int LN> struct GradSmem {
-    static constexpr int CBK = kIters * kScanThreads / LN, NP = 4 * LN;
-    float2 dd[kScanChunk][CBK];  // delta, delta u
-    float dyy[kScanChunk][CBK];
-    float y[kSub][CBK], sB[kSub][CBK], sA[kSub][CBK];
-    float4 h[kIters][kScanThreads], e[kIters][kScanThreads], dA[kIters][kScanThreads];
+template <typename TI, int LN> struct GradTile {
+    static constexpr int CB = 2 * kGradThreads / LN, NP = 4 * LN;
+    static constexpr int CP = kGradThreads / LN;  // channel pairs
+    static constexpr int PLANE = kRound * CB + (LN > 4 ? 4 : 8);
+    static constexpr int RED = CP + 8;            // pitch of one sum's terms
+    struct Raw {
+        TI u[kScanChunk][CB], dt[kScanChunk][CB], z[kScanChunk][CB], dy[kScanChunk][CB];
+        TI m[kScanChunk][NP], c[kScanChunk][NP];
+    } raw[2];                           // as loaded: this chunk and the next
+    float2 dx[kScanChunk][CB];          // delta, delta u
+    float dyy[kScanChunk][CB];          // dout silu(z)
     float m[kScanChunk * NP], c[kScanChunk * NP];
-    float red[kSub * 4][kScanThreads];
+    float part[3][LN * PLANE];          // each lane's part of sum C h, sum e B, sum q A
+    float red[2 * kPiece * NP * RED];   // each channel pair's part of dB, dC
 };
 
-__device__ __forceinline__ void to4(const float4 &f, float (&v)[4])
+__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes)
 {
-    v[0] = f.x;
-    v[1] = f.y;
-    v[2] = f.z;
-    v[3] = f.w;
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    if (bytes == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
 }
-
-// Adds each thread's kSub x 4 values over the block's channels and writes the
-// [kSub][N] sums of live tokens.
-template <int LN>
-__device__ __forceinline__ void block_rows_sum(const float (&v)[kSub][4], float (*red)[kScanThreads], float *out,
-                                               int nt, int N)
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_async_wait()
 {
-    constexpr int CB = kScanThreads / LN;
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kSub; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            red[t * 4 + e][threadIdx.x] = v[t][e];
-    __syncthreads();
-    for (int o = threadIdx.x; o < kSub * 4 * LN; o += kScanThreads) {
-        const int j = o % LN, r = o / LN, t = r / 4, n = 4 * j + r % 4;
-        float s = 0.f;
-        for (int i = 0; i < CB; ++i)  // starting channels differ to spread the banks
-            s += red[r][((i + r) % CB) * LN + j];
-        if (t < nt && n < N)
-            out[t * N + n] = s;
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 template <typename TI, int LN>
-__global__ void __launch_bounds__(kScanThreads) scan_grad_kernel(GradArgs<TI> a, ScanGeom g)
+__global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kernel(GradArgs<TI> a, ScanGeom g)
 {
-    constexpr int CB = kScanThreads / LN, CBK = kIters * CB, T = kScanChunk, NP = 4 * LN;
-    constexpr int COLS = CBK / 4, TPR = kScanThreads / COLS;  // elementwise: 4-channel columns x token rows
+    using Tile = GradTile<TI, LN>;
+    constexpr int NT = kGradThreads, CB = Tile::CB, CP = Tile::CP, T = kScanChunk, NP = 4 * LN;
+    // elementwise work: columns of four channels, TROWS tokens apart
+    constexpr int COLS = CB / 4, TROWS = NT / COLS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    GradSmem<LN> &s = *reinterpret_cast<GradSmem<LN> *>(smem_raw);
+    Tile &s = *reinterpret_cast<Tile *>(smem_raw);
     const int tid = threadIdx.x;
-    const int64_t nblk = (g.kpg + CBK - 1) / CBK;
+    const int64_t nblk = (g.kpg + CB - 1) / CB;
     const int grp = (int)(blockIdx.x / nblk);
-    const int64_t c0 = (blockIdx.x - grp * nblk) * CBK;
-    const int nch = (int)min64(CBK, g.kpg - c0);
+    const int64_t c0 = (blockIdx.x - grp * nblk) * CB;
+    const int nch = (int)min64(CB, g.kpg - c0);
     const int64_t ch0 = grp * g.kpg + c0;
     const int64_t b = blockIdx.z;
     const int64_t nc = (g.seqlen + T - 1) / T;
     const int64_t cbeg = blockIdx.y * a.chunks_per_group, cend = min64(cbeg + a.chunks_per_group, nc);
-    const int cl = tid / LN, n0 = 4 * (tid % LN);
-    const int N = (int)g.N, nn = N - n0;
-    const int col = 4 * (tid % COLS), trow = tid / COLS;
-    float accD[4] = {}, accb[4] = {};
-#pragma unroll
-    for (int k = 0; k < kIters; ++k)
-        s.dA[k][tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int N = (int)g.N;
+    const int cp = tid / LN, c = 2 * cp, n0 = 4 * (tid % LN);
+    const int col = 4 * (tid % COLS), trow = tid / COLS, nq = nch - col;
 
-    for (int64_t chunk = cbeg; chunk < cend; ++chunk) {
-        const int64_t t0 = chunk * T;
-        const int nt = (int)min64(T, g.seqlen - t0);
-        const int64_t tok0 = b * g.seqlen + t0;
-        __syncthreads();  // the chunk before is done with the tiles
-        for (int t = trow; t < T; t += TPR) {
-            const int n = t < nt ? nch - col : 0;
-            const int64_t tok = tok0 + t;
-            Raw4<TI> ur{}, dr{}, zr{}, yr{};
-            if (n > 0) {
-                ur = load_raw4(a.u + tok * g.row_u + ch0 + col, n, a.vec);
-                dr = load_raw4(a.dt + tok * g.row_dt + ch0 + col, n, a.vec);
-                yr = load_raw4(a.dy + tok * g.row_dy + ch0 + col, n, a.vec);
-                if (a.z)
-                    zr = load_raw4(a.z + tok * g.row_z + ch0 + col, n, a.vec);
-            }
-            float uv[4], dv[4], zv[4], yv[4];
-            unpack<TI, 4>(ur, uv);
-            unpack<TI, 4>(dr, dv);
-            unpack<TI, 4>(zr, zv);
-            unpack<TI, 4>(yr, yv);
+    f32x2 A[2][2] = {}, dA[2][2] = {};
+    int nn[2];
+    const int64_t st = (ch0 + c) * g.N + n0;  // the thread's place in a [dim][N] array
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float d = 0.f;
-                if (e < n) {
-                    d = dv[e] + (a.bias ? a.bias[ch0 + col + e] : 0.f);
-                    d = g.softplus ? softplus(d) : d;
-                }
-                s.dd[t][col + e] = make_float2(d, d * uv[e]);
-                s.dyy[t][col + e] = a.z ? yv[e] * fast_silu(zv[e]) : yv[e];
+    for (int j = 0; j < 2; ++j) {
+        nn[j] = c + j < nch ? N - n0 : 0;
+        if (nn[j] > 0) {
+            float v[4];
+            load_states(a.A + st + j * g.N, nn[j], v);
+            A[j][0] = pk2(decay_rate(v[0]), decay_rate(v[1]));
+            A[j][1] = pk2(decay_rate(v[2]), decay_rate(v[3]));
+        }
+    }
+    float bias[4] = {}, Dv[4] = {}, accD[4] = {}, accb[4] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < nq) {
+            bias[e] = a.bias ? a.bias[ch0 + col + e] : 0.f;
+            Dv[e] = a.D ? a.D[ch0 + col + e] : 0.f;
+        }
+
+    // the chunk's inputs into raw[w]; elements past the tokens, channels and
+    // states are zero
+    auto fetch = [&](int64_t chunk, int w) {
+        const int64_t tok0 = b * g.seqlen + chunk * T;
+        const int nt = (int)min64(T, g.seqlen - chunk * T);
+        typename Tile::Raw &r = s.raw[w];
+#pragma unroll
+        for (int t = trow; t < T; t += TROWS) {
+            const int64_t tok = tok0 + t;
+            if (a.vec && nq >= 4 && t < nt) {
+                copy_async(&r.u[t][col], a.u + tok * g.row_u + ch0 + col, 4 * sizeof(TI));
+                copy_async(&r.dt[t][col], a.dt + tok * g.row_dt + ch0 + col, 4 * sizeof(TI));
+                copy_async(&r.dy[t][col], a.dy + tok * g.row_dy + ch0 + col, 4 * sizeof(TI));
+                if (a.z)
+                    copy_async(&r.z[t][col], a.z + tok * g.row_z + ch0 + col, 4 * sizeof(TI));
+            } else {
+                const int n = t < nt ? nq : 0;
+                *reinterpret_cast<Raw4<TI> *>(&r.u[t][col]) = load_raw4(a.u + tok * g.row_u + ch0 + col, n, false);
+                *reinterpret_cast<Raw4<TI> *>(&r.dt[t][col]) = load_raw4(a.dt + tok * g.row_dt + ch0 + col, n, false);
+                *reinterpret_cast<Raw4<TI> *>(&r.dy[t][col]) = load_raw4(a.dy + tok * g.row_dy + ch0 + col, n, false);
+                if (a.z)
+                    *reinterpret_cast<Raw4<TI> *>(&r.z[t][col]) =
+                        load_raw4(a.z + tok * g.row_z + ch0 + col, n, false);
             }
         }
-        load_rows<TI, LN>(a.bm + tok0 * g.row_b + grp * g.N, g.row_b, nt, N, s.m);
-        load_rows<TI, LN>(a.cm + tok0 * g.row_c + grp * g.N, g.row_c, nt, N, s.c);
+        for (int i = tid; i < 2 * T * LN; i += NT) {
+            const int q = i / (T * LN), t = i / LN % T, n = 4 * (i % LN);
+            TI *dst = q ? &r.c[t][n] : &r.m[t][n];
+            const TI *src = (q ? a.cm + (tok0 + t) * g.row_c : a.bm + (tok0 + t) * g.row_b) + grp * g.N + n;
+            if (a.vec_bc && t < nt && N - n >= 4)
+                copy_async(dst, src, 4 * sizeof(TI));
+            else
+                *reinterpret_cast<Raw4<TI> *>(dst) = load_raw4(src, t < nt ? N - n : 0, false);
+        }
+        copy_async_commit();
+    };
+
+    fetch(cbeg, 0);
+    for (int64_t chunk = cbeg; chunk < cend; ++chunk) {
+        const int w = (int)(chunk - cbeg) & 1;
+        const int nt = (int)min64(T, g.seqlen - chunk * T);
+        const int64_t tok0 = b * g.seqlen + chunk * T;
+        // the state entering the chunk and the gradient leaving it
+        f32x2 h0[2][2] = {}, e[2][2] = {};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (nn[j] > 0) {
+                const int64_t at = (b * nc + chunk) * g.dim * g.N + st + j * g.N;
+                float v[4];
+                load_states(a.h0 + at, nn[j], v);
+                h0[j][0] = pk2(v[0], v[1]);
+                h0[j][1] = pk2(v[2], v[3]);
+                load_states(a.g1 + at, nn[j], v);
+                e[j][0] = pk2(v[0], v[1]);
+                e[j][1] = pk2(v[2], v[3]);
+            }
+        copy_async_wait<0>();
+        __syncthreads();  // raw[w] is complete, and the chunk before is done with everything
+        if (chunk + 1 < cend)
+            fetch(chunk + 1, w ^ 1);
+        const typename Tile::Raw &r = s.raw[w];
+#pragma unroll
+        for (int t = trow; t < T; t += TROWS) {
+            float uv[4], dv[4], zv[4], yv[4], o[8];
+            load_vec<TI, 4>(&r.u[t][col], uv);
+            load_vec<TI, 4>(&r.dt[t][col], dv);
+            load_vec<TI, 4>(&r.dy[t][col], yv);
+            if (a.z)
+                load_vec<TI, 4>(&r.z[t][col], zv);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                float d0 = dv[i] + bias[i], d1 = dv[i + 1] + bias[i + 1];
+                if (g.softplus)
+                    softplus2(d0, d1, d0, d1);
+                if (nt < T || nq < 4) {
+                    d0 = t < nt && i < nq ? d0 : 0.f;
+                    d1 = t < nt && i + 1 < nq ? d1 : 0.f;
+                }
+                o[2 * i] = d0;
+                o[2 * i + 2] = d1;
+                un2(mul2(pk2(d0, d1), pk2(uv[i], uv[i + 1])), o[2 * i + 1], o[2 * i + 3]);
+                if (a.z) {
+                    const f32x2 z = pk2(zv[i], zv[i + 1]);
+                    un2(mul2(pk2(yv[i], yv[i + 1]), mul2(z, sigmoid2(z))), yv[i], yv[i + 1]);
+                }
+            }
+            *reinterpret_cast<float4 *>(&s.dx[t][col]) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(&s.dx[t][col + 2]) = make_float4(o[4], o[5], o[6], o[7]);
+            store_vec<float, 4>(&s.dyy[t][col], yv);
+        }
+        for (int i = tid; i < 2 * T * LN; i += NT) {
+            const int q = i / (T * LN), k = 4 * (i % (T * LN));
+            float v[4];
+            load_vec<TI, 4>((q ? &r.c[0][0] : &r.m[0][0]) + k, v);
+            store_vec<float, 4>((q ? s.c : s.m) + k, v);
+        }
         __syncthreads();
 
-        const int64_t kept = (b * nc + chunk) * g.dim;
-        // the state after the first eight tokens, and the gradient entering the chunk
-#pragma unroll 1
-        for (int k = 0; k < kIters; ++k) {
-            const int c = k * CB + cl;
-            float h[4] = {}, A2[4] = {}, e0[4] = {};
-            if (c < nch && nn > 0) {
-                const int64_t st = (kept + ch0 + c) * g.N + n0;
-                load_states(a.h0 + st, nn, h);
-                load_states(a.g1 + st, nn, e0);
-                load_states(a.A + (ch0 + c) * g.N + n0, nn, A2);
+        // a walk to each piece's start state
+        constexpr int PIECES = T / kPiece;
+        f32x2 hs[PIECES][2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            hs[0][j][0] = h0[j][0], hs[0][j][1] = h0[j][1];
+#pragma unroll
+        for (int p = 1; p < PIECES; ++p) {
+            f32x2 h[2][2] = {{hs[p - 1][0][0], hs[p - 1][0][1]}, {hs[p - 1][1][0], hs[p - 1][1][1]}};
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) {
+                const int t = (p - 1) * kPiece + i;
+                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    h[j][0] = fma2(ex2_2(mul2(dl[j], A[j][0])), h[j][0], mul2(xv[j], m.x));
+                    h[j][1] = fma2(ex2_2(mul2(dl[j], A[j][1])), h[j][1], mul2(xv[j], m.y));
+                }
             }
 #pragma unroll
-            for (int t = 0; t < kSub; ++t) {
-                const float2 dd = s.dd[t][c];
-                float m[4];
-                to4(*reinterpret_cast<const float4 *>(&s.m[t * NP + n0]), m);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    h[e] = fmaf(ex2(dd.x * decay_rate(A2[e])), h[e], dd.y * m[e]);
-            }
-            s.h[k][tid] = make_float4(h[0], h[1], h[2], h[3]);
-            s.e[k][tid] = make_float4(e0[0], e0[1], e0[2], e0[3]);
+            for (int j = 0; j < 2; ++j)
+                hs[p][j][0] = h[j][0], hs[p][j][1] = h[j][1];
         }
-#pragma unroll 1
-        for (int sub = 1; sub >= 0; --sub) {
-            const int ts = sub * kSub;
-            if (ts >= nt && sub > 0)
-                continue;
-            float dB[kSub][4] = {}, dC[kSub][4] = {};
-#pragma unroll 1
-            for (int k = 0; k < kIters; ++k) {
-                const int c = k * CB + cl;
-                if (k * CB >= nch)
-                    break;
-                float h[4] = {}, A2[4] = {}, e0[4], acc[4];
-                if (c < nch && nn > 0)
-                    load_states(a.A + (ch0 + c) * g.N + n0, nn, A2);
+
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    A2[e] = decay_rate(A2[e]);
-                if (sub)
-                    to4(s.h[k][tid], h);
-                else if (c < nch && nn > 0)
-                    load_states(a.h0 + (kept + ch0 + c) * g.N + n0, nn, h);
-                to4(s.e[k][tid], e0);
-                to4(s.dA[k][tid], acc);
-                float av[kSub][4], ah[kSub][4];
+        for (int p = PIECES - 1; p >= 0; --p) {
+            const int t0 = p * kPiece;
+            f32x2 dB[kPiece][2] = {}, dC[kPiece][2] = {};
+            f32x2 av[kPiece][2][2], ah[kPiece][2][2];
+            ulonglong2 m[kPiece], cv[kPiece];
+            f32x2 h[2][2] = {{hs[p][0][0], hs[p][0][1]}, {hs[p][1][0], hs[p][1][1]}};
 #pragma unroll
-                for (int t = 0; t < kSub; ++t) {
-                    const float2 dd = s.dd[ts + t][c];
-                    const float dyy = s.dyy[ts + t][c];
-                    float m[4], cv[4], y = 0.f;
-                    to4(*reinterpret_cast<const float4 *>(&s.m[(ts + t) * NP + n0]), m);
-                    to4(*reinterpret_cast<const float4 *>(&s.c[(ts + t) * NP + n0]), cv);
+            for (int i = 0; i < kPiece; ++i) {
+                const int t = t0 + i;
+                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+                const float2 dyy = *reinterpret_cast<const float2 *>(&s.dyy[t][c]);
+                m[i] = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                cv[i] = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
+                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
+                const f32x2 yv[2] = {dup2(dyy.x), dup2(dyy.y)};
+                float y[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        av[t][e] = ex2(dd.x * A2[e]);
-                        ah[t][e] = av[t][e] * h[e];
-                        h[e] = fmaf(dd.y, m[e], ah[t][e]);
-                        dC[t][e] = fmaf(dyy, h[e], dC[t][e]);
-                        y = fmaf(cv[e], h[e], y);
-                    }
-                    y = lane_sum<LN>(y);
-                    if (n0 == 0)
-                        s.y[t][c] = y;
+                for (int j = 0; j < 2; ++j) {
+                    av[i][j][0] = ex2_2(mul2(dl[j], A[j][0]));
+                    av[i][j][1] = ex2_2(mul2(dl[j], A[j][1]));
+                    ah[i][j][0] = mul2(av[i][j][0], h[j][0]);
+                    ah[i][j][1] = mul2(av[i][j][1], h[j][1]);
+                    h[j][0] = fma2(xv[j], m[i].x, ah[i][j][0]);
+                    h[j][1] = fma2(xv[j], m[i].y, ah[i][j][1]);
+                    dC[i][0] = fma2(yv[j], h[j][0], dC[i][0]);
+                    dC[i][1] = fma2(yv[j], h[j][1], dC[i][1]);
+                    y[j] = hsum(fma2(h[j][1], cv[i].y, mul2(h[j][0], cv[i].x)));
                 }
-#pragma unroll
-                for (int t = kSub - 1; t >= 0; --t) {
-                    const float2 dd = s.dd[ts + t][c];
-                    const float dyy = s.dyy[ts + t][c];
-                    float m[4], cv[4], sB = 0.f, sA = 0.f;
-                    to4(*reinterpret_cast<const float4 *>(&s.m[(ts + t) * NP + n0]), m);
-                    to4(*reinterpret_cast<const float4 *>(&s.c[(ts + t) * NP + n0]), cv);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        e0[e] = fmaf(dyy, cv[e], e0[e]);
-                        dB[t][e] = fmaf(e0[e], dd.y, dB[t][e]);
-                        sB = fmaf(e0[e], m[e], sB);
-                        const float q = e0[e] * ah[t][e];
-                        acc[e] = fmaf(q, dd.x, acc[e]);
-                        sA = fmaf(q, A2[e], sA);
-                        e0[e] *= av[t][e];
-                    }
-                    sB = lane_sum<LN>(sB);
-                    sA = lane_sum<LN>(sA);
-                    if (n0 == 0) {
-                        s.sB[t][c] = sB;
-                        s.sA[t][c] = sA;
-                    }
-                }
-                s.e[k][tid] = make_float4(e0[0], e0[1], e0[2], e0[3]);
-                s.dA[k][tid] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            }
-            const int ns = nt - ts;
-            float *rows = a.dB + ((int64_t)blockIdx.x * g.batch * g.seqlen + tok0 + ts) * g.N;
-            block_rows_sum<LN>(dB, s.red, rows, ns, N);
-            rows = a.dC + ((int64_t)blockIdx.x * g.batch * g.seqlen + tok0 + ts) * g.N;
-            block_rows_sum<LN>(dC, s.red, rows, ns, N);
-            // per (token, channel) results
-            for (int t = trow; t < kSub; t += TPR) {
-                const int n = t < ns ? nch - col : 0;
-                if (n <= 0)
-                    continue;
-                const int64_t tok = tok0 + ts + t;
-                float uv[4], dv[4], zv[4], yv[4], du[4], ddt[4], dz[4];
-                unpack<TI, 4>(load_raw4(a.u + tok * g.row_u + ch0 + col, n, a.vec), uv);
-                unpack<TI, 4>(load_raw4(a.dt + tok * g.row_dt + ch0 + col, n, a.vec), dv);
-                if (a.z) {
-                    unpack<TI, 4>(load_raw4(a.z + tok * g.row_z + ch0 + col, n, a.vec), zv);
-                    unpack<TI, 4>(load_raw4(a.dy + tok * g.row_dy + ch0 + col, n, a.vec), yv);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (e >= n)
-                        continue;
-                    const float Dv = a.D ? a.D[ch0 + col + e] : 0.f;
-                    const float dyy = s.dyy[ts + t][col + e], delta = s.dd[ts + t][col + e].x;
-                    const float sB = s.sB[t][col + e];
-                    du[e] = fmaf(delta, sB, Dv * dyy);
-                    ddt[e] = fmaf(uv[e], sB, s.sA[t][col + e] * kLn2);
-                    if (g.softplus)
-                        ddt[e] *= fast_sigmoid(dv[e] + (a.bias ? a.bias[ch0 + col + e] : 0.f));
-                    if (a.z) {
-                        const float yy = fmaf(Dv, uv[e], s.y[t][col + e]);
-                        dz[e] = yv[e] * yy * silu_grad(zv[e], fast_sigmoid(zv[e]));
-                    }
-                    accD[e] = fmaf(dyy, uv[e], accD[e]);
-                    accb[e] += ddt[e];
-                }
-                store4(a.du + tok * g.dim + ch0 + col, du, n, a.vec);
-                store4(a.ddt + tok * g.dim + ch0 + col, ddt, n, a.vec);
                 if (a.z)
-                    store4(a.dz + tok * g.dim + ch0 + col, dz, n, a.vec);
+                    *reinterpret_cast<float2 *>(&s.part[0][(tid % LN) * Tile::PLANE + t % kRound * CB + c]) =
+                        make_float2(y[0], y[1]);
+            }
+#pragma unroll
+            for (int i = kPiece - 1; i >= 0; --i) {
+                const int t = t0 + i;
+                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+                const float2 dyy = *reinterpret_cast<const float2 *>(&s.dyy[t][c]);
+                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
+                const f32x2 yv[2] = {dup2(dyy.x), dup2(dyy.y)};
+                float sB[2], sA[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    e[j][0] = fma2(yv[j], cv[i].x, e[j][0]);
+                    e[j][1] = fma2(yv[j], cv[i].y, e[j][1]);
+                    dB[i][0] = fma2(e[j][0], xv[j], dB[i][0]);
+                    dB[i][1] = fma2(e[j][1], xv[j], dB[i][1]);
+                    sB[j] = hsum(fma2(e[j][1], m[i].y, mul2(e[j][0], m[i].x)));
+                    const f32x2 q0 = mul2(e[j][0], ah[i][j][0]), q1 = mul2(e[j][1], ah[i][j][1]);
+                    dA[j][0] = fma2(q0, dl[j], dA[j][0]);
+                    dA[j][1] = fma2(q1, dl[j], dA[j][1]);
+                    sA[j] = hsum(fma2(q1, A[j][1], mul2(q0, A[j][0])));
+                    e[j][0] = mul2(e[j][0], av[i][j][0]);
+                    e[j][1] = mul2(e[j][1], av[i][j][1]);
+                }
+                const int at = (tid % LN) * Tile::PLANE + t % kRound * CB + c;
+                *reinterpret_cast<float2 *>(&s.part[1][at]) = make_float2(sB[0], sB[1]);
+                *reinterpret_cast<float2 *>(&s.part[2][at]) = make_float2(sA[0], sA[1]);
+            }
+            // dB and dC of the piece: red[which][token][state][channel pair]
+#pragma unroll
+            for (int i = 0; i < kPiece; ++i) {
+                float v[8];
+                un2(dB[i][0], v[0], v[1]);
+                un2(dB[i][1], v[2], v[3]);
+                un2(dC[i][0], v[4], v[5]);
+                un2(dC[i][1], v[6], v[7]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    s.red[(((k / 4) * kPiece + i) * NP + n0 + k % 4) * Tile::RED + cp] = v[k];
             }
             __syncthreads();
+            for (int o = tid; o < 2 * kPiece * NP; o += NT) {
+                const int t = t0 + o / NP % kPiece, n = o % NP;
+                const float *q = s.red + o * Tile::RED;
+                f32x2 v0 = 0, v1 = 0;
+#pragma unroll
+                for (int i = 0; i < CP / 4; ++i) {  // starts differ to spread the banks
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + 4 * ((i + (o >> 2)) % (CP / 4)));
+                    v0 = add2(v0, x.x);
+                    v1 = add2(v1, x.y);
+                }
+                if (t < nt && n < N) {
+                    float *out = o < kPiece * NP ? a.dB : a.dC;
+                    out[((int64_t)blockIdx.x * g.batch * g.seqlen + tok0 + t) * g.N + n] = hsum(add2(v0, v1));
+                }
+            }
+            if (t0 % kRound == 0) {  // per (token, channel) results of the last kRound tokens
+#pragma unroll
+                for (int t = t0 + trow; t < t0 + kRound; t += TROWS) {
+                    if (t >= nt || nq <= 0)
+                        break;
+                    f32x2 sum[3][2];
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const float *q = &s.part[k][t % kRound * CB + col];
+                        ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(q);
+#pragma unroll
+                        for (int j = 1; j < LN; ++j) {
+                            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + j * Tile::PLANE);
+                            v.x = add2(v.x, x.x);
+                            v.y = add2(v.y, x.y);
+                        }
+                        sum[k][0] = v.x;
+                        sum[k][1] = v.y;
+                    }
+                    float uv[4], dv[4], zv[4], yv[4], du[4], ddt[4], dz[4], dyy[4];
+                    load_vec<TI, 4>(&r.u[t][col], uv);
+                    load_vec<TI, 4>(&r.dt[t][col], dv);
+                    load_vec<float, 4>(&s.dyy[t][col], dyy);
+                    if (a.z) {
+                        load_vec<TI, 4>(&r.z[t][col], zv);
+                        load_vec<TI, 4>(&r.dy[t][col], yv);
+                    }
+                    const float4 x0 = *reinterpret_cast<const float4 *>(&s.dx[t][col]);
+                    const float4 x1 = *reinterpret_cast<const float4 *>(&s.dx[t][col + 2]);
+                    const float delta[4] = {x0.x, x0.z, x1.x, x1.z};
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const f32x2 Dp = pk2(Dv[k], Dv[k + 1]), up = pk2(uv[k], uv[k + 1]);
+                        const f32x2 gp = pk2(dyy[k], dyy[k + 1]);
+                        const f32x2 sB = sum[1][k / 2];
+                        un2(fma2(pk2(delta[k], delta[k + 1]), sB, mul2(Dp, gp)), du[k], du[k + 1]);
+                        f32x2 d = fma2(sum[2][k / 2], dup2(kLn2), mul2(up, sB));
+                        if (g.softplus)
+                            d = mul2(d, sigmoid2(pk2(dv[k] + bias[k], dv[k + 1] + bias[k + 1])));
+                        un2(d, ddt[k], ddt[k + 1]);
+                        if (a.z) {
+                            const f32x2 z = pk2(zv[k], zv[k + 1]);
+                            const f32x2 y = fma2(Dp, up, sum[0][k / 2]);
+                            un2(mul2(mul2(pk2(yv[k], yv[k + 1]), y), silu_grad2(z, sigmoid2(z))), dz[k], dz[k + 1]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < nq) {
+                            accD[k] = fmaf(dyy[k], uv[k], accD[k]);
+                            accb[k] += ddt[k];
+                        }
+                    const int64_t at = (tok0 + t) * g.dim + ch0 + col;
+                    store4(a.du + at, du, nq, a.vec);
+                    store4(a.ddt + at, ddt, nq, a.vec);
+                    if (a.z)
+                        store4(a.dz + at, dz, nq, a.vec);
+                }
+            }
+            __syncthreads();  // red and part may be written again
         }
     }
     // this block's partial sums over its tokens
     const int64_t item = b * gridDim.y + blockIdx.y;
 #pragma unroll
-    for (int k = 0; k < kIters; ++k) {
-        const int c = k * CB + cl;
-        if (c < nch && nn > 0) {
+    for (int j = 0; j < 2; ++j)
+        if (nn[j] > 0) {
             float v[4];
-            to4(s.dA[k][tid], v);
-            store_states(a.dA + (item * g.dim + ch0 + c) * g.N + n0, nn, v);
+            un2(dA[j][0], v[0], v[1]);
+            un2(dA[j][1], v[2], v[3]);
+            store_states(a.dA + item * g.dim * g.N + st + j * g.N, nn[j], v);
         }
-    }
-    __syncthreads();
-    float *red = &s.red[0][0];  // [TPR][2][CBK]
+    float *red = s.red;  // [TROWS][2][CB]
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        red[(trow * 2) * CBK + col + e] = accD[e];
-        red[(trow * 2 + 1) * CBK + col + e] = accb[e];
+    for (int k = 0; k < 4; ++k) {
+        red[(trow * 2) * CB + col + k] = accD[k];
+        red[(trow * 2 + 1) * CB + col + k] = accb[k];
     }
     __syncthreads();
-    for (int i = tid; i < 2 * CBK; i += kScanThreads) {
-        const int w = i / CBK, c = i % CBK;
+    for (int i = tid; i < 2 * CB; i += NT) {
+        const int which = i / CB, k = i % CB;
         float v = 0.f;
-        for (int r = 0; r < TPR; ++r)
-            v += red[(r * 2 + w) * CBK + c];
-        if (c < nch)
-            a.dD[(item * 2 + w) * g.dim + ch0 + c] = v;
+        for (int q = 0; q < TROWS; ++q)
+            v += red[(q * 2 + which) * CB + k];
+        if (k < nch)
+            a.dD[(item * 2 + which) * g.dim + ch0 + k] = v;
     }
 }
 
-// out[i][g][n] = sum over the group's channel blocks k of src[g nblk + k][i][n].
+// out[i][g][n] = sum over the group's channel blocks k of src[g nblk + k][i][n],
+// for dB (blockIdx.y = 0) and dC.
 template <typename TI>
-__global__ void __launch_bounds__(256) sum_blocks_kernel(const float *__restrict__ src, TI *__restrict__ out,
+__global__ void __launch_bounds__(256) sum_blocks_kernel(const float *__restrict__ src0, const float *__restrict__ src1,
+                                                         TI *__restrict__ out0, TI *__restrict__ out1,
                                                          int64_t tokens, int64_t G, int64_t N, int64_t nblk)
 {
+    const float *src = blockIdx.y ? src1 : src0;
+    TI *out = blockIdx.y ? out1 : out0;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= tokens * G * N)
         return;
@@ -339,15 +451,14 @@ struct GradPlan {
 GradPlan grad_plan(const ScanGeom &g)
 {
     GradPlan p;
-    const int64_t cbk = kIters * kScanThreads / scan_lanes(g.N);
-    p.nblk = (g.kpg + cbk - 1) / cbk;
+    const int64_t cb = 2 * kGradThreads / scan_lanes(g.N);
+    p.nblk = (g.kpg + cb - 1) / cb;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    // several blocks per SM, each over a run of chunks so that the sums over
-    // tokens leave few partials
-    const int64_t want = (int64_t)device_sm_count() * 4;
+    // about four waves of two blocks an SM, each over a run of chunks so that
+    // the sums over tokens leave few partials
     const int64_t cols = p.nblk * g.G * g.batch;
-    int64_t n = (want + cols - 1) / cols;
-    n = n > nc ? nc : n;
+    int64_t n = (int64_t)device_sm_count() * 8 / cols;
+    n = n < 1 ? 1 : (n > nc ? nc : n);
     p.chunks_per_group = (nc + n - 1) / n;
     p.n_groups = (nc + p.chunks_per_group - 1) / p.chunks_per_group;
     return p;
@@ -358,11 +469,11 @@ cudaError_t grad_ln(const GradArgs<TI> &a, const ScanGeom &g, const GradPlan &p,
 {
     auto k = scan_grad_kernel<TI, LN>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(GradSmem<LN>));
+                                               (int)sizeof(GradTile<TI, LN>));
     if (e != cudaSuccess)
         return e;
-    k<<<dim3((unsigned)(g.G * p.nblk), (unsigned)p.n_groups, (unsigned)g.batch), kScanThreads,
-        sizeof(GradSmem<LN>), st>>>(a, g);
+    k<<<dim3((unsigned)(g.G * p.nblk), (unsigned)p.n_groups, (unsigned)g.batch), kGradThreads,
+        sizeof(GradTile<TI, LN>), st>>>(a, g);
     note_launch(1);
     return cudaGetLastError();
 }
@@ -420,6 +531,7 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     const size_t al = 4 * sizeof(TI);
     a.vec = (g.kpg % 4 == 0 || g.G == 1) && g.dim % 4 == 0 && g.row_u % 4 == 0 && g.row_dt % 4 == 0 &&
             g.row_dy % 4 == 0 && (!z || g.row_z % 4 == 0);
+    a.vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al);
     for (const void *q : {u, dt, z, dy, static_cast<const void *>(du), static_cast<const void *>(ddt),
                           static_cast<const void *>(dz)})
         a.vec = a.vec && aligned(q, al);
@@ -434,12 +546,11 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     if (e != cudaSuccess)
         return e;
     const int64_t tokens = g.batch * g.seqlen, nbc = tokens * g.G * g.N;
-    const unsigned bb = (unsigned)((nbc + 255) / 256);
-    sum_blocks_kernel<TI><<<bb, 256, 0, st>>>(w.dB, static_cast<TI *>(dB), tokens, g.G, g.N, p.nblk);
-    sum_blocks_kernel<TI><<<bb, 256, 0, st>>>(w.dC, static_cast<TI *>(dC), tokens, g.G, g.N, p.nblk);
+    sum_blocks_kernel<TI><<<dim3((unsigned)((nbc + 255) / 256), 2), 256, 0, st>>>(
+        w.dB, w.dC, static_cast<TI *>(dB), static_cast<TI *>(dC), tokens, g.G, g.N, p.nblk);
     const int64_t items = g.batch * p.n_groups, dn = g.dim * g.N;
     sum_items_kernel<<<(unsigned)((dn + 255) / 256), 256, 0, st>>>(w.dA, dA, dn, items, dn);
-    note_launch(3);
+    note_launch(2);
     const unsigned db = (unsigned)((g.dim + 255) / 256);
     if (dD) {
         sum_items_kernel<<<db, 256, 0, st>>>(w.dD, dD, g.dim, items, 2 * g.dim);

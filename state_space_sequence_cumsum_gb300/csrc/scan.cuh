@@ -5,10 +5,8 @@
 
 namespace ssd {
 
-// A block has kScanThreads threads.  A thread holds four of a channel's
-// states, LN = 1, 2, 4, 8 or 16 lanes hold the channel (up to 4 LN states;
-// the ones past dstate stay zero).
-constexpr int kScanThreads = 128;
+// A thread holds four of a channel's states; LN = 1, 2, 4, 8 or 16 lanes hold
+// the channel (up to 4 LN states; the ones past dstate stay zero).
 // Tokens of one chunk: a state is kept at each chunk's start for the backward.
 constexpr int kScanChunk = 16;
 
@@ -95,17 +93,6 @@ __device__ __forceinline__ float decay_rate(float a)
 {
     const float r = a * kLog2e;
     return r == -INFINITY ? -3.402823466e38f : r;
-}
-
-// The rows of B or C of a tile, as f32 [kScanChunk][4 LN], zero past N and
-// past the last token.
-template <typename TI, int LN>
-__device__ __forceinline__ void load_rows(const TI *m, int64_t row, int nt, int N, float *s)
-{
-    for (int i = threadIdx.x; i < kScanChunk * 4 * LN; i += kScanThreads) {
-        const int t = i / (4 * LN), n = i % (4 * LN);
-        s[i] = (t < nt && n < N) ? to_f32(m[t * row + n]) : 0.f;
-    }
 }
 
 }  // namespace ssd

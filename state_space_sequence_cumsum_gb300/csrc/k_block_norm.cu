@@ -20,7 +20,9 @@
 namespace ssd {
 namespace {
 
-constexpr int kMaxTeam = 512;  // threads of a row's team
+// Threads of a row's team at most.  The backward's fewer leave registers for
+// two blocks an SM (a row's four inputs, the next row's, and three sums).
+constexpr int kFwdTeam = 512, kBwdTeam = 320;
 
 // Adds K values over the team (blockDim.x threads, a multiple of 32); every
 // thread of the block must call it.  One barrier: `buf` (one Sum<K> per warp
@@ -67,7 +69,7 @@ template <int VEC> __device__ __forceinline__ void scale_by(const float *p, floa
 // One row per team; blockDim = (team, teams).  A thread holds VPT vectors of
 // VEC channels, `team` vectors apart.
 template <typename TI, typename TR, int VEC, int VPT>
-__global__ void __launch_bounds__(kMaxTeam)
+__global__ void __launch_bounds__(kFwdTeam)
 block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__restrict__ weight,
                   const float *__restrict__ post_weight, const float *__restrict__ gate, TI *__restrict__ out,
                   TR *residual_out, NormGeom g)
@@ -156,7 +158,7 @@ __device__ __forceinline__ float minus_radial(float v, float x, float m, float r
 // weight, [1] post_weight), the gate's over an item (written as it is where
 // an item is a whole gate row, else one partial per item).
 template <typename TI, typename TR, int VEC, int VPT>
-__global__ void __launch_bounds__(kMaxTeam)
+__global__ void __launch_bounds__(kBwdTeam, VEC * VPT <= 8 ? 2 : 1)
 block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const float *__restrict__ weight,
                       const float *__restrict__ post_weight, const float *__restrict__ gate,
                       const TI *__restrict__ dout, const TR *dr, TI *__restrict__ dy, TR *dresidual,
@@ -328,13 +330,13 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float *__restrict__
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Threads of a row's team, and vectors of each, for a row of nv vectors: few
-// vectors a thread while the team stays within kMaxTeam.
-void team_shape(int64_t nv, int *team, int *vpt)
+// vectors a thread while the team stays within `most` threads.
+void team_shape(int64_t nv, int most, int *team, int *vpt)
 {
-    for (int v : {1, 2, 4, 16, 64}) {
+    for (int v : {1, 2, 4, 8, 32, 128}) {
         *vpt = v;
         *team = (int)((nv + v * 32 - 1) / (v * 32)) * 32;
-        if (*team <= kMaxTeam)
+        if (*team <= most)
             return;
     }
 }
@@ -386,12 +388,13 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
 }
 
 // F<TI, TR, VEC, VPT> for the team's vectors per thread; MAXV: the most (a
-// row of four-channel vectors needs 16, one of single channels 64).
+// row of four-channel vectors needs 32, one of single channels 128).
 #define SSD_NORM_VPT(F, TI, TR, VEC, MAXV, ...)                                                     \
     (vpt == 1    ? F<TI, TR, VEC, 1>(__VA_ARGS__)                                                   \
      : vpt == 2  ? F<TI, TR, VEC, 2>(__VA_ARGS__)                                                   \
      : vpt == 4  ? F<TI, TR, VEC, 4>(__VA_ARGS__)                                                   \
-     : vpt == 16 ? F<TI, TR, VEC, 16>(__VA_ARGS__)                                                  \
+     : vpt == 8  ? F<TI, TR, VEC, 8>(__VA_ARGS__)                                                   \
+     : vpt == 32 ? F<TI, TR, VEC, 32>(__VA_ARGS__)                                                  \
                  : F<TI, TR, VEC, MAXV>(__VA_ARGS__))
 #define SSD_NORM_TYPES(F, VEC, MAXV, ...)                                                           \
     (bf16 ? (res_bf16 ? SSD_NORM_VPT(F, __nv_bfloat16, __nv_bfloat16, VEC, MAXV, __VA_ARGS__)       \
@@ -410,12 +413,12 @@ cudaError_t launch_block_norm(const void *y, const void *residual, const float *
     const size_t a = bf16 ? 8 : 16, ar = res_bf16 ? 8 : 16;
     if (g.dim % 4 == 0 && aligned(y, a) && aligned(out, a) && aligned(residual, ar) &&
         aligned(residual_out, ar) && aligned(weight, 16) && aligned(post_weight, 16) && aligned(gate, 16)) {
-        team_shape(g.dim / 4, &team, &vpt);
-        return SSD_NORM_TYPES(fwd_v, 4, 16, y, residual, weight, post_weight, gate, out, residual_out, g, team,
+        team_shape(g.dim / 4, kFwdTeam, &team, &vpt);
+        return SSD_NORM_TYPES(fwd_v, 4, 32, y, residual, weight, post_weight, gate, out, residual_out, g, team,
                               st);
     }
-    team_shape(g.dim, &team, &vpt);
-    return SSD_NORM_TYPES(fwd_v, 1, 64, y, residual, weight, post_weight, gate, out, residual_out, g, team, st);
+    team_shape(g.dim, kFwdTeam, &team, &vpt);
+    return SSD_NORM_TYPES(fwd_v, 1, 128, y, residual, weight, post_weight, gate, out, residual_out, g, team, st);
 }
 
 // Partials: two rows per block (weight, post_weight), one per item of the
@@ -446,12 +449,12 @@ cudaError_t launch_block_norm_bwd(const void *y, const void *r, const float *wei
         al = al && aligned(q, ar);
     cudaError_t e;
     if (al) {
-        team_shape(g.dim / 4, &team, &vpt);
-        e = SSD_NORM_TYPES(bwd_v, 4, 16, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
+        team_shape(g.dim / 4, kBwdTeam, &team, &vpt);
+        e = SSD_NORM_TYPES(bwd_v, 4, 32, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
                            g, p, team, st);
     } else {
-        team_shape(g.dim, &team, &vpt);
-        e = SSD_NORM_TYPES(bwd_v, 1, 64, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
+        team_shape(g.dim, kBwdTeam, &team, &vpt);
+        e = SSD_NORM_TYPES(bwd_v, 1, 128, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
                            g, p, team, st);
     }
     if (e != cudaSuccess)

@@ -94,14 +94,14 @@ template <int P, int W> __device__ __forceinline__ void shift(f32x2 (&win)[W][P]
 }
 
 // One thread: VEC channels of `run` consecutive tokens of one sequence, in
-// groups of kGroup tokens whose loads are issued together.
+// groups of kGroup tokens, the next group's loads in flight.
 template <typename TI, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const TI *__restrict__ init, TI *__restrict__ y, TI *__restrict__ fin, ConvGeom g, int run,
             int64_t n_runs)
 {
-    constexpr int P = kPairs<VEC>, kGroup = 8;
+    constexpr int P = kPairs<VEC>, kGroup = 4;
     const int64_t nv = g.dim / VEC;
     const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
     const int64_t r = idx / nv;
@@ -139,16 +139,25 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
         yp += g.dim;
     };
     int t = 0;
+    RawV<TI, VEC> next[kGroup];
+    auto fetch = [&](int at) {
+        if (at + kGroup <= n)
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                next[j] = load_ahead_as<RawV<TI, VEC>>(xp + (at + j) * g.row);
+    };
+    fetch(0);
     for (; t + kGroup <= n; t += kGroup) {
         RawV<TI, VEC> raw[kGroup];
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
-            raw[j] = load_raw<TI, VEC>(xp + j * g.row);
-        xp += kGroup * g.row;
+            raw[j] = next[j];
+        fetch(t + kGroup);
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
             token(raw[j]);
     }
+    xp += t * g.row;
     for (; t < n; ++t) {
         token(load_raw<TI, VEC>(xp));
         xp += g.row;
@@ -202,7 +211,7 @@ conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const fl
 constexpr int kBwdCols = 32, kBwdRuns = 8;
 
 template <typename TI, int VEC, int W>
-__global__ void __launch_bounds__(kBwdCols *kBwdRuns)
+__global__ void __launch_bounds__(kBwdCols *kBwdRuns, 2)
 conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
                 const TI *__restrict__ init, const TI *__restrict__ dy, const TI *__restrict__ dfinal,
                 TI *__restrict__ dx, TI *__restrict__ dinit, float *__restrict__ part, ConvGeom g, int run,
@@ -320,19 +329,30 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
         int64_t e = e0 - (W - 1);
         for (const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0; e < own; ++e)
             edge(e);
-        // rows inside the sequence, kGroup tokens' loads at a time
+        // rows inside the sequence, the next kGroup tokens' loads in flight
         const int64_t inner = min64(e1, L);
         const TI *xp = xb + e * g.row, *yp = dyb + e * g.row_dy;
         TI *op = dxb + (e - (W - 1)) * g.dim;
+        V xn[kGroup], yn[kGroup];
+        auto fetch = [&](int64_t at) {
+            if (at + kGroup <= inner)
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j) {
+                    xn[j] = load_ahead_as<V>(xp + j * g.row);
+                    yn[j] = load_ahead_as<V>(yp + j * g.row_dy);
+                }
+            xp += kGroup * g.row;
+            yp += kGroup * g.row_dy;
+        };
+        fetch(e);
         for (; e + kGroup <= inner; e += kGroup) {
             V xr[kGroup], yr[kGroup];
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
-                xr[j] = load_raw<TI, VEC>(xp + j * g.row);
-                yr[j] = load_raw<TI, VEC>(yp + j * g.row_dy);
+                xr[j] = xn[j];
+                yr[j] = yn[j];
             }
-            xp += kGroup * g.row;
-            yp += kGroup * g.row_dy;
+            fetch(e + kGroup);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
                 step_in(xr[j], yr[j]);

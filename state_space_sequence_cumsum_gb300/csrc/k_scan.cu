@@ -27,12 +27,13 @@ enum PassMode { kOut, kStates, kReverse };
 template <typename TI> struct PassArgs {
     const TI *x, *dt, *z, *m, *cm;
     const float *A, *D, *bias;
-    const float *start;  // [B][segments][dim][N], nullptr: zeros
+    const float *start;  // [B][segments][dim][N] (reverse: [B][dim][N], the last segment's), nullptr: zeros
     TI *y;               // forward output
     float *last;         // final state (forward), initial state's gradient (reverse), or nullptr
     float *kept;         // [B][nc][dim][N] state entering each chunk, or nullptr
     float *seg_end;      // [B][segments][dim][N] end state of each segment, or nullptr
     float *seg_dsum;     // [B][segments][dim] sum of delta of each segment
+    float *after;        // reverse: [B][nc][dim] sum of delta from a chunk's end to its segment's, or nullptr
     int64_t row_x, row_m;
     int64_t chunks_per_seg, first_seg, n_seg;
     bool vec, vec_bc;
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) 
             load_states(a.A + st + i * g.N, nn[i], v);
             A[i][0] = pk2(decay_rate(v[0]), decay_rate(v[1]));
             A[i][1] = pk2(decay_rate(v[2]), decay_rate(v[3]));
-            if (a.start) {
-                load_states(a.start + (b * a.n_seg + seg) * g.dim * g.N + st + i * g.N, nn[i], v);
+            if (a.start && (!REV || seg == a.n_seg - 1)) {
+                load_states(a.start + (REV ? b : b * a.n_seg + seg) * g.dim * g.N + st + i * g.N, nn[i], v);
                 h[i][0] = pk2(v[0], v[1]);
                 h[i][1] = pk2(v[2], v[3]);
             }
@@ -145,6 +146,11 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) 
         typename Tile::Buf &s = sm.buf[k & 1];
         if (a.kept)
             save(a.kept + (b * nc + at(k)) * g.dim * g.N);
+        if (REV && a.after && n0 == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (nn[i] > 0)
+                    a.after[(b * nc + at(k)) * g.dim + ch0 + c + i] = dsum[i];
         // Tokens past the end have delta = x = 0 and change nothing.  A group's
         // decays and inputs do not depend on the states: the next group's are
         // formed before this one's recurrence, which hides their latencies.
@@ -245,10 +251,10 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) 
                 break;
             const TI *qx = px + i * TROWS * a.row_x, *qd = pd + i * TROWS * g.row_dt, *qz = pz + i * TROWS * g.row_z;
             if (whole && nt == T) {
-                xr[i] = load_ahead(qx);
-                dr[i] = load_ahead(qd);
+                xr[i] = load_ahead_as<Raw4<TI>>(qx);
+                dr[i] = load_ahead_as<Raw4<TI>>(qd);
                 if (pz)
-                    zr[i] = load_ahead(qz);
+                    zr[i] = load_ahead_as<Raw4<TI>>(qz);
             } else {
                 const int n = t < nt ? nq : 0;
                 xr[i] = load_raw4(qx, n, a.vec);
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) 
                 break;
             const TI *q = i < PER ? pm + i % PER * BT * a.row_m : pc + i % PER * BT * g.row_c;
             if (whole_bc && nt == T)
-                br[i] = load_ahead(q);
+                br[i] = load_ahead_as<Raw4<TI>>(q);
             else
                 br[i] = load_raw4(q, t < nt ? N - n0 : 0, a.vec_bc);
         }
@@ -388,13 +394,16 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) 
     }
 }
 
-// Segment end states -> segment start states, in place, in the order of the
-// pass: start' = exp(A dsum) start + end.  kJoin segments' values are read
-// before the first is replaced.
+// Segment end states -> what enters each segment, in place, in the order of
+// the pass: enter' = exp(A dsum) enter + end.  Forward: from the initial
+// state, the last segment's end is not there and not needed.  Reverse: the
+// last segment's own pass began with what enters it, so from zero; `last`
+// receives what leaves the first.  kJoin segments' values are read before the
+// first is replaced.
 template <bool REV>
 __global__ void __launch_bounds__(256)
 scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const float *__restrict__ A,
-                 const float *start, int64_t batch, int64_t dim, int64_t N, int64_t n_seg)
+                 const float *start, float *last, int64_t batch, int64_t dim, int64_t N, int64_t n_seg)
 {
     constexpr int kJoin = 8;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -409,22 +418,28 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
             const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
-            // the last segment's end is not needed (nor computed)
-            end[j] = k < n_seg - 1 ? seg[s * DN + r] : 0.f;
-            q[j] = k < n_seg - 1 ? dsum[s * dim + d] : 0.f;
+            const bool there = REV ? k < n_seg : k < n_seg - 1;
+            end[j] = there ? seg[s * DN + r] : 0.f;
+            q[j] = there ? dsum[s * dim + d] : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
             const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
-            if (k < n_seg)
+            if (k < n_seg) {
                 seg[s * DN + r] = h;
-            h = fmaf(ex2(A2 * q[j]), h, end[j]);
+                h = fmaf(ex2(A2 * q[j]), h, end[j]);
+            }
         }
     }
+    if (REV && last)
+        last[i] = h;
 }
 
-// One token: four states of a channel per thread, LN lanes per channel;
-// blockIdx.y is the sequence.
+// One token.  A thread holds four states of a channel, LN lanes a channel, for
+// R sequences (blockIdx.y: which R).  What a (sequence, channel) needs once --
+// its step, input, gate and output -- is the work of one lane: lane r of a
+// channel has sequence r's, passes the step to the others and receives the
+// sum of their outputs.
 template <typename TI, int LN>
 __global__ void __launch_bounds__(256)
 scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const float *__restrict__ A,
@@ -432,43 +447,68 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
                  const TI *__restrict__ z, const float *__restrict__ bias, const float *state,
                  float *state_out, TI *__restrict__ y, ScanGeom g, bool vec_bc)
 {
+    constexpr int R = LN < 4 ? LN : 4;
     const unsigned i = blockIdx.x * 256u + threadIdx.x;
     const unsigned d = i / LN;
-    const int n0 = 4 * (int)(i % LN);
+    const int lane = (int)(i % LN), n0 = 4 * lane;
     const bool live = d < (unsigned)g.dim;
-    const int64_t b = blockIdx.y;
     const int nn = live ? (int)g.N - n0 : 0;
-    float s = 0.f, uv = 0.f, zv = 0.f;
-    if (nn > 0) {
-        const unsigned grp = g.G == 1 ? 0 : d / (unsigned)g.kpg;
-        const int64_t st = (b * g.dim + d) * g.N + n0;
-        float h[4], av[4], bv[4], cv[4];
-        load_states(state + st, nn, h);
-        load_states(A + (int64_t)d * g.N + n0, nn, av);
+    const unsigned grp = g.G == 1 || !live ? 0 : d / (unsigned)g.kpg;
+    const int64_t b0 = (int64_t)blockIdx.y * R;
+    float h[R][4], bv[R][4], cv[R][4], av[4] = {};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = b0 + r < g.batch ? nn : 0;
+        const int64_t b = b0 + r;
+        load_states(state + (b * g.dim + d) * g.N + n0, n, h[r]);
+        unpack<TI, 4>(load_raw4(Bm + b * g.row_b + grp * g.N + n0, n, vec_bc), bv[r]);
+        unpack<TI, 4>(load_raw4(Cm + b * g.row_c + grp * g.N + n0, n, vec_bc), cv[r]);
+    }
+    load_states(A + (int64_t)d * g.N + n0, nn, av);
+    // this lane's sequence
+    const int64_t b = b0 + lane;
+    const bool mine = live && lane < R && b < g.batch;
+    float dl = 0.f, uv = 0.f, zv = 0.f;
+    if (mine) {
         uv = to_f32(u[b * g.row_u + d]);
-        float dl = to_f32(dt[b * g.row_dt + d]);
+        dl = to_f32(dt[b * g.row_dt + d]) + (bias ? bias[d] : 0.f);
         if (z)
             zv = to_f32(z[b * g.row_z + d]);
-        unpack<TI, 4>(load_raw4(Bm + b * g.row_b + grp * g.N + n0, nn, vec_bc), bv);
-        unpack<TI, 4>(load_raw4(Cm + b * g.row_c + grp * g.N + n0, nn, vec_bc), cv);
-        if (bias)
-            dl += bias[d];
         dl = g.softplus ? softplus(dl) : dl;
-        const float du = dl * uv;
+    }
+    const float du = dl * uv;
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float dr = __shfl_sync(0xffffffffu, dl, r, LN), xr = __shfl_sync(0xffffffffu, du, r, LN);
+        s[r] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            h[e] = fmaf(ex2(dl * decay_rate(av[e])), h[e], du * bv[e]);
-            s = fmaf(h[e], cv[e], s);
+            h[r][e] = fmaf(ex2(dr * decay_rate(av[e])), h[r][e], xr * bv[r][e]);
+            s[r] = fmaf(h[r][e], cv[r][e], s[r]);
         }
-        store_states(state_out + st, nn, h);
+        if (nn > 0 && b0 + r < g.batch)
+            store_states(state_out + ((b0 + r) * g.dim + d) * g.N + n0, nn, h[r]);
     }
-    s = lane_sum<LN>(s);
-    if (live && n0 == 0) {
+    // each exchange sends the sums of half the sequences and keeps the other
+    // half's; lane r ends with sequence r's
+#pragma unroll
+    for (int o = 1, n = R; o < R; o *= 2, n /= 2)
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = lane & o ? s[2 * k + 1] : s[2 * k], send = lane & o ? s[2 * k] : s[2 * k + 1];
+            s[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+#pragma unroll
+    for (int o = R; o < LN; o *= 2)
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+    if (mine) {
+        float out = s[0];
         if (D)
-            s = fmaf(D[d], uv, s);
+            out = fmaf(D[d], uv, out);
         if (z)
-            s *= fast_silu(zv);
-        y[b * g.dim + d] = from_f32<TI>(s);
+            out *= fast_silu(zv);
+        y[b * g.dim + d] = from_f32<TI>(out);
     }
 }
 
@@ -502,48 +542,53 @@ cudaError_t launch_pass(const PassArgs<TI> &a, const ScanGeom &g, int64_t segs, 
     }
 }
 
-// Runs a pass, in segments where the channels alone cannot fill the GPU: the
-// segments' end states from zero, their join, then all segments at once.
-template <typename TI, bool REV>
-cudaError_t run_pass(PassArgs<TI> a, const float *start, void *ws, const ScanGeom &g, cudaStream_t st)
+template <bool REV>
+cudaError_t launch_join(float *seg, const float *dsum, const float *A, const float *start, float *last,
+                        const ScanGeom &g, int64_t n_seg, cudaStream_t st)
 {
-    constexpr int ENDS = REV ? kReverse : kStates;
+    const int64_t n = g.batch * g.dim * g.N;
+    scan_join_kernel<REV><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(seg, dsum, A, start, last, g.batch, g.dim, g.N,
+                                                                     n_seg);
+    note_launch(1);
+    return cudaGetLastError();
+}
+
+template <typename TI> void matrix_args(PassArgs<TI> *a, const ScanGeom &g, int64_t row_m)
+{
+    const size_t al = 4 * sizeof(TI);
+    a->row_m = row_m;
+    a->vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(a->m, al) && aligned(a->cm, al);
+}
+
+// The forward, in segments where the channels alone cannot fill the GPU: the
+// segments' end states from zero, their join, then all segments at once.
+template <typename TI>
+cudaError_t run_forward(PassArgs<TI> a, const float *start, void *ws, const ScanGeom &g, cudaStream_t st)
+{
     const ScanSegs sp = scan_segments(g);
     a.chunks_per_seg = sp.chunks_per_seg;
     a.n_seg = sp.n_seg;
-    a.first_seg = 0;
-    a.seg_end = a.seg_dsum = nullptr;
     a.start = start;
-    a.row_m = REV ? g.row_c : g.row_b;
-    const size_t al = 4 * sizeof(TI);
-    a.vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(a.m, al) && aligned(a.cm, al);
+    matrix_args(&a, g, g.row_b);
     if (sp.n_seg > 1) {
         float *seg = static_cast<float *>(ws);
         float *dsum = seg + g.batch * sp.n_seg * g.dim * g.N;
         PassArgs<TI> e = a;
         e.start = nullptr;
         e.y = nullptr;
-        if (!REV)
-            e.z = nullptr;
+        e.z = nullptr;
         e.last = e.kept = nullptr;
         e.seg_end = seg;
         e.seg_dsum = dsum;
-        e.first_seg = REV ? 1 : 0;
-        cudaError_t err = launch_pass<TI, ENDS>(e, g, sp.n_seg - 1, st);
+        cudaError_t err = launch_pass<TI, kStates>(e, g, sp.n_seg - 1, st);
         if (err != cudaSuccess)
             return err;
-        const int64_t n = g.batch * g.dim * g.N;
-        scan_join_kernel<REV><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(seg, dsum, a.A, start, g.batch, g.dim,
-                                                                         g.N, sp.n_seg);
-        note_launch(1);
-        err = cudaGetLastError();
+        err = launch_join<false>(seg, dsum, a.A, start, nullptr, g, sp.n_seg, st);
         if (err != cudaSuccess)
             return err;
         a.start = seg;
     }
-    if (REV || !a.y)
-        return launch_pass<TI, ENDS>(a, g, sp.n_seg, st);
-    return launch_pass<TI, kOut>(a, g, sp.n_seg, st);
+    return a.y ? launch_pass<TI, kOut>(a, g, sp.n_seg, st) : launch_pass<TI, kStates>(a, g, sp.n_seg, st);
 }
 
 bool quads_ok(const ScanGeom &g, const void *x, int64_t row_x, const void *dt, const void *z, const void *y,
@@ -573,14 +618,18 @@ cudaError_t fwd_t(const void *u, const void *dt, const float *A, const void *Bm,
     a.kept = kept;
     a.row_x = g.row_u;
     a.vec = quads_ok(g, u, g.row_u, dt, a.z, y, sizeof(TI));
-    return run_pass<TI, false>(a, init, ws, g, st);
+    return run_forward<TI>(a, init, ws, g, st);
 }
 
+// The reverse pass.  Nothing but the states comes of it, so its segments are
+// passed through once, from zero, and the gradients add what entered a
+// segment to its chunks' states as they read them.
 template <typename TI>
 cudaError_t rev_t(const void *dy, const void *dt, const float *A, const void *Cm, const void *z,
-                  const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws,
+                  const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws, ScanEnter *enter,
                   const ScanGeom &g, cudaStream_t st)
 {
+    const ScanSegs sp = scan_reverse_segments(g);
     PassArgs<TI> a{};
     a.x = static_cast<const TI *>(dy);
     a.dt = static_cast<const TI *>(dt);
@@ -588,11 +637,28 @@ cudaError_t rev_t(const void *dy, const void *dt, const float *A, const void *Cm
     a.m = static_cast<const TI *>(Cm);
     a.A = A;
     a.bias = bias;
-    a.last = dinit;
+    a.start = dfinal;
     a.kept = dkept;
     a.row_x = g.row_dy;
     a.vec = quads_ok(g, dy, g.row_dy, dt, z, nullptr, sizeof(TI));
-    return run_pass<TI, true>(a, dfinal, ws, g, st);
+    a.chunks_per_seg = sp.chunks_per_seg;
+    a.n_seg = sp.n_seg;
+    matrix_args(&a, g, g.row_c);
+    *enter = ScanEnter{nullptr, nullptr, sp.n_seg, sp.chunks_per_seg};
+    if (sp.n_seg == 1) {
+        a.last = dinit;
+        return launch_pass<TI, kReverse>(a, g, 1, st);
+    }
+    float *seg = static_cast<float *>(ws);
+    a.seg_end = seg;
+    a.seg_dsum = seg + g.batch * sp.n_seg * g.dim * g.N;
+    a.after = a.seg_dsum + g.batch * sp.n_seg * g.dim;
+    const cudaError_t err = launch_pass<TI, kReverse>(a, g, sp.n_seg, st);
+    if (err != cudaSuccess)
+        return err;
+    enter->state = seg;
+    enter->after = a.after;
+    return launch_join<true>(seg, a.seg_dsum, A, nullptr, dinit, g, sp.n_seg, st);
 }
 
 template <typename TI>
@@ -601,7 +667,8 @@ cudaError_t step_t(const void *u, const void *dt, const float *A, const void *Bm
                    const ScanGeom &g, cudaStream_t st)
 {
     const int LN = scan_lanes(g.N);
-    const dim3 blocks((unsigned)((g.dim * LN + 255) / 256), (unsigned)g.batch);
+    const int64_t R = LN < 4 ? LN : 4;
+    const dim3 blocks((unsigned)((g.dim * LN + 255) / 256), (unsigned)((g.batch + R - 1) / R));
     const size_t al = 4 * sizeof(TI);
     const bool vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al);
 #define SSD_STEP(LANES)                                                                              \
@@ -656,10 +723,32 @@ ScanSegs scan_segments(const ScanGeom &g)
     return s;
 }
 
+// The reverse pass's segments cost only their join: as many as one wave holds.
+ScanSegs scan_reverse_segments(const ScanGeom &g)
+{
+    const int64_t per_warp = 2 * 32 / scan_lanes(g.N);
+    const int64_t warps = g.G * ((g.kpg + per_warp - 1) / per_warp) * g.batch;
+    const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
+    const int64_t n = min64(9 * (int64_t)device_sm_count() / warps, nc / 8);
+    ScanSegs s{1, nc};
+    if (n > 1) {
+        s.chunks_per_seg = (nc + n - 1) / n;
+        s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;
+    }
+    return s;
+}
+
 size_t scan_pass_workspace(const ScanGeom &g)
 {
     const ScanSegs s = scan_segments(g);
     return s.n_seg > 1 ? (size_t)(g.batch * s.n_seg * g.dim * (g.N + 1)) * sizeof(float) : 0;
+}
+
+size_t scan_reverse_workspace(const ScanGeom &g)
+{
+    const ScanSegs s = scan_reverse_segments(g);
+    const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
+    return s.n_seg > 1 ? (size_t)(g.batch * (s.n_seg * g.dim * (g.N + 1) + nc * g.dim)) * sizeof(float) : 0;
 }
 
 cudaError_t launch_selective_scan(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
@@ -673,10 +762,10 @@ cudaError_t launch_selective_scan(const void *u, const void *dt, const float *A,
 
 cudaError_t launch_scan_reverse(const void *dy, const void *dt, const float *A, const void *Cm, const void *z,
                                 const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws,
-                                const ScanGeom &g, bool bf16, cudaStream_t st)
+                                ScanEnter *enter, const ScanGeom &g, bool bf16, cudaStream_t st)
 {
-    return bf16 ? rev_t<__nv_bfloat16>(dy, dt, A, Cm, z, bias, dfinal, dkept, dinit, ws, g, st)
-                : rev_t<float>(dy, dt, A, Cm, z, bias, dfinal, dkept, dinit, ws, g, st);
+    return bf16 ? rev_t<__nv_bfloat16>(dy, dt, A, Cm, z, bias, dfinal, dkept, dinit, ws, enter, g, st)
+                : rev_t<float>(dy, dt, A, Cm, z, bias, dfinal, dkept, dinit, ws, enter, g, st);
 }
 
 cudaError_t launch_scan_step(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,

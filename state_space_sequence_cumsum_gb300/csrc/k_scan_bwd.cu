@@ -33,6 +33,7 @@ template <typename TI> struct GradArgs {
     float *dB, *dC;        // [channel blocks][B * L][N]
     float *dA;             // [B * chunk groups][dim][N]
     float *dD;             // [B * chunk groups][2][dim]: dD, dbias
+    ScanEnter enter;
     int64_t chunks_per_group;
     bool vec, vec_bc;
 };
@@ -165,6 +166,13 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 load_states(a.g1 + at, nn[j], v);
                 e[j][0] = pk2(v[0], v[1]);
                 e[j][1] = pk2(v[2], v[3]);
+                if (a.enter.state) {  // and what entered the reverse pass's segment, decayed to here
+                    const int64_t seg = b * a.enter.n_seg + chunk / a.enter.chunks_per_seg;
+                    const float q = a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j];
+                    load_states(a.enter.state + seg * g.dim * g.N + st + j * g.N, nn[j], v);
+                    e[j][0] = fma2(ex2_2(mul2(dup2(q), A[j][0])), pk2(v[0], v[1]), e[j][0]);
+                    e[j][1] = fma2(ex2_2(mul2(dup2(q), A[j][1])), pk2(v[2], v[3]), e[j][1]);
+                }
             }
         copy_async_wait<0>();
         __syncthreads();  // raw[w] is complete, and the chunk before is done with everything
@@ -293,7 +301,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 *reinterpret_cast<float2 *>(&s.part[1][at]) = make_float2(sB[0], sB[1]);
                 *reinterpret_cast<float2 *>(&s.part[2][at]) = make_float2(sA[0], sA[1]);
             }
-            // dB and dC of the piece: red[which][token][state][channel pair]
+            // dB and dC of the piece: red[which][token][state % 4][lane][channel pair]
+            // (a row's lanes are then eight banks apart)
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) {
                 float v[8];
@@ -303,11 +312,11 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 un2(dC[i][1], v[6], v[7]);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    s.red[(((k / 4) * kPiece + i) * NP + n0 + k % 4) * Tile::RED + cp] = v[k];
+                    s.red[((((k / 4) * kPiece + i) * 4 + k % 4) * LN + tid % LN) * Tile::RED + cp] = v[k];
             }
             __syncthreads();
             for (int o = tid; o < 2 * kPiece * NP; o += NT) {
-                const int t = t0 + o / NP % kPiece, n = o % NP;
+                const int t = t0 + o / NP % kPiece, n = 4 * (o % LN) + o / LN % 4;
                 const float *q = s.red + o * Tile::RED;
                 f32x2 v0 = 0, v1 = 0;
 #pragma unroll
@@ -502,8 +511,8 @@ GradWs grad_layout(const ScanGeom &g, char *base)
 
 template <typename TI>
 cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
-                   const void *z, const float *bias, const void *dy, const float *h0, const float *g1, void *du,
-                   void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *dbias, void *ws,
+                   const void *z, const float *bias, const void *dy, const float *h0, const float *g1,
+                   const ScanEnter &enter, void *du, void *ddt, float *dA, void *dB, void *dC, float *dD, void *dz, float *dbias, void *ws,
                    const ScanGeom &g, cudaStream_t st)
 {
     const GradPlan p = grad_plan(g);
@@ -520,6 +529,7 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     a.bias = bias;
     a.h0 = h0;
     a.g1 = g1;
+    a.enter = enter;
     a.du = static_cast<TI *>(du);
     a.ddt = static_cast<TI *>(ddt);
     a.dz = static_cast<TI *>(dz);
@@ -569,12 +579,12 @@ size_t scan_grad_workspace(const ScanGeom &g) { return grad_layout(g, nullptr).b
 
 cudaError_t launch_scan_grad(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
                              const float *D, const void *z, const float *bias, const void *dy, const float *h0,
-                             const float *g1, void *du, void *ddt, float *dA, void *dB, void *dC, float *dD,
-                             void *dz, float *dbias, void *ws, const ScanGeom &g, bool bf16, cudaStream_t st)
+                             const float *g1, const ScanEnter &enter, void *du, void *ddt, float *dA, void *dB,
+                             void *dC, float *dD, void *dz, float *dbias, void *ws, const ScanGeom &g, bool bf16, cudaStream_t st)
 {
-    return bf16 ? grad_t<__nv_bfloat16>(u, dt, A, Bm, Cm, D, z, bias, dy, h0, g1, du, ddt, dA, dB, dC, dD, dz,
+    return bf16 ? grad_t<__nv_bfloat16>(u, dt, A, Bm, Cm, D, z, bias, dy, h0, g1, enter, du, ddt, dA, dB, dC, dD, dz,
                                         dbias, ws, g, st)
-                : grad_t<float>(u, dt, A, Bm, Cm, D, z, bias, dy, h0, g1, du, ddt, dA, dB, dC, dD, dz, dbias, ws,
+                : grad_t<float>(u, dt, A, Bm, Cm, D, z, bias, dy, h0, g1, enter, du, ddt, dA, dB, dC, dD, dz, dbias, ws,
                                 g, st);
 }
 

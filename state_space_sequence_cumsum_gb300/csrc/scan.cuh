@@ -15,23 +15,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Four consecutive elements as loaded; elements past n are zero.
 template <typename TI> using Raw4 = typename Pack<TI, 4>::T;
 
-// An aligned quad.  Volatile, so that a load issued ahead of a tile stays
-// there: the compiler would otherwise sink it to its use a tile later.
-__device__ __forceinline__ uint2 load_ahead(const __nv_bfloat16 *p)
-{
-    uint2 r;
-    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ float4 load_ahead(const float *p)
-{
-    float4 r;
-    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-                 : "l"(p));
-    return r;
-}
-
 template <typename TI> __device__ __forceinline__ Raw4<TI> load_raw4(const TI *p, int n, bool vec)
 {
     Raw4<TI> r{};

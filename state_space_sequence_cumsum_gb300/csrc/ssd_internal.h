@@ -182,22 +182,31 @@ struct ScanSegs {
 int scan_lanes(int64_t N);  // lanes that hold a channel's states, four each
 int scan_chunk();           // tokens between kept states
 ScanSegs scan_segments(const ScanGeom &g);
+ScanSegs scan_reverse_segments(const ScanGeom &g);
 size_t scan_pass_workspace(const ScanGeom &g);
+size_t scan_reverse_workspace(const ScanGeom &g);
+// What entered each segment of the reverse pass (nullptr: one segment), and
+// the sum of delta between a chunk's end and its segment's.
+struct ScanEnter {
+    const float *state;  // [B][n_seg][dim][N]
+    const float *after;  // [B][nc][dim]
+    int64_t n_seg, chunks_per_seg;
+};
 cudaError_t launch_selective_scan(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
                                   const float *D, const void *z, const float *bias, const float *init, void *y,
                                   float *fin, float *kept, void *ws, const ScanGeom &g, bool bf16,
                                   cudaStream_t st);
 cudaError_t launch_scan_reverse(const void *dy, const void *dt, const float *A, const void *Cm, const void *z,
                                 const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws,
-                                const ScanGeom &g, bool bf16, cudaStream_t st);
+                                ScanEnter *enter, const ScanGeom &g, bool bf16, cudaStream_t st);
 cudaError_t launch_scan_step(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
                              const float *D, const void *z, const float *bias, const float *state,
                              float *state_out, void *y, const ScanGeom &g, bool bf16, cudaStream_t st);
 size_t scan_grad_workspace(const ScanGeom &g);
 cudaError_t launch_scan_grad(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,
                              const float *D, const void *z, const float *bias, const void *dy, const float *h0,
-                             const float *g1, void *du, void *ddt, float *dA, void *dB, void *dC, float *dD,
-                             void *dz, float *dbias, void *ws, const ScanGeom &g, bool bf16, cudaStream_t st);
+                             const float *g1, const ScanEnter &enter, void *du, void *ddt, float *dA, void *dB,
+                             void *dC, float *dD, void *dz, float *dbias, void *ws, const ScanGeom &g, bool bf16, cudaStream_t st);
 
 // Norms around a block (k_block_norm.cu).
 struct NormGeom {

@@ -188,7 +188,8 @@ BwdWs scan_bwd_layout(const ScanGeom &g, bool have_kept, char *base)
     };
     w.kept = have_kept ? nullptr : reinterpret_cast<float *>(take((size_t)kept_elems(g) * 4));
     w.dkept = reinterpret_cast<float *>(take((size_t)kept_elems(g) * 4));
-    w.pass = take(scan_pass_workspace(g));
+    const size_t fwd = have_kept ? 0 : scan_pass_workspace(g), rev = scan_reverse_workspace(g);
+    w.pass = take(fwd > rev ? fwd : rev);
     w.grad = take(scan_grad_workspace(g));
     w.bytes = off;
     return w;
@@ -409,9 +410,11 @@ ssd_status_t ssd_selective_scan_bwd(const void *u, const void *dt, const float *
                                                   nullptr, w.kept, w.pass, g, bf16, st)));
         chunk_states = w.kept;
     }
-    SSD_TRY(cuda_status(launch_scan_reverse(dy, dt, A, Cm, z, dt_bias, dfinal, w.dkept, dinit, w.pass, g, bf16, st)));
-    return cuda_status(launch_scan_grad(u, dt, A, Bm, Cm, D, z, dt_bias, dy, chunk_states, w.dkept, du, ddt, dA,
-                                        dB, dC, dD, dz, ddt_bias, w.grad, g, bf16, st));
+    ScanEnter enter;
+    SSD_TRY(cuda_status(launch_scan_reverse(dy, dt, A, Cm, z, dt_bias, dfinal, w.dkept, dinit, w.pass, &enter, g, bf16,
+                                            st)));
+    return cuda_status(launch_scan_grad(u, dt, A, Bm, Cm, D, z, dt_bias, dy, chunk_states, w.dkept, enter, du, ddt,
+                                        dA, dB, dC, dD, dz, ddt_bias, w.grad, g, bf16, st));
 }
 
 ssd_status_t ssd_selective_scan_step(const void *u, const void *dt, const float *A, const void *Bm,

@@ -27,6 +27,28 @@ template <typename TI> struct Pack<TI, 1> {
     using T = TI;
 };
 
+// An aligned vector.  Volatile, so that a load issued ahead of its use stays
+// there: the compiler would otherwise sink it to the use.
+template <typename T> __device__ __forceinline__ T load_ahead_as(const void *p)
+{
+    static_assert(sizeof(T) == 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "one access");
+    T r;
+    if constexpr (sizeof(T) == 2)
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(*reinterpret_cast<unsigned short *>(&r)) : "l"(p));
+    else if constexpr (sizeof(T) == 4)
+        asm volatile("ld.global.u32 %0, [%1];" : "=r"(*reinterpret_cast<unsigned *>(&r)) : "l"(p));
+    else if constexpr (sizeof(T) == 8)
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(reinterpret_cast<unsigned *>(&r)[0]), "=r"(reinterpret_cast<unsigned *>(&r)[1])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(reinterpret_cast<unsigned *>(&r)[0]), "=r"(reinterpret_cast<unsigned *>(&r)[1]),
+                       "=r"(reinterpret_cast<unsigned *>(&r)[2]), "=r"(reinterpret_cast<unsigned *>(&r)[3])
+                     : "l"(p));
+    return r;
+}
+
 template <typename TI, int NV>
 __device__ __forceinline__ void unpack(const typename Pack<TI, NV>::T &p, float (&v)[NV])
 {

@@ -143,12 +143,27 @@ block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__r
     }
 }
 
-// v - x m, the part of a row's gradient across the row's direction.  In a row
-// of one channel the two terms differ by the eps term alone (the gradient is
-// all radial), which their difference in f32 would lose: there it is v eps rs^2.
-__device__ __forceinline__ float minus_radial(float v, float x, float m, float rs, const NormGeom &g)
+template <typename TI, int VEC>
+__device__ __forceinline__ void to_pairs(const typename Pack<TI, VEC>::T &r, f32x2 (&p)[(VEC + 1) / 2])
 {
-    return g.dim == 1 ? v * (g.eps * rs * rs) : fmaf(-x, m, v);
+    float v[VEC];
+    unpack<TI, VEC>(r, v);
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i)
+        p[i] = pk2(v[2 * i], 2 * i + 1 < VEC ? v[(2 * i + 1) % VEC] : 0.f);
+}
+template <typename TI, int VEC> __device__ __forceinline__ void store_pairs(TI *p, const f32x2 (&o)[(VEC + 1) / 2])
+{
+    float v[VEC];
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i) {
+        float x, y;
+        un2(o[i], x, y);
+        v[2 * i] = x;
+        if (2 * i + 1 < VEC)
+            v[(2 * i + 1) % VEC] = y;
+    }
+    store_vec<TI, VEC>(p, v);
 }
 
 // Backward.  A block walks the rows of its items one after another; an item
@@ -156,8 +171,12 @@ __device__ __forceinline__ float minus_radial(float v, float x, float m, float r
 // The parameters' gradients stay in the thread that owns the channels: the
 // weights' over all its rows (one partial per block: part[block][0] is
 // weight, [1] post_weight), the gate's over an item (written as it is where
-// an item is a whole gate row, else one partial per item).
-template <typename TI, typename TR, int VEC, int VPT>
+// an item is a whole gate row, else one partial per item).  Values are held
+// as f32 pairs; the next row's inputs are in flight while a row is reduced.
+//   ONE: rows of one channel.  There a gradient is all radial, so g - x m,
+//   its part across the row's direction, is the eps term alone, g eps rs^2,
+//   which the difference of the two nearly equal terms would lose.
+template <typename TI, typename TR, int VEC, int VPT, bool ONE>
 __global__ void __launch_bounds__(kBwdTeam, VEC * VPT <= 8 ? 2 : 1)
 block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const float *__restrict__ weight,
                       const float *__restrict__ post_weight, const float *__restrict__ gate,
@@ -167,109 +186,133 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
 {
     __shared__ Sum<3> sum_row[2][16];
     __shared__ Sum<1> sum_p[16];
+    constexpr int P = (VEC + 1) / 2;
+    using VI = typename Pack<TI, VEC>::T;
+    using VR = typename Pack<TR, VEC>::T;
     int flip = 0;
     const int team = blockDim.x;
     const int nv = (int)(g.dim / VEC);
-    float dw[VPT][VEC], dpw[VPT][VEC], dg[VPT][VEC];
+    f32x2 dw[VPT][P], dpw[VPT][P], dg[VPT][P];
 #pragma unroll
     for (int q = 0; q < VPT; ++q)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            dw[q][i] = dpw[q][i] = 0.f;
+        for (int i = 0; i < P; ++i)
+            dw[q][i] = dpw[q][i] = 0;
     const int64_t tokens = g.ntokens / groups;
+    auto across = [&](f32x2 v, f32x2 x, float m, float rs) {
+        return ONE ? mul2(v, dup2(g.eps * rs * rs)) : fma2(x, dup2(-m), v);
+    };
     for (int64_t item = blockIdx.x; item < groups * spans; item += gridDim.x) {
         const int64_t j = item / spans, sp = item - j * spans;
         const int64_t t0 = j * tokens + tokens * sp / spans, t1 = j * tokens + tokens * (sp + 1) / spans;
 #pragma unroll
         for (int q = 0; q < VPT; ++q)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                dg[q][i] = 0.f;
-        using VI = typename Pack<TI, VEC>::T;
-        using VR = typename Pack<TR, VEC>::T;
+            for (int i = 0; i < P; ++i)
+                dg[q][i] = 0;
         VI y_raw[VPT], n_raw[VPT];
         VR r_raw[VPT], d_raw[VPT];
-        auto fetch = [&](int64_t row) {
+        int64_t at = t0 * g.dim + threadIdx.x * VEC;  // of the row to fetch
+        auto fetch = [&]() {
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
-                const int v = threadIdx.x + q * team;
                 y_raw[q] = n_raw[q] = VI{};
                 r_raw[q] = d_raw[q] = VR{};
-                if (v < nv) {
-                    const int64_t at = row * g.dim + v * VEC;
-                    y_raw[q] = *reinterpret_cast<const VI *>(y + at);
-                    r_raw[q] = *reinterpret_cast<const VR *>(r + at);
-                    n_raw[q] = *reinterpret_cast<const VI *>(dout + at);
+                if ((int)threadIdx.x + q * team < nv) {
+                    const int64_t k = at + q * team * VEC;
+                    y_raw[q] = *reinterpret_cast<const VI *>(y + k);
+                    r_raw[q] = *reinterpret_cast<const VR *>(r + k);
+                    n_raw[q] = *reinterpret_cast<const VI *>(dout + k);
                     if (dr)
-                        d_raw[q] = *reinterpret_cast<const VR *>(dr + at);
+                        d_raw[q] = *reinterpret_cast<const VR *>(dr + k);
                 }
             }
+            at += g.dim;
         };
         if (t0 < t1)
-            fetch(t0);
+            fetch();
         for (int64_t row = t0; row < t1; ++row) {
-            float yv[VPT][VEC], rv[VPT][VEC], gn[VPT][VEC], gr[VPT][VEC];
-            float s[3] = {0.f, 0.f, 0.f};
+            f32x2 yv[VPT][P], rv[VPT][P], gn[VPT][P], gr[VPT][P];
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
-                unpack<TI, VEC>(y_raw[q], yv[q]);
-                unpack<TR, VEC>(r_raw[q], rv[q]);
-                unpack<TI, VEC>(n_raw[q], gn[q]);
-                unpack<TR, VEC>(d_raw[q], gr[q]);
+                to_pairs<TI, VEC>(y_raw[q], yv[q]);
+                to_pairs<TR, VEC>(r_raw[q], rv[q]);
+                to_pairs<TI, VEC>(n_raw[q], gn[q]);
+                to_pairs<TR, VEC>(d_raw[q], gr[q]);
             }
-            if (row + 1 < t1)  // in flight while this row is reduced
-                fetch(row + 1);
+            if (row + 1 < t1)
+                fetch();
+            const int64_t out = row * g.dim;
+            f32x2 s0 = 0, s1 = 0, s2 = 0;
+            // (the weights are read again after the sums: registers are short)
+            auto weights = [&](int v, f32x2 (&w)[P]) {
+                typename Pack<float, VEC>::T wr{};
+                if (v < nv)
+                    wr = *reinterpret_cast<const typename Pack<float, VEC>::T *>(weight + v * VEC);
+                to_pairs<float, VEC>(wr, w);
+            };
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
-                const int v = threadIdx.x + q * team;
-                float w[VEC] = {};
-                if (v < nv)
-                    load_vec<float, VEC>(weight + v * VEC, w);
+                f32x2 w[P];
+                weights(threadIdx.x + q * team, w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    s[0] = fmaf(yv[q][i], yv[q][i], s[0]);
-                    s[1] = fmaf(rv[q][i], rv[q][i], s[1]);
-                    s[2] = fmaf(gn[q][i] * w[i], rv[q][i], s[2]);
+                for (int i = 0; i < P; ++i) {
+                    s0 = fma2(yv[q][i], yv[q][i], s0);
+                    s1 = fma2(rv[q][i], rv[q][i], s1);
+                    s2 = fma2(mul2(gn[q][i], w[i]), rv[q][i], s2);
                 }
             }
+            float s[3] = {hsum(s0), hsum(s1), hsum(s2)};
             team_sum<3>(s, sum_row[flip]);
             flip ^= 1;
             const float rs_y = post_weight ? rsqrtf(s[0] * g.inv_dim + g.eps) : 1.f;
             const float rs_r = rsqrtf(s[1] * g.inv_dim + g.eps);
             const float c = s[2] * g.inv_dim * rs_r * rs_r;  // mean(gn rh) rs_r
-            float u[1] = {0.f};
+            f32x2 u2 = 0;
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
                 const int v = threadIdx.x + q * team;
                 if (v < nv) {
-                    float w[VEC], pw[VEC], k[VEC];
-                    load_vec<float, VEC>(weight + v * VEC, w);
+                    f32x2 w[P];
+                    weights(v, w);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        dw[q][i] = fmaf(gn[q][i], rv[q][i] * rs_r, dw[q][i]);
-                        gr[q][i] += rs_r * minus_radial(gn[q][i] * w[i], rv[q][i], c, rs_r, g);
-                        pw[i] = 1.f;
-                        k[i] = g.scale;
+                    for (int i = 0; i < P; ++i) {
+                        dw[q][i] = fma2(gn[q][i], mul2(rv[q][i], dup2(rs_r)), dw[q][i]);
+                        gr[q][i] = fma2(across(mul2(gn[q][i], w[i]), rv[q][i], c, rs_r), dup2(rs_r), gr[q][i]);
                     }
-                    store_vec<TR, VEC>(dresidual + row * g.dim + v * VEC, gr[q]);
-                    if (post_weight)
-                        load_vec<float, VEC>(post_weight + v * VEC, pw);
-                    if (gate)
-                        scale_by<VEC>(gate + j * g.dim + v * VEC, k);
+                    store_pairs<TR, VEC>(dresidual + out + v * VEC, gr[q]);
+                    f32x2 pw[P], k[P];
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float yh = yv[q][i] * rs_y;
-                        dg[q][i] = fmaf(gr[q][i], yh * pw[i], dg[q][i]);
-                        const float dp = k[i] * gr[q][i];
-                        dpw[q][i] = fmaf(dp, yh, dpw[q][i]);
-                        gr[q][i] = dp * pw[i];
+                    for (int i = 0; i < P; ++i) {
+                        pw[i] = dup2(1.f);
+                        k[i] = dup2(g.scale);
+                    }
+                    if (post_weight)
+                        to_pairs<float, VEC>(
+                            *reinterpret_cast<const typename Pack<float, VEC>::T *>(post_weight + v * VEC), pw);
+                    if (gate) {
+                        f32x2 gv[P];
+                        to_pairs<float, VEC>(
+                            *reinterpret_cast<const typename Pack<float, VEC>::T *>(gate + j * g.dim + v * VEC), gv);
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+                            k[i] = mul2(k[i], gv[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const f32x2 yh = mul2(yv[q][i], dup2(rs_y)), yp = mul2(yh, pw[i]);
+                        dg[q][i] = fma2(gr[q][i], yp, dg[q][i]);
+                        const f32x2 dp = mul2(k[i], gr[q][i]);
+                        dpw[q][i] = fma2(dp, yh, dpw[q][i]);
+                        u2 = fma2(dp, yp, u2);
+                        gr[q][i] = mul2(dp, pw[i]);
                         yv[q][i] = yh;
-                        u[0] = fmaf(gr[q][i], yh, u[0]);
                     }
                 }
             }
             float m = 0.f;
             if (post_weight) {
+                float u[1] = {hsum(u2)};
                 team_sum<1>(u, sum_p);
                 m = u[0] * g.inv_dim;
             }
@@ -277,10 +320,11 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
             for (int q = 0; q < VPT; ++q) {
                 const int v = threadIdx.x + q * team;
                 if (v < nv) {
+                    if (post_weight)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        gr[q][i] = post_weight ? rs_y * minus_radial(gr[q][i], yv[q][i], m, rs_y, g) : gr[q][i];
-                    store_vec<TI, VEC>(dy + row * g.dim + v * VEC, gr[q]);
+                        for (int i = 0; i < P; ++i)
+                            gr[q][i] = mul2(across(gr[q][i], yv[q][i], m, rs_y), dup2(rs_y));
+                    store_pairs<TI, VEC>(dy + out + v * VEC, gr[q]);
                 }
             }
         }
@@ -288,43 +332,55 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
                 const int v = threadIdx.x + q * team;
-                if (v < nv)
+                if (v < nv) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        dgate_part[item * g.dim + v * VEC + i] = g.scale * dg[q][i];
+                    for (int i = 0; i < P; ++i)
+                        dg[q][i] = mul2(dg[q][i], dup2(g.scale));
+                    store_pairs<float, VEC>(dgate_part + item * g.dim + v * VEC, dg[q]);
+                }
             }
     }
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
         const int v = threadIdx.x + q * team;
         if (v < nv) {
-            store_vec<float, VEC>(part + ((int64_t)blockIdx.x * 2) * g.dim + v * VEC, dw[q]);
-            store_vec<float, VEC>(part + ((int64_t)blockIdx.x * 2 + 1) * g.dim + v * VEC, dpw[q]);
+            store_pairs<float, VEC>(part + ((int64_t)blockIdx.x * 2) * g.dim + v * VEC, dw[q]);
+            store_pairs<float, VEC>(part + ((int64_t)blockIdx.x * 2 + 1) * g.dim + v * VEC, dpw[q]);
         }
     }
 }
 
-// out[row][c] = sum over n of src[(row * n_stride_row + p * stride) + c], in a
-// fixed order; blockDim = (32, 8).
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float *__restrict__ src, int64_t n, int64_t stride,
-                                                       int64_t row_stride, int64_t dim, float *__restrict__ out)
+// Adds the partials in a fixed order: blockIdx.y 0 is dweight, 1 dpost_weight
+// (may be nullptr), 2 + j row j of dgate.  blockDim = (32, 32).
+struct NormSums {
+    const float *part, *gate_part;
+    float *dweight, *dpost_weight, *dgate;
+    int64_t blocks, spans, dim;
+};
+__global__ void __launch_bounds__(1024) norm_sums_kernel(NormSums a)
 {
-    __shared__ float red[8][32];
+    __shared__ float red[32][33];
     const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
-    const float *p0 = src + (int64_t)blockIdx.y * row_stride + c;
+    const int which = blockIdx.y;
+    const float *src = which < 2 ? a.part + which * a.dim : a.gate_part + (int64_t)(which - 2) * a.spans * a.dim;
+    float *out = which == 0 ? a.dweight : which == 1 ? a.dpost_weight : a.dgate + (int64_t)(which - 2) * a.dim;
+    if (!out)
+        return;
+    const int64_t n = which < 2 ? a.blocks : a.spans, stride = which < 2 ? 2 * a.dim : a.dim;
     float s = 0.f;
-    if (c < dim)
-        for (int64_t p = threadIdx.y; p < n; p += 8)
-            s += p0[p * stride];
+    if (c < a.dim)
+#pragma unroll 4
+        for (int64_t p = threadIdx.y; p < n; p += 32)
+            s += src[p * stride + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && c < dim) {
-        s = 0.f;
+    s = red[threadIdx.x][threadIdx.y];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            s += red[q][threadIdx.x];
-        out[(int64_t)blockIdx.y * dim + c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t cw = (int64_t)blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && cw < a.dim)
+        out[cw] = s;
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -379,7 +435,9 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
                   float *part, float *dgate_part, const NormGeom &g, const BwdPlan &p, int team,
                   cudaStream_t st)
 {
-    block_norm_bwd_kernel<TI, TR, VEC, VPT><<<(unsigned)p.blocks, team, 0, st>>>(
+    auto k = VEC == 1 && VPT == 1 && g.dim == 1 ? block_norm_bwd_kernel<TI, TR, VEC, VPT, VEC == 1 && VPT == 1>
+                                                : block_norm_bwd_kernel<TI, TR, VEC, VPT, false>;
+    k<<<(unsigned)p.blocks, team, 0, st>>>(
         static_cast<const TI *>(y), static_cast<const TR *>(r), weight, post_weight, gate,
         static_cast<const TI *>(dout), static_cast<const TR *>(dr), static_cast<TI *>(dy),
         static_cast<TR *>(dresidual), part, dgate_part, g, p.groups, p.spans);
@@ -459,19 +517,11 @@ cudaError_t launch_block_norm_bwd(const void *y, const void *r, const float *wei
     }
     if (e != cudaSuccess)
         return e;
-    const unsigned cols = (unsigned)((g.dim + 31) / 32);
-    sum_rows_kernel<<<dim3(cols, 1), dim3(32, 8), 0, st>>>(part, p.blocks, 2 * g.dim, 0, g.dim, dweight);
+    const bool gate_sums = gate && p.spans > 1;
+    const NormSums sums{part, gpart, dweight, dpost_weight, dgate, p.blocks, p.spans, g.dim};
+    norm_sums_kernel<<<dim3((unsigned)((g.dim + 31) / 32), (unsigned)(2 + (gate_sums ? p.groups : 0))), dim3(32, 32),
+                       0, st>>>(sums);
     note_launch(1);
-    if (dpost_weight) {
-        sum_rows_kernel<<<dim3(cols, 1), dim3(32, 8), 0, st>>>(part + g.dim, p.blocks, 2 * g.dim, 0, g.dim,
-                                                               dpost_weight);
-        note_launch(1);
-    }
-    if (gate && p.spans > 1) {
-        sum_rows_kernel<<<dim3(cols, (unsigned)p.groups), dim3(32, 8), 0, st>>>(gpart, p.spans, g.dim,
-                                                                               p.spans * g.dim, g.dim, dgate);
-        note_launch(1);
-    }
     return cudaGetLastError();
 }
 

@@ -74,6 +74,73 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ w, const 
     }
 }
 
+// A thread's own ring of groups in shared memory: the copies of the groups
+// ahead are in flight without holding registers, and as a thread reads only
+// what it copied itself, no barrier is needed.  (Two-byte elements, one
+// channel a thread, are too small to copy and are loaded when their group is
+// due.)
+constexpr int kGroup = 4;   // tokens of a group
+constexpr int kStages = 4;  // groups in flight
+template <typename TI, int VEC, int TENSORS> struct Ring {
+    static constexpr bool kAsync = sizeof(RawV<TI, VEC>) >= 4;
+    static constexpr size_t kBytes = kAsync ? sizeof(RawV<TI, VEC>) * kGroup * kStages * TENSORS * kConvThreads : 0;
+    const TI *p[TENSORS];   // the next group to copy
+    int64_t row[TENSORS];
+    int ahead = 0, left;    // groups copied and not yet taken; groups still to copy
+    int slot_in = 0, slot_out = 0;
+    RawV<TI, VEC> *buf;     // [stage][tensor][token][thread]
+
+    __device__ __forceinline__ RawV<TI, VEC> *at(int slot, int k, int j)
+    {
+        return buf + ((slot * TENSORS + k) * kGroup + j) * kConvThreads;
+    }
+    __device__ __forceinline__ void push()
+    {
+        if (left > 0) {
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    copy_async<sizeof(RawV<TI, VEC>) < 4 ? 4 : sizeof(RawV<TI, VEC>)>(at(slot_in, k, j),
+                                                                                   p[k] + j * row[k]);
+                p[k] += kGroup * row[k];
+            }
+            --left;
+        }
+        copy_async_commit();  // a group for every push, so that the waits count alike
+        slot_in = slot_in + 1 == kStages ? 0 : slot_in + 1;
+    }
+    __device__ __forceinline__ void start(void *smem, int thread, int groups)
+    {
+        left = groups;
+        buf = static_cast<RawV<TI, VEC> *>(smem) + thread;
+        if constexpr (kAsync)
+            for (int i = 0; i < kStages - 1; ++i)
+                push();
+    }
+    __device__ __forceinline__ void take(RawV<TI, VEC> (&v)[TENSORS][kGroup])
+    {
+        if constexpr (kAsync) {
+            push();
+            copy_async_wait<kStages - 1>();
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k)
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    v[k][j] = *at(slot_out, k, j);
+            slot_out = slot_out + 1 == kStages ? 0 : slot_out + 1;
+        } else {
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    v[k][j] = p[k][j * row[k]];
+                p[k] += kGroup * row[k];
+            }
+        }
+    }
+};
+
 // The convolution of one window.
 template <int P, int W>
 __device__ __forceinline__ f32x2 window_sum(const f32x2 (&wv)[W][P], const f32x2 (&bv)[P], const f32x2 (&win)[W][P], int i)
@@ -94,14 +161,14 @@ template <int P, int W> __device__ __forceinline__ void shift(f32x2 (&win)[W][P]
 }
 
 // One thread: VEC channels of `run` consecutive tokens of one sequence, in
-// groups of kGroup tokens, the next group's loads in flight.
+// groups of kGroup tokens through the ring.
 template <typename TI, int VEC, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const TI *__restrict__ init, TI *__restrict__ y, TI *__restrict__ fin, ConvGeom g, int run,
             int64_t n_runs)
 {
-    constexpr int P = kPairs<VEC>, kGroup = 4;
+    constexpr int P = kPairs<VEC>;
     const int64_t nv = g.dim / VEC;
     const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
     const int64_t r = idx / nv;
@@ -138,24 +205,18 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
         store_pairs<TI, VEC>(yp, o);
         yp += g.dim;
     };
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Ring<TI, VEC, 1> ring;
+    ring.p[0] = xp;
+    ring.row[0] = g.row;
+    ring.start(smem_raw, threadIdx.x, n / kGroup);
     int t = 0;
-    RawV<TI, VEC> next[kGroup];
-    auto fetch = [&](int at) {
-        if (at + kGroup <= n)
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j)
-                next[j] = load_ahead_as<RawV<TI, VEC>>(xp + (at + j) * g.row);
-    };
-    fetch(0);
     for (; t + kGroup <= n; t += kGroup) {
-        RawV<TI, VEC> raw[kGroup];
+        RawV<TI, VEC> raw[1][kGroup];
+        ring.take(raw);
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
-            raw[j] = next[j];
-        fetch(t + kGroup);
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-            token(raw[j]);
+            token(raw[0][j]);
     }
     xp += t * g.row;
     for (; t < n; ++t) {
@@ -209,6 +270,7 @@ conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const fl
 // their weight gradients are added in shared memory and written as one
 // partial per block: part[p][k][c], k = W for the bias.
 constexpr int kBwdCols = 32, kBwdRuns = 8;
+static_assert(kBwdCols * kBwdRuns == kConvThreads, "the ring is laid out for kConvThreads");
 
 template <typename TI, int VEC, int W>
 __global__ void __launch_bounds__(kBwdCols *kBwdRuns, 2)
@@ -217,9 +279,10 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 TI *__restrict__ dx, TI *__restrict__ dinit, float *__restrict__ part, ConvGeom g, int run,
                 int64_t parts_per_seq)
 {
-    constexpr int P = kPairs<VEC>, kGroup = 4;
+    constexpr int P = kPairs<VEC>;
     using V = RawV<TI, VEC>;
     __shared__ f32x2 red[kBwdRuns][P][kBwdCols];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
     const int64_t c = ((int64_t)blockIdx.x * kBwdCols + threadIdx.x) * VEC;
     const int64_t b = blockIdx.y / parts_per_seq;
     const int64_t e0 = ((blockIdx.y - b * parts_per_seq) * kBwdRuns + threadIdx.y) * run;
@@ -329,33 +392,21 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
         int64_t e = e0 - (W - 1);
         for (const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0; e < own; ++e)
             edge(e);
-        // rows inside the sequence, the next kGroup tokens' loads in flight
+        // rows inside the sequence, kGroup tokens at a time through the ring
         const int64_t inner = min64(e1, L);
-        const TI *xp = xb + e * g.row, *yp = dyb + e * g.row_dy;
         TI *op = dxb + (e - (W - 1)) * g.dim;
-        V xn[kGroup], yn[kGroup];
-        auto fetch = [&](int64_t at) {
-            if (at + kGroup <= inner)
-#pragma unroll
-                for (int j = 0; j < kGroup; ++j) {
-                    xn[j] = load_ahead_as<V>(xp + j * g.row);
-                    yn[j] = load_ahead_as<V>(yp + j * g.row_dy);
-                }
-            xp += kGroup * g.row;
-            yp += kGroup * g.row_dy;
-        };
-        fetch(e);
+        Ring<TI, VEC, 2> ring;
+        ring.p[0] = xb + e * g.row;
+        ring.p[1] = dyb + e * g.row_dy;
+        ring.row[0] = g.row;
+        ring.row[1] = g.row_dy;
+        ring.start(smem_raw, threadIdx.y * kBwdCols + threadIdx.x, inner > e ? (int)(inner - e) / kGroup : 0);
         for (; e + kGroup <= inner; e += kGroup) {
-            V xr[kGroup], yr[kGroup];
+            V raw[2][kGroup];
+            ring.take(raw);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
-                xr[j] = xn[j];
-                yr[j] = yn[j];
-            }
-            fetch(e + kGroup);
-#pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                step_in(xr[j], yr[j]);
+                step_in(raw[0][j], raw[1][j]);
                 sums();
                 f32x2 o[P];
                 grad(o);
@@ -422,7 +473,7 @@ int conv_run(const ConvGeom &g, int vec)
 {
     const int64_t threads = g.batch * (g.dim / vec);
     const int64_t want = (int64_t)device_sm_count() * 1024;
-    int run = 32;
+    int run = 64;
     while (run > 4 && threads * ((g.seqlen + run - 1) / run) < want)
         run /= 2;
     return run;
@@ -438,7 +489,7 @@ int conv_bwd_run(const ConvGeom &g, int vec)
 {
     const int64_t cols = (g.dim / vec + kBwdCols - 1) / kBwdCols;
     const int64_t want = (int64_t)device_sm_count() * 4;
-    int run = 32;
+    int run = 64;
     while (run > 4 && cols * g.batch * ((g.seqlen + g.width - 1 + 8 * run - 1) / (8 * run)) < want)
         run /= 2;
     while (conv_bwd_parts_per_seq(g, run) * g.batch > 65535)  // one grid row each
@@ -453,7 +504,14 @@ cudaError_t fwd_w(const void *x, const float *w, const float *bias, const void *
     const int run = conv_run(g, VEC);
     const int64_t n_runs = (g.seqlen + run - 1) / run;
     const int64_t threads = g.batch * n_runs * (g.dim / VEC);
-    conv_kernel<TI, VEC, W><<<(unsigned)((threads + kConvThreads - 1) / kConvThreads), kConvThreads, 0, st>>>(
+    constexpr size_t smem = Ring<TI, VEC, 1>::kBytes;
+    auto k = conv_kernel<TI, VEC, W>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    k<<<(unsigned)((threads + kConvThreads - 1) / kConvThreads), kConvThreads, smem, st>>>(
         static_cast<const TI *>(x), w, bias, static_cast<const TI *>(init), static_cast<TI *>(y),
         static_cast<TI *>(fin), g, run, n_runs);
     note_launch(1);
@@ -477,7 +535,14 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
 {
     const int64_t pps = conv_bwd_parts_per_seq(g, run);
     const dim3 grid((unsigned)((g.dim / VEC + kBwdCols - 1) / kBwdCols), (unsigned)(pps * g.batch));
-    conv_bwd_kernel<TI, VEC, W><<<grid, dim3(kBwdCols, kBwdRuns), 0, st>>>(
+    constexpr size_t smem = Ring<TI, VEC, 2>::kBytes;
+    auto k = conv_bwd_kernel<TI, VEC, W>;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    k<<<grid, dim3(kBwdCols, kBwdRuns), smem, st>>>(
         static_cast<const TI *>(x), w, bias, static_cast<const TI *>(init), static_cast<const TI *>(dy),
         static_cast<const TI *>(dfinal), static_cast<TI *>(dx), static_cast<TI *>(dinit), part, g, run, pps);
     note_launch(1);

@@ -440,42 +440,73 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
 // its step, input, gate and output -- is the work of one lane: lane r of a
 // channel has sequence r's, passes the step to the others and receives the
 // sum of their outputs.
-template <typename TI, int LN>
+//   WHOLE: every lane holds four states and every quad is one access, so all
+//   loads are issued before the first is used (threads and sequences past the
+//   end load the last one's and store nothing).
+template <typename TI, int LN, bool WHOLE>
 __global__ void __launch_bounds__(256)
 scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const float *__restrict__ A,
                  const TI *__restrict__ Bm, const TI *__restrict__ Cm, const float *__restrict__ D,
                  const TI *__restrict__ z, const float *__restrict__ bias, const float *state,
-                 float *state_out, TI *__restrict__ y, ScanGeom g, bool vec_bc)
+                 float *state_out, TI *__restrict__ y, ScanGeom g)
 {
     constexpr int R = LN < 4 ? LN : 4;
     const unsigned i = blockIdx.x * 256u + threadIdx.x;
-    const unsigned d = i / LN;
+    const bool live = i / LN < (unsigned)g.dim;
+    const unsigned d = live ? i / LN : (unsigned)g.dim - 1;
     const int lane = (int)(i % LN), n0 = 4 * lane;
-    const bool live = d < (unsigned)g.dim;
     const int nn = live ? (int)g.N - n0 : 0;
-    const unsigned grp = g.G == 1 || !live ? 0 : d / (unsigned)g.kpg;
+    const unsigned grp = g.G == 1 ? 0 : d / (unsigned)g.kpg;
     const int64_t b0 = (int64_t)blockIdx.y * R;
-    float h[R][4], bv[R][4], cv[R][4], av[4] = {};
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int n = b0 + r < g.batch ? nn : 0;
-        const int64_t b = b0 + r;
-        load_states(state + (b * g.dim + d) * g.N + n0, n, h[r]);
-        unpack<TI, 4>(load_raw4(Bm + b * g.row_b + grp * g.N + n0, n, vec_bc), bv[r]);
-        unpack<TI, 4>(load_raw4(Cm + b * g.row_c + grp * g.N + n0, n, vec_bc), cv[r]);
-    }
-    load_states(A + (int64_t)d * g.N + n0, nn, av);
     // this lane's sequence
-    const int64_t b = b0 + lane;
-    const bool mine = live && lane < R && b < g.batch;
-    float dl = 0.f, uv = 0.f, zv = 0.f;
-    if (mine) {
-        uv = to_f32(u[b * g.row_u + d]);
-        dl = to_f32(dt[b * g.row_dt + d]) + (bias ? bias[d] : 0.f);
-        if (z)
-            zv = to_f32(z[b * g.row_z + d]);
-        dl = g.softplus ? softplus(dl) : dl;
+    const int64_t b = min64(b0 + lane % R, g.batch - 1);
+    const bool mine = live && lane < R && b0 + lane < g.batch;
+    float h[R][4], bv[R][4], cv[R][4], av[4];
+    float uv, dl, zv, bs, Dv;
+    {
+        float4 hr[R], ar;
+        Raw4<TI> br[R], cr[R];
+        if (WHOLE) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t q = min64(b0 + r, g.batch - 1);
+                hr[r] = load_ahead_as<float4>(state + (q * g.dim + d) * g.N + n0);
+                br[r] = load_ahead_as<Raw4<TI>>(Bm + q * g.row_b + grp * g.N + n0);
+                cr[r] = load_ahead_as<Raw4<TI>>(Cm + q * g.row_c + grp * g.N + n0);
+            }
+            ar = load_ahead_as<float4>(A + (int64_t)d * g.N + n0);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int n = b0 + r < g.batch ? nn : 0;
+                const int64_t q = b0 + r;
+                load_states(state + (q * g.dim + d) * g.N + n0, n, h[r]);
+                unpack<TI, 4>(load_raw4(Bm + q * g.row_b + grp * g.N + n0, n, false), bv[r]);
+                unpack<TI, 4>(load_raw4(Cm + q * g.row_c + grp * g.N + n0, n, false), cv[r]);
+            }
+            load_states(A + (int64_t)d * g.N + n0, nn, av);
+        }
+        const TI ur = u[b * g.row_u + d], dr = dt[b * g.row_dt + d];
+        const TI zr = z ? z[b * g.row_z + d] : ur;
+        bs = bias ? bias[d] : 0.f;
+        Dv = D ? D[d] : 0.f;
+        if (WHOLE) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                unpack<float, 4>(hr[r], h[r]);
+                unpack<TI, 4>(br[r], bv[r]);
+                unpack<TI, 4>(cr[r], cv[r]);
+            }
+            unpack<float, 4>(ar, av);
+        }
+        uv = to_f32(ur);
+        dl = to_f32(dr) + bs;
+        zv = to_f32(zr);
     }
+    dl = g.softplus ? softplus(dl) : dl;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        av[e] = decay_rate(av[e]);
     const float du = dl * uv;
     float s[R];
 #pragma unroll
@@ -484,7 +515,7 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
         s[r] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            h[r][e] = fmaf(ex2(dr * decay_rate(av[e])), h[r][e], xr * bv[r][e]);
+            h[r][e] = fmaf(ex2(dr * av[e]), h[r][e], xr * bv[r][e]);
             s[r] = fmaf(h[r][e], cv[r][e], s[r]);
         }
         if (nn > 0 && b0 + r < g.batch)
@@ -504,8 +535,7 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
         s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
     if (mine) {
         float out = s[0];
-        if (D)
-            out = fmaf(D[d], uv, out);
+        out = fmaf(Dv, uv, out);
         if (z)
             out *= fast_silu(zv);
         y[b * g.dim + d] = from_f32<TI>(out);
@@ -670,12 +700,13 @@ cudaError_t step_t(const void *u, const void *dt, const float *A, const void *Bm
     const int64_t R = LN < 4 ? LN : 4;
     const dim3 blocks((unsigned)((g.dim * LN + 255) / 256), (unsigned)((g.batch + R - 1) / R));
     const size_t al = 4 * sizeof(TI);
-    const bool vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al);
+    const bool whole = g.N == 4 * LN && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al) &&
+                       aligned(A, 16) && aligned(state, 16) && aligned(state_out, 16);
 #define SSD_STEP(LANES)                                                                              \
-    scan_step_kernel<TI, LANES><<<blocks, 256, 0, st>>>(                                             \
+    (whole ? scan_step_kernel<TI, LANES, true> : scan_step_kernel<TI, LANES, false>)<<<blocks, 256, 0, st>>>( \
         static_cast<const TI *>(u), static_cast<const TI *>(dt), A, static_cast<const TI *>(Bm),     \
         static_cast<const TI *>(Cm), D, static_cast<const TI *>(z), bias, state, state_out,          \
-        static_cast<TI *>(y), g, vec_bc)
+        static_cast<TI *>(y), g)
     switch (LN) {
     case 1: SSD_STEP(1); break;
     case 2: SSD_STEP(2); break;

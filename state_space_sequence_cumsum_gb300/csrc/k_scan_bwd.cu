@@ -54,20 +54,6 @@ template <typename TI, int LN> struct GradTile {
     float red[2 * kPiece * NP * RED];   // each channel pair's part of dB, dC
 };
 
-__device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes)
-{
-    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
-    if (bytes == 8)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT> __device__ __forceinline__ void copy_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
 template <typename TI, int LN>
 __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kernel(GradArgs<TI> a, ScanGeom g)
 {
@@ -121,11 +107,11 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         for (int t = trow; t < T; t += TROWS) {
             const int64_t tok = tok0 + t;
             if (a.vec && nq >= 4 && t < nt) {
-                copy_async(&r.u[t][col], a.u + tok * g.row_u + ch0 + col, 4 * sizeof(TI));
-                copy_async(&r.dt[t][col], a.dt + tok * g.row_dt + ch0 + col, 4 * sizeof(TI));
-                copy_async(&r.dy[t][col], a.dy + tok * g.row_dy + ch0 + col, 4 * sizeof(TI));
+                copy_async<4 * sizeof(TI)>(&r.u[t][col], a.u + tok * g.row_u + ch0 + col);
+                copy_async<4 * sizeof(TI)>(&r.dt[t][col], a.dt + tok * g.row_dt + ch0 + col);
+                copy_async<4 * sizeof(TI)>(&r.dy[t][col], a.dy + tok * g.row_dy + ch0 + col);
                 if (a.z)
-                    copy_async(&r.z[t][col], a.z + tok * g.row_z + ch0 + col, 4 * sizeof(TI));
+                    copy_async<4 * sizeof(TI)>(&r.z[t][col], a.z + tok * g.row_z + ch0 + col);
             } else {
                 const int n = t < nt ? nq : 0;
                 *reinterpret_cast<Raw4<TI> *>(&r.u[t][col]) = load_raw4(a.u + tok * g.row_u + ch0 + col, n, false);
@@ -141,7 +127,7 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
             TI *dst = q ? &r.c[t][n] : &r.m[t][n];
             const TI *src = (q ? a.cm + (tok0 + t) * g.row_c : a.bm + (tok0 + t) * g.row_b) + grp * g.N + n;
             if (a.vec_bc && t < nt && N - n >= 4)
-                copy_async(dst, src, 4 * sizeof(TI));
+                copy_async<4 * sizeof(TI)>(dst, src);
             else
                 *reinterpret_cast<Raw4<TI> *>(dst) = load_raw4(src, t < nt ? N - n : 0, false);
         }
@@ -167,7 +153,7 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 e[j][0] = pk2(v[0], v[1]);
                 e[j][1] = pk2(v[2], v[3]);
                 if (a.enter.state) {  // and what entered the reverse pass's segment, decayed to here
-                    const int64_t seg = b * a.enter.n_seg + chunk / a.enter.chunks_per_seg;
+                    const int64_t seg = b * a.enter.n_seg + (unsigned)chunk / (unsigned)a.enter.chunks_per_seg;
                     const float q = a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j];
                     load_states(a.enter.state + seg * g.dim * g.N + st + j * g.N, nn[j], v);
                     e[j][0] = fma2(ex2_2(mul2(dup2(q), A[j][0])), pk2(v[0], v[1]), e[j][0]);

@@ -100,6 +100,21 @@ __device__ __forceinline__ float rcp(float x)
     return r;
 }
 
+// Asynchronous copies of 4, 8 or 16 bytes into shared memory.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src)
+{
+    static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "one copy");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most LEFT of the thread's groups are in flight.
+template <int LEFT> __device__ __forceinline__ void copy_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // 1 / (1 + e^-z) with the hardware's exponential and reciprocal (a few ulp);
 // e^-z overflows to inf for z < -88 and the result is then 0.
 __device__ __forceinline__ float fast_sigmoid(float z) { return rcp(1.f + ex2(-kLog2e * z)); }

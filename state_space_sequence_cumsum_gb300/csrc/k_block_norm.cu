@@ -23,6 +23,7 @@ namespace {
 // Threads of a row's team at most.  The backward's fewer leave registers for
 // two blocks an SM (a row's four inputs, the next row's, and three sums).
 constexpr int kFwdTeam = 512, kBwdTeam = 320;
+constexpr int kMaxWarps = 16;  // of a team; a power of two
 
 // Adds K values over the team (blockDim.x threads, a multiple of 32); every
 // thread of the block must call it.  One barrier: `buf` (one Sum<K> per warp
@@ -46,15 +47,20 @@ template <int K> __device__ __forceinline__ void team_sum(float (&v)[K], Sum<K> 
         for (int k = 0; k < K; ++k)
             s[threadIdx.x >> 5].v[k] = v[k];
     __syncthreads();
+    // each lane takes one warp's sums and all add them by shuffles (every
+    // thread reading every warp's costs more of the shared memory pipe)
+    const int other = threadIdx.x % kMaxWarps;
+    Sum<K> t{};
+    if (other < warps)
+        t = s[other];
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        v[k] = 0.f;
-    for (int q = 0; q < warps; ++q) {
-        const Sum<K> t = s[q];
+        v[k] = t.v[k];
+#pragma unroll
+    for (int o = kMaxWarps / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            v[k] += t.v[k];
-    }
+            v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
 
 template <int VEC> __device__ __forceinline__ void scale_by(const float *p, float (&v)[VEC])
@@ -74,7 +80,7 @@ block_norm_kernel(const TI *__restrict__ y, const TR *residual, const float *__r
                   const float *__restrict__ post_weight, const float *__restrict__ gate, TI *__restrict__ out,
                   TR *residual_out, NormGeom g)
 {
-    __shared__ Sum<1> sum_y[16], sum_r[16];
+    __shared__ Sum<1> sum_y[kMaxWarps], sum_r[kMaxWarps];
     const int team = blockDim.x;
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = row < g.ntokens;
@@ -166,13 +172,35 @@ template <typename TI, int VEC> __device__ __forceinline__ void store_pairs(TI *
     store_vec<TI, VEC>(p, v);
 }
 
+// A thread's inputs of one vector of a row.  Rows of four-channel vectors, at
+// most four a thread, come by asynchronous copies two rows ahead into the
+// thread's own slots (no barrier: it reads what it copied itself).
+template <typename TI, typename TR, int VEC> struct NormSlot {
+    typename Pack<TR, VEC>::T r, d;
+    typename Pack<TI, VEC>::T y, n;
+};
+// The slots' components each in an array of their own (`n` entries): neighbouring
+// threads' then lie side by side.
+template <typename TI, typename TR, int VEC> struct NormRing {
+    typename Pack<TR, VEC>::T *r, *d;
+    typename Pack<TI, VEC>::T *y, *n;
+    __device__ NormRing(void *smem, int entries)
+    {
+        r = static_cast<typename Pack<TR, VEC>::T *>(smem);
+        d = r + entries;
+        y = reinterpret_cast<typename Pack<TI, VEC>::T *>(d + entries);
+        n = y + entries;
+    }
+};
+template <int VEC, int VPT> constexpr bool norm_ring = VEC == 4 && VPT <= 4;
+
 // Backward.  A block walks the rows of its items one after another; an item
 // is one of `spans` runs of the tokens of one gate row (or of all tokens).
 // The parameters' gradients stay in the thread that owns the channels: the
 // weights' over all its rows (one partial per block: part[block][0] is
 // weight, [1] post_weight), the gate's over an item (written as it is where
 // an item is a whole gate row, else one partial per item).  Values are held
-// as f32 pairs; the next row's inputs are in flight while a row is reduced.
+// as f32 pairs; the next rows' inputs are in flight while a row is reduced.
 //   ONE: rows of one channel.  There a gradient is all radial, so g - x m,
 //   its part across the row's direction, is the eps term alone, g eps rs^2,
 //   which the difference of the two nearly equal terms would lose.
@@ -184,13 +212,18 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                       float *__restrict__ part, float *__restrict__ dgate_part, NormGeom g, int64_t groups,
                       int64_t spans)
 {
-    __shared__ Sum<3> sum_row[2][16];
-    __shared__ Sum<1> sum_p[16];
+    __shared__ Sum<3> sum_row[2][kMaxWarps];
+    __shared__ Sum<1> sum_p[kMaxWarps];
     constexpr int P = (VEC + 1) / 2;
     using VI = typename Pack<TI, VEC>::T;
     using VR = typename Pack<TR, VEC>::T;
+    using Slot = NormSlot<TI, TR, VEC>;
+    constexpr bool kRing = norm_ring<VEC, VPT>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
     int flip = 0;
     const int team = blockDim.x;
+    const NormRing<TI, TR, VEC> ring(smem_raw, 2 * VPT * team);  // [row & 1][vector][thread]
+    auto slot = [&](int64_t row, int q) { return (((int)row & 1) * VPT + q) * team + (int)threadIdx.x; };
     const int nv = (int)(g.dim / VEC);
     f32x2 dw[VPT][P], dpw[VPT][P], dg[VPT][P];
 #pragma unroll
@@ -210,38 +243,57 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 dg[q][i] = 0;
-        VI y_raw[VPT], n_raw[VPT];
-        VR r_raw[VPT], d_raw[VPT];
-        int64_t at = t0 * g.dim + threadIdx.x * VEC;  // of the row to fetch
-        auto fetch = [&]() {
+        // the inputs of `row` into its slot of the thread's ring, or nothing
+        auto fetch = [&](int64_t row) {
+            if (row < t1)
 #pragma unroll
-            for (int q = 0; q < VPT; ++q) {
-                y_raw[q] = n_raw[q] = VI{};
-                r_raw[q] = d_raw[q] = VR{};
-                if ((int)threadIdx.x + q * team < nv) {
-                    const int64_t k = at + q * team * VEC;
-                    y_raw[q] = *reinterpret_cast<const VI *>(y + k);
-                    r_raw[q] = *reinterpret_cast<const VR *>(r + k);
-                    n_raw[q] = *reinterpret_cast<const VI *>(dout + k);
-                    if (dr)
-                        d_raw[q] = *reinterpret_cast<const VR *>(dr + k);
-                }
-            }
-            at += g.dim;
+                for (int q = 0; q < VPT; ++q)
+                    if ((int)threadIdx.x + q * team < nv) {
+                        const int64_t k = row * g.dim + (threadIdx.x + q * team) * VEC;
+                        const int o = slot(row, q);
+                        copy_async<kRing ? (int)sizeof(VI) : 4>(ring.y + o, y + k);
+                        copy_async<kRing ? (int)sizeof(VR) : 4>(ring.r + o, r + k);
+                        copy_async<kRing ? (int)sizeof(VI) : 4>(ring.n + o, dout + k);
+                        if (dr)
+                            copy_async<kRing ? (int)sizeof(VR) : 4>(ring.d + o, dr + k);
+                    }
+            copy_async_commit();
         };
-        if (t0 < t1)
-            fetch();
+        if constexpr (kRing) {
+            fetch(t0);
+            fetch(t0 + 1);
+        }
         for (int64_t row = t0; row < t1; ++row) {
             f32x2 yv[VPT][P], rv[VPT][P], gn[VPT][P], gr[VPT][P];
+            if constexpr (kRing)
+                copy_async_wait<1>();
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
-                to_pairs<TI, VEC>(y_raw[q], yv[q]);
-                to_pairs<TR, VEC>(r_raw[q], rv[q]);
-                to_pairs<TI, VEC>(n_raw[q], gn[q]);
-                to_pairs<TR, VEC>(d_raw[q], gr[q]);
+                Slot o{};
+                if ((int)threadIdx.x + q * team < nv) {
+                    if constexpr (kRing) {
+                        const int i = slot(row, q);
+                        o.y = ring.y[i];
+                        o.r = ring.r[i];
+                        o.n = ring.n[i];
+                        if (dr)
+                            o.d = ring.d[i];
+                    } else {
+                        const int64_t k = row * g.dim + (threadIdx.x + q * team) * VEC;
+                        o.y = *reinterpret_cast<const VI *>(y + k);
+                        o.r = *reinterpret_cast<const VR *>(r + k);
+                        o.n = *reinterpret_cast<const VI *>(dout + k);
+                        if (dr)
+                            o.d = *reinterpret_cast<const VR *>(dr + k);
+                    }
+                }
+                to_pairs<TI, VEC>(o.y, yv[q]);
+                to_pairs<TR, VEC>(o.r, rv[q]);
+                to_pairs<TI, VEC>(o.n, gn[q]);
+                to_pairs<TR, VEC>(o.d, gr[q]);
             }
-            if (row + 1 < t1)
-                fetch();
+            if constexpr (kRing)
+                fetch(row + 2);
             const int64_t out = row * g.dim;
             f32x2 s0 = 0, s1 = 0, s2 = 0;
             // (the weights are read again after the sums: registers are short)
@@ -437,7 +489,13 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
 {
     auto k = VEC == 1 && VPT == 1 && g.dim == 1 ? block_norm_bwd_kernel<TI, TR, VEC, VPT, VEC == 1 && VPT == 1>
                                                 : block_norm_bwd_kernel<TI, TR, VEC, VPT, false>;
-    k<<<(unsigned)p.blocks, team, 0, st>>>(
+    const size_t smem = norm_ring<VEC, VPT> ? sizeof(NormSlot<TI, TR, VEC>) * 2 * VPT * team : 0;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    k<<<(unsigned)p.blocks, team, smem, st>>>(
         static_cast<const TI *>(y), static_cast<const TR *>(r), weight, post_weight, gate,
         static_cast<const TI *>(dout), static_cast<const TR *>(dr), static_cast<TI *>(dy),
         static_cast<TR *>(dresidual), part, dgate_part, g, p.groups, p.spans);

@@ -81,9 +81,9 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ w, const 
 // due.)
 constexpr int kGroup = 4;   // tokens of a group
 constexpr int kStages = 4;  // groups in flight
-template <typename TI, int VEC, int TENSORS> struct Ring {
+template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
     static constexpr bool kAsync = sizeof(RawV<TI, VEC>) >= 4;
-    static constexpr size_t kBytes = kAsync ? sizeof(RawV<TI, VEC>) * kGroup * kStages * TENSORS * kConvThreads : 0;
+    static constexpr size_t kBytes = kAsync ? sizeof(RawV<TI, VEC>) * kGroup * kStages * TENSORS * NT : 0;
     const TI *p[TENSORS];   // the next group to copy
     int64_t row[TENSORS];
     int ahead = 0, left;    // groups copied and not yet taken; groups still to copy
@@ -92,7 +92,7 @@ template <typename TI, int VEC, int TENSORS> struct Ring {
 
     __device__ __forceinline__ RawV<TI, VEC> *at(int slot, int k, int j)
     {
-        return buf + ((slot * TENSORS + k) * kGroup + j) * kConvThreads;
+        return buf + ((slot * TENSORS + k) * kGroup + j) * NT;
     }
     __device__ __forceinline__ void push()
     {
@@ -206,7 +206,7 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
         yp += g.dim;
     };
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Ring<TI, VEC, 1> ring;
+    Ring<TI, VEC, 1, kConvThreads> ring;
     ring.p[0] = xp;
     ring.row[0] = g.row;
     ring.start(smem_raw, threadIdx.x, n / kGroup);
@@ -266,14 +266,14 @@ conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const fl
 // xf[i .. i + W - 1] and xf[e] receives sum_k w[k] dpre[e - k] (dpre = 0
 // outside [0, L)).  A thread owns rows [e0, e0 + run) of xf: it walks i from
 // e0 - (W - 1), keeping the last W values of xf and of dpre, and sums the
-// weight gradient over its own i.  Eight such runs share a block's channels;
+// weight gradient over its own i.  Four such runs share a block's channels;
 // their weight gradients are added in shared memory and written as one
 // partial per block: part[p][k][c], k = W for the bias.
-constexpr int kBwdCols = 32, kBwdRuns = 8;
-static_assert(kBwdCols * kBwdRuns == kConvThreads, "the ring is laid out for kConvThreads");
+constexpr int kBwdCols = 32, kBwdRuns = 4;
+constexpr int kBwdThreads = kBwdCols * kBwdRuns;
 
 template <typename TI, int VEC, int W>
-__global__ void __launch_bounds__(kBwdCols *kBwdRuns, 2)
+__global__ void __launch_bounds__(kBwdThreads, 3)
 conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
                 const TI *__restrict__ init, const TI *__restrict__ dy, const TI *__restrict__ dfinal,
                 TI *__restrict__ dx, TI *__restrict__ dinit, float *__restrict__ part, ConvGeom g, int run,
@@ -395,7 +395,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
         // rows inside the sequence, kGroup tokens at a time through the ring
         const int64_t inner = min64(e1, L);
         TI *op = dxb + (e - (W - 1)) * g.dim;
-        Ring<TI, VEC, 2> ring;
+        Ring<TI, VEC, 2, kBwdThreads> ring;
         ring.p[0] = xb + e * g.row;
         ring.p[1] = dyb + e * g.row_dy;
         ring.row[0] = g.row;
@@ -484,13 +484,13 @@ int64_t conv_bwd_parts_per_seq(const ConvGeom &g, int run)
     return (g.seqlen + g.width - 1 + (int64_t)kBwdRuns * run - 1) / ((int64_t)kBwdRuns * run);
 }
 
-// Tokens a backward thread walks, eight such runs in a block.
+// Tokens a backward thread walks, kBwdRuns such runs in a block.
 int conv_bwd_run(const ConvGeom &g, int vec)
 {
     const int64_t cols = (g.dim / vec + kBwdCols - 1) / kBwdCols;
-    const int64_t want = (int64_t)device_sm_count() * 4;
+    const int64_t want = (int64_t)device_sm_count() * 6;
     int run = 64;
-    while (run > 4 && cols * g.batch * ((g.seqlen + g.width - 1 + 8 * run - 1) / (8 * run)) < want)
+    while (run > 4 && cols * g.batch * conv_bwd_parts_per_seq(g, run) < want)
         run /= 2;
     while (conv_bwd_parts_per_seq(g, run) * g.batch > 65535)  // one grid row each
         run *= 2;
@@ -504,7 +504,7 @@ cudaError_t fwd_w(const void *x, const float *w, const float *bias, const void *
     const int run = conv_run(g, VEC);
     const int64_t n_runs = (g.seqlen + run - 1) / run;
     const int64_t threads = g.batch * n_runs * (g.dim / VEC);
-    constexpr size_t smem = Ring<TI, VEC, 1>::kBytes;
+    constexpr size_t smem = Ring<TI, VEC, 1, kConvThreads>::kBytes;
     auto k = conv_kernel<TI, VEC, W>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -535,7 +535,7 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
 {
     const int64_t pps = conv_bwd_parts_per_seq(g, run);
     const dim3 grid((unsigned)((g.dim / VEC + kBwdCols - 1) / kBwdCols), (unsigned)(pps * g.batch));
-    constexpr size_t smem = Ring<TI, VEC, 2>::kBytes;
+    constexpr size_t smem = Ring<TI, VEC, 2, kBwdThreads>::kBytes;
     auto k = conv_bwd_kernel<TI, VEC, W>;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -600,33 +600,32 @@ cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, c
 size_t conv_bwd_workspace(const ConvGeom &g)
 {
     int64_t parts = 0;
-    for (int vec : {2, 1}) {
+    for (int vec : {4, 1}) {
         const int64_t p = conv_bwd_parts_per_seq(g, conv_bwd_run(g, vec)) * g.batch;
         parts = p > parts ? p : parts;
     }
     return (size_t)(parts * (g.width + 1) * g.dim) * sizeof(float);
 }
 
-// Two channels a thread (the window, the gradients behind it and the weight
-// sums of four would not leave registers for two blocks an SM), or one.
+// Four channels a thread where every row starts on a boundary of four, else one.
 cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, const void *init,
                             const void *dy, const void *dfinal, void *dx, float *dw, float *dbias,
                             void *dinit, float *part, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
-    const size_t a = bf16 ? 4 : 8;
-    bool al = g.dim % 2 == 0 && g.row % 2 == 0 && g.row_dy % 2 == 0 && aligned(w, 8);
+    const size_t a = bf16 ? 8 : 16;
+    bool al = g.dim % 4 == 0 && g.row % 4 == 0 && g.row_dy % 4 == 0 && aligned(w, 8);
     for (const void *p : {x, init, dy, dfinal, static_cast<const void *>(dx), static_cast<const void *>(dinit)})
         al = al && aligned(p, a);
-    const int run = conv_bwd_run(g, al ? 2 : 1);
+    const int run = conv_bwd_run(g, al ? 4 : 1);
     if (bf16) {
         if (al)
-            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 2, x, w, bias, init, dy, dfinal, dx, dw, dbias,
+            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias,
                                    dinit, part, g, run, st);
         return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit,
                                part, g, run, st);
     }
     if (al)
-        return SSD_CONV_WIDTHS(bwd_w, float, 2, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g,
+        return SSD_CONV_WIDTHS(bwd_w, float, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g,
                                run, st);
     return SSD_CONV_WIDTHS(bwd_w, float, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, run,
                            st);

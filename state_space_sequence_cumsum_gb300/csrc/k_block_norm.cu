@@ -232,17 +232,35 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
         for (int i = 0; i < P; ++i)
             dw[q][i] = dpw[q][i] = 0;
     const int64_t tokens = g.ntokens / groups;
+    // a vector of a parameter, ones without it
+    auto params = [&](const float *p, int v, f32x2 (&o)[P]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            o[i] = dup2(1.f);
+        if (p && v < nv)
+            to_pairs<float, VEC>(*reinterpret_cast<const typename Pack<float, VEC>::T *>(p + v * VEC), o);
+    };
     auto across = [&](f32x2 v, f32x2 x, float m, float rs) {
         return ONE ? mul2(v, dup2(g.eps * rs * rs)) : fma2(x, dup2(-m), v);
     };
     for (int64_t item = blockIdx.x; item < groups * spans; item += gridDim.x) {
         const int64_t j = item / spans, sp = item - j * spans;
         const int64_t t0 = j * tokens + tokens * sp / spans, t1 = j * tokens + tokens * (sp + 1) / spans;
+        // what a row's gradient is scaled by on its way to the block's output:
+        // scale gate post_weight, the same for all rows of an item
+        f32x2 kp[VPT][P];
 #pragma unroll
-        for (int q = 0; q < VPT; ++q)
+        for (int q = 0; q < VPT; ++q) {
+            const int v = threadIdx.x + q * team;
+            f32x2 pw[P], gv[P];
+            params(post_weight, v, pw);
+            params(gate ? gate + j * g.dim : nullptr, v, gv);
 #pragma unroll
-            for (int i = 0; i < P; ++i)
+            for (int i = 0; i < P; ++i) {
                 dg[q][i] = 0;
+                kp[q][i] = mul2(mul2(gv[i], dup2(g.scale)), pw[i]);
+            }
+        }
         // the inputs of `row` into its slot of the thread's ring, or nothing
         auto fetch = [&](int64_t row) {
             if (row < t1)
@@ -296,17 +314,10 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                 fetch(row + 2);
             const int64_t out = row * g.dim;
             f32x2 s0 = 0, s1 = 0, s2 = 0;
-            // (the weights are read again after the sums: registers are short)
-            auto weights = [&](int v, f32x2 (&w)[P]) {
-                typename Pack<float, VEC>::T wr{};
-                if (v < nv)
-                    wr = *reinterpret_cast<const typename Pack<float, VEC>::T *>(weight + v * VEC);
-                to_pairs<float, VEC>(wr, w);
-            };
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
                 f32x2 w[P];
-                weights(threadIdx.x + q * team, w);
+                params(weight, threadIdx.x + q * team, w);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     s0 = fma2(yv[q][i], yv[q][i], s0);
@@ -326,38 +337,19 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                 const int v = threadIdx.x + q * team;
                 if (v < nv) {
                     f32x2 w[P];
-                    weights(v, w);
+                    params(weight, v, w);  // (read again: registers are short)
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
                         dw[q][i] = fma2(gn[q][i], mul2(rv[q][i], dup2(rs_r)), dw[q][i]);
                         gr[q][i] = fma2(across(mul2(gn[q][i], w[i]), rv[q][i], c, rs_r), dup2(rs_r), gr[q][i]);
                     }
                     store_pairs<TR, VEC>(dresidual + out + v * VEC, gr[q]);
-                    f32x2 pw[P], k[P];
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
-                        pw[i] = dup2(1.f);
-                        k[i] = dup2(g.scale);
-                    }
-                    if (post_weight)
-                        to_pairs<float, VEC>(
-                            *reinterpret_cast<const typename Pack<float, VEC>::T *>(post_weight + v * VEC), pw);
-                    if (gate) {
-                        f32x2 gv[P];
-                        to_pairs<float, VEC>(
-                            *reinterpret_cast<const typename Pack<float, VEC>::T *>(gate + j * g.dim + v * VEC), gv);
-#pragma unroll
-                        for (int i = 0; i < P; ++i)
-                            k[i] = mul2(k[i], gv[i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        const f32x2 yh = mul2(yv[q][i], dup2(rs_y)), yp = mul2(yh, pw[i]);
-                        dg[q][i] = fma2(gr[q][i], yp, dg[q][i]);
-                        const f32x2 dp = mul2(k[i], gr[q][i]);
-                        dpw[q][i] = fma2(dp, yh, dpw[q][i]);
-                        u2 = fma2(dp, yp, u2);
-                        gr[q][i] = mul2(dp, pw[i]);
+                        const f32x2 yh = mul2(yv[q][i], dup2(rs_y));
+                        dg[q][i] = fma2(gr[q][i], yh, dg[q][i]);
+                        gr[q][i] = mul2(gr[q][i], kp[q][i]);
+                        u2 = fma2(gr[q][i], yh, u2);
                         yv[q][i] = yh;
                     }
                 }
@@ -380,17 +372,23 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
                 }
             }
         }
-        if (gate)
+        // sum gr yh of the item: times scale gate it is post_weight's gradient,
+        // times scale post_weight the gate's
 #pragma unroll
-            for (int q = 0; q < VPT; ++q) {
-                const int v = threadIdx.x + q * team;
-                if (v < nv) {
+        for (int q = 0; q < VPT; ++q) {
+            const int v = threadIdx.x + q * team;
+            f32x2 pw[P], gv[P];
+            params(post_weight, v, pw);
+            params(gate ? gate + j * g.dim : nullptr, v, gv);
 #pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        dg[q][i] = mul2(dg[q][i], dup2(g.scale));
-                    store_pairs<float, VEC>(dgate_part + item * g.dim + v * VEC, dg[q]);
-                }
+            for (int i = 0; i < P; ++i) {
+                dg[q][i] = mul2(dg[q][i], dup2(g.scale));
+                dpw[q][i] = fma2(dg[q][i], gv[i], dpw[q][i]);
+                dg[q][i] = mul2(dg[q][i], pw[i]);
             }
+            if (gate && v < nv)
+                store_pairs<float, VEC>(dgate_part + item * g.dim + v * VEC, dg[q]);
+        }
     }
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
@@ -398,6 +396,176 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
         if (v < nv) {
             store_pairs<float, VEC>(part + ((int64_t)blockIdx.x * 2) * g.dim + v * VEC, dw[q]);
             store_pairs<float, VEC>(part + ((int64_t)blockIdx.x * 2 + 1) * g.dim + v * VEC, dpw[q]);
+        }
+    }
+}
+
+// Rows too wide for the register kernels: a block of kWideThreads per row that
+// goes over it in turns, keeping the residual (or its gradient) in shared
+// memory.  A thread always has the same channels, so only the sums need
+// barriers, and the parameters' gradients are added up in the partials
+// themselves.
+constexpr int kWideThreads = 512;
+
+template <int VEC> __device__ __forceinline__ void load_or(const float *p, int c, float other, float (&v)[VEC])
+{
+    if (p)
+        load_vec<float, VEC>(p + c, v);
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] = other;
+}
+
+template <typename TI, typename TR, int VEC>
+__global__ void __launch_bounds__(kWideThreads)
+block_norm_wide_kernel(const TI *__restrict__ y, const TR *residual, const float *__restrict__ weight,
+                       const float *__restrict__ post_weight, const float *__restrict__ gate,
+                       TI *__restrict__ out, TR *residual_out, NormGeom g)
+{
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    float *r = reinterpret_cast<float *>(smem_raw);
+    __shared__ Sum<1> sum_y[kMaxWarps], sum_r[kMaxWarps];
+    const int64_t at = (int64_t)blockIdx.x * g.dim;
+    const int first = threadIdx.x * VEC, step = kWideThreads * VEC, dim = (int)g.dim;
+    float f = g.scale, s[1] = {0.f};
+    if (post_weight) {
+        for (int c = first; c < dim; c += step) {
+            float v[VEC];
+            load_vec<TI, VEC>(y + at + c, v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                s[0] = fmaf(v[i], v[i], s[0]);
+        }
+        team_sum<1>(s, sum_y);
+        f *= rsqrtf(s[0] * g.inv_dim + g.eps);
+    }
+    const float *gr = gate ? gate + blockIdx.x / g.tokens_per_gate * g.dim : nullptr;
+    s[0] = 0.f;
+    for (int c = first; c < dim; c += step) {
+        float v[VEC], rv[VEC] = {}, pw[VEC], gv[VEC];
+        load_vec<TI, VEC>(y + at + c, v);
+        if (residual)
+            load_vec<TR, VEC>(residual + at + c, rv);
+        load_or<VEC>(post_weight, c, 1.f, pw);
+        load_or<VEC>(gr, c, 1.f, gv);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            rv[i] = fmaf(f * pw[i] * gv[i], v[i], rv[i]);
+            s[0] = fmaf(rv[i], rv[i], s[0]);
+        }
+        store_vec<float, VEC>(r + c, rv);
+        store_vec<TR, VEC>(residual_out + at + c, rv);
+    }
+    team_sum<1>(s, sum_r);
+    const float rs = rsqrtf(s[0] * g.inv_dim + g.eps);
+    for (int c = first; c < dim; c += step) {
+        float v[VEC], w[VEC];
+        load_vec<float, VEC>(r + c, v);
+        load_vec<float, VEC>(weight + c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            v[i] *= rs * w[i];
+        store_vec<TI, VEC>(out + at + c, v);
+    }
+}
+
+template <typename TI, typename TR, int VEC>
+__global__ void __launch_bounds__(kWideThreads)
+block_norm_bwd_wide_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const float *__restrict__ weight,
+                           const float *__restrict__ post_weight, const float *__restrict__ gate,
+                           const TI *__restrict__ dout, const TR *dr, TI *__restrict__ dy, TR *dresidual,
+                           float *part, float *dgate_part, NormGeom g, int64_t groups, int64_t spans)
+{
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    float *grad = reinterpret_cast<float *>(smem_raw);
+    __shared__ Sum<3> sum_row[2][kMaxWarps];
+    __shared__ Sum<1> sum_p[kMaxWarps];
+    const int first = threadIdx.x * VEC, step = kWideThreads * VEC, dim = (int)g.dim;
+    float *dw = part + (int64_t)blockIdx.x * 2 * g.dim, *dpw = dw + g.dim;
+    for (int c = first; c < dim; c += step)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            dw[c + i] = dpw[c + i] = 0.f;
+    int flip = 0;
+    const int64_t tokens = g.ntokens / groups;
+    for (int64_t item = blockIdx.x; item < groups * spans; item += gridDim.x) {
+        const int64_t j = item / spans, sp = item - j * spans;
+        const int64_t t0 = j * tokens + tokens * sp / spans, t1 = j * tokens + tokens * (sp + 1) / spans;
+        const float *gj = gate ? gate + j * g.dim : nullptr;
+        float *dg = gate ? dgate_part + item * g.dim : nullptr;
+        if (dg)
+            for (int c = first; c < dim; c += step)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    dg[c + i] = 0.f;
+        for (int64_t row = t0; row < t1; ++row) {
+            const int64_t at = row * g.dim;
+            float s[3] = {0.f, 0.f, 0.f};
+            for (int c = first; c < dim; c += step) {
+                float yv[VEC], rv[VEC], gn[VEC], w[VEC];
+                load_vec<TI, VEC>(y + at + c, yv);
+                load_vec<TR, VEC>(r + at + c, rv);
+                load_vec<TI, VEC>(dout + at + c, gn);
+                load_vec<float, VEC>(weight + c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    s[0] = fmaf(yv[i], yv[i], s[0]);
+                    s[1] = fmaf(rv[i], rv[i], s[1]);
+                    s[2] = fmaf(gn[i] * w[i], rv[i], s[2]);
+                }
+            }
+            team_sum<3>(s, sum_row[flip]);
+            flip ^= 1;
+            const float rs_y = post_weight ? rsqrtf(s[0] * g.inv_dim + g.eps) : 1.f;
+            const float rs_r = rsqrtf(s[1] * g.inv_dim + g.eps);
+            const float k = s[2] * g.inv_dim * rs_r * rs_r;
+            float u[1] = {0.f};
+            for (int c = first; c < dim; c += step) {
+                float yv[VEC], rv[VEC], gn[VEC], w[VEC], gr[VEC] = {}, pw[VEC], gv[VEC], a[VEC], b[VEC], d[VEC] = {};
+                load_vec<TI, VEC>(y + at + c, yv);
+                load_vec<TR, VEC>(r + at + c, rv);
+                load_vec<TI, VEC>(dout + at + c, gn);
+                load_vec<float, VEC>(weight + c, w);
+                if (dr)
+                    load_vec<TR, VEC>(dr + at + c, gr);
+                load_or<VEC>(post_weight, c, 1.f, pw);
+                load_or<VEC>(gj, c, 1.f, gv);
+                load_vec<float, VEC>(dw + c, a);
+                load_vec<float, VEC>(dpw + c, b);
+                if (dg)
+                    load_vec<float, VEC>(dg + c, d);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    a[i] = fmaf(gn[i], rv[i] * rs_r, a[i]);
+                    gr[i] = fmaf(rs_r, fmaf(-rv[i], k, gn[i] * w[i]), gr[i]);
+                    const float yh = yv[i] * rs_y, q = g.scale * gr[i] * yh;
+                    b[i] = fmaf(q, gv[i], b[i]);
+                    d[i] = fmaf(q, pw[i], d[i]);
+                    gn[i] = g.scale * gv[i] * pw[i] * gr[i];  // the gradient of yh
+                    u[0] = fmaf(gn[i], yh, u[0]);
+                }
+                store_vec<TR, VEC>(dresidual + at + c, gr);
+                store_vec<float, VEC>(grad + c, gn);
+                store_vec<float, VEC>(dw + c, a);
+                store_vec<float, VEC>(dpw + c, b);
+                if (dg)
+                    store_vec<float, VEC>(dg + c, d);
+            }
+            float m = 0.f;
+            if (post_weight) {
+                team_sum<1>(u, sum_p);
+                m = u[0] * g.inv_dim;
+            }
+            for (int c = first; c < dim; c += step) {
+                float yv[VEC], gn[VEC];
+                load_vec<float, VEC>(grad + c, gn);
+                load_vec<TI, VEC>(y + at + c, yv);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    gn[i] = post_weight ? rs_y * fmaf(-yv[i] * rs_y, m, gn[i]) : gn[i];
+                store_vec<TI, VEC>(dy + at + c, gn);
+            }
         }
     }
 }
@@ -438,15 +606,40 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(NormSums a)
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Threads of a row's team, and vectors of each, for a row of nv vectors: few
-// vectors a thread while the team stays within `most` threads.
+// vectors a thread while the team stays within `most` threads.  0 vectors:
+// the row needs the wide kernel.
 void team_shape(int64_t nv, int most, int *team, int *vpt)
 {
-    for (int v : {1, 2, 4, 8, 32, 128}) {
+    for (int v : {1, 2, 4}) {
         *vpt = v;
         *team = (int)((nv + v * 32 - 1) / (v * 32)) * 32;
         if (*team <= most)
             return;
     }
+    *vpt = 0;
+}
+
+cudaError_t allow_smem(const void *kernel, size_t bytes)
+{
+    return bytes > 40 * 1024
+               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
+               : cudaSuccess;
+}
+
+template <typename TI, typename TR, int VEC>
+cudaError_t fwd_wide(const void *y, const void *residual, const float *weight, const float *post_weight,
+                     const float *gate, void *out, void *residual_out, const NormGeom &g, int, cudaStream_t st)
+{
+    auto k = block_norm_wide_kernel<TI, TR, VEC>;
+    const size_t smem = (size_t)g.dim * sizeof(float);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    if (e != cudaSuccess)
+        return e;
+    k<<<(unsigned)g.ntokens, kWideThreads, smem, st>>>(
+        static_cast<const TI *>(y), static_cast<const TR *>(residual), weight, post_weight, gate,
+        static_cast<TI *>(out), static_cast<TR *>(residual_out), g);
+    note_launch(1);
+    return cudaGetLastError();
 }
 
 template <typename TI, typename TR, int VEC, int VPT>
@@ -490,11 +683,9 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
     auto k = VEC == 1 && VPT == 1 && g.dim == 1 ? block_norm_bwd_kernel<TI, TR, VEC, VPT, VEC == 1 && VPT == 1>
                                                 : block_norm_bwd_kernel<TI, TR, VEC, VPT, false>;
     const size_t smem = norm_ring<VEC, VPT> ? sizeof(NormSlot<TI, TR, VEC>) * 2 * VPT * team : 0;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    if (e != cudaSuccess)
+        return e;
     k<<<(unsigned)p.blocks, team, smem, st>>>(
         static_cast<const TI *>(y), static_cast<const TR *>(r), weight, post_weight, gate,
         static_cast<const TI *>(dout), static_cast<const TR *>(dr), static_cast<TI *>(dy),
@@ -503,19 +694,34 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
     return cudaGetLastError();
 }
 
-// F<TI, TR, VEC, VPT> for the team's vectors per thread; MAXV: the most (a
-// row of four-channel vectors needs 32, one of single channels 128).
-#define SSD_NORM_VPT(F, TI, TR, VEC, MAXV, ...)                                                     \
-    (vpt == 1    ? F<TI, TR, VEC, 1>(__VA_ARGS__)                                                   \
-     : vpt == 2  ? F<TI, TR, VEC, 2>(__VA_ARGS__)                                                   \
-     : vpt == 4  ? F<TI, TR, VEC, 4>(__VA_ARGS__)                                                   \
-     : vpt == 8  ? F<TI, TR, VEC, 8>(__VA_ARGS__)                                                   \
-     : vpt == 32 ? F<TI, TR, VEC, 32>(__VA_ARGS__)                                                  \
-                 : F<TI, TR, VEC, MAXV>(__VA_ARGS__))
-#define SSD_NORM_TYPES(F, VEC, MAXV, ...)                                                           \
-    (bf16 ? (res_bf16 ? SSD_NORM_VPT(F, __nv_bfloat16, __nv_bfloat16, VEC, MAXV, __VA_ARGS__)       \
-                      : SSD_NORM_VPT(F, __nv_bfloat16, float, VEC, MAXV, __VA_ARGS__))              \
-          : SSD_NORM_VPT(F, float, float, VEC, MAXV, __VA_ARGS__))
+template <typename TI, typename TR, int VEC>
+cudaError_t bwd_wide(const void *y, const void *r, const float *weight, const float *post_weight, const float *gate,
+                     const void *dout, const void *dr, void *dy, void *dresidual, float *part, float *dgate_part,
+                     const NormGeom &g, const BwdPlan &p, int, cudaStream_t st)
+{
+    auto k = block_norm_bwd_wide_kernel<TI, TR, VEC>;
+    const size_t smem = (size_t)g.dim * sizeof(float);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    if (e != cudaSuccess)
+        return e;
+    k<<<(unsigned)p.blocks, kWideThreads, smem, st>>>(
+        static_cast<const TI *>(y), static_cast<const TR *>(r), weight, post_weight, gate,
+        static_cast<const TI *>(dout), static_cast<const TR *>(dr), static_cast<TI *>(dy),
+        static_cast<TR *>(dresidual), part, dgate_part, g, p.groups, p.spans);
+    note_launch(1);
+    return cudaGetLastError();
+}
+
+// F##_v<TI, TR, VEC, VPT> for the team's vectors per thread, or F##_wide.
+#define SSD_NORM_VPT(F, TI, TR, VEC, ...)                                                           \
+    (vpt == 1   ? F##_v<TI, TR, VEC, 1>(__VA_ARGS__)                                                \
+     : vpt == 2 ? F##_v<TI, TR, VEC, 2>(__VA_ARGS__)                                                \
+     : vpt == 4 ? F##_v<TI, TR, VEC, 4>(__VA_ARGS__)                                                \
+                : F##_wide<TI, TR, VEC>(__VA_ARGS__))
+#define SSD_NORM_TYPES(F, VEC, ...)                                                                 \
+    (bf16 ? (res_bf16 ? SSD_NORM_VPT(F, __nv_bfloat16, __nv_bfloat16, VEC, __VA_ARGS__)             \
+                      : SSD_NORM_VPT(F, __nv_bfloat16, float, VEC, __VA_ARGS__))                    \
+          : SSD_NORM_VPT(F, float, float, VEC, __VA_ARGS__))
 
 }  // namespace
 
@@ -530,11 +736,11 @@ cudaError_t launch_block_norm(const void *y, const void *residual, const float *
     if (g.dim % 4 == 0 && aligned(y, a) && aligned(out, a) && aligned(residual, ar) &&
         aligned(residual_out, ar) && aligned(weight, 16) && aligned(post_weight, 16) && aligned(gate, 16)) {
         team_shape(g.dim / 4, kFwdTeam, &team, &vpt);
-        return SSD_NORM_TYPES(fwd_v, 4, 32, y, residual, weight, post_weight, gate, out, residual_out, g, team,
+        return SSD_NORM_TYPES(fwd, 4, y, residual, weight, post_weight, gate, out, residual_out, g, team,
                               st);
     }
     team_shape(g.dim, kFwdTeam, &team, &vpt);
-    return SSD_NORM_TYPES(fwd_v, 1, 128, y, residual, weight, post_weight, gate, out, residual_out, g, team, st);
+    return SSD_NORM_TYPES(fwd, 1, y, residual, weight, post_weight, gate, out, residual_out, g, team, st);
 }
 
 // Partials: two rows per block (weight, post_weight), one per item of the
@@ -566,11 +772,11 @@ cudaError_t launch_block_norm_bwd(const void *y, const void *r, const float *wei
     cudaError_t e;
     if (al) {
         team_shape(g.dim / 4, kBwdTeam, &team, &vpt);
-        e = SSD_NORM_TYPES(bwd_v, 4, 32, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
+        e = SSD_NORM_TYPES(bwd, 4, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
                            g, p, team, st);
     } else {
         team_shape(g.dim, kBwdTeam, &team, &vpt);
-        e = SSD_NORM_TYPES(bwd_v, 1, 128, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
+        e = SSD_NORM_TYPES(bwd, 1, y, r, weight, post_weight, gate, dout, dr, dy, dresidual, part, gpart,
                            g, p, team, st);
     }
     if (e != cudaSuccess)

@@ -47,9 +47,9 @@ template <int LN> struct PassShape {
     // threads of a block: one warp where that gives rows of 16 channels or more
     static constexpr int NT = LN <= 4 ? 32 : 8 * LN;
     static constexpr int CB = 2 * NT / LN;  // channels
-    // blocks an SM holds (2 NT threads each); nine of two warps leave 112
+    // blocks an SM holds (2 NT threads each); nine of two warps leave 96
     // registers a thread, and take the 8.4 blocks an SM of four sequences of
-    // 5120 channels in one wave
+    // 5120 channels in one wave (f32 inputs in flight need more: eight)
     static constexpr int BLOCKS = LN == 1 ? 3 : LN == 2 ? 5 : (LN == 4 ? 9 : 72 / (2 * LN));
 };
 
@@ -71,7 +71,7 @@ template <int LN, int MODE> struct PassTile {
 // k - 1.  One barrier a step.  A walker alone has too few independent
 // instructions to fill its scheduler; the makers fill the gaps.
 template <typename TI, int LN, int MODE>
-__global__ void __launch_bounds__(2 * PassShape<LN>::NT, PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
+__global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN == 4 ? 8 : PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
 {
     constexpr int NT = PassShape<LN>::NT, CB = PassShape<LN>::CB, T = kScanChunk, NP = 4 * LN;
     // a thread's quads of a tile: QPT of one column of channels, TROWS tokens
@@ -745,7 +745,7 @@ ScanSegs scan_segments(const ScanGeom &g)
     const int64_t sms = device_sm_count();
     ScanSegs s{1, nc};
     if (warps < 3 * sms && nc >= 32) {
-        const int64_t n = min64(9 * sms / warps, nc / 8);
+        const int64_t n = min64(9 * sms / warps, nc / 4);
         if (n > 1) {
             s.chunks_per_seg = (nc + n - 1) / n;
             s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;

@@ -35,7 +35,7 @@ template <typename TI> struct GradArgs {
     float *dD;             // [B * chunk groups][2][dim]: dD, dbias
     ScanEnter enter;
     int64_t chunks_per_group;
-    bool vec, vec_bc;
+    bool vec, vec_bc, vec_st;
 };
 
 template <typename TI, int LN> struct GradTile {
@@ -134,8 +134,23 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         copy_async_commit();
     };
 
+    // the thread's four states of channel j at p
+    auto quad = [&](const float *p, int j, f32x2 (&o)[2]) {
+        if (a.vec_st) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p + j * NP);
+            o[0] = v.x;
+            o[1] = v.y;
+        } else {
+            float v[4];
+            load_states(p + j * g.N, nn[j], v);
+            o[0] = pk2(v[0], v[1]);
+            o[1] = pk2(v[2], v[3]);
+        }
+    };
+    const int64_t dn = g.dim * g.N;
+    int64_t kept = (b * nc + cbeg) * dn + st;
     fetch(cbeg, 0);
-    for (int64_t chunk = cbeg; chunk < cend; ++chunk) {
+    for (int64_t chunk = cbeg; chunk < cend; ++chunk, kept += dn) {
         const int w = (int)(chunk - cbeg) & 1;
         const int nt = (int)min64(T, g.seqlen - chunk * T);
         const int64_t tok0 = b * g.seqlen + chunk * T;
@@ -144,22 +159,22 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (nn[j] > 0) {
-                const int64_t at = (b * nc + chunk) * g.dim * g.N + st + j * g.N;
-                float v[4];
-                load_states(a.h0 + at, nn[j], v);
-                h0[j][0] = pk2(v[0], v[1]);
-                h0[j][1] = pk2(v[2], v[3]);
-                load_states(a.g1 + at, nn[j], v);
-                e[j][0] = pk2(v[0], v[1]);
-                e[j][1] = pk2(v[2], v[3]);
-                if (a.enter.state) {  // and what entered the reverse pass's segment, decayed to here
-                    const int64_t seg = b * a.enter.n_seg + (unsigned)chunk / (unsigned)a.enter.chunks_per_seg;
-                    const float q = a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j];
-                    load_states(a.enter.state + seg * g.dim * g.N + st + j * g.N, nn[j], v);
-                    e[j][0] = fma2(ex2_2(mul2(dup2(q), A[j][0])), pk2(v[0], v[1]), e[j][0]);
-                    e[j][1] = fma2(ex2_2(mul2(dup2(q), A[j][1])), pk2(v[2], v[3]), e[j][1]);
-                }
+                quad(a.h0 + kept, j, h0[j]);
+                quad(a.g1 + kept, j, e[j]);
             }
+        if (a.enter.state) {  // and what entered the reverse pass's segment, decayed to here
+            const float *pe = a.enter.state +
+                              (b * a.enter.n_seg + (unsigned)chunk / (unsigned)a.enter.chunks_per_seg) * dn + st;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (nn[j] > 0) {
+                    f32x2 v[2];
+                    quad(pe, j, v);
+                    const f32x2 q = dup2(a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j]);
+                    e[j][0] = fma2(ex2_2(mul2(q, A[j][0])), v[0], e[j][0]);
+                    e[j][1] = fma2(ex2_2(mul2(q, A[j][1])), v[1], e[j][1]);
+                }
+        }
         copy_async_wait<0>();
         __syncthreads();  // raw[w] is complete, and the chunk before is done with everything
         if (chunk + 1 < cend)
@@ -405,37 +420,40 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
     }
 }
 
-// out[i][g][n] = sum over the group's channel blocks k of src[g nblk + k][i][n],
-// for dB (blockIdx.y = 0) and dC.
-template <typename TI>
-__global__ void __launch_bounds__(256) sum_blocks_kernel(const float *__restrict__ src0, const float *__restrict__ src1,
-                                                         TI *__restrict__ out0, TI *__restrict__ out1,
-                                                         int64_t tokens, int64_t G, int64_t N, int64_t nblk)
-{
-    const float *src = blockIdx.y ? src1 : src0;
-    TI *out = blockIdx.y ? out1 : out0;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= tokens * G * N)
-        return;
-    const int64_t n = i % N, r = i / N, grp = r % G, t = r / G;
-    const float *p = src + ((grp * nblk) * tokens + t) * N + n;
-    float s = 0.f;
-    for (int64_t k = 0; k < nblk; ++k)
-        s += p[k * tokens * N];
-    out[i] = from_f32<TI>(s);
-}
-
-// out[i] = sum over p of src[p * stride + i].
-__global__ void __launch_bounds__(256) sum_items_kernel(const float *__restrict__ src, float *__restrict__ out,
-                                                        int64_t n, int64_t items, int64_t stride)
+// Adds the partials in a fixed order.  blockIdx.y: 0 dB, 1 dC (over the
+// group's channel blocks, out[t][g][n] = sum_k src[g nblk + k][t][n]), 2 dA,
+// 3 dD, 4 dbias (over the items; nullptr: not wanted).
+template <typename TI> struct ScanSums {
+    const float *bc[2], *item[3];
+    TI *bc_out[2];
+    float *item_out[3];
+    int64_t tokens, G, N, nblk, dim, items;
+};
+template <typename TI> __global__ void __launch_bounds__(256) scan_sums_kernel(ScanSums<TI> a)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n)
-        return;
+    const int which = blockIdx.y;
     float s = 0.f;
-    for (int64_t p = 0; p < items; ++p)
-        s += src[p * stride + i];
-    out[i] = s;
+    if (which < 2) {
+        if (i >= a.tokens * a.G * a.N)
+            return;
+        const int64_t n = i % a.N, r = i / a.N, grp = a.G == 1 ? 0 : r % a.G, t = a.G == 1 ? r : r / a.G;
+        const int64_t stride = a.tokens * a.N;
+        const float *p = a.bc[which] + grp * a.nblk * stride + t * a.N + n;
+#pragma unroll 8
+        for (int64_t k = 0; k < a.nblk; ++k)
+            s += p[k * stride];
+        a.bc_out[which][i] = from_f32<TI>(s);
+    } else {
+        const int w = which - 2;
+        const int64_t n = w == 0 ? a.dim * a.N : a.dim, stride = w == 0 ? n : 2 * a.dim;
+        if (i >= n || !a.item_out[w])
+            return;
+#pragma unroll 8
+        for (int64_t k = 0; k < a.items; ++k)
+            s += a.item[w][k * stride + i];
+        a.item_out[w][i] = s;
+    }
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -449,10 +467,12 @@ GradPlan grad_plan(const ScanGeom &g)
     const int64_t cb = 2 * kGradThreads / scan_lanes(g.N);
     p.nblk = (g.kpg + cb - 1) / cb;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    // about four waves of two blocks an SM, each over a run of chunks so that
-    // the sums over tokens leave few partials
+    // about twenty waves of two blocks an SM (the last one's idle slots then
+    // cost little; 4096 tokens of 2 x 5120 channels: 4 waves 1.86 ms a training
+    // step, 20 1.81 ms, 40 1.83 ms), each over a run of chunks so that the sums
+    // over tokens leave few partials
     const int64_t cols = p.nblk * g.G * g.batch;
-    int64_t n = (int64_t)device_sm_count() * 8 / cols;
+    int64_t n = (int64_t)device_sm_count() * 40 / cols;
     n = n < 1 ? 1 : (n > nc ? nc : n);
     p.chunks_per_group = (nc + n - 1) / n;
     p.n_groups = (nc + p.chunks_per_group - 1) / p.chunks_per_group;
@@ -527,6 +547,7 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     const size_t al = 4 * sizeof(TI);
     a.vec = (g.kpg % 4 == 0 || g.G == 1) && g.dim % 4 == 0 && g.row_u % 4 == 0 && g.row_dt % 4 == 0 &&
             g.row_dy % 4 == 0 && (!z || g.row_z % 4 == 0);
+    a.vec_st = g.N == 4 * scan_lanes(g.N) && aligned(h0, 16) && aligned(g1, 16) && aligned(enter.state, 16);
     a.vec_bc = g.N % 4 == 0 && g.row_b % 4 == 0 && g.row_c % 4 == 0 && aligned(Bm, al) && aligned(Cm, al);
     for (const void *q : {u, dt, z, dy, static_cast<const void *>(du), static_cast<const void *>(ddt),
                           static_cast<const void *>(dz)})
@@ -541,21 +562,27 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     }
     if (e != cudaSuccess)
         return e;
-    const int64_t tokens = g.batch * g.seqlen, nbc = tokens * g.G * g.N;
-    sum_blocks_kernel<TI><<<dim3((unsigned)((nbc + 255) / 256), 2), 256, 0, st>>>(
-        w.dB, w.dC, static_cast<TI *>(dB), static_cast<TI *>(dC), tokens, g.G, g.N, p.nblk);
-    const int64_t items = g.batch * p.n_groups, dn = g.dim * g.N;
-    sum_items_kernel<<<(unsigned)((dn + 255) / 256), 256, 0, st>>>(w.dA, dA, dn, items, dn);
-    note_launch(2);
-    const unsigned db = (unsigned)((g.dim + 255) / 256);
-    if (dD) {
-        sum_items_kernel<<<db, 256, 0, st>>>(w.dD, dD, g.dim, items, 2 * g.dim);
-        note_launch(1);
-    }
-    if (dbias) {
-        sum_items_kernel<<<db, 256, 0, st>>>(w.dD + g.dim, dbias, g.dim, items, 2 * g.dim);
-        note_launch(1);
-    }
+    ScanSums<TI> sums{};
+    sums.bc[0] = w.dB;
+    sums.bc[1] = w.dC;
+    sums.bc_out[0] = static_cast<TI *>(dB);
+    sums.bc_out[1] = static_cast<TI *>(dC);
+    sums.item[0] = w.dA;
+    sums.item[1] = w.dD;
+    sums.item[2] = w.dD + g.dim;
+    sums.item_out[0] = dA;
+    sums.item_out[1] = dD;
+    sums.item_out[2] = dbias;
+    sums.tokens = g.batch * g.seqlen;
+    sums.G = g.G;
+    sums.N = g.N;
+    sums.nblk = p.nblk;
+    sums.dim = g.dim;
+    sums.items = g.batch * p.n_groups;
+    const int64_t nbc = sums.tokens * g.G * g.N, dn = g.dim * g.N;
+    const int64_t most = nbc > dn ? nbc : dn;
+    scan_sums_kernel<TI><<<dim3((unsigned)((most + 255) / 256), 5), 256, 0, st>>>(sums);
+    note_launch(1);
     return cudaGetLastError();
 }
 

@@ -454,7 +454,8 @@ ssd_status_t ssd_causal_conv_step(const void *x, int64_t row, const float *weigh
  * dstate] f32, nc = ceil(L / ssd_selective_scan_chunk()), the state before
  * each chunk, which the backward starts from.  1 <= dstate <= 64, dim %
  * ngroups == 0, batch <= 65535.  Arithmetic is f32; the decay is exp2 of
- * delta A log2(e) with the hardware's approximation (relative error 2^-22).
+ * delta A log2(e) with the hardware's approximation (relative error 2^-22,
+ * its mean taken out); delta = 0 keeps the state exactly.
  */
 typedef struct {
     int64_t batch, seqlen, dim, dstate, ngroups;

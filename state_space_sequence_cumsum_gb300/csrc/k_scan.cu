@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
         // Each lane stores its part of the output, which the tile's last step
         // adds up.
         constexpr int GROUP = 2;
+        const f32x2 nudge = dup2(kDecayNudge);
         f32x2 d[2][GROUP][2][2], x[2][GROUP][2][2];
         auto prepare = [&](int i0, int w) {
 #pragma unroll
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
                 const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    d[w][i][j][0] = ex2_2(mul2(dl[j], A[j][0]));
-                    d[w][i][j][1] = ex2_2(mul2(dl[j], A[j][1]));
+                    d[w][i][j][0] = ex2_2(fma2(dl[j], A[j][0], nudge));
+                    d[w][i][j][1] = ex2_2(fma2(dl[j], A[j][1], nudge));
                     x[w][i][j][0] = mul2(xv[j], m.x);
                     x[w][i][j][1] = mul2(xv[j], m.y);
                 }
@@ -515,7 +516,7 @@ scan_step_kernel(const TI *__restrict__ u, const TI *__restrict__ dt, const floa
         s[r] = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            h[r][e] = fmaf(ex2(dr * av[e]), h[r][e], xr * bv[r][e]);
+            h[r][e] = fmaf(ex2(fmaf(dr, av[e], kDecayNudge)), h[r][e], xr * bv[r][e]);
             s[r] = fmaf(h[r][e], cv[r][e], s[r]);
         }
         if (nn > 0 && b0 + r < g.batch)

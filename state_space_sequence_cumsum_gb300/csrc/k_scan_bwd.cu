@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         }
         __syncthreads();
 
+        const f32x2 nudge = dup2(kDecayNudge);
         // a walk to each piece's start state
         constexpr int PIECES = T / kPiece;
         f32x2 hs[PIECES][2][2];
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    h[j][0] = fma2(ex2_2(mul2(dl[j], A[j][0])), h[j][0], mul2(xv[j], m.x));
-                    h[j][1] = fma2(ex2_2(mul2(dl[j], A[j][1])), h[j][1], mul2(xv[j], m.y));
+                    h[j][0] = fma2(ex2_2(fma2(dl[j], A[j][0], nudge)), h[j][0], mul2(xv[j], m.x));
+                    h[j][1] = fma2(ex2_2(fma2(dl[j], A[j][1], nudge)), h[j][1], mul2(xv[j], m.y));
                 }
             }
 #pragma unroll
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 float y[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    av[i][j][0] = ex2_2(mul2(dl[j], A[j][0]));
-                    av[i][j][1] = ex2_2(mul2(dl[j], A[j][1]));
+                    av[i][j][0] = ex2_2(fma2(dl[j], A[j][0], nudge));
+                    av[i][j][1] = ex2_2(fma2(dl[j], A[j][1], nudge));
                     ah[i][j][0] = mul2(av[i][j][0], h[j][0]);
                     ah[i][j][1] = mul2(av[i][j][1], h[j][1]);
                     h[j][0] = fma2(xv[j], m[i].x, ah[i][j][0]);

@@ -97,7 +97,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     # the binding finds libssd.so beside itself and PyTorch's libraries as loaded by torch
     tmp = NATIVE + f".tmp{os.getpid()}"
     r = subprocess.run(["g++", "-shared", "-o", tmp, binding_obj, "-L", PKG, "-l:libssd.so", "-L", torch_lib,
-                        "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+                        "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
                         f"-Wl,-rpath,{torch_lib}"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of _native.so failed:\n{r.stdout}{r.stderr}")

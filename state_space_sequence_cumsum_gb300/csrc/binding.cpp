@@ -6,7 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -129,9 +129,11 @@ int64_t row_of(const Tensor &t, const char *name, int inner = 1)
     return row;
 }
 
+// A new tensor beside `like` (allocated directly: a backward returns nine, and
+// the dispatcher would cost as much as the allocation).
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor &like)
 {
-    return at::empty(shape, like.options().dtype(type));
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 // The caller's output, checked, or a new one.

@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(NormSums a)
     const int64_t n = which < 2 ? a.blocks : a.spans, stride = which < 2 ? 2 * a.dim : a.dim;
     float s = 0.f;
     if (c < a.dim)
-#pragma unroll 4
+#pragma unroll 16
         for (int64_t p = threadIdx.y; p < n; p += 32)
             s += src[p * stride + c];
     red[threadIdx.y][threadIdx.x] = s;
@@ -619,20 +619,14 @@ void team_shape(int64_t nv, int most, int *team, int *vpt)
     *vpt = 0;
 }
 
-cudaError_t allow_smem(const void *kernel, size_t bytes)
-{
-    return bytes > 40 * 1024
-               ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-               : cudaSuccess;
-}
-
 template <typename TI, typename TR, int VEC>
 cudaError_t fwd_wide(const void *y, const void *residual, const float *weight, const float *post_weight,
                      const float *gate, void *out, void *residual_out, const NormGeom &g, int, cudaStream_t st)
 {
     auto k = block_norm_wide_kernel<TI, TR, VEC>;
     const size_t smem = (size_t)g.dim * sizeof(float);
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    static SmemGrant granted;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
     if (e != cudaSuccess)
         return e;
     k<<<(unsigned)g.ntokens, kWideThreads, smem, st>>>(
@@ -663,11 +657,18 @@ BwdPlan bwd_plan(const NormGeom &g, bool gate)
 {
     BwdPlan p;
     p.groups = gate ? g.ntokens / g.tokens_per_gate : 1;
-    const int64_t want = (int64_t)device_sm_count() * 4;
+    // twice the blocks an SM holds: short rows' blocks have few warps
+    int team, vpt;
+    team_shape(g.dim % 4 == 0 ? g.dim / 4 : g.dim, kBwdTeam, &team, &vpt);
+    const int per_sm = vpt == 0 || team >= 192 ? 4 : (team <= 48 ? 16 : 768 / team);
+    const int64_t want = (int64_t)device_sm_count() * per_sm;
     const int64_t per = g.ntokens / p.groups;
     p.spans = (want + p.groups - 1) / p.groups;
-    if (p.spans > per)
-        p.spans = per;
+    // one row an item where there are few, up to four where there are many (an
+    // item's partials then cost less than its rows)
+    const int64_t rows = per < 128 ? 1 : (per < 256 ? 2 : 4);
+    if (p.spans > per / rows)
+        p.spans = per / rows;
     p.blocks = p.groups * p.spans;
     if (p.blocks > want)
         p.blocks = want;
@@ -683,7 +684,8 @@ cudaError_t bwd_v(const void *y, const void *r, const float *weight, const float
     auto k = VEC == 1 && VPT == 1 && g.dim == 1 ? block_norm_bwd_kernel<TI, TR, VEC, VPT, VEC == 1 && VPT == 1>
                                                 : block_norm_bwd_kernel<TI, TR, VEC, VPT, false>;
     const size_t smem = norm_ring<VEC, VPT> ? sizeof(NormSlot<TI, TR, VEC>) * 2 * VPT * team : 0;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    static SmemGrant granted;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
     if (e != cudaSuccess)
         return e;
     k<<<(unsigned)p.blocks, team, smem, st>>>(
@@ -701,7 +703,8 @@ cudaError_t bwd_wide(const void *y, const void *r, const float *weight, const fl
 {
     auto k = block_norm_bwd_wide_kernel<TI, TR, VEC>;
     const size_t smem = (size_t)g.dim * sizeof(float);
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem);
+    static SmemGrant granted;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
     if (e != cudaSuccess)
         return e;
     k<<<(unsigned)p.blocks, kWideThreads, smem, st>>>(

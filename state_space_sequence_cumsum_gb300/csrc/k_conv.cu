@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(256) conv_bwd_reduce_kernel(const float *__res
     const int k = blockIdx.y;
     float s = 0.f;
     if (c < dim)
+#pragma unroll 8
         for (int64_t p = threadIdx.y; p < n_parts; p += 8)
             s += part[(p * (W + 1) + k) * dim + c];
     red[threadIdx.y][threadIdx.x] = s;
@@ -506,11 +507,10 @@ cudaError_t fwd_w(const void *x, const float *w, const float *bias, const void *
     const int64_t threads = g.batch * n_runs * (g.dim / VEC);
     constexpr size_t smem = Ring<TI, VEC, 1, kConvThreads>::kBytes;
     auto k = conv_kernel<TI, VEC, W>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    static SmemGrant granted;
+    const cudaError_t allowed = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
+    if (allowed != cudaSuccess)
+        return allowed;
     k<<<(unsigned)((threads + kConvThreads - 1) / kConvThreads), kConvThreads, smem, st>>>(
         static_cast<const TI *>(x), w, bias, static_cast<const TI *>(init), static_cast<TI *>(y),
         static_cast<TI *>(fin), g, run, n_runs);
@@ -537,11 +537,10 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
     const dim3 grid((unsigned)((g.dim / VEC + kBwdCols - 1) / kBwdCols), (unsigned)(pps * g.batch));
     constexpr size_t smem = Ring<TI, VEC, 2, kBwdThreads>::kBytes;
     auto k = conv_bwd_kernel<TI, VEC, W>;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
+    static SmemGrant granted;
+    const cudaError_t allowed = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
+    if (allowed != cudaSuccess)
+        return allowed;
     k<<<grid, dim3(kBwdCols, kBwdRuns), smem, st>>>(
         static_cast<const TI *>(x), w, bias, static_cast<const TI *>(init), static_cast<const TI *>(dy),
         static_cast<const TI *>(dfinal), static_cast<TI *>(dx), static_cast<TI *>(dinit), part, g, run, pps);

@@ -44,12 +44,15 @@ template <typename TI> struct PassArgs {
 // then serves eight states.  With one channel a thread those reads, not the
 // arithmetic, bounded the walk.
 template <int LN> struct PassShape {
-    // threads of a block: one warp where that gives rows of 16 channels or more
+    // walking threads of a block: one warp where that gives rows of 16 channels
+    // or more; and tile-making ones: as many, or more where a walking thread's
+    // few lanes a channel leave them more channels to convert
     static constexpr int NT = LN <= 4 ? 32 : 8 * LN;
+    static constexpr int MT = LN == 1 ? 128 : LN == 2 ? 64 : NT;
     static constexpr int CB = 2 * NT / LN;  // channels
-    // blocks an SM holds (2 NT threads each); nine of two warps leave 96
-    // registers a thread, and take the 8.4 blocks an SM of four sequences of
-    // 5120 channels in one wave (f32 inputs in flight need more: eight)
+    // blocks an SM holds; nine of two warps leave 96 registers a thread, and
+    // take the 8.4 blocks an SM of four sequences of 5120 channels in one wave
+    // (f32 inputs in flight need more registers: eight)
     static constexpr int BLOCKS = LN == 1 ? 3 : LN == 2 ? 5 : (LN == 4 ? 9 : 72 / (2 * LN));
 };
 
@@ -65,20 +68,21 @@ template <int LN, int MODE> struct PassTile {
     } buf[2];
 };
 
-// Half of a block's warps walk tiles (the states live in their registers), the
-// other half make them: per step the walkers go through tile k while the
+// Some of a block's warps walk tiles (the states live in their registers), the
+// others make them: per step the walkers go through tile k while the
 // makers convert tile k + 1, fetch tile k + 2 and finish the output of tile
 // k - 1.  One barrier a step.  A walker alone has too few independent
 // instructions to fill its scheduler; the makers fill the gaps.
 template <typename TI, int LN, int MODE>
-__global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN == 4 ? 8 : PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
+__global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
+                                  sizeof(TI) == 4 && LN == 4 ? 8 : PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
 {
-    constexpr int NT = PassShape<LN>::NT, CB = PassShape<LN>::CB, T = kScanChunk, NP = 4 * LN;
+    constexpr int NT = PassShape<LN>::NT, MT = PassShape<LN>::MT, CB = PassShape<LN>::CB, T = kScanChunk, NP = 4 * LN;
     // a thread's quads of a tile: QPT of one column of channels, TROWS tokens
     // apart, and PER of a matrix, BT tokens apart (in the widest and narrowest
     // shapes half the threads have none)
-    constexpr int COLS = CB / 4, TROWS = NT / COLS, QPT = TROWS < T ? T / TROWS : 1;
-    constexpr int MATS = MODE == kOut ? 2 : 1, BT = NT / LN, PER = BT < T ? T / BT : 1, BQ = MATS * PER;
+    constexpr int COLS = CB / 4, TROWS = MT / COLS, QPT = TROWS < T ? T / TROWS : 1;
+    constexpr int MATS = MODE == kOut ? 2 : 1, BT = MT / LN, PER = BT < T ? T / BT : 1, BQ = MATS * PER;
     constexpr bool REV = MODE == kReverse;
     using Tile = PassTile<LN, MODE>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -86,15 +90,19 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
     // A block's warps go to the SM's schedulers in turn, so with fixed roles all
     // walkers of two-warp blocks would share two of the four: blocks in the
     // upper half of every eight warp slots swap theirs.
-    __shared__ int s_swap;
-    if (threadIdx.x == 0) {
-        unsigned slot;
-        asm("mov.u32 %0, %%warpid;" : "=r"(slot));
-        s_swap = slot >> 2 & 1;
+    bool walker = threadIdx.x < NT;
+    int tid = threadIdx.x < NT ? threadIdx.x : threadIdx.x - NT;
+    if constexpr (NT == 32 && MT == 32) {
+        __shared__ int s_swap;
+        if (threadIdx.x == 0) {
+            unsigned slot;
+            asm("mov.u32 %0, %%warpid;" : "=r"(slot));
+            s_swap = slot >> 2 & 1;
+        }
+        __syncthreads();
+        walker = (threadIdx.x < NT) != (s_swap != 0);
+        tid = threadIdx.x % NT;
     }
-    __syncthreads();
-    const bool walker = (threadIdx.x < NT) != (s_swap != 0);
-    const int tid = threadIdx.x % NT;
     const int64_t nblk = (g.kpg + CB - 1) / CB;
     const int grp = (int)(blockIdx.x / nblk);
     const int64_t c0 = (blockIdx.x - grp * nblk) * CB;  // first channel, within the group
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
     const TI *pz = a.z ? a.z + tok * g.row_z + ch0 + cq : nullptr;
     const TI *pm = a.m + (tok0 + tid / LN) * a.row_m + grp * g.N + n0;
     const TI *pc = MODE == kOut ? a.cm + (tok0 + tid / LN) * g.row_c + grp * g.N + n0 : nullptr;
-    const bool whole = a.vec && nq >= 4, whole_bc = a.vec_bc && N == NP;
+    const bool four = nq >= 4, whole_bc = a.vec_bc && N == NP;
     auto fetch = [&](int nt) {
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
@@ -251,11 +259,16 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
             if (TROWS > T && t >= T)
                 break;
             const TI *qx = px + i * TROWS * a.row_x, *qd = pd + i * TROWS * g.row_dt, *qz = pz + i * TROWS * g.row_z;
-            if (whole && nt == T) {
+            if (four && nt == T && a.vec) {
                 xr[i] = load_ahead_as<Raw4<TI>>(qx);
                 dr[i] = load_ahead_as<Raw4<TI>>(qd);
                 if (pz)
                     zr[i] = load_ahead_as<Raw4<TI>>(qz);
+            } else if (four && nt == T) {  // rows off the quads' boundaries
+                xr[i] = load_four(qx);
+                dr[i] = load_four(qd);
+                if (pz)
+                    zr[i] = load_four(qz);
             } else {
                 const int n = t < nt ? nq : 0;
                 xr[i] = load_raw4(qx, n, a.vec);
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(2 * PassShape<LN>::NT, sizeof(TI) == 4 && LN =
             if (BT > T && tid / LN >= T)
                 break;
             unpack<TI, 4>(br[i], v);
-            store_vec<float, 4>((i < PER ? s.m : s.c) + 4 * (tid + i % PER * NT), v);
+            store_vec<float, 4>((i < PER ? s.m : s.c) + 4 * (tid + i % PER * MT), v);
         }
     };
     TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
@@ -552,12 +565,11 @@ cudaError_t launch_pass_ln(const PassArgs<TI> &a, const ScanGeom &g, int64_t seg
     const dim3 grid((unsigned)(g.G * ((g.kpg + CB - 1) / CB)), (unsigned)segs, (unsigned)g.batch);
     constexpr size_t smem = sizeof(PassTile<LN, MODE>);
     auto k = scan_pass_kernel<TI, LN, MODE>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
-    k<<<grid, 2 * PassShape<LN>::NT, smem, st>>>(a, g);
+    static SmemGrant granted;
+    const cudaError_t allowed = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
+    if (allowed != cudaSuccess)
+        return allowed;
+    k<<<grid, PassShape<LN>::NT + PassShape<LN>::MT, smem, st>>>(a, g);
     note_launch(1);
     return cudaGetLastError();
 }
@@ -761,7 +773,7 @@ ScanSegs scan_reverse_segments(const ScanGeom &g)
     const int64_t per_warp = 2 * 32 / scan_lanes(g.N);
     const int64_t warps = g.G * ((g.kpg + per_warp - 1) / per_warp) * g.batch;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    const int64_t n = min64(9 * (int64_t)device_sm_count() / warps, nc / 8);
+    const int64_t n = min64(9 * (int64_t)device_sm_count() / warps, nc / 4);
     ScanSegs s{1, nc};
     if (n > 1) {
         s.chunks_per_seg = (nc + n - 1) / n;

@@ -42,7 +42,9 @@ template <typename TI, int LN> struct GradTile {
     static constexpr int CB = 2 * kGradThreads / LN, NP = 4 * LN;
     static constexpr int CP = kGradThreads / LN;  // channel pairs
     static constexpr int PLANE = kRound * CB + (LN > 4 ? 4 : 8);
-    static constexpr int RED = CP + 8;            // pitch of one sum's terms
+    // pitch of one sum's terms: a warp's channel pairs and lanes then store to
+    // different banks (two to a bank for 16 lanes)
+    static constexpr int RED = CP + (LN == 2 ? 16 : LN > 4 ? 4 : 8);
     struct Raw {
         TI u[kScanChunk][CB], dt[kScanChunk][CB], z[kScanChunk][CB], dy[kScanChunk][CB];
         TI m[kScanChunk][NP], c[kScanChunk][NP];
@@ -61,6 +63,9 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
     constexpr int NT = kGradThreads, CB = Tile::CB, CP = Tile::CP, T = kScanChunk, NP = 4 * LN;
     // elementwise work: columns of four channels, TROWS tokens apart
     constexpr int COLS = CB / 4, TROWS = NT / COLS;
+    // where a round has fewer quads than the block threads, TPQ share one and
+    // each adds up LN / TPQ lanes' parts
+    constexpr int TPQ = LN > 4 ? LN / 4 : 1, RROWS = NT / TPQ / COLS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Tile &s = *reinterpret_cast<Tile *>(smem_raw);
     const int tid = threadIdx.x;
@@ -74,7 +79,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
     const int64_t cbeg = blockIdx.y * a.chunks_per_group, cend = min64(cbeg + a.chunks_per_group, nc);
     const int N = (int)g.N;
     const int cp = tid / LN, c = 2 * cp, n0 = 4 * (tid % LN);
-    const int col = 4 * (tid % COLS), trow = tid / COLS, nq = nch - col;
+    const int col = 4 * (tid / TPQ % COLS), rrow = tid / TPQ / COLS, nq = nch - col;
+    const int trow = rrow + RROWS * (tid % TPQ);
 
     f32x2 A[2][2] = {}, dA[2][2] = {};
     int nn[2];
@@ -112,6 +118,15 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 copy_async<4 * sizeof(TI)>(&r.dy[t][col], a.dy + tok * g.row_dy + ch0 + col);
                 if (a.z)
                     copy_async<4 * sizeof(TI)>(&r.z[t][col], a.z + tok * g.row_z + ch0 + col);
+            } else if (nq >= 4 && t < nt) {  // rows off the quads' boundaries
+                const Raw4<TI> ur = load_four(a.u + tok * g.row_u + ch0 + col);
+                const Raw4<TI> dr = load_four(a.dt + tok * g.row_dt + ch0 + col);
+                const Raw4<TI> yr = load_four(a.dy + tok * g.row_dy + ch0 + col);
+                if (a.z)
+                    *reinterpret_cast<Raw4<TI> *>(&r.z[t][col]) = load_four(a.z + tok * g.row_z + ch0 + col);
+                *reinterpret_cast<Raw4<TI> *>(&r.u[t][col]) = ur;
+                *reinterpret_cast<Raw4<TI> *>(&r.dt[t][col]) = dr;
+                *reinterpret_cast<Raw4<TI> *>(&r.dy[t][col]) = yr;
             } else {
                 const int n = t < nt ? nq : 0;
                 *reinterpret_cast<Raw4<TI> *>(&r.u[t][col]) = load_raw4(a.u + tok * g.row_u + ch0 + col, n, false);
@@ -322,8 +337,9 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 const float *q = s.red + o * Tile::RED;
                 f32x2 v0 = 0, v1 = 0;
 #pragma unroll
-                for (int i = 0; i < CP / 4; ++i) {  // starts differ to spread the banks
-                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + 4 * ((i + (o >> 2)) % (CP / 4)));
+                for (int i = 0; i < CP / 4; ++i) {  // starts differ where the pitch does not spread the banks
+                    const int k = Tile::RED % 8 ? i : (i + (o >> 2)) % (CP / 4);
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + 4 * k);
                     v0 = add2(v0, x.x);
                     v1 = add2(v1, x.y);
                 }
@@ -334,23 +350,28 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
             }
             if (t0 % kRound == 0) {  // per (token, channel) results of the last kRound tokens
 #pragma unroll
-                for (int t = t0 + trow; t < t0 + kRound; t += TROWS) {
-                    if (t >= nt || nq <= 0)
-                        break;
+                for (int t = t0 + rrow; t < t0 + kRound; t += RROWS) {
                     f32x2 sum[3][2];
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
-                        const float *q = &s.part[k][t % kRound * CB + col];
+                        const float *q = &s.part[k][tid % TPQ * Tile::PLANE + t % kRound * CB + col];
                         ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(q);
 #pragma unroll
-                        for (int j = 1; j < LN; ++j) {
+                        for (int j = TPQ; j < LN; j += TPQ) {
                             const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + j * Tile::PLANE);
                             v.x = add2(v.x, x.x);
                             v.y = add2(v.y, x.y);
                         }
+#pragma unroll
+                        for (int o = 1; o < TPQ; o *= 2) {
+                            v.x = add2(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+                            v.y = add2(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+                        }
                         sum[k][0] = v.x;
                         sum[k][1] = v.y;
                     }
+                    if (t >= nt || nq <= 0 || tid % TPQ)
+                        continue;
                     float uv[4], dv[4], zv[4], yv[4], du[4], ddt[4], dz[4], dyy[4];
                     load_vec<TI, 4>(&r.u[t][col], uv);
                     load_vec<TI, 4>(&r.dt[t][col], dv);
@@ -421,39 +442,71 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
     }
 }
 
-// Adds the partials in a fixed order.  blockIdx.y: 0 dB, 1 dC (over the
-// group's channel blocks, out[t][g][n] = sum_k src[g nblk + k][t][n]), 2 dA,
-// 3 dD, 4 dbias (over the items; nullptr: not wanted).
+// Adds the partials in a fixed order.  The first 2 G bc_blocks blocks add the
+// groups' channel blocks, out[t][grp][n] = sum_k src[grp nblk + k][t][n] (dB of
+// the first group, its dC, dB of the second, ...), four values a thread where
+// V = 4 (dstate a multiple of four); the next a_blocks add dA over the items,
+// then d_blocks each dD and dbias (nullptr: not wanted), 32 values a block.
 template <typename TI> struct ScanSums {
     const float *bc[2], *item[3];
     TI *bc_out[2];
     float *item_out[3];
-    int64_t tokens, G, N, nblk, dim, items;
+    int64_t tokens, N, G, nblk, dim, items;
+    unsigned bc_blocks, a_blocks, d_blocks;
 };
-template <typename TI> __global__ void __launch_bounds__(256) scan_sums_kernel(ScanSums<TI> a)
+template <typename TI, int V> __global__ void __launch_bounds__(256) scan_sums_kernel(ScanSums<TI> a)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int which = blockIdx.y;
-    float s = 0.f;
-    if (which < 2) {
-        if (i >= a.tokens * a.G * a.N)
-            return;
-        const int64_t n = i % a.N, r = i / a.N, grp = a.G == 1 ? 0 : r % a.G, t = a.G == 1 ? r : r / a.G;
+    const unsigned first = 2 * (unsigned)a.G * a.bc_blocks;
+    if (blockIdx.x < first) {
+        const unsigned y = blockIdx.x / a.bc_blocks, x = blockIdx.x - y * a.bc_blocks;
+        const int64_t i = ((int64_t)x * 256 + threadIdx.x) * V;
         const int64_t stride = a.tokens * a.N;
-        const float *p = a.bc[which] + grp * a.nblk * stride + t * a.N + n;
-#pragma unroll 8
-        for (int64_t k = 0; k < a.nblk; ++k)
-            s += p[k * stride];
-        a.bc_out[which][i] = from_f32<TI>(s);
-    } else {
-        const int w = which - 2;
-        const int64_t n = w == 0 ? a.dim * a.N : a.dim, stride = w == 0 ? n : 2 * a.dim;
-        if (i >= n || !a.item_out[w])
+        if (i >= stride)
             return;
+        const int64_t grp = y / 2;
+        const float *p = a.bc[y & 1] + grp * a.nblk * stride + i;
+        float s[V] = {};
 #pragma unroll 8
-        for (int64_t k = 0; k < a.items; ++k)
-            s += a.item[w][k * stride + i];
-        a.item_out[w][i] = s;
+        for (int64_t k = 0; k < a.nblk; ++k) {
+            float v[V];
+            load_vec<float, V>(p + k * stride, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                s[e] += v[e];
+        }
+        const int64_t to = a.G == 1 ? i : i / a.N * (a.G * a.N) + grp * a.N + i % a.N;
+        store_vec<TI, V>(a.bc_out[y & 1] + to, s);
+    } else {  // 32 values a block, eight runs of items each
+        __shared__ float red[8][32];
+        unsigned x = blockIdx.x - first;
+        int which = 0;
+        if (x >= a.a_blocks) {
+            x -= a.a_blocks;
+            which = 1;
+            if (x >= a.d_blocks) {
+                x -= a.d_blocks;
+                which = 2;
+            }
+        }
+        const int64_t n = which == 0 ? a.dim * a.N : a.dim, stride = which == 0 ? n : 2 * a.dim;
+        const int64_t j = (int64_t)x * 32 + threadIdx.x % 32;
+        const int run = threadIdx.x / 32;
+        if (!a.item_out[which])
+            return;
+        float s = 0.f;
+        if (j < n)
+#pragma unroll 8
+            for (int64_t k = run; k < a.items; k += 8)
+                s += a.item[which][k * stride + j];
+        red[run][threadIdx.x % 32] = s;
+        __syncthreads();
+        if (run == 0 && j < n) {
+            s = 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                s += red[q][threadIdx.x];
+            a.item_out[which][j] = s;
+        }
     }
 }
 
@@ -484,8 +537,8 @@ template <typename TI, int LN>
 cudaError_t grad_ln(const GradArgs<TI> &a, const ScanGeom &g, const GradPlan &p, cudaStream_t st)
 {
     auto k = scan_grad_kernel<TI, LN>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(GradTile<TI, LN>));
+    static SmemGrant granted;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), sizeof(GradTile<TI, LN>), &granted);
     if (e != cudaSuccess)
         return e;
     k<<<dim3((unsigned)(g.G * p.nblk), (unsigned)p.n_groups, (unsigned)g.batch), kGradThreads,
@@ -580,9 +633,12 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     sums.nblk = p.nblk;
     sums.dim = g.dim;
     sums.items = g.batch * p.n_groups;
-    const int64_t nbc = sums.tokens * g.G * g.N, dn = g.dim * g.N;
-    const int64_t most = nbc > dn ? nbc : dn;
-    scan_sums_kernel<TI><<<dim3((unsigned)((most + 255) / 256), 5), 256, 0, st>>>(sums);
+    const bool quads = g.N % 4 == 0 && aligned(dB, 4 * sizeof(TI)) && aligned(dC, 4 * sizeof(TI));
+    sums.bc_blocks = (unsigned)((sums.tokens * g.N + (quads ? 1023 : 255)) / (quads ? 1024 : 256));
+    sums.a_blocks = (unsigned)((g.dim * g.N + 31) / 32);
+    sums.d_blocks = (unsigned)((g.dim + 31) / 32);
+    const unsigned grid = (unsigned)(2 * g.G) * sums.bc_blocks + sums.a_blocks + 2 * sums.d_blocks;
+    (quads ? scan_sums_kernel<TI, 4> : scan_sums_kernel<TI, 1>)<<<grid, 256, 0, st>>>(sums);
     note_launch(1);
     return cudaGetLastError();
 }

@@ -27,10 +27,26 @@ template <typename TI> __device__ __forceinline__ Raw4<TI> load_raw4(const TI *p
             e[i] = p[i];
     return r;
 }
+// Four elements at any address.
+template <typename TI> __device__ __forceinline__ Raw4<TI> load_four(const TI *p)
+{
+    Raw4<TI> r;
+    TI *e = reinterpret_cast<TI *>(&r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        e[i] = load_ahead_as<TI>(p + i);
+    return r;
+}
 template <typename TI> __device__ __forceinline__ void store4(TI *p, const float (&v)[4], int n, bool vec)
 {
     if (vec && n >= 4) {
         store_vec<TI, 4>(p, v);
+        return;
+    }
+    if (n >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = from_f32<TI>(v[i]);
         return;
     }
 #pragma unroll

@@ -1,6 +1,7 @@
 // Host-side declarations shared by the library's translation units.
 // Not part of the public ABI (include/ssd.h is).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -152,6 +153,13 @@ cudaError_t launch_fused_pair_tc(const void *x, const void *Bm, const void *Cm, 
 
 // SMs of the current device.
 int device_sm_count();
+// Lets a kernel take `bytes` of dynamic shared memory on the current device;
+// `granted` remembers per device what it was given (one array per kernel).
+constexpr int kSmemDevices = 64;
+struct SmemGrant {
+    std::atomic<int> bytes[kSmemDevices];
+};
+cudaError_t allow_smem(const void *kernel, size_t bytes, SmemGrant *granted);
 
 // Short causal convolution (k_conv.cu): rows are elements between the tokens
 // of x and dy.

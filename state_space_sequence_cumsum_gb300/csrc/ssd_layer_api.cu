@@ -9,13 +9,38 @@ namespace ssd {
 
 int device_sm_count()
 {
+    static std::atomic<int> known[kSmemDevices];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();  // sizes are also asked for where there is no device
         return 152;
     }
+    if (dev < kSmemDevices && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+        return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
+        cudaGetLastError();
+        return 152;
+    }
+    if (dev < kSmemDevices)
+        known[dev].store(n, std::memory_order_relaxed);
     return n;
+}
+
+cudaError_t allow_smem(const void *kernel, size_t bytes, SmemGrant *granted)
+{
+    if (bytes <= 40 * 1024)  // with the kernels' static arrays, within what any kernel may take
+        return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const bool cached = dev < kSmemDevices;
+    if (cached && granted->bytes[dev].load(std::memory_order_relaxed) >= (int)bytes)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && cached)
+        granted->bytes[dev].store((int)bytes, std::memory_order_relaxed);
+    return e;
 }
 
 namespace {
@@ -137,7 +162,7 @@ ssd_status_t scan_geom(const ssd_scan_dims_t &d, const ssd_scan_rows_t &r, bool 
         if (tokens * (double)row > kMostElems)
             return SSD_ERR_UNSUPPORTED;
     // one element per thread, 256 a block, in the sums over channel blocks and in the step
-    if (tokens * (double)bc > 256.0 * 2147483647.0 || (double)d.batch * d.dim * d.dstate * 4 > 256.0 * 2147483647.0)
+    if (2.0 * tokens * (double)bc > 256.0 * 2147483647.0 || (double)d.batch * d.dim * d.dstate * 4 > 256.0 * 2147483647.0)
         return SSD_ERR_UNSUPPORTED;
     g->batch = d.batch;
     g->seqlen = d.seqlen;

@@ -1,4 +1,4 @@
-"""GB300 (sm_103a) Mamba-2 chunked SSD forward.
+"""GB300 (sm_103a) Mamba-2 chunked SSD forward, and the layer operators around it.
 
 The compute lives in ``libssd.so`` (hand-written CUDA behind the C ABI in
 ``include/ssd.h``); this package is its thin binding.  Importing it does not

@@ -9,11 +9,15 @@
 //     dresidual = gr,  dgate[j] = scale sum gr p,  dp = scale gate gr
 //     dy = (gp - yh mean(gp yh)) rs_y,  gp = dp post_weight,  yh = y rs_y
 //     dweight = sum dout rh,  dpost_weight = sum dp yh
-// Both directions are bound by HBM traffic.  A team of threads holds a row in
-// registers from its one read to its one write; the row sums are the only
-// communication (shuffles, and shared memory between a team's warps).
+// Both directions should be bound by HBM traffic.  A team of threads holds a
+// row in registers from its one read to its one write; the row sums are the
+// only communication (shuffles, and shared memory between a team's warps).
 // Statistics and sums are f32; r is kept in f32 for `out` and rounded once to
-// the residual's type where it is stored.
+// the residual's type where it is stored.  On a GB300, 16384 rows of 2560 bf16
+// channels with an f32 residual, a post norm and a gate:
+//     forward   88 us, 5.7 TB/s (85% of the measured copy rate)
+//     backward 176 us, 4.3 TB/s (64%): the shared memory pipe (the rows' way
+//              through it, the weights, the row sums' shuffles) is 70% busy
 #include "ssd_internal.h"
 #include "vec.cuh"
 

@@ -6,10 +6,16 @@
 // Backward, with dpre = dy act'(pre) recomputed from x:
 //     dx[t] = sum_k w[k] dpre[t + (W-1) - k]  (+ the gradient of the carried rows)
 //     dw[k] = sum_t dpre[t] x[t - (W-1) + k],   dbias = sum_t dpre[t]
-// Both directions are bound by HBM traffic (one read of x and dy, one write
-// of y or dx, about 2 W flops an element): a thread keeps a window of W
-// tokens of a few adjacent channels in registers and walks a run of tokens,
-// so each element is read once but for the W - 1 tokens before a run.
+// Both directions should be bound by HBM traffic (one read of x and dy, one
+// write of y or dx): a thread keeps a window of W tokens of four adjacent
+// channels in registers as f32 pairs and walks a run of tokens, so each element
+// is read once but for the W - 1 tokens before a run; its inputs come through
+// a ring of asynchronous copies, as loads ahead of time in registers left too
+// few threads to cover HBM's latency.  On a GB300, 4 x 4096 tokens of 5376
+// bf16 channels, W = 4 (DRAM traffic as computed, nothing read twice):
+//     forward   64 us, 5.5 TB/s (82% of the measured copy rate)
+//     backward 137 us, 3.9 TB/s (57%); about 25 instructions an element and
+//              146 registers (12 warps an SM) hold it back, not the copies
 #include "ssd_internal.h"
 #include "vec.cuh"
 

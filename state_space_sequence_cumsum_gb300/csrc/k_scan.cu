@@ -7,8 +7,14 @@
 // and the reverse recurrence the backward starts from,
 //     g_t[n] = exp(delta_t A[d,n]) (g_{t+1}[n] + dy_t C_t[n]).
 // With no decay shared between states there is no matrix product to form:
-// a token costs one exponential and about six f32 operations per (channel,
-// state), which at 16 states outweigh the HBM traffic (u, dt, z in, out).
+// a token costs one exponential and four f32 operations per (channel, state),
+// which at 16 states outweigh the HBM traffic (u, dt, z in, out).  On a GB300,
+// bf16 with gate, 16 states, 5120 channels:
+//     4 x 4096 tokens  525 us; the exponentials alone (32 a clock an SM) take
+//                      180 us and the HBM traffic 100 us.  Half of the issue
+//                      slots and 71% of the shared memory pipe are busy.
+//     reverse pass of 2 x 4096 tokens, states kept: 209 us
+//     one token of 128 sequences 18.5 us, 4.8 TB/s (71% of the measured rate)
 #include "scan.cuh"
 
 namespace ssd {

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
                             }
                             un2(v, o[e], o[e + 1]);
                         }
-                        store4(py + i * TROWS * g.dim, o, nq, a.vec);
+                        store_some<TI, 4>(py + i * TROWS * g.dim, o, nq, a.vec);
                     }
                 }
                 py += T * g.dim;

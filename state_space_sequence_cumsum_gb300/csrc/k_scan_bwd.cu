@@ -10,21 +10,22 @@
 //     dz = dout (sum_n C h + D u) silu'(z),        dD += dyy u,  dbias += ddt
 // dB and dC are sums over the group's channels.  A thread owns four states of
 // two adjacent channels and walks a chunk in pieces of kPiece tokens, last to
-// first: forward through the piece from its start state (kept in registers by
-// a first walk over the chunk) holding each token's a and a h, then back.  Its
+// first: forward through the piece from its start state (kept in shared memory
+// by a first walk over the chunk) holding each token's a and a h, then back.  Its
 // parts of dB and dC are added over the block's threads in shared memory once
 // a piece and written as one partial per channel block; a last kernel adds
 // those in a fixed order (no atomics, so results do not depend on scheduling).
-// About 21 issue slots per (token, channel, state) and eight warps an SM (all
-// 255 registers) bound it: 2 x 4096 tokens of 5120 channels and 16 states take
-// 1010 us on a GB300, issue slots 38% busy, the shared memory pipe 51%.
+// 2 x 4096 tokens of 5120 channels and 16 states take 821 us on a GB300; the
+// shared memory pipe (75 passes for a warp's 256 entries a token) is 76% busy,
+// issue slots (207) 53%.  With the start states, B, C and the piece's sums in
+// registers (255, two blocks an SM instead of three) it took 1010 us, and with
+// the pieces unrolled, which overran the instruction cache, 950 us.
 #include "scan.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kPiece = 4;      // tokens whose a and a h a thread holds
-constexpr int kRound = 8;      // tokens between two elementwise rounds
 constexpr int kGradThreads = 128;
 
 template <typename TI> struct GradArgs {
@@ -42,10 +43,13 @@ template <typename TI> struct GradArgs {
 template <typename TI, int LN> struct GradTile {
     static constexpr int CB = 2 * kGradThreads / LN, NP = 4 * LN;
     static constexpr int CP = kGradThreads / LN;  // channel pairs
-    static constexpr int PLANE = kRound * CB + (LN > 4 ? 4 : 8);
-    // pitch of one sum's terms: a warp's channel pairs and lanes then store to
-    // different banks (two to a bank for 16 lanes)
-    static constexpr int RED = CP + (LN == 2 ? 16 : LN > 4 ? 4 : 8);
+    static constexpr int PLANE = kPiece * CB + (LN > 4 ? 4 : 8);
+    // One sum's terms are a row of red, CP wide.  Terms are placed by XOR so that
+    // a warp's channel pairs and lanes store to different banks, and eight
+    // threads' quads of rows are read from different ones.
+    static constexpr int PAIRS = 32 / LN, ROWS_SHIFT = LN == 8 ? 1 : LN == 16 ? 2 : 0;
+    static __device__ int term(int cp, int lane) { return cp ^ PAIRS * (lane >> ROWS_SHIFT); }
+    static __device__ int quad(int i, int row) { return 4 * (i ^ ((row >> ROWS_SHIFT) & (CP / 4 - 1) & 7)); }
     struct Raw {
         TI u[kScanChunk][CB], dt[kScanChunk][CB], z[kScanChunk][CB], dy[kScanChunk][CB];
         TI m[kScanChunk][NP], c[kScanChunk][NP];
@@ -53,20 +57,31 @@ template <typename TI, int LN> struct GradTile {
     float2 dx[kScanChunk][CB];          // delta, delta u
     float dyy[kScanChunk][CB];          // dout silu(z)
     float m[kScanChunk * NP], c[kScanChunk * NP];
+    float bias[CB], D[CB];
     float part[3][LN * PLANE];          // each lane's part of sum C h, sum e B, sum q A
-    float red[2 * kPiece * NP * RED];   // each channel pair's part of dB, dC
+    float red[2 * kPiece * NP * CP];    // each channel pair's part of dB, dC
+    ulonglong2 hs[kScanChunk / kPiece - 1][2][kGradThreads];  // states entering the pieces but the first
 };
 
+// Blocks an SM holds: as shared memory allows, up to three, which leave a
+// thread 168 registers.
+template <typename TI, int LN> constexpr int grad_blocks()
+{
+    constexpr int n = 228 * 1024 / (sizeof(GradTile<TI, LN>) + 1024);
+    return n < 3 ? n : 3;
+}
+
 template <typename TI, int LN>
-__global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kernel(GradArgs<TI> a, ScanGeom g)
+__global__ void __launch_bounds__(kGradThreads, grad_blocks<TI, LN>()) scan_grad_kernel(GradArgs<TI> a, ScanGeom g)
 {
     using Tile = GradTile<TI, LN>;
     constexpr int NT = kGradThreads, CB = Tile::CB, CP = Tile::CP, T = kScanChunk, NP = 4 * LN;
     // elementwise work: columns of four channels, TROWS tokens apart
     constexpr int COLS = CB / 4, TROWS = NT / COLS;
-    // where a round has fewer quads than the block threads, TPQ share one and
-    // each adds up LN / TPQ lanes' parts
-    constexpr int TPQ = LN > 4 ? LN / 4 : 1, RROWS = NT / TPQ / COLS;
+    // a piece's results: PW channels of a token; where a piece has fewer of those
+    // than the block threads, TPQ share one and each adds up LN / TPQ lanes' parts
+    constexpr int PW = LN <= 2 ? 4 : 2, PCOLS = CB / PW;
+    constexpr int TPQ = LN > 4 ? LN / 4 : 1, RROWS = NT / TPQ / PCOLS;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Tile &s = *reinterpret_cast<Tile *>(smem_raw);
     const int tid = threadIdx.x;
@@ -80,8 +95,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
     const int64_t cbeg = blockIdx.y * a.chunks_per_group, cend = min64(cbeg + a.chunks_per_group, nc);
     const int N = (int)g.N;
     const int cp = tid / LN, c = 2 * cp, n0 = 4 * (tid % LN);
-    const int col = 4 * (tid / TPQ % COLS), rrow = tid / TPQ / COLS, nq = nch - col;
-    const int trow = rrow + RROWS * (tid % TPQ);
+    const int col = 4 * (tid % COLS), trow = tid / COLS, nq = nch - col;
+    const int pcol = PW * (tid / TPQ % PCOLS), prow = tid / TPQ / PCOLS, np = nch - pcol;
 
     f32x2 A[2][2] = {}, dA[2][2] = {};
     int nn[2];
@@ -96,13 +111,11 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
             A[j][1] = pk2(decay_rate(v[2]), decay_rate(v[3]));
         }
     }
-    float bias[4] = {}, Dv[4] = {}, accD[4] = {}, accb[4] = {};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < nq) {
-            bias[e] = a.bias ? a.bias[ch0 + col + e] : 0.f;
-            Dv[e] = a.D ? a.D[ch0 + col + e] : 0.f;
-        }
+    float accD[PW] = {}, accb[PW] = {};
+    for (int i = tid; i < CB; i += NT) {
+        s.bias[i] = a.bias && i < nch ? a.bias[ch0 + i] : 0.f;
+        s.D[i] = a.D && i < nch ? a.D[ch0 + i] : 0.f;
+    }
 
     // the chunk's inputs into raw[w]; elements past the tokens, channels and
     // states are zero
@@ -110,7 +123,7 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         const int64_t tok0 = b * g.seqlen + chunk * T;
         const int nt = (int)min64(T, g.seqlen - chunk * T);
         typename Tile::Raw &r = s.raw[w];
-#pragma unroll
+#pragma unroll 1
         for (int t = trow; t < T; t += TROWS) {
             const int64_t tok = tok0 + t;
             if (a.vec && nq >= 4 && t < nt) {
@@ -171,7 +184,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         const int nt = (int)min64(T, g.seqlen - chunk * T);
         const int64_t tok0 = b * g.seqlen + chunk * T;
         // the state entering the chunk and the gradient leaving it
-        f32x2 h0[2][2] = {}, e[2][2] = {};
+        f32x2 h0[2][2] = {}, e[2][2] = {}, in[2][2] = {};
+        float after[2] = {};
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (nn[j] > 0) {
@@ -184,11 +198,8 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 if (nn[j] > 0) {
-                    f32x2 v[2];
-                    quad(pe, j, v);
-                    const f32x2 q = dup2(a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j]);
-                    e[j][0] = fma2(ex2_2(mul2(q, A[j][0])), v[0], e[j][0]);
-                    e[j][1] = fma2(ex2_2(mul2(q, A[j][1])), v[1], e[j][1]);
+                    quad(pe, j, in[j]);
+                    after[j] = a.enter.after[(b * nc + chunk) * g.dim + ch0 + c + j];
                 }
         }
         copy_async_wait<0>();
@@ -196,9 +207,10 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         if (chunk + 1 < cend)
             fetch(chunk + 1, w ^ 1);
         const typename Tile::Raw &r = s.raw[w];
-#pragma unroll
+#pragma unroll 1
         for (int t = trow; t < T; t += TROWS) {
-            float uv[4], dv[4], zv[4], yv[4], o[8];
+            float uv[4], dv[4], zv[4], yv[4], bias[4], o[8];
+            load_vec<float, 4>(&s.bias[col], bias);
             load_vec<TI, 4>(&r.u[t][col], uv);
             load_vec<TI, 4>(&r.dt[t][col], dv);
             load_vec<TI, 4>(&r.dy[t][col], yv);
@@ -234,63 +246,84 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
         __syncthreads();
 
         const f32x2 nudge = dup2(kDecayNudge);
+        if (a.enter.state)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x2 q = dup2(after[j]);
+                e[j][0] = fma2(ex2_2(mul2(q, A[j][0])), in[j][0], e[j][0]);
+                e[j][1] = fma2(ex2_2(mul2(q, A[j][1])), in[j][1], e[j][1]);
+            }
         // a walk to each piece's start state
         constexpr int PIECES = T / kPiece;
-        f32x2 hs[PIECES][2][2];
+        {
+            f32x2 h[2][2] = {{h0[0][0], h0[0][1]}, {h0[1][0], h0[1][1]}};
+#pragma unroll 1
+            for (int p = 1; p < PIECES; ++p) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            hs[0][j][0] = h0[j][0], hs[0][j][1] = h0[j][1];
+                for (int i = 0; i < kPiece; ++i) {
+                    const int t = (p - 1) * kPiece + i;
+                    const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+                    const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                    const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
 #pragma unroll
-        for (int p = 1; p < PIECES; ++p) {
-            f32x2 h[2][2] = {{hs[p - 1][0][0], hs[p - 1][0][1]}, {hs[p - 1][1][0], hs[p - 1][1][1]}};
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i) {
-                const int t = (p - 1) * kPiece + i;
-                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
-                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
-                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    h[j][0] = fma2(ex2_2(fma2(dl[j], A[j][0], nudge)), h[j][0], mul2(xv[j], m.x));
-                    h[j][1] = fma2(ex2_2(fma2(dl[j], A[j][1], nudge)), h[j][1], mul2(xv[j], m.y));
+                    for (int j = 0; j < 2; ++j) {
+                        h[j][0] = fma2(ex2_2(fma2(dl[j], A[j][0], nudge)), h[j][0], mul2(xv[j], m.x));
+                        h[j][1] = fma2(ex2_2(fma2(dl[j], A[j][1], nudge)), h[j][1], mul2(xv[j], m.y));
+                    }
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                hs[p][j][0] = h[j][0], hs[p][j][1] = h[j][1];
+                for (int j = 0; j < 2; ++j)
+                    s.hs[p - 1][j][tid] = make_ulonglong2(h[j][0], h[j][1]);
+            }
         }
 
-#pragma unroll
+#pragma unroll 1
         for (int p = PIECES - 1; p >= 0; --p) {
             const int t0 = p * kPiece;
-            f32x2 dB[kPiece][2] = {}, dC[kPiece][2] = {};
             f32x2 av[kPiece][2][2], ah[kPiece][2][2];
-            ulonglong2 m[kPiece], cv[kPiece];
-            f32x2 h[2][2] = {{hs[p][0][0], hs[p][0][1]}, {hs[p][1][0], hs[p][1][1]}};
+            f32x2 h[2][2] = {{h0[0][0], h0[0][1]}, {h0[1][0], h0[1][1]}};
+            if (p > 0)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const ulonglong2 v = s.hs[p - 1][j][tid];
+                    h[j][0] = v.x;
+                    h[j][1] = v.y;
+                }
+            // a token's parts of dB and dC: red[which][token][state % 4][lane][channel pair]
+            auto put = [&](int which, int i, f32x2 v0, f32x2 v1) {
+                float v[4];
+                un2(v0, v[0], v[1]);
+                un2(v1, v[2], v[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s.red[(((which * kPiece + i) * 4 + k) * LN + tid % LN) * CP + Tile::term(cp, tid % LN)] = v[k];
+            };
 #pragma unroll
             for (int i = 0; i < kPiece; ++i) {
                 const int t = t0 + i;
                 const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
                 const float2 dyy = *reinterpret_cast<const float2 *>(&s.dyy[t][c]);
-                m[i] = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
-                cv[i] = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
                 const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
                 const f32x2 yv[2] = {dup2(dyy.x), dup2(dyy.y)};
                 float y[2];
+                f32x2 dC[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     av[i][j][0] = ex2_2(fma2(dl[j], A[j][0], nudge));
                     av[i][j][1] = ex2_2(fma2(dl[j], A[j][1], nudge));
                     ah[i][j][0] = mul2(av[i][j][0], h[j][0]);
                     ah[i][j][1] = mul2(av[i][j][1], h[j][1]);
-                    h[j][0] = fma2(xv[j], m[i].x, ah[i][j][0]);
-                    h[j][1] = fma2(xv[j], m[i].y, ah[i][j][1]);
-                    dC[i][0] = fma2(yv[j], h[j][0], dC[i][0]);
-                    dC[i][1] = fma2(yv[j], h[j][1], dC[i][1]);
-                    y[j] = hsum(fma2(h[j][1], cv[i].y, mul2(h[j][0], cv[i].x)));
+                    h[j][0] = fma2(xv[j], m.x, ah[i][j][0]);
+                    h[j][1] = fma2(xv[j], m.y, ah[i][j][1]);
+                    dC[0] = j ? fma2(yv[j], h[j][0], dC[0]) : mul2(yv[j], h[j][0]);
+                    dC[1] = j ? fma2(yv[j], h[j][1], dC[1]) : mul2(yv[j], h[j][1]);
+                    y[j] = hsum(fma2(h[j][1], cv.y, mul2(h[j][0], cv.x)));
                 }
+                put(1, i, dC[0], dC[1]);
                 if (a.z)
-                    *reinterpret_cast<float2 *>(&s.part[0][(tid % LN) * Tile::PLANE + t % kRound * CB + c]) =
+                    *reinterpret_cast<float2 *>(&s.part[0][(tid % LN) * Tile::PLANE + i * CB + c]) =
                         make_float2(y[0], y[1]);
             }
 #pragma unroll
@@ -300,14 +333,17 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                 const float2 dyy = *reinterpret_cast<const float2 *>(&s.dyy[t][c]);
                 const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
                 const f32x2 yv[2] = {dup2(dyy.x), dup2(dyy.y)};
+                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+                const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(&s.c[t * NP + n0]);
                 float sB[2], sA[2];
+                f32x2 dB[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    e[j][0] = fma2(yv[j], cv[i].x, e[j][0]);
-                    e[j][1] = fma2(yv[j], cv[i].y, e[j][1]);
-                    dB[i][0] = fma2(e[j][0], xv[j], dB[i][0]);
-                    dB[i][1] = fma2(e[j][1], xv[j], dB[i][1]);
-                    sB[j] = hsum(fma2(e[j][1], m[i].y, mul2(e[j][0], m[i].x)));
+                    e[j][0] = fma2(yv[j], cv.x, e[j][0]);
+                    e[j][1] = fma2(yv[j], cv.y, e[j][1]);
+                    dB[0] = j ? fma2(e[j][0], xv[j], dB[0]) : mul2(e[j][0], xv[j]);
+                    dB[1] = j ? fma2(e[j][1], xv[j], dB[1]) : mul2(e[j][1], xv[j]);
+                    sB[j] = hsum(fma2(e[j][1], m.y, mul2(e[j][0], m.x)));
                     const f32x2 q0 = mul2(e[j][0], ah[i][j][0]), q1 = mul2(e[j][1], ah[i][j][1]);
                     dA[j][0] = fma2(q0, dl[j], dA[j][0]);
                     dA[j][1] = fma2(q1, dl[j], dA[j][1]);
@@ -315,32 +351,19 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                     e[j][0] = mul2(e[j][0], av[i][j][0]);
                     e[j][1] = mul2(e[j][1], av[i][j][1]);
                 }
-                const int at = (tid % LN) * Tile::PLANE + t % kRound * CB + c;
+                put(0, i, dB[0], dB[1]);
+                const int at = (tid % LN) * Tile::PLANE + i * CB + c;
                 *reinterpret_cast<float2 *>(&s.part[1][at]) = make_float2(sB[0], sB[1]);
                 *reinterpret_cast<float2 *>(&s.part[2][at]) = make_float2(sA[0], sA[1]);
-            }
-            // dB and dC of the piece: red[which][token][state % 4][lane][channel pair]
-            // (a row's lanes are then eight banks apart)
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i) {
-                float v[8];
-                un2(dB[i][0], v[0], v[1]);
-                un2(dB[i][1], v[2], v[3]);
-                un2(dC[i][0], v[4], v[5]);
-                un2(dC[i][1], v[6], v[7]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    s.red[((((k / 4) * kPiece + i) * 4 + k % 4) * LN + tid % LN) * Tile::RED + cp] = v[k];
             }
             __syncthreads();
             for (int o = tid; o < 2 * kPiece * NP; o += NT) {
                 const int t = t0 + o / NP % kPiece, n = 4 * (o % LN) + o / LN % 4;
-                const float *q = s.red + o * Tile::RED;
+                const float *q = s.red + o * CP;
                 f32x2 v0 = 0, v1 = 0;
 #pragma unroll
-                for (int i = 0; i < CP / 4; ++i) {  // starts differ where the pitch does not spread the banks
-                    const int k = Tile::RED % 8 ? i : (i + (o >> 2)) % (CP / 4);
-                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + 4 * k);
+                for (int i = 0; i < CP / 4; ++i) {
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + Tile::quad(i, o));
                     v0 = add2(v0, x.x);
                     v1 = add2(v1, x.y);
                 }
@@ -349,69 +372,73 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
                     out[((int64_t)blockIdx.x * g.batch * g.seqlen + tok0 + t) * g.N + n] = hsum(add2(v0, v1));
                 }
             }
-            if (t0 % kRound == 0) {  // per (token, channel) results of the last kRound tokens
+            // per (token, channel) results of the piece
 #pragma unroll
-                for (int t = t0 + rrow; t < t0 + kRound; t += RROWS) {
-                    f32x2 sum[3][2];
+            for (int i = prow; i < kPiece; i += RROWS) {
+                const int t = t0 + i;
+                f32x2 sum[3][PW / 2];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const float *q = &s.part[k][tid % TPQ * Tile::PLANE + t % kRound * CB + col];
-                        ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(q);
+                for (int k = 0; k < 3; ++k) {
+                    const float *q = &s.part[k][tid % TPQ * Tile::PLANE + i * CB + pcol];
 #pragma unroll
-                        for (int j = TPQ; j < LN; j += TPQ) {
-                            const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(q + j * Tile::PLANE);
-                            v.x = add2(v.x, x.x);
-                            v.y = add2(v.y, x.y);
-                        }
+                    for (int h = 0; h < PW / 2; ++h)
+                        sum[k][h] = 0;
 #pragma unroll
-                        for (int o = 1; o < TPQ; o *= 2) {
-                            v.x = add2(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
-                            v.y = add2(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
-                        }
-                        sum[k][0] = v.x;
-                        sum[k][1] = v.y;
-                    }
-                    if (t >= nt || nq <= 0 || tid % TPQ)
-                        continue;
-                    float uv[4], dv[4], zv[4], yv[4], du[4], ddt[4], dz[4], dyy[4];
-                    load_vec<TI, 4>(&r.u[t][col], uv);
-                    load_vec<TI, 4>(&r.dt[t][col], dv);
-                    load_vec<float, 4>(&s.dyy[t][col], dyy);
-                    if (a.z) {
-                        load_vec<TI, 4>(&r.z[t][col], zv);
-                        load_vec<TI, 4>(&r.dy[t][col], yv);
-                    }
-                    const float4 x0 = *reinterpret_cast<const float4 *>(&s.dx[t][col]);
-                    const float4 x1 = *reinterpret_cast<const float4 *>(&s.dx[t][col + 2]);
-                    const float delta[4] = {x0.x, x0.z, x1.x, x1.z};
+                    for (int j = 0; j < LN; j += TPQ) {
+                        float v[PW];
+                        load_vec<float, PW>(q + j * Tile::PLANE, v);
 #pragma unroll
-                    for (int k = 0; k < 4; k += 2) {
-                        const f32x2 Dp = pk2(Dv[k], Dv[k + 1]), up = pk2(uv[k], uv[k + 1]);
-                        const f32x2 gp = pk2(dyy[k], dyy[k + 1]);
-                        const f32x2 sB = sum[1][k / 2];
-                        un2(fma2(pk2(delta[k], delta[k + 1]), sB, mul2(Dp, gp)), du[k], du[k + 1]);
-                        f32x2 d = fma2(sum[2][k / 2], dup2(kLn2), mul2(up, sB));
-                        if (g.softplus)
-                            d = mul2(d, sigmoid2(pk2(dv[k] + bias[k], dv[k + 1] + bias[k + 1])));
-                        un2(d, ddt[k], ddt[k + 1]);
-                        if (a.z) {
-                            const f32x2 z = pk2(zv[k], zv[k + 1]);
-                            const f32x2 y = fma2(Dp, up, sum[0][k / 2]);
-                            un2(mul2(mul2(pk2(yv[k], yv[k + 1]), y), silu_grad2(z, sigmoid2(z))), dz[k], dz[k + 1]);
-                        }
+                        for (int h = 0; h < PW / 2; ++h)
+                            sum[k][h] = j ? add2(sum[k][h], pk2(v[2 * h], v[2 * h + 1])) : pk2(v[2 * h], v[2 * h + 1]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nq) {
-                            accD[k] = fmaf(dyy[k], uv[k], accD[k]);
-                            accb[k] += ddt[k];
-                        }
-                    const int64_t at = (tok0 + t) * g.dim + ch0 + col;
-                    store4(a.du + at, du, nq, a.vec);
-                    store4(a.ddt + at, ddt, nq, a.vec);
-                    if (a.z)
-                        store4(a.dz + at, dz, nq, a.vec);
+                    for (int o = 1; o < TPQ; o *= 2)
+#pragma unroll
+                        for (int h = 0; h < PW / 2; ++h)
+                            sum[k][h] = add2(sum[k][h], __shfl_xor_sync(0xffffffffu, sum[k][h], o));
                 }
+                if (t >= nt || np <= 0 || tid % TPQ)
+                    continue;
+                float uv[PW], dv[PW], zv[PW], yv[PW], du[PW], ddt[PW], dz[PW], dyy[PW], bias[PW], Dv[PW], dx[2 * PW];
+                load_vec<TI, PW>(&r.u[t][pcol], uv);
+                load_vec<TI, PW>(&r.dt[t][pcol], dv);
+                load_vec<float, PW>(&s.dyy[t][pcol], dyy);
+                load_vec<float, PW>(&s.bias[pcol], bias);
+                load_vec<float, PW>(&s.D[pcol], Dv);
+                load_vec<float, 4>(&s.dx[t][pcol].x, *reinterpret_cast<float(*)[4]>(dx));
+                if constexpr (PW == 4)
+                    load_vec<float, 4>(&s.dx[t][pcol + 2].x, *reinterpret_cast<float(*)[4]>(dx + 4));
+                if (a.z) {
+                    load_vec<TI, PW>(&r.z[t][pcol], zv);
+                    load_vec<TI, PW>(&r.dy[t][pcol], yv);
+                }
+#pragma unroll
+                for (int k = 0; k < PW; k += 2) {
+                    const f32x2 Dp = pk2(Dv[k], Dv[k + 1]), up = pk2(uv[k], uv[k + 1]);
+                    const f32x2 gp = pk2(dyy[k], dyy[k + 1]);
+                    const f32x2 sB = sum[1][k / 2];
+                    un2(fma2(pk2(dx[2 * k], dx[2 * k + 2]), sB, mul2(Dp, gp)), du[k], du[k + 1]);
+                    f32x2 d = fma2(sum[2][k / 2], dup2(kLn2), mul2(up, sB));
+                    if (g.softplus)
+                        d = mul2(d, sigmoid2(pk2(dv[k] + bias[k], dv[k + 1] + bias[k + 1])));
+                    un2(d, ddt[k], ddt[k + 1]);
+                    if (a.z) {
+                        const f32x2 z = pk2(zv[k], zv[k + 1]);
+                        const f32x2 y = fma2(Dp, up, sum[0][k / 2]);
+                        un2(mul2(mul2(pk2(yv[k], yv[k + 1]), y), silu_grad2(z, sigmoid2(z))), dz[k], dz[k + 1]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < PW; ++k)
+                    if (k < np) {
+                        accD[k] = fmaf(dyy[k], uv[k], accD[k]);
+                        accb[k] += ddt[k];
+                    }
+                const int64_t at = (tok0 + t) * g.dim + ch0 + pcol;
+                store_some<TI, PW>(a.du + at, du, np, a.vec);
+                store_some<TI, PW>(a.ddt + at, ddt, np, a.vec);
+                if (a.z)
+                    store_some<TI, PW>(a.dz + at, dz, np, a.vec);
             }
             __syncthreads();  // red and part may be written again
         }
@@ -426,17 +453,18 @@ __global__ void __launch_bounds__(kGradThreads, LN == 1 ? 1 : 2) scan_grad_kerne
             un2(dA[j][1], v[2], v[3]);
             store_states(a.dA + item * g.dim * g.N + st + j * g.N, nn[j], v);
         }
-    float *red = s.red;  // [TROWS][2][CB]
+    float *red = s.red;  // [RROWS][2][CB]
+    if (tid % TPQ == 0)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        red[(trow * 2) * CB + col + k] = accD[k];
-        red[(trow * 2 + 1) * CB + col + k] = accb[k];
-    }
+        for (int k = 0; k < PW; ++k) {
+            red[(prow * 2) * CB + pcol + k] = accD[k];
+            red[(prow * 2 + 1) * CB + pcol + k] = accb[k];
+        }
     __syncthreads();
     for (int i = tid; i < 2 * CB; i += NT) {
         const int which = i / CB, k = i % CB;
         float v = 0.f;
-        for (int q = 0; q < TROWS; ++q)
+        for (int q = 0; q < RROWS; ++q)
             v += red[(q * 2 + which) * CB + k];
         if (k < nch)
             a.dD[(item * 2 + which) * g.dim + ch0 + k] = v;

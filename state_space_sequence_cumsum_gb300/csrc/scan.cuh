@@ -37,20 +37,21 @@ template <typename TI> __device__ __forceinline__ Raw4<TI> load_four(const TI *p
         e[i] = load_ahead_as<TI>(p + i);
     return r;
 }
-template <typename TI> __device__ __forceinline__ void store4(TI *p, const float (&v)[4], int n, bool vec)
+// The first n of W values.
+template <typename TI, int W> __device__ __forceinline__ void store_some(TI *p, const float (&v)[W], int n, bool vec)
 {
-    if (vec && n >= 4) {
-        store_vec<TI, 4>(p, v);
+    if (vec && n >= W) {
+        store_vec<TI, W>(p, v);
         return;
     }
-    if (n >= 4) {
+    if (n >= W) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < W; ++i)
             p[i] = from_f32<TI>(v[i]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < W; ++i)
         if (i < n)
             p[i] = from_f32<TI>(v[i]);
 }

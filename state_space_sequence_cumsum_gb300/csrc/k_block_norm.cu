@@ -16,8 +16,8 @@
 // the residual's type where it is stored.  On a GB300, 16384 rows of 2560 bf16
 // channels with an f32 residual, a post norm and a gate:
 //     forward   88 us, 5.7 TB/s (85% of the measured copy rate)
-//     backward 176 us, 4.3 TB/s (64%): the shared memory pipe (the rows' way
-//              through it, the weights, the row sums' shuffles) is 70% busy
+//     backward 129 us, 5.9 TB/s (87%); 176 us with the weights read again for
+//              every row, row sums of fifteen shuffles and twice the blocks
 #include "ssd_internal.h"
 #include "vec.cuh"
 
@@ -65,6 +65,42 @@ template <int K> __device__ __forceinline__ void team_sum(float (&v)[K], Sum<K> 
 #pragma unroll
         for (int k = 0; k < K; ++k)
             v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+}
+
+// The same for three values, which share shuffles: at the first two steps a
+// lane passes on the values that other lanes go on with (six shuffles instead
+// of fifteen), and of the warps' sums a quarter warp adds up one value's.
+__device__ __forceinline__ void team_sum3(float (&v)[3], Sum<3> *buf)
+{
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & 16, odd = lane & 8;
+    // lanes 0-15 go on with v[0] and v[1], the others with v[2] and nothing
+    float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    const float from = __shfl_xor_sync(0xffffffffu, v[1], 16);
+    const float b = hi ? 0.f : v[1] + from;
+    // then each quarter with one
+    a = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+    const int warps = blockDim.x >> 5;
+    if (warps > 1) {
+        float *s = reinterpret_cast<float *>(buf + threadIdx.y * warps);
+        if ((lane & 7) == 0)
+            s[(threadIdx.x >> 5) * 4 + lane / 8] = a;
+        __syncthreads();
+        a = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; w += 8)
+            if (w + (lane & 7) < warps)
+                a += s[(w + (lane & 7)) * 4 + lane / 8];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+    }
+    v[0] = __shfl_sync(0xffffffffu, a, 0);
+    v[1] = __shfl_sync(0xffffffffu, a, 8);
+    v[2] = __shfl_sync(0xffffffffu, a, 16);
 }
 
 template <int VEC> __device__ __forceinline__ void scale_by(const float *p, float (&v)[VEC])
@@ -244,6 +280,13 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
         if (p && v < nv)
             to_pairs<float, VEC>(*reinterpret_cast<const typename Pack<float, VEC>::T *>(p + v * VEC), o);
     };
+    // the weights stay in registers where a thread has few
+    constexpr bool kKeepW = VEC * VPT <= 8;
+    f32x2 w[VPT][P];
+    if (kKeepW)
+#pragma unroll
+        for (int q = 0; q < VPT; ++q)
+            params(weight, threadIdx.x + q * team, w[q]);
     auto across = [&](f32x2 v, f32x2 x, float m, float rs) {
         return ONE ? mul2(v, dup2(g.eps * rs * rs)) : fma2(x, dup2(-m), v);
     };
@@ -320,17 +363,17 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
             f32x2 s0 = 0, s1 = 0, s2 = 0;
 #pragma unroll
             for (int q = 0; q < VPT; ++q) {
-                f32x2 w[P];
-                params(weight, threadIdx.x + q * team, w);
+                if (!kKeepW)
+                    params(weight, threadIdx.x + q * team, w[q]);
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     s0 = fma2(yv[q][i], yv[q][i], s0);
                     s1 = fma2(rv[q][i], rv[q][i], s1);
-                    s2 = fma2(mul2(gn[q][i], w[i]), rv[q][i], s2);
+                    s2 = fma2(mul2(gn[q][i], w[q][i]), rv[q][i], s2);
                 }
             }
             float s[3] = {hsum(s0), hsum(s1), hsum(s2)};
-            team_sum<3>(s, sum_row[flip]);
+            team_sum3(s, sum_row[flip]);
             flip ^= 1;
             const float rs_y = post_weight ? rsqrtf(s[0] * g.inv_dim + g.eps) : 1.f;
             const float rs_r = rsqrtf(s[1] * g.inv_dim + g.eps);
@@ -340,12 +383,12 @@ block_norm_bwd_kernel(const TI *__restrict__ y, const TR *__restrict__ r, const 
             for (int q = 0; q < VPT; ++q) {
                 const int v = threadIdx.x + q * team;
                 if (v < nv) {
-                    f32x2 w[P];
-                    params(weight, v, w);  // (read again: registers are short)
+                    if (!kKeepW)
+                        params(weight, v, w[q]);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
                         dw[q][i] = fma2(gn[q][i], mul2(rv[q][i], dup2(rs_r)), dw[q][i]);
-                        gr[q][i] = fma2(across(mul2(gn[q][i], w[i]), rv[q][i], c, rs_r), dup2(rs_r), gr[q][i]);
+                        gr[q][i] = fma2(across(mul2(gn[q][i], w[q][i]), rv[q][i], c, rs_r), dup2(rs_r), gr[q][i]);
                     }
                     store_pairs<TR, VEC>(dresidual + out + v * VEC, gr[q]);
 #pragma unroll
@@ -519,7 +562,7 @@ block_norm_bwd_wide_kernel(const TI *__restrict__ y, const TR *__restrict__ r, c
                     s[2] = fmaf(gn[i] * w[i], rv[i], s[2]);
                 }
             }
-            team_sum<3>(s, sum_row[flip]);
+            team_sum3(s, sum_row[flip]);
             flip ^= 1;
             const float rs_y = post_weight ? rsqrtf(s[0] * g.inv_dim + g.eps) : 1.f;
             const float rs_r = rsqrtf(s[1] * g.inv_dim + g.eps);
@@ -661,10 +704,10 @@ BwdPlan bwd_plan(const NormGeom &g, bool gate)
 {
     BwdPlan p;
     p.groups = gate ? g.ntokens / g.tokens_per_gate : 1;
-    // twice the blocks an SM holds: short rows' blocks have few warps
+    // the blocks an SM holds: one wave, and few partials to add up
     int team, vpt;
     team_shape(g.dim % 4 == 0 ? g.dim / 4 : g.dim, kBwdTeam, &team, &vpt);
-    const int per_sm = vpt == 0 || team >= 192 ? 4 : (team <= 48 ? 16 : 768 / team);
+    const int per_sm = vpt == 0 ? 4 : team <= 48 ? 16 : (team > 256 ? 2 : 768 / team);
     const int64_t want = (int64_t)device_sm_count() * per_sm;
     const int64_t per = g.ntokens / p.groups;
     p.spans = (want + p.groups - 1) / p.groups;

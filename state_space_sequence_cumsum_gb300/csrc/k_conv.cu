@@ -55,6 +55,14 @@ template <typename TI, int VEC> __device__ __forceinline__ RawV<TI, VEC> load_ra
     return *reinterpret_cast<const RawV<TI, VEC> *>(p);
 }
 
+template <typename TI, int VEC> __device__ __forceinline__ RawV<TI, VEC> load_or_zero(const TI *p)
+{
+    RawV<TI, VEC> v{};
+    if (p)
+        v = load_ahead_as<RawV<TI, VEC>>(p);
+    return v;
+}
+
 // A thread's VEC x W weights are one run of floats: two at a time where
 // VEC > 1 (rows then start on 8-byte boundaries).
 template <int VEC, int W>
@@ -287,7 +295,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
 {
     constexpr int P = kPairs<VEC>;
     using V = RawV<TI, VEC>;
-    __shared__ f32x2 red[kBwdRuns][P][kBwdCols];
+    __shared__ f32x2 red[W + 1][kBwdRuns][P][kBwdCols];
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const int64_t c = ((int64_t)blockIdx.x * kBwdCols + threadIdx.x) * VEC;
     const int64_t b = blockIdx.y / parts_per_seq;
@@ -302,28 +310,43 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
             dw[k][i] = 0;
     if (live && e0 < L + W - 1) {
         f32x2 wv[W][P], bv[P], win[W][P], dp[W][P];
-        load_weights<VEC, W>(w, bias, c, wv, bv);
         const TI *xb = x + b * L * g.row + c;
         const TI *dyb = dy + b * L * g.row_dy + c;
         TI *dxb = dx + b * L * g.dim + c;
         auto load_xf = [&](int64_t e) {
             const int64_t t = e - (W - 1);
-            V v{};
-            if (t >= 0 && t < L)
-                v = load_raw<TI, VEC>(xb + t * g.row);
-            else if (t < 0 && e >= 0 && init)
-                v = load_raw<TI, VEC>(init + (b * (W - 1) + e) * g.dim + c);
-            return v;
+            return load_or_zero<TI, VEC>(t >= 0 && t < L                 ? xb + t * g.row
+                                         : t < 0 && e >= 0 && init ? init + (b * (W - 1) + e) * g.dim + c
+                                                                         : nullptr);
         };
+        auto load_dy = [&](int64_t e) { return load_or_zero<TI, VEC>(e >= 0 && e < L ? dyb + e * g.row_dy : nullptr); };
+        // All loads of the start are issued before the first is used: the ring's
+        // (rows inside the sequence, kGroup tokens at a time, from `own` on), the
+        // W - 1 rows of dpre before this thread's own, and what those read.
+        const int64_t e1 = min64(e0 + run, L + W - 1), inner = min64(e1, L);
+        const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0;
+        Ring<TI, VEC, 2, kBwdThreads> ring;
+        ring.p[0] = xb + own * g.row;
+        ring.p[1] = dyb + own * g.row_dy;
+        ring.row[0] = g.row;
+        ring.row[1] = g.row_dy;
+        ring.start(smem_raw, threadIdx.y * kBwdCols + threadIdx.x, inner > own ? (int)(inner - own) / kGroup : 0);
+        V before[2 * (W - 1)], before_dy[W - 1];
+#pragma unroll
+        for (int k = 0; k < 2 * (W - 1); ++k)
+            before[k] = load_xf(e0 - (W - 1) + k);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            before_dy[k] = load_dy(e0 - (W - 1) + k);
+        load_weights<VEC, W>(w, bias, c, wv, bv);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
                 dp[k][i] = 0;
             if (k < W - 1)
-                to_pairs<TI, VEC>(load_xf(e0 - (W - 1) + k), win[k]);
+                to_pairs<TI, VEC>(before[k], win[k]);
         }
-        const int64_t e1 = min64(e0 + run, L + W - 1);
         // dp[0] = dpre[e] from xf[e + W - 1] = x[e] and dy[e]; dp[k] = dpre[e - k]
         auto step_in = [&](const V &xr, const V &yr) {
             to_pairs<TI, VEC>(xr, win[W - 1]);
@@ -360,11 +383,9 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
             }
         };
         // any row: before the sequence, past its end, or not yet this thread's own
-        auto edge = [&](int64_t e) {
-            V xr = load_xf(e + W - 1), yr{};
+        auto edge = [&](int64_t e, const V &xr, const V &yr) {
             const bool in = e >= 0 && e < L;
             if (in) {
-                yr = load_raw<TI, VEC>(dyb + e * g.row_dy);
                 step_in(xr, yr);
             } else {
                 to_pairs<TI, VEC>(xr, win[W - 1]);
@@ -395,18 +416,13 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
             }
             shift<P, W>(win);
         };
-        int64_t e = e0 - (W - 1);
-        for (const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0; e < own; ++e)
-            edge(e);
-        // rows inside the sequence, kGroup tokens at a time through the ring
-        const int64_t inner = min64(e1, L);
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            edge(e0 - (W - 1) + k, before[W - 1 + k], before_dy[k]);
+        int64_t e = e0;
+        for (; e < own; ++e)
+            edge(e, load_xf(e + W - 1), load_dy(e));
         TI *op = dxb + (e - (W - 1)) * g.dim;
-        Ring<TI, VEC, 2, kBwdThreads> ring;
-        ring.p[0] = xb + e * g.row;
-        ring.p[1] = dyb + e * g.row_dy;
-        ring.row[0] = g.row;
-        ring.row[1] = g.row_dy;
-        ring.start(smem_raw, threadIdx.y * kBwdCols + threadIdx.x, inner > e ? (int)(inner - e) / kGroup : 0);
         for (; e + kGroup <= inner; e += kGroup) {
             V raw[2][kGroup];
             ring.take(raw);
@@ -422,27 +438,26 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
             }
         }
         for (; e < e1; ++e)
-            edge(e);
+            edge(e, load_xf(e + W - 1), load_dy(e));
     }
 #pragma unroll
-    for (int k = 0; k <= W; ++k) {
-        __syncthreads();
+    for (int k = 0; k <= W; ++k)
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            red[threadIdx.y][i][threadIdx.x] = dw[k][i];
-        __syncthreads();
-        if (threadIdx.y == 0 && live) {
+            red[k][threadIdx.y][i][threadIdx.x] = dw[k][i];
+    __syncthreads();
+    if (live)
+        for (int k = threadIdx.y; k <= W; k += kBwdRuns) {
             f32x2 s[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                s[i] = red[0][i][threadIdx.x];
+                s[i] = red[k][0][i][threadIdx.x];
 #pragma unroll
                 for (int q = 1; q < kBwdRuns; ++q)
-                    s[i] = add2(s[i], red[q][i][threadIdx.x]);
+                    s[i] = add2(s[i], red[k][q][i][threadIdx.x]);
             }
             store_pairs<float, VEC>(part + ((int64_t)blockIdx.y * (W + 1) + k) * g.dim + c, s);
         }
-    }
 }
 
 // Sums the partials in a fixed order: dweight[c][k], dbias[c].

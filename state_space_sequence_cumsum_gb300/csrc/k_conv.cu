@@ -14,15 +14,15 @@
 // few threads to cover HBM's latency.  On a GB300, 4 x 4096 tokens of 5376
 // bf16 channels, W = 4 (DRAM traffic as computed, nothing read twice):
 //     forward   64 us, 5.5 TB/s (82% of the measured copy rate)
-//     backward 137 us, 3.9 TB/s (57%); about 25 instructions an element and
-//              146 registers (12 warps an SM) hold it back, not the copies
+//     backward 115 us, 4.6 TB/s (68%); 25 instructions an element at 12 warps
+//              an SM hold it back, not the copies
 #include "ssd_internal.h"
 #include "vec.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kConvThreads = 256;
+constexpr int kConvThreads = 256, kConvBlocks = 3;  // blocks an SM holds
 
 // A thread's VEC channels (VEC even, or one) as f32 pairs; with one channel
 // the second of the pair is unused.
@@ -177,7 +177,7 @@ template <int P, int W> __device__ __forceinline__ void shift(f32x2 (&win)[W][P]
 // One thread: VEC channels of `run` consecutive tokens of one sequence, in
 // groups of kGroup tokens through the ring.
 template <typename TI, int VEC, int W>
-__global__ void __launch_bounds__(kConvThreads)
+__global__ void __launch_bounds__(kConvThreads, kConvBlocks)
 conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const TI *__restrict__ init, TI *__restrict__ y, TI *__restrict__ fin, ConvGeom g, int run,
             int64_t n_runs)
@@ -278,16 +278,17 @@ conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const fl
 
 // Backward.  With xf = (initial state | x), L + W - 1 rows, pre[i] reads
 // xf[i .. i + W - 1] and xf[e] receives sum_k w[k] dpre[e - k] (dpre = 0
-// outside [0, L)).  A thread owns rows [e0, e0 + run) of xf: it walks i from
-// e0 - (W - 1), keeping the last W values of xf and of dpre, and sums the
-// weight gradient over its own i.  Four such runs share a block's channels;
-// their weight gradients are added in shared memory and written as one
-// partial per block: part[p][k][c], k = W for the bias.
+// outside [0, L)).  A thread owns rows [e0, e0 + run) of xf (the last one also
+// the rows past L): it walks i from e0 - (W - 1), keeping the last W values of
+// xf and of dpre, and sums the weight gradient over its own i.  Four such runs
+// share a block's channels; their weight gradients are added in shared memory
+// and written as one partial per block: part[p][k][c], k = W for the bias.
 constexpr int kBwdCols = 32, kBwdRuns = 4;
 constexpr int kBwdThreads = kBwdCols * kBwdRuns;
+constexpr int kBwdBlocks = 3;  // an SM holds (four, with 128 registers a thread, are no faster)
 
 template <typename TI, int VEC, int W>
-__global__ void __launch_bounds__(kBwdThreads, 3)
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
 conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
                 const TI *__restrict__ init, const TI *__restrict__ dy, const TI *__restrict__ dfinal,
                 TI *__restrict__ dx, TI *__restrict__ dinit, float *__restrict__ part, ConvGeom g, int run,
@@ -308,7 +309,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
 #pragma unroll
         for (int i = 0; i < P; ++i)
             dw[k][i] = 0;
-    if (live && e0 < L + W - 1) {
+    if (live && (e0 < L || e0 == 0)) {
         f32x2 wv[W][P], bv[P], win[W][P], dp[W][P];
         const TI *xb = x + b * L * g.row + c;
         const TI *dyb = dy + b * L * g.row_dy + c;
@@ -323,7 +324,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
         // All loads of the start are issued before the first is used: the ring's
         // (rows inside the sequence, kGroup tokens at a time, from `own` on), the
         // W - 1 rows of dpre before this thread's own, and what those read.
-        const int64_t e1 = min64(e0 + run, L + W - 1), inner = min64(e1, L);
+        const int64_t e1 = e0 + run < L ? e0 + run : L + W - 1, inner = min64(e1, L);
         const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0;
         Ring<TI, VEC, 2, kBwdThreads> ring;
         ring.p[0] = xb + own * g.row;
@@ -489,31 +490,43 @@ __global__ void __launch_bounds__(256) conv_bwd_reduce_kernel(const float *__res
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Tokens a forward thread walks: long runs re-read fewer tokens, short ones
-// keep the GPU filled when the call is small.
+// Tokens a thread walks: the run of least waves x (run + start), where `start`
+// is what the rows before a run and its first loads cost in tokens.  blocks(run)
+// are the call's blocks, `slots` those that the GPU holds at once.
+template <typename F> int pick_run(int64_t seqlen, int64_t slots, int start, F blocks)
+{
+    int best = 4;
+    int64_t least = INT64_MAX;
+    for (int run = 4; run <= 256; run += 4) {
+        const int64_t waves = (blocks(run) + slots - 1) / slots;
+        if (waves * (run + start) < least) {
+            least = waves * (run + start);
+            best = run;
+        }
+        if (waves == 1 || run >= seqlen)  // longer runs only leave slots idle
+            break;
+    }
+    return best;
+}
 int conv_run(const ConvGeom &g, int vec)
 {
     const int64_t threads = g.batch * (g.dim / vec);
-    const int64_t want = (int64_t)device_sm_count() * 1024;
-    int run = 64;
-    while (run > 4 && threads * ((g.seqlen + run - 1) / run) < want)
-        run /= 2;
-    return run;
+    return pick_run(g.seqlen, (int64_t)device_sm_count() * kConvBlocks, 8, [&](int run) {
+        return (threads * ((g.seqlen + run - 1) / run) + kConvThreads - 1) / kConvThreads;
+    });
 }
 
 int64_t conv_bwd_parts_per_seq(const ConvGeom &g, int run)
 {
-    return (g.seqlen + g.width - 1 + (int64_t)kBwdRuns * run - 1) / ((int64_t)kBwdRuns * run);
+    return ((g.seqlen > 0 ? g.seqlen : 1) + (int64_t)kBwdRuns * run - 1) / ((int64_t)kBwdRuns * run);
 }
 
-// Tokens a backward thread walks, kBwdRuns such runs in a block.
+// kBwdRuns runs in a block.
 int conv_bwd_run(const ConvGeom &g, int vec)
 {
     const int64_t cols = (g.dim / vec + kBwdCols - 1) / kBwdCols;
-    const int64_t want = (int64_t)device_sm_count() * 6;
-    int run = 64;
-    while (run > 4 && cols * g.batch * conv_bwd_parts_per_seq(g, run) < want)
-        run /= 2;
+    int run = pick_run(g.seqlen, (int64_t)device_sm_count() * kBwdBlocks, 12,
+                       [&](int r) { return cols * g.batch * conv_bwd_parts_per_seq(g, r); });
     while (conv_bwd_parts_per_seq(g, run) * g.batch > 65535)  // one grid row each
         run *= 2;
     return run;

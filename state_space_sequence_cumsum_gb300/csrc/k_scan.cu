@@ -10,7 +10,7 @@
 // a token costs one exponential and four f32 operations per (channel, state),
 // which at 16 states outweigh the HBM traffic (u, dt, z in, out).  On a GB300,
 // bf16 with gate, 16 states, 5120 channels:
-//     4 x 4096 tokens  525 us; the exponentials alone (32 a clock an SM) take
+//     4 x 4096 tokens  517 us; the exponentials alone (32 a clock an SM) take
 //                      180 us and the HBM traffic 100 us.  Half of the issue
 //                      slots and 71% of the shared memory pipe are busy.
 //     reverse pass of 2 x 4096 tokens, states kept: 209 us
@@ -165,62 +165,51 @@ __global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
             for (int i = 0; i < 2; ++i)
                 if (nn[i] > 0)
                     a.after[(b * nc + at(k)) * g.dim + ch0 + c + i] = dsum[i];
-        // Tokens past the end have delta = x = 0 and change nothing.  A group's
-        // decays and inputs do not depend on the states: the next group's are
+        // Tokens past the end have delta = x = 0 and change nothing.  A token's
+        // decays and inputs do not depend on the states: the next token's are
         // formed before this one's recurrence, which hides their latencies.
         // Each lane stores its part of the output, which the tile's last step
         // adds up.
-        constexpr int GROUP = 2;
         const f32x2 nudge = dup2(kDecayNudge);
-        f32x2 d[2][GROUP][2][2], x[2][GROUP][2][2];
-        auto prepare = [&](int i0, int w) {
+        f32x2 d[2][2][2], x[2][2][2];
+        auto prepare = [&](int i, int w) {
+            const int t = REV ? T - 1 - i : i;
+            const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
+            const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
 #pragma unroll
-            for (int i = 0; i < GROUP; ++i) {
-                const int t = REV ? T - 1 - i0 - i : i0 + i;
-                const float4 dx = *reinterpret_cast<const float4 *>(&s.dx[t][c]);
-                const ulonglong2 m = *reinterpret_cast<const ulonglong2 *>(&s.m[t * NP + n0]);
-                const f32x2 dl[2] = {dup2(dx.x), dup2(dx.z)}, xv[2] = {dup2(dx.y), dup2(dx.w)};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    d[w][i][j][0] = ex2_2(fma2(dl[j], A[j][0], nudge));
-                    d[w][i][j][1] = ex2_2(fma2(dl[j], A[j][1], nudge));
-                    x[w][i][j][0] = mul2(xv[j], m.x);
-                    x[w][i][j][1] = mul2(xv[j], m.y);
-                }
-                if (MODE != kOut) {
-                    dsum[0] += dx.x;
-                    dsum[1] += dx.z;
-                }
+            for (int j = 0; j < 2; ++j) {
+                d[w][j][0] = ex2_2(fma2(dl[j], A[j][0], nudge));
+                d[w][j][1] = ex2_2(fma2(dl[j], A[j][1], nudge));
+                x[w][j][0] = mul2(xv[j], m.x);
+                x[w][j][1] = mul2(xv[j], m.y);
+            }
+            if (MODE != kOut) {
+                dsum[0] += dx.x;
+                dsum[1] += dx.z;
             }
         };
         prepare(0, 0);
 #pragma unroll
-        for (int i0 = 0; i0 < T; i0 += GROUP) {
-            const int w = i0 / GROUP & 1;
-            ulonglong2 cv[GROUP];
+        for (int i = 0; i < T; ++i) {
+            const int w = i & 1;
+            ulonglong2 cv;
             if (MODE == kOut)
+                cv = *reinterpret_cast<const ulonglong2 *>(&s.c[i * NP + n0]);
+            if (i + 1 < T)
+                prepare(i + 1, w ^ 1);
+            float part[2];
 #pragma unroll
-                for (int i = 0; i < GROUP; ++i)
-                    cv[i] = *reinterpret_cast<const ulonglong2 *>(&s.c[(i0 + i) * NP + n0]);
-            if (i0 + GROUP < T)
-                prepare(i0 + GROUP, w ^ 1);
-            float part[GROUP][2];
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-            for (int i = 0; i < GROUP; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        h[j][e] = REV ? mul2(d[w][i][j][e], add2(x[w][i][j][e], h[j][e]))
-                                      : fma2(d[w][i][j][e], h[j][e], x[w][i][j][e]);
-                    if (MODE == kOut)
-                        part[i][j] = hsum(fma2(h[j][1], cv[i].y, mul2(h[j][0], cv[i].x)));
-                }
+                for (int e = 0; e < 2; ++e)
+                    h[j][e] = REV ? mul2(d[w][j][e], add2(x[w][j][e], h[j][e]))
+                                  : fma2(d[w][j][e], h[j][e], x[w][j][e]);
+                if (MODE == kOut)
+                    part[j] = hsum(fma2(h[j][1], cv.y, mul2(h[j][0], cv.x)));
+            }
             if (MODE == kOut)
-#pragma unroll
-                for (int i = 0; i < GROUP; ++i)
-                    *reinterpret_cast<float2 *>(&s.y[(tid % LN) * Tile::YP + (i0 + i) * CB + c]) =
-                        make_float2(part[i][0], part[i][1]);
+                *reinterpret_cast<float2 *>(&s.y[(tid % LN) * Tile::YP + i * CB + c]) = make_float2(part[0], part[1]);
         }
         __syncthreads();
     }

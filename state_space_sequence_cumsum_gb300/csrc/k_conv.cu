@@ -91,8 +91,8 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ w, const 
 // A thread's own ring of groups in shared memory: the copies of the groups
 // ahead are in flight without holding registers, and as a thread reads only
 // what it copied itself, no barrier is needed.  (Two-byte elements, one
-// channel a thread, are too small to copy and are loaded when their group is
-// due.)
+// channel a thread, are too small to copy: they are loaded into registers a
+// group ahead.)
 constexpr int kGroup = 4;   // tokens of a group
 constexpr int kStages = 4;  // groups in flight
 template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
@@ -103,6 +103,7 @@ template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
     int ahead = 0, left;    // groups copied and not yet taken; groups still to copy
     int slot_in = 0, slot_out = 0;
     RawV<TI, VEC> *buf;     // [stage][tensor][token][thread]
+    RawV<TI, VEC> next[TENSORS][kAsync ? 1 : kGroup];
 
     __device__ __forceinline__ RawV<TI, VEC> *at(int slot, int k, int j)
     {
@@ -131,6 +132,21 @@ template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
         if constexpr (kAsync)
             for (int i = 0; i < kStages - 1; ++i)
                 push();
+        else
+            load_next();
+    }
+    __device__ __forceinline__ void load_next()
+    {
+        if (left > 0) {
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k) {
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    next[k][j] = load_ahead_as<RawV<TI, VEC>>(p[k] + j * row[k]);
+                p[k] += kGroup * row[k];
+            }
+            --left;
+        }
     }
     __device__ __forceinline__ void take(RawV<TI, VEC> (&v)[TENSORS][kGroup])
     {
@@ -145,12 +161,11 @@ template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
             slot_out = slot_out + 1 == kStages ? 0 : slot_out + 1;
         } else {
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k) {
+            for (int k = 0; k < TENSORS; ++k)
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j)
-                    v[k][j] = p[k][j * row[k]];
-                p[k] += kGroup * row[k];
-            }
+                    v[k][j] = next[k][j];
+            load_next();
         }
     }
 };

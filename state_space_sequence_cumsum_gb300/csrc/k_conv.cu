@@ -37,7 +37,10 @@ template <typename TI, int VEC> __device__ __forceinline__ void to_pairs(const R
     for (int i = 0; i < kPairs<VEC>; ++i)
         p[i] = pk2(v[2 * i], 2 * i + 1 < VEC ? v[(2 * i + 1) % VEC] : 0.f);
 }
-template <typename TI, int VEC> __device__ __forceinline__ void store_pairs(TI *p, const f32x2 (&o)[kPairs<VEC>])
+// A thread's VEC channels are S apart: adjacent (S = 1, one access), or a warp
+// apart (S = 32, rows off vector boundaries; accesses of single elements, which
+// a warp's threads make side by side).
+template <typename TI, int VEC, int S = 1> __device__ __forceinline__ void store_pairs(TI *p, const f32x2 (&o)[kPairs<VEC>])
 {
     float v[VEC];
 #pragma unroll
@@ -48,33 +51,65 @@ template <typename TI, int VEC> __device__ __forceinline__ void store_pairs(TI *
         if (2 * i + 1 < VEC)
             v[(2 * i + 1) % VEC] = y;
     }
-    store_vec<TI, VEC>(p, v);
+    if constexpr (S == 1) {
+        store_vec<TI, VEC>(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            p[e * S] = from_f32<TI>(v[e]);
+    }
 }
-template <typename TI, int VEC> __device__ __forceinline__ RawV<TI, VEC> load_raw(const TI *p)
+template <typename TI, int VEC, int S = 1> __device__ __forceinline__ RawV<TI, VEC> load_raw(const TI *p)
 {
-    return *reinterpret_cast<const RawV<TI, VEC> *>(p);
+    RawV<TI, VEC> r;
+    if constexpr (S == 1)
+        r = *reinterpret_cast<const RawV<TI, VEC> *>(p);
+    else
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            reinterpret_cast<TI *>(&r)[e] = p[e * S];
+    return r;
 }
 
-template <typename TI, int VEC> __device__ __forceinline__ RawV<TI, VEC> load_or_zero(const TI *p)
+template <typename TI, int VEC, int S> __device__ __forceinline__ RawV<TI, VEC> load_or_zero(const TI *p)
 {
     RawV<TI, VEC> v{};
-    if (p)
-        v = load_ahead_as<RawV<TI, VEC>>(p);
+    if (p) {
+        if constexpr (S == 1)
+            v = load_ahead_as<RawV<TI, VEC>>(p);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                reinterpret_cast<TI *>(&v)[e] = load_ahead_as<TI>(p + e * S);
+    }
     return v;
 }
 
-// A thread's VEC x W weights are one run of floats: two at a time where
-// VEC > 1 (rows then start on 8-byte boundaries).
-template <int VEC, int W>
+// Threads that hold a row's channels, and the first channel of thread v.  Where
+// channels are a warp apart, the last warp's begin early enough to end with the
+// row (dim >= VEC S): the channels it shares with its neighbour are computed
+// twice, to the same values.
+template <int VEC, int S> __host__ __device__ __forceinline__ int64_t conv_columns(int64_t dim)
+{
+    return S == 1 ? dim / VEC : (dim + VEC * S - 1) / (VEC * S) * S;
+}
+template <int VEC, int S> __device__ __forceinline__ int64_t first_channel(int64_t v, int64_t dim)
+{
+    return S == 1 ? v * VEC : min64(v / S * (VEC * S), dim - VEC * S) + v % S;
+}
+
+// A channel's W weights are one run of floats, adjacent channels' too: two at a
+// time where VEC channels start on 8-byte boundaries.
+template <int VEC, int S, int W>
 __device__ __forceinline__ void load_weights(const float *__restrict__ w, const float *__restrict__ bias,
                                              int64_t c, f32x2 (&wv)[W][kPairs<VEC>], f32x2 (&bv)[kPairs<VEC>])
 {
-    constexpr int NL = VEC > 1 ? 2 : 1;
+    constexpr int NL = VEC > 1 && S == 1 ? 2 : 1;
     float t[kPairs<VEC> * 2 * W] = {};
 #pragma unroll
     for (int q = 0; q < VEC * W; q += NL) {
         float v[NL];
-        load_vec<float, NL>(w + c * W + q, v);
+        load_vec<float, NL>(w + (c + q / W * (S - 1)) * W + q, v);
 #pragma unroll
         for (int e = 0; e < NL; ++e)
             t[q + e] = v[e];
@@ -84,7 +119,7 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ w, const 
 #pragma unroll
         for (int k = 0; k < W; ++k)
             wv[k][i] = pk2(t[2 * i * W + k], t[(2 * i + 1) * W + k]);
-        bv[i] = bias ? pk2(bias[c + 2 * i], 2 * i + 1 < VEC ? bias[c + 2 * i + 1] : 0.f) : 0;
+        bv[i] = bias ? pk2(bias[c + 2 * i * S], 2 * i + 1 < VEC ? bias[c + (2 * i + 1) * S] : 0.f) : 0;
     }
 }
 
@@ -95,15 +130,15 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ w, const 
 // group ahead.)
 constexpr int kGroup = 4;   // tokens of a group
 constexpr int kStages = 4;  // groups in flight
-template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
-    static constexpr bool kAsync = sizeof(RawV<TI, VEC>) >= 4;
+template <typename TI, int VEC, int S, int TENSORS, int NT> struct Ring {
+    static constexpr bool kAsync = S == 1 && sizeof(RawV<TI, VEC>) >= 4;
     static constexpr size_t kBytes = kAsync ? sizeof(RawV<TI, VEC>) * kGroup * kStages * TENSORS * NT : 0;
     const TI *p[TENSORS];   // the next group to copy
     int64_t row[TENSORS];
     int ahead = 0, left;    // groups copied and not yet taken; groups still to copy
     int slot_in = 0, slot_out = 0;
     RawV<TI, VEC> *buf;     // [stage][tensor][token][thread]
-    RawV<TI, VEC> next[TENSORS][kAsync ? 1 : kGroup];
+    TI next[TENSORS][kAsync ? 1 : kGroup][VEC];
 
     __device__ __forceinline__ RawV<TI, VEC> *at(int slot, int k, int j)
     {
@@ -142,7 +177,9 @@ template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
             for (int k = 0; k < TENSORS; ++k) {
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j)
-                    next[k][j] = load_ahead_as<RawV<TI, VEC>>(p[k] + j * row[k]);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        next[k][j][e] = load_ahead_as<TI>(p[k] + j * row[k] + e * S);
                 p[k] += kGroup * row[k];
             }
             --left;
@@ -164,7 +201,9 @@ template <typename TI, int VEC, int TENSORS, int NT> struct Ring {
             for (int k = 0; k < TENSORS; ++k)
 #pragma unroll
                 for (int j = 0; j < kGroup; ++j)
-                    v[k][j] = next[k][j];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        reinterpret_cast<TI *>(&v[k][j])[e] = next[k][j][e];
             load_next();
         }
     }
@@ -191,22 +230,22 @@ template <int P, int W> __device__ __forceinline__ void shift(f32x2 (&win)[W][P]
 
 // One thread: VEC channels of `run` consecutive tokens of one sequence, in
 // groups of kGroup tokens through the ring.
-template <typename TI, int VEC, int W>
+template <typename TI, int VEC, int S, int W>
 __global__ void __launch_bounds__(kConvThreads, kConvBlocks)
 conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
             const TI *__restrict__ init, TI *__restrict__ y, TI *__restrict__ fin, ConvGeom g, int run,
             int64_t n_runs)
 {
     constexpr int P = kPairs<VEC>;
-    const int64_t nv = g.dim / VEC;
+    const int64_t nv = conv_columns<VEC, S>(g.dim);
     const int64_t idx = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
     const int64_t r = idx / nv;
     if (r >= g.batch * n_runs)
         return;
-    const int64_t c = (idx - r * nv) * VEC;
+    const int64_t c = first_channel<VEC, S>(idx - r * nv, g.dim);
     const int64_t b = r / n_runs, t0 = (r - b * n_runs) * run;
     f32x2 wv[W][P], bv[P], win[W][P];
-    load_weights<VEC, W>(w, bias, c, wv, bv);
+    load_weights<VEC, S, W>(w, bias, c, wv, bv);
     const TI *xp = x + (b * g.seqlen + t0) * g.row + c;
     TI *yp = y + (b * g.seqlen + t0) * g.dim + c;
     // the W - 1 tokens before the run
@@ -215,9 +254,9 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
         const int64_t t = t0 - (W - 1) + k;
         RawV<TI, VEC> v{};
         if (t >= 0)
-            v = load_raw<TI, VEC>(xp + (k - (W - 1)) * g.row);
+            v = load_raw<TI, VEC, S>(xp + (k - (W - 1)) * g.row);
         else if (init)
-            v = load_raw<TI, VEC>(init + (b * (W - 1) + (W - 1) + t) * g.dim + c);
+            v = load_raw<TI, VEC, S>(init + (b * (W - 1) + (W - 1) + t) * g.dim + c);
         to_pairs<TI, VEC>(v, win[k]);
     }
     const int n = (int)min64(run, g.seqlen - t0);
@@ -231,11 +270,11 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
                 o[i] = mul2(o[i], sigmoid2(o[i]));
         }
         shift<P, W>(win);
-        store_pairs<TI, VEC>(yp, o);
+        store_pairs<TI, VEC, S>(yp, o);
         yp += g.dim;
     };
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    Ring<TI, VEC, 1, kConvThreads> ring;
+    Ring<TI, VEC, S, 1, kConvThreads> ring;
     ring.p[0] = xp;
     ring.row[0] = g.row;
     ring.start(smem_raw, threadIdx.x, n / kGroup);
@@ -249,13 +288,13 @@ conv_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *
     }
     xp += t * g.row;
     for (; t < n; ++t) {
-        token(load_raw<TI, VEC>(xp));
+        token(load_raw<TI, VEC, S>(xp));
         xp += g.row;
     }
     if (fin && t0 + n == g.seqlen)
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
-            store_pairs<TI, VEC>(fin + (b * (W - 1) + k) * g.dim + c, win[k]);
+            store_pairs<TI, VEC, S>(fin + (b * (W - 1) + k) * g.dim + c, win[k]);
 }
 
 // One token of every sequence (blockIdx.y); state and state_out may be one buffer.
@@ -275,7 +314,7 @@ conv_step_kernel(const TI *__restrict__ x, const float *__restrict__ w, const fl
     for (int k = 0; k < W - 1; ++k)
         raw[k] = load_raw<TI, VEC>(state + (b * (W - 1) + k) * g.dim + c);
     raw[W - 1] = load_raw<TI, VEC>(x + b * g.row + c);
-    load_weights<VEC, W>(w, bias, c, wv, bv);
+    load_weights<VEC, 1, W>(w, bias, c, wv, bv);
 #pragma unroll
     for (int k = 0; k < W; ++k)
         to_pairs<TI, VEC>(raw[k], win[k]);
@@ -302,7 +341,7 @@ constexpr int kBwdCols = 32, kBwdRuns = 4;
 constexpr int kBwdThreads = kBwdCols * kBwdRuns;
 constexpr int kBwdBlocks = 3;  // an SM holds (four, with 128 registers a thread, are no faster)
 
-template <typename TI, int VEC, int W>
+template <typename TI, int VEC, int S, int W>
 __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks)
 conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const float *__restrict__ bias,
                 const TI *__restrict__ init, const TI *__restrict__ dy, const TI *__restrict__ dfinal,
@@ -313,11 +352,13 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
     using V = RawV<TI, VEC>;
     __shared__ f32x2 red[W + 1][kBwdRuns][P][kBwdCols];
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    const int64_t c = ((int64_t)blockIdx.x * kBwdCols + threadIdx.x) * VEC;
+    static_assert(S == 1 || S == kBwdCols, "a block's channels");
+    const int64_t v = (int64_t)blockIdx.x * kBwdCols + threadIdx.x;
+    const int64_t c = first_channel<VEC, S>(v, g.dim);
     const int64_t b = blockIdx.y / parts_per_seq;
     const int64_t e0 = ((blockIdx.y - b * parts_per_seq) * kBwdRuns + threadIdx.y) * run;
     const int64_t L = g.seqlen;
-    const bool live = c < g.dim;
+    const bool live = v < conv_columns<VEC, S>(g.dim);
     f32x2 dw[W + 1][P];
 #pragma unroll
     for (int k = 0; k <= W; ++k)
@@ -331,17 +372,17 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
         TI *dxb = dx + b * L * g.dim + c;
         auto load_xf = [&](int64_t e) {
             const int64_t t = e - (W - 1);
-            return load_or_zero<TI, VEC>(t >= 0 && t < L                 ? xb + t * g.row
+            return load_or_zero<TI, VEC, S>(t >= 0 && t < L                 ? xb + t * g.row
                                          : t < 0 && e >= 0 && init ? init + (b * (W - 1) + e) * g.dim + c
                                                                          : nullptr);
         };
-        auto load_dy = [&](int64_t e) { return load_or_zero<TI, VEC>(e >= 0 && e < L ? dyb + e * g.row_dy : nullptr); };
+        auto load_dy = [&](int64_t e) { return load_or_zero<TI, VEC, S>(e >= 0 && e < L ? dyb + e * g.row_dy : nullptr); };
         // All loads of the start are issued before the first is used: the ring's
         // (rows inside the sequence, kGroup tokens at a time, from `own` on), the
         // W - 1 rows of dpre before this thread's own, and what those read.
         const int64_t e1 = e0 + run < L ? e0 + run : L + W - 1, inner = min64(e1, L);
         const int64_t own = e0 < W - 1 ? min64(W - 1, e1) : e0;
-        Ring<TI, VEC, 2, kBwdThreads> ring;
+        Ring<TI, VEC, S, 2, kBwdThreads> ring;
         ring.p[0] = xb + own * g.row;
         ring.p[1] = dyb + own * g.row_dy;
         ring.row[0] = g.row;
@@ -354,7 +395,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
             before_dy[k] = load_dy(e0 - (W - 1) + k);
-        load_weights<VEC, W>(w, bias, c, wv, bv);
+        load_weights<VEC, S, W>(w, bias, c, wv, bv);
 #pragma unroll
         for (int k = 0; k < W; ++k) {
 #pragma unroll
@@ -420,15 +461,15 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 grad(o);
                 if (dfinal && e >= L) {  // the carried rows are the last W - 1 of xf
                     f32x2 f[P];
-                    to_pairs<TI, VEC>(load_raw<TI, VEC>(dfinal + (b * (W - 1) + e - L) * g.dim + c), f);
+                    to_pairs<TI, VEC>(load_raw<TI, VEC, S>(dfinal + (b * (W - 1) + e - L) * g.dim + c), f);
 #pragma unroll
                     for (int i = 0; i < P; ++i)
                         o[i] = add2(o[i], f[i]);
                 }
                 if (e >= W - 1)
-                    store_pairs<TI, VEC>(dxb + (e - (W - 1)) * g.dim, o);
+                    store_pairs<TI, VEC, S>(dxb + (e - (W - 1)) * g.dim, o);
                 else if (dinit)
-                    store_pairs<TI, VEC>(dinit + (b * (W - 1) + e) * g.dim + c, o);
+                    store_pairs<TI, VEC, S>(dinit + (b * (W - 1) + e) * g.dim + c, o);
             }
             shift<P, W>(win);
         };
@@ -448,7 +489,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 sums();
                 f32x2 o[P];
                 grad(o);
-                store_pairs<TI, VEC>(op, o);
+                store_pairs<TI, VEC, S>(op, o);
                 op += g.dim;
                 shift<P, W>(win);
             }
@@ -472,7 +513,7 @@ conv_bwd_kernel(const TI *__restrict__ x, const float *__restrict__ w, const flo
                 for (int q = 1; q < kBwdRuns; ++q)
                     s[i] = add2(s[i], red[k][q][i][threadIdx.x]);
             }
-            store_pairs<float, VEC>(part + ((int64_t)blockIdx.y * (W + 1) + k) * g.dim + c, s);
+            store_pairs<float, VEC, S>(part + ((int64_t)blockIdx.y * (W + 1) + k) * g.dim + c, s);
         }
 }
 
@@ -523,9 +564,9 @@ template <typename F> int pick_run(int64_t seqlen, int64_t slots, int start, F b
     }
     return best;
 }
-int conv_run(const ConvGeom &g, int vec)
+int conv_run(const ConvGeom &g, int64_t columns)
 {
-    const int64_t threads = g.batch * (g.dim / vec);
+    const int64_t threads = g.batch * columns;
     return pick_run(g.seqlen, (int64_t)device_sm_count() * kConvBlocks, 8, [&](int run) {
         return (threads * ((g.seqlen + run - 1) / run) + kConvThreads - 1) / kConvThreads;
     });
@@ -537,9 +578,9 @@ int64_t conv_bwd_parts_per_seq(const ConvGeom &g, int run)
 }
 
 // kBwdRuns runs in a block.
-int conv_bwd_run(const ConvGeom &g, int vec)
+int conv_bwd_run(const ConvGeom &g, int64_t columns)
 {
-    const int64_t cols = (g.dim / vec + kBwdCols - 1) / kBwdCols;
+    const int64_t cols = (columns + kBwdCols - 1) / kBwdCols;
     int run = pick_run(g.seqlen, (int64_t)device_sm_count() * kBwdBlocks, 12,
                        [&](int r) { return cols * g.batch * conv_bwd_parts_per_seq(g, r); });
     while (conv_bwd_parts_per_seq(g, run) * g.batch > 65535)  // one grid row each
@@ -547,15 +588,16 @@ int conv_bwd_run(const ConvGeom &g, int vec)
     return run;
 }
 
-template <typename TI, int VEC, int W>
+template <typename TI, int VEC, int S, int W>
 cudaError_t fwd_w(const void *x, const float *w, const float *bias, const void *init, void *y, void *fin,
                   const ConvGeom &g, cudaStream_t st)
 {
-    const int run = conv_run(g, VEC);
+    const int64_t columns = conv_columns<VEC, S>(g.dim);
+    const int run = conv_run(g, columns);
     const int64_t n_runs = (g.seqlen + run - 1) / run;
-    const int64_t threads = g.batch * n_runs * (g.dim / VEC);
-    constexpr size_t smem = Ring<TI, VEC, 1, kConvThreads>::kBytes;
-    auto k = conv_kernel<TI, VEC, W>;
+    const int64_t threads = g.batch * n_runs * columns;
+    constexpr size_t smem = Ring<TI, VEC, S, 1, kConvThreads>::kBytes;
+    auto k = conv_kernel<TI, VEC, S, W>;
     static SmemGrant granted;
     const cudaError_t allowed = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
     if (allowed != cudaSuccess)
@@ -566,7 +608,7 @@ cudaError_t fwd_w(const void *x, const float *w, const float *bias, const void *
     note_launch(1);
     return cudaGetLastError();
 }
-template <typename TI, int VEC, int W>
+template <typename TI, int VEC, int S, int W>
 cudaError_t step_w(const void *x, const float *w, const float *bias, const void *state, void *state_out,
                    void *y, const ConvGeom &g, cudaStream_t st)
 {
@@ -577,15 +619,17 @@ cudaError_t step_w(const void *x, const float *w, const float *bias, const void 
     note_launch(1);
     return cudaGetLastError();
 }
-template <typename TI, int VEC, int W>
+template <typename TI, int VEC, int S, int W>
 cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *init, const void *dy,
                   const void *dfinal, void *dx, float *dw, float *dbias, void *dinit, float *part,
-                  const ConvGeom &g, int run, cudaStream_t st)
+                  const ConvGeom &g, cudaStream_t st)
 {
+    const int64_t columns = conv_columns<VEC, S>(g.dim);
+    const int run = conv_bwd_run(g, columns);
     const int64_t pps = conv_bwd_parts_per_seq(g, run);
-    const dim3 grid((unsigned)((g.dim / VEC + kBwdCols - 1) / kBwdCols), (unsigned)(pps * g.batch));
-    constexpr size_t smem = Ring<TI, VEC, 2, kBwdThreads>::kBytes;
-    auto k = conv_bwd_kernel<TI, VEC, W>;
+    const dim3 grid((unsigned)((columns + kBwdCols - 1) / kBwdCols), (unsigned)(pps * g.batch));
+    constexpr size_t smem = Ring<TI, VEC, S, 2, kBwdThreads>::kBytes;
+    auto k = conv_bwd_kernel<TI, VEC, S, W>;
     static SmemGrant granted;
     const cudaError_t allowed = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
     if (allowed != cudaSuccess)
@@ -603,15 +647,18 @@ cudaError_t bwd_w(const void *x, const float *w, const float *bias, const void *
     return cudaGetLastError();
 }
 
-// F<TI, VEC, W>: VEC channels by vector accesses where rows allow it.
-#define SSD_CONV_WIDTHS(F, TI, VEC, ...)                                                            \
-    (g.width == 2 ? F<TI, VEC, 2>(__VA_ARGS__)                                                      \
-                  : (g.width == 3 ? F<TI, VEC, 3>(__VA_ARGS__) : F<TI, VEC, 4>(__VA_ARGS__)))
+// F<TI, VEC, S, W> for the call's width and layout: four adjacent channels a
+// thread where every row starts on a boundary of four (8 bytes of bf16, 16 of
+// f32).  Off them, two channels a warp apart where the type is bf16 (6 x 1769
+// tokens of 2707 channels: forward 29 us instead of 42 with one, backward 58
+// instead of 86), one where it is f32, whose elements the rings can copy (3 x
+// 3331 tokens of 1537 channels: 25 us, 72% of the measured copy rate).
+#define SSD_CONV_WIDTHS(F, TI, VEC, S, ...)                                                         \
+    (g.width == 2 ? F<TI, VEC, S, 2>(__VA_ARGS__)                                                   \
+                  : (g.width == 3 ? F<TI, VEC, S, 3>(__VA_ARGS__) : F<TI, VEC, S, 4>(__VA_ARGS__)))
 
 }  // namespace
 
-// Four channels a thread where every row starts on a boundary of four (8
-// bytes of bf16, 16 of f32), else one.
 cudaError_t launch_conv(const void *x, const float *w, const float *bias, const void *init, void *y,
                         void *fin, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
@@ -620,14 +667,18 @@ cudaError_t launch_conv(const void *x, const float *w, const float *bias, const 
                     g.dim % 4 == 0 && g.row % 4 == 0;
     if (bf16) {
         if (al)
-            return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 4, x, w, bias, init, y, fin, g, st);
-        return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 1, x, w, bias, init, y, fin, g, st);
+            return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 4, 1, x, w, bias, init, y, fin, g, st);
+        if (g.dim >= 64)
+            return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 2, 32, x, w, bias, init, y, fin, g, st);
+        return SSD_CONV_WIDTHS(fwd_w, __nv_bfloat16, 1, 1, x, w, bias, init, y, fin, g, st);
     }
     if (al)
-        return SSD_CONV_WIDTHS(fwd_w, float, 4, x, w, bias, init, y, fin, g, st);
-    return SSD_CONV_WIDTHS(fwd_w, float, 1, x, w, bias, init, y, fin, g, st);
+        return SSD_CONV_WIDTHS(fwd_w, float, 4, 1, x, w, bias, init, y, fin, g, st);
+    return SSD_CONV_WIDTHS(fwd_w, float, 1, 1, x, w, bias, init, y, fin, g, st);
 }
 
+// One channel a thread off the boundaries: state_out may be state, so no channel
+// is computed twice.
 cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, const void *state,
                              void *state_out, void *y, const ConvGeom &g, bool bf16, cudaStream_t st)
 {
@@ -636,26 +687,25 @@ cudaError_t launch_conv_step(const void *x, const float *w, const float *bias, c
                     aligned(w, 8) && g.dim % 4 == 0 && g.row % 4 == 0;
     if (bf16) {
         if (al)
-            return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 4, x, w, bias, state, state_out, y, g, st);
-        return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 1, x, w, bias, state, state_out, y, g, st);
+            return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 4, 1, x, w, bias, state, state_out, y, g, st);
+        return SSD_CONV_WIDTHS(step_w, __nv_bfloat16, 1, 1, x, w, bias, state, state_out, y, g, st);
     }
     if (al)
-        return SSD_CONV_WIDTHS(step_w, float, 4, x, w, bias, state, state_out, y, g, st);
-    return SSD_CONV_WIDTHS(step_w, float, 1, x, w, bias, state, state_out, y, g, st);
+        return SSD_CONV_WIDTHS(step_w, float, 4, 1, x, w, bias, state, state_out, y, g, st);
+    return SSD_CONV_WIDTHS(step_w, float, 1, 1, x, w, bias, state, state_out, y, g, st);
 }
 
-// Room for the partials of either vector width (alignment is not known here).
+// Room for the partials of any layout (alignment is not known here).
 size_t conv_bwd_workspace(const ConvGeom &g)
 {
     int64_t parts = 0;
-    for (int vec : {4, 1}) {
-        const int64_t p = conv_bwd_parts_per_seq(g, conv_bwd_run(g, vec)) * g.batch;
+    for (int64_t columns : {conv_columns<4, 1>(g.dim), conv_columns<2, 32>(g.dim), g.dim}) {
+        const int64_t p = conv_bwd_parts_per_seq(g, conv_bwd_run(g, columns)) * g.batch;
         parts = p > parts ? p : parts;
     }
     return (size_t)(parts * (g.width + 1) * g.dim) * sizeof(float);
 }
 
-// Four channels a thread where every row starts on a boundary of four, else one.
 cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, const void *init,
                             const void *dy, const void *dfinal, void *dx, float *dw, float *dbias,
                             void *dinit, float *part, const ConvGeom &g, bool bf16, cudaStream_t st)
@@ -664,19 +714,16 @@ cudaError_t launch_conv_bwd(const void *x, const float *w, const float *bias, co
     bool al = g.dim % 4 == 0 && g.row % 4 == 0 && g.row_dy % 4 == 0 && aligned(w, 8);
     for (const void *p : {x, init, dy, dfinal, static_cast<const void *>(dx), static_cast<const void *>(dinit)})
         al = al && aligned(p, a);
-    const int run = conv_bwd_run(g, al ? 4 : 1);
     if (bf16) {
         if (al)
-            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias,
-                                   dinit, part, g, run, st);
-        return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit,
-                               part, g, run, st);
+            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 4, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, st);
+        if (g.dim >= 64)
+            return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 2, 32, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, st);
+        return SSD_CONV_WIDTHS(bwd_w, __nv_bfloat16, 1, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, st);
     }
     if (al)
-        return SSD_CONV_WIDTHS(bwd_w, float, 4, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g,
-                               run, st);
-    return SSD_CONV_WIDTHS(bwd_w, float, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, run,
-                           st);
+        return SSD_CONV_WIDTHS(bwd_w, float, 4, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, st);
+    return SSD_CONV_WIDTHS(bwd_w, float, 1, 1, x, w, bias, init, dy, dfinal, dx, dw, dbias, dinit, part, g, st);
 }
 
 }  // namespace ssd

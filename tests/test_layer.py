@@ -104,6 +104,23 @@ def test_conv_bwd(case, with_dfinal):
             close(v, want[k], PLAIN)
 
 
+# Two-byte rows off vector boundaries, 64 channels and more: channels a warp
+# apart, the last warp's shared with its neighbour.
+CONV_ODD = [
+    (1, 1, 65, 4, BF16, True, True, True, None),
+    (2, 19, 64, 3, BF16, True, True, True, (7, 3)),
+    (2, 70, 127, 2, BF16, True, False, False, None),
+    (3, 133, 193, 4, BF16, False, True, True, (8, 5)),
+    (2, 1030, 131, 4, BF16, True, True, True, (4, 1)),
+]
+
+
+@pytest.mark.parametrize("case", CONV_ODD)
+def test_conv_off_boundaries(case):
+    test_conv(case)
+    test_conv_bwd(case, True)
+
+
 @pytest.mark.parametrize("b,D,W,dt,rows", [(1, 8, 4, F32, None), (7, 260, 3, BF16, (12, 4)), (130, 33, 2, BF16, None),
                                            (3, 5, 4, F32, (2, 1))])
 def test_conv_step_continues_a_prompt(b, D, W, dt, rows):

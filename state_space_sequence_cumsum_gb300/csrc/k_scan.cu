@@ -60,6 +60,7 @@ template <int LN> struct PassShape {
     // take the 8.4 blocks an SM of four sequences of 5120 channels in one wave
     // (f32 inputs in flight need more registers: eight)
     static constexpr int BLOCKS = LN == 1 ? 3 : LN == 2 ? 5 : (LN == 4 ? 9 : 72 / (2 * LN));
+    static constexpr int blocks(size_t elem) { return elem == 4 && LN == 4 ? 8 : BLOCKS; }
 };
 
 template <int LN, int MODE> struct PassTile {
@@ -81,7 +82,7 @@ template <int LN, int MODE> struct PassTile {
 // instructions to fill its scheduler; the makers fill the gaps.
 template <typename TI, int LN, int MODE>
 __global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
-                                  sizeof(TI) == 4 && LN == 4 ? 8 : PassShape<LN>::BLOCKS) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
+                                  PassShape<LN>::blocks(sizeof(TI))) scan_pass_kernel(PassArgs<TI> a, ScanGeom g)
 {
     constexpr int NT = PassShape<LN>::NT, MT = PassShape<LN>::MT, CB = PassShape<LN>::CB, T = kScanChunk, NP = 4 * LN;
     // a thread's quads of a tile: QPT of one column of channels, TROWS tokens
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(256)
 scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const float *__restrict__ A,
                  const float *start, float *last, int64_t batch, int64_t dim, int64_t N, int64_t n_seg)
 {
-    constexpr int kJoin = 8;
+    constexpr int kJoin = 24;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t DN = dim * N;
     if (i >= batch * DN)
@@ -591,6 +592,58 @@ cudaError_t launch_join(float *seg, const float *dsum, const float *A, const flo
     return cudaGetLastError();
 }
 
+struct ScanSegs {
+    int64_t n_seg, chunks_per_seg;
+};
+// A pass's blocks for one segment, and as many as the GPU holds at once.
+struct PassFill {
+    int64_t blocks, slots;
+};
+PassFill pass_fill(const ScanGeom &g, size_t elem)
+{
+    auto fill = [&](auto shape) {
+        return PassFill{g.G * ((g.kpg + shape.CB - 1) / shape.CB) * g.batch, shape.blocks(elem) * (int64_t)device_sm_count()};
+    };
+    switch (scan_lanes(g.N)) {
+    case 1: return fill(PassShape<1>());
+    case 2: return fill(PassShape<2>());
+    case 4: return fill(PassShape<4>());
+    case 8: return fill(PassShape<8>());
+    default: return fill(PassShape<16>());
+    }
+}
+int64_t chunks(const ScanGeom &g) { return (g.seqlen + kScanChunk - 1) / kScanChunk; }
+// As many segments as fit with all their blocks, of four chunks at least.
+ScanSegs cut(const PassFill &f, int64_t nc)
+{
+    const int64_t n = min64(f.slots / f.blocks, nc / 4);
+    ScanSegs s{1, nc};
+    if (n > 1) {
+        s.chunks_per_seg = (nc + n - 1) / n;
+        s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;
+    }
+    return s;
+}
+
+// Segments of a pass: one where the channels alone give the GPU a third of the
+// blocks it holds, or the sequence is short.  Measured on 4096 tokens of 5120
+// channels, 16 states (nine blocks an SM): one sequence (2.1 blocks an SM) 283
+// us whole, 246 us in four segments; two sequences 342 us whole, 389 us in two.
+ScanSegs scan_segments(const ScanGeom &g, size_t elem)
+{
+    const int64_t nc = chunks(g);
+    const PassFill f = pass_fill(g, elem);
+    return 3 * f.blocks < f.slots && nc >= 32 ? cut(f, nc) : ScanSegs{1, nc};
+}
+
+// The reverse pass's segments cost only their join.
+ScanSegs scan_reverse_segments(const ScanGeom &g, size_t elem) { return cut(pass_fill(g, elem), chunks(g)); }
+
+size_t segment_bytes(const ScanGeom &g, const ScanSegs &s, int64_t more)
+{
+    return s.n_seg > 1 ? (size_t)(g.batch * (s.n_seg * g.dim * (g.N + 1) + more)) * sizeof(float) : 0;
+}
+
 template <typename TI> void matrix_args(PassArgs<TI> *a, const ScanGeom &g, int64_t row_m)
 {
     const size_t al = 4 * sizeof(TI);
@@ -603,7 +656,7 @@ template <typename TI> void matrix_args(PassArgs<TI> *a, const ScanGeom &g, int6
 template <typename TI>
 cudaError_t run_forward(PassArgs<TI> a, const float *start, void *ws, const ScanGeom &g, cudaStream_t st)
 {
-    const ScanSegs sp = scan_segments(g);
+    const ScanSegs sp = scan_segments(g, sizeof(TI));
     a.chunks_per_seg = sp.chunks_per_seg;
     a.n_seg = sp.n_seg;
     a.start = start;
@@ -667,7 +720,7 @@ cudaError_t rev_t(const void *dy, const void *dt, const float *A, const void *Cm
                   const float *bias, const float *dfinal, float *dkept, float *dinit, void *ws, ScanEnter *enter,
                   const ScanGeom &g, cudaStream_t st)
 {
-    const ScanSegs sp = scan_reverse_segments(g);
+    const ScanSegs sp = scan_reverse_segments(g, sizeof(TI));
     PassArgs<TI> a{};
     a.x = static_cast<const TI *>(dy);
     a.dt = static_cast<const TI *>(dt);
@@ -739,55 +792,18 @@ int scan_lanes(int64_t N)
 
 int scan_chunk() { return kScanChunk; }
 
-// Segments of a pass: one where the channels alone give an SM three walking
-// warps or more, or the sequence is short; else as many as one wave of blocks
-// holds.  Measured on 4096 tokens of 5120 channels: one sequence (2.1 warps an
-// SM) 283 us whole, 246 us in four segments; two sequences 342 us whole, 389
-// us in two.
-ScanSegs scan_segments(const ScanGeom &g)
-{
-    const int LN = scan_lanes(g.N);
-    const int64_t per_warp = 2 * 32 / LN;  // channels
-    const int64_t warps = g.G * ((g.kpg + per_warp - 1) / per_warp) * g.batch;
-    const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    const int64_t sms = device_sm_count();
-    ScanSegs s{1, nc};
-    if (warps < 3 * sms && nc >= 32) {
-        const int64_t n = min64(9 * sms / warps, nc / 4);
-        if (n > 1) {
-            s.chunks_per_seg = (nc + n - 1) / n;
-            s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;
-        }
-    }
-    return s;
-}
-
-// The reverse pass's segments cost only their join: as many as one wave holds.
-ScanSegs scan_reverse_segments(const ScanGeom &g)
-{
-    const int64_t per_warp = 2 * 32 / scan_lanes(g.N);
-    const int64_t warps = g.G * ((g.kpg + per_warp - 1) / per_warp) * g.batch;
-    const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    const int64_t n = min64(9 * (int64_t)device_sm_count() / warps, nc / 4);
-    ScanSegs s{1, nc};
-    if (n > 1) {
-        s.chunks_per_seg = (nc + n - 1) / n;
-        s.n_seg = (nc + s.chunks_per_seg - 1) / s.chunks_per_seg;
-    }
-    return s;
-}
-
+// Room for either type.
 size_t scan_pass_workspace(const ScanGeom &g)
 {
-    const ScanSegs s = scan_segments(g);
-    return s.n_seg > 1 ? (size_t)(g.batch * s.n_seg * g.dim * (g.N + 1)) * sizeof(float) : 0;
+    const size_t a = segment_bytes(g, scan_segments(g, 2), 0), b = segment_bytes(g, scan_segments(g, 4), 0);
+    return a > b ? a : b;
 }
-
 size_t scan_reverse_workspace(const ScanGeom &g)
 {
-    const ScanSegs s = scan_reverse_segments(g);
-    const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    return s.n_seg > 1 ? (size_t)(g.batch * (s.n_seg * g.dim * (g.N + 1) + nc * g.dim)) * sizeof(float) : 0;
+    const int64_t after = chunks(g) * g.dim;
+    const size_t a = segment_bytes(g, scan_reverse_segments(g, 2), after);
+    const size_t b = segment_bytes(g, scan_reverse_segments(g, 4), after);
+    return a > b ? a : b;
 }
 
 cudaError_t launch_selective_scan(const void *u, const void *dt, const float *A, const void *Bm, const void *Cm,

@@ -483,12 +483,13 @@ template <typename TI> struct ScanSums {
     int64_t tokens, N, G, nblk, dim, items;
     unsigned bc_blocks, a_blocks, d_blocks;
 };
-template <typename TI, int V> __global__ void __launch_bounds__(256) scan_sums_kernel(ScanSums<TI> a)
+constexpr int kSumThreads = 512;
+template <typename TI, int V> __global__ void __launch_bounds__(kSumThreads) scan_sums_kernel(ScanSums<TI> a)
 {
     const unsigned first = 2 * (unsigned)a.G * a.bc_blocks;
     if (blockIdx.x < first) {
         const unsigned y = blockIdx.x / a.bc_blocks, x = blockIdx.x - y * a.bc_blocks;
-        const int64_t i = ((int64_t)x * 256 + threadIdx.x) * V;
+        const int64_t i = ((int64_t)x * kSumThreads + threadIdx.x) * V;
         const int64_t stride = a.tokens * a.N;
         if (i >= stride)
             return;
@@ -505,8 +506,9 @@ template <typename TI, int V> __global__ void __launch_bounds__(256) scan_sums_k
         }
         const int64_t to = a.G == 1 ? i : i / a.N * (a.G * a.N) + grp * a.N + i % a.N;
         store_vec<TI, V>(a.bc_out[y & 1] + to, s);
-    } else {  // 32 values a block, eight runs of items each
-        __shared__ float red[8][32];
+    } else {  // 32 values a block, a run of items a warp
+        constexpr int RUNS = kSumThreads / 32;
+        __shared__ float red[RUNS][32];
         unsigned x = blockIdx.x - first;
         int which = 0;
         if (x >= a.a_blocks) {
@@ -524,15 +526,15 @@ template <typename TI, int V> __global__ void __launch_bounds__(256) scan_sums_k
             return;
         float s = 0.f;
         if (j < n)
-#pragma unroll 8
-            for (int64_t k = run; k < a.items; k += 8)
+#pragma unroll 16
+            for (int64_t k = run; k < a.items; k += RUNS)
                 s += a.item[which][k * stride + j];
         red[run][threadIdx.x % 32] = s;
         __syncthreads();
         if (run == 0 && j < n) {
             s = 0.f;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < RUNS; ++q)
                 s += red[q][threadIdx.x];
             a.item_out[which][j] = s;
         }
@@ -550,12 +552,15 @@ GradPlan grad_plan(const ScanGeom &g)
     const int64_t cb = 2 * kGradThreads / scan_lanes(g.N);
     p.nblk = (g.kpg + cb - 1) / cb;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    // about twenty waves of two blocks an SM (the last one's idle slots then
-    // cost little; 4096 tokens of 2 x 5120 channels: 4 waves 1.86 ms a training
-    // step, 20 1.81 ms, 40 1.83 ms), each over a run of chunks so that the sums
-    // over tokens leave few partials
-    const int64_t cols = p.nblk * g.G * g.batch;
-    int64_t n = (int64_t)device_sm_count() * 40 / cols;
+    // Many waves (the last one's idle slots then cost little; 2 x 4096 tokens of
+    // 5120 channels, two blocks an SM: 4 waves 1.86 ms a training step, 20 1.81,
+    // 40 1.83), each block over a run of chunks so that the sums over tokens
+    // leave few partials and a chunk's copies overlap the one before; but no
+    // run so long that an SM has less than twelve (1408 channels of 64 f32
+    // states, 256 tokens: 111 us a training step with three, 97 with twelve).
+    const int64_t cols = p.nblk * g.G * g.batch, sms = device_sm_count();
+    int64_t n = min64(sms * 40 / cols, nc / 4);
+    n = n < sms * 12 / cols ? sms * 12 / cols : n;
     n = n < 1 ? 1 : (n > nc ? nc : n);
     p.chunks_per_group = (nc + n - 1) / n;
     p.n_groups = (nc + p.chunks_per_group - 1) / p.chunks_per_group;
@@ -663,11 +668,12 @@ cudaError_t grad_t(const void *u, const void *dt, const float *A, const void *Bm
     sums.dim = g.dim;
     sums.items = g.batch * p.n_groups;
     const bool quads = g.N % 4 == 0 && aligned(dB, 4 * sizeof(TI)) && aligned(dC, 4 * sizeof(TI));
-    sums.bc_blocks = (unsigned)((sums.tokens * g.N + (quads ? 1023 : 255)) / (quads ? 1024 : 256));
+    const int64_t per_block = kSumThreads * (quads ? 4 : 1);
+    sums.bc_blocks = (unsigned)((sums.tokens * g.N + per_block - 1) / per_block);
     sums.a_blocks = (unsigned)((g.dim * g.N + 31) / 32);
     sums.d_blocks = (unsigned)((g.dim + 31) / 32);
     const unsigned grid = (unsigned)(2 * g.G) * sums.bc_blocks + sums.a_blocks + 2 * sums.d_blocks;
-    (quads ? scan_sums_kernel<TI, 4> : scan_sums_kernel<TI, 1>)<<<grid, 256, 0, st>>>(sums);
+    (quads ? scan_sums_kernel<TI, 4> : scan_sums_kernel<TI, 1>)<<<grid, kSumThreads, 0, st>>>(sums);
     note_launch(1);
     return cudaGetLastError();
 }

@@ -184,13 +184,8 @@ struct ScanGeom {
     int64_t row_u, row_dt, row_z, row_b, row_c, row_dy;
     bool softplus;
 };
-struct ScanSegs {
-    int64_t n_seg, chunks_per_seg;
-};
 int scan_lanes(int64_t N);  // lanes that hold a channel's states, four each
 int scan_chunk();           // tokens between kept states
-ScanSegs scan_segments(const ScanGeom &g);
-ScanSegs scan_reverse_segments(const ScanGeom &g);
 size_t scan_pass_workspace(const ScanGeom &g);
 size_t scan_reverse_workspace(const ScanGeom &g);
 // What entered each segment of the reverse pass (nullptr: one segment), and

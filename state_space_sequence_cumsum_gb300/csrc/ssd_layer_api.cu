@@ -151,7 +151,7 @@ ssd_status_t scan_geom(const ssd_scan_dims_t &d, const ssd_scan_rows_t &r, bool 
 {
     if (d.batch < 1 || d.seqlen < 0 || d.dim < 1 || d.dstate < 1 || d.ngroups < 1 || d.dim % d.ngroups != 0)
         return SSD_ERR_INVALID_ARG;
-    if (d.dstate > 64 || d.batch > 65535 || d.dim > (1LL << 24) || d.seqlen > (1LL << 40))
+    if (d.dstate > 64 || d.batch > 65535 || d.dim > (1LL << 24) || d.seqlen > (1LL << 35))
         return SSD_ERR_UNSUPPORTED;
     const int64_t bc = d.ngroups * d.dstate;
     if (r.u < d.dim || r.dt < d.dim || (has_z && r.z < d.dim) || r.b < bc || r.c < bc || (has_dy && r.dy < d.dim))

@@ -336,37 +336,37 @@ __global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
         }
     };
     TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
-            auto finish = [&](int nt, const typename Tile::Buf &s, const Raw4<TI> (&xq)[QPT], const Raw4<TI> (&zq)[QPT]) {
-#pragma unroll
-                for (int i = 0; i < QPT; ++i) {
-                    const int t = t_first + i * TROWS;
-                    if (t < nt && nq > 0) {
-                        float xv[4], zv[4], o[4];
-                        unpack<TI, 4>(xq[i], xv);
-                        unpack<TI, 4>(zq[i], zv);
-                        ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&s.y[t * CB + cq]);
-#pragma unroll
-                        for (int j = 1; j < LN; ++j) {
-                            const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(&s.y[j * Tile::YP + t * CB + cq]);
-                            y.x = add2(y.x, p.x);
-                            y.y = add2(y.y, p.y);
-                        }
-                        un2(y.x, o[0], o[1]);
-                        un2(y.y, o[2], o[3]);
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
-                            if (pz) {
-                                const f32x2 z = pk2(zv[e], zv[e + 1]);
-                                v = mul2(v, mul2(z, sigmoid2(z)));
-                            }
-                            un2(v, o[e], o[e + 1]);
-                        }
-                        store_some<TI, 4>(py + i * TROWS * g.dim, o, nq, a.vec);
-                    }
+    auto finish = [&](int nt, const typename Tile::Buf &s, const Raw4<TI> (&xq)[QPT], const Raw4<TI> (&zq)[QPT]) {
+unroll
+        for (int i = 0; i < QPT; ++i) {
+            const int t = t_first + i * TROWS;
+            if (t < nt && nq > 0) {
+                float xv[4], zv[4], o[4];
+                unpack<TI, 4>(xq[i], xv);
+                unpack<TI, 4>(zq[i], zv);
+                ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&s.y[t * CB + cq]);
+unroll
+                for (int j = 1; j < LN; ++j) {
+                    const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(&s.y[j * Tile::YP + t * CB + cq]);
+                    y.x = add2(y.x, p.x);
+                    y.y = add2(y.y, p.y);
                 }
-                py += T * g.dim;
-            };
+                un2(y.x, o[0], o[1]);
+                un2(y.y, o[2], o[3]);
+unroll
+                for (int e = 0; e < 4; e += 2) {
+                    f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
+                    if (pz) {
+                        const f32x2 z = pk2(zv[e], zv[e + 1]);
+                        v = mul2(v, mul2(z, sigmoid2(z)));
+                    }
+                    un2(v, o[e], o[e + 1]);
+                }
+                store_some<TI, 4>(py + i * TROWS * g.dim, o, nq, a.vec);
+            }
+        }
+        py += T * g.dim;
+    };
     // x and z of the tile in the fetch registers, kept for its output
     auto keep = [&](Raw4<TI> (&xq)[QPT], Raw4<TI> (&zq)[QPT]) {
 #pragma unroll

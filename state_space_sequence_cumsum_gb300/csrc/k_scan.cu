@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(PassShape<LN>::NT + PassShape<LN>::MT,
     };
     TI *py = MODE == kOut ? a.y + tok * g.dim + ch0 + cq : nullptr;
     auto finish = [&](int nt, const typename Tile::Buf &s, const Raw4<TI> (&xq)[QPT], const Raw4<TI> (&zq)[QPT]) {
-unroll
+#pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int t = t_first + i * TROWS;
             if (t < nt && nq > 0) {
@@ -345,7 +345,7 @@ unroll
                 unpack<TI, 4>(xq[i], xv);
                 unpack<TI, 4>(zq[i], zv);
                 ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&s.y[t * CB + cq]);
-unroll
+#pragma unroll
                 for (int j = 1; j < LN; ++j) {
                     const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(&s.y[j * Tile::YP + t * CB + cq]);
                     y.x = add2(y.x, p.x);
@@ -353,7 +353,7 @@ unroll
                 }
                 un2(y.x, o[0], o[1]);
                 un2(y.y, o[2], o[3]);
-unroll
+#pragma unroll
                 for (int e = 0; e < 4; e += 2) {
                     f32x2 v = fma2(pk2(Dv[e], Dv[e + 1]), pk2(xv[e], xv[e + 1]), pk2(o[e], o[e + 1]));
                     if (pz) {

@@ -39,8 +39,9 @@
  *   failed launch returns SSD_ERR_CUDA.  Errors raised inside a kernel (a
  *   bounded wait that ran out) are recorded in a per-device status word that
  *   ssd_stream_status() reads.
- * Threads: calls are thread-safe; the only shared host state is a
- *   mutex-guarded cache of TMA descriptors and tuning choices.
+ * Threads: calls are thread-safe; the only shared host state is mutex-guarded:
+ *   a cache of TMA descriptors and tuning choices, and how much shared memory
+ *   each kernel has been allowed.
  * Device lifetime: the library caches, per device, the device addresses of
  *   its own __device__ arrays (the status word, the scratch array of
  *   ssd_fwd_noalloc) for the life of the process; do not use it on a device

@@ -1,10 +1,10 @@
 // Host-side declarations shared by the library's translation units.
 // Not part of the public ABI (include/ssd.h is).
 #pragma once
-#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include "smem_grant.h"
 
 #include "../../include/ssd.h"
 
@@ -154,11 +154,7 @@ cudaError_t launch_fused_pair_tc(const void *x, const void *Bm, const void *Cm, 
 // SMs of the current device.
 int device_sm_count();
 // Lets a kernel take `bytes` of dynamic shared memory on the current device;
-// `granted` remembers per device what it was given (one array per kernel).
-constexpr int kSmemDevices = 64;
-struct SmemGrant {
-    std::atomic<int> bytes[kSmemDevices];
-};
+// `granted` remembers per device what it was given (one object per kernel).
 cudaError_t allow_smem(const void *kernel, size_t bytes, SmemGrant *granted);
 
 // Short causal convolution (k_conv.cu): rows are elements between the tokens

@@ -34,13 +34,9 @@ cudaError_t allow_smem(const void *kernel, size_t bytes, SmemGrant *granted)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
-    const bool cached = dev < kSmemDevices;
-    if (cached && granted->bytes[dev].load(std::memory_order_relaxed) >= (int)bytes)
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && cached)
-        granted->bytes[dev].store((int)bytes, std::memory_order_relaxed);
-    return e;
+    return raise_smem(*granted, dev, bytes, [&](int n) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    });
 }
 
 namespace {

@@ -299,7 +299,8 @@ cudaError_t launch_norm_v(const void *y, const void *z, const float *w, void *ou
             return cudaErrorUnknown;
         const size_t smem = 4 * row_bytes;
         auto k = gated_rmsnorm_stream_kernel<TI, VEC>;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static SmemGrant granted;
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted);
         if (e != cudaSuccess)
             return e;
         int per_sm = (int)((200 * 1024) / (smem + 1024));

@@ -304,16 +304,16 @@ cudaError_t launch_chunk_out_simt(const void *x, const void *Bm, const void *Cm,
     cudaError_t e;
     if (bf16) {
         auto k = chunk_out_simt_kernel<__nv_bfloat16>;
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)smem)) != cudaSuccess)
+        static SmemGrant granted;
+        if ((e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted)) != cudaSuccess)
             return e;
         k<<<grid, kCoThreads, smem, st>>>((const __nv_bfloat16 *)x, (const __nv_bfloat16 *)Bm,
                                           (const __nv_bfloat16 *)Cm, dtT, Gc, states, D,
                                           (__nv_bfloat16 *)y, g);
     } else {
         auto k = chunk_out_simt_kernel<float>;
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)smem)) != cudaSuccess)
+        static SmemGrant granted;
+        if ((e = allow_smem(reinterpret_cast<const void *>(k), smem, &granted)) != cudaSuccess)
             return e;
         k<<<grid, kCoThreads, smem, st>>>((const float *)x, (const float *)Bm,
                                           (const float *)Cm, dtT, Gc, states, D, (float *)y, g);

@@ -72,3 +72,40 @@ def test_norms_of_two_widths():
     # backward through rings of 80 and 160 KB, wide rows of 40 to 128 KB both ways
     in_two_threads([norm_calls(2560) + norm_calls(10240) + norm_calls(32768),
                     norm_calls(5120) + norm_calls(12288) + norm_calls(20480)])
+
+
+def gated_norm_calls(dim, rows=64):
+    lib = _lib.load()
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    y, z = (torch.randn(rows, dim, generator=g, device="cuda") for _ in range(2))
+    w, out = torch.randn(dim, generator=g, device="cuda"), torch.empty_like(y)
+
+    def call(s):
+        return lib.ssd_gated_rmsnorm(ptr(y), ptr(z), ptr(w), ptr(out), rows, dim, dim, 1e-5, _lib.SSD_F32,
+                                     ctypes.c_void_p(s.cuda_stream))
+    return [(call, [out])]
+
+
+def chunk_out_calls(chunk, headdim):
+    """The chunk output of f32 inputs, one head of two chunks."""
+    import state_space_sequence_cumsum_gb300 as ssd
+    lib, L, N = _lib.load(), 2 * chunk, 16
+    g = torch.Generator(device="cuda").manual_seed(chunk + headdim)
+    x = torch.randn(1, L, 1, headdim, generator=g, device="cuda")
+    B, C = (torch.randn(1, L, 1, N, generator=g, device="cuda") for _ in range(2))
+    dt, A, D = (torch.rand(s, generator=g, device="cuda") * m for s, m in (((1, L, 1), 0.1), ((1,), -1.0), ((1,), 1.0)))
+    G, dt_t = ssd.ssd_chunk_cumsum(dt, A, chunk)
+    states, _ = ssd.ssd_state_pass(x, B, dt_t, G, chunk)
+    y = torch.empty_like(x)
+    d = _lib.ssd_dims_t(1, L, 1, headdim, N, 1)
+
+    def call(s):
+        return lib.ssd_chunk_out(ptr(x), ptr(B), ptr(C), ptr(dt_t), ptr(G), ptr(states), ptr(D), ptr(y), d,
+                                 _lib.SSD_F32, chunk, ctypes.c_void_p(s.cuda_stream))
+    return [(call, [y])]
+
+
+def test_gated_norms_and_chunk_outputs_of_two_sizes():
+    # rows staged in 64 and 96 KB; chunk tiles of about 92 and 50 KB
+    in_two_threads([gated_norm_calls(4096) + chunk_out_calls(256, 256),
+                    gated_norm_calls(6144) + chunk_out_calls(128, 64)], rounds=200)

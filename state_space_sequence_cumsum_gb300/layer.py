@@ -13,6 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from ._autograd import first_order
 from .ssd import Workspace
 
 __all__ = ["ssd_causal_conv", "ssd_causal_conv_bwd", "ssd_causal_conv_step", "ssd_selective_scan",
@@ -86,6 +87,7 @@ class CausalConvFunction(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, dfinal):
         x, weight, bias, init = ctx.saved_tensors
         g = ssd_causal_conv_bwd(x, weight, dy.contiguous(), bias, ctx.activation, init,
@@ -150,6 +152,7 @@ class SelectiveScanFunction(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, dfinal):
         u, dt, A, B, C, D, z, dt_bias, init, kept = ctx.saved_tensors
         g = ssd_selective_scan_bwd(u, dt, A, B, C, D, dy.contiguous(), z, dt_bias, ctx.dt_softplus,
@@ -199,6 +202,7 @@ class BlockNormFunction(torch.autograd.Function):
         return out, res
 
     @staticmethod
+    @first_order
     def backward(ctx, dout, dres):
         y, res, weight, post_weight, gate = ctx.saved_tensors
         g = ssd_block_norm_bwd(y, res, weight, dout.contiguous(), dres.contiguous(), post_weight,

@@ -12,6 +12,7 @@ import ctypes
 import torch
 
 from . import _lib
+from ._autograd import first_order
 from ._lib import SsdError, check, dims as _dims
 
 __all__ = ["ssd_chunk_cumsum", "ssd_state_pass", "ssd_chunk_out", "ssd_state_out", "ssd_fwd",
@@ -202,6 +203,7 @@ class SsdFunction(torch.autograd.Function):
         return y, final
 
     @staticmethod
+    @first_order
     def backward(ctx, dy, dfinal):
         x, dt, A, B, C, D, init = ctx.saved_tensors
         g = ssd_bwd(x, dt, A, B, C, D, dy.contiguous(), initial_state=init,

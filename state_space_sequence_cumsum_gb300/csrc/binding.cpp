@@ -147,6 +147,22 @@ Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::Scal
     return t;
 }
 
+// Tells autograd that a tensor of the caller's was written: a backward that
+// saved it before then raises instead of using the new values.  (Inference
+// tensors keep no count and cannot be saved.)
+void written(const Tensor &t)
+{
+    if (t.defined() && !t.is_inference())
+        t.unsafeGetTensorImpl()->bump_version();
+}
+template <typename... Ts> void written_if(PyObject *given, const Tensor &t, const Ts &...more)
+{
+    if (given != Py_None)
+        written(t);
+    if constexpr (sizeof...(more) > 0)
+        written_if(more...);
+}
+
 // Workspace of n bytes: the caller's Workspace object grown to it, or a buffer
 // that the allocator takes back in stream order.
 struct Scratch {
@@ -238,7 +254,10 @@ PyObject *causal_conv(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor fin = output(a[7], "final_state", c.state_shape(), x.scalar_type(), x, truth(a[5]));
     const ssd_status_t s = ssd_causal_conv(ptr(x), row, ptr<float>(w), ptr<float>(bias), ptr(init), ptr(y), ptr(fin),
                                            c.d, truth(a[3]), c.code, on.stream);
-    return s == SSD_OK ? tuple(y, fin) : raise_status(s, "ssd_causal_conv");
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_causal_conv");
+    written_if(a[6], y, a[7], fin);
+    return tuple(y, fin);
     END_HANDLE_TH_ERRORS
 }
 
@@ -288,7 +307,11 @@ PyObject *causal_conv_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor y = output(a[6], "y", x.sizes(), x.scalar_type(), x);
     const ssd_status_t s = ssd_causal_conv_step(ptr(x), row, ptr<float>(w), ptr<float>(bias), ptr(state), ptr(out),
                                                 ptr(y), c.d, truth(a[4]), c.code, on.stream);
-    return s == SSD_OK ? tuple(y, out) : raise_status(s, "ssd_causal_conv_step");
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_causal_conv_step");
+    written(out);
+    written_if(a[6], y);
+    return tuple(y, out);
     END_HANDLE_TH_ERRORS
 }
 
@@ -368,7 +391,10 @@ PyObject *selective_scan(PyObject *, PyObject *const *a, Py_ssize_t n)
     const ssd_status_t s = ssd_selective_scan(ptr(u), ptr(dt), ptr<float>(A), ptr(B), ptr(C), ptr<float>(D), ptr(z),
                                               ptr<float>(bias), ptr<float>(init), ptr(y), ptr<float>(fin),
                                               ptr<float>(kept), c.d, c.r, truth(a[8]), c.code, ws.p(), ws.n(), on.stream);
-    return s == SSD_OK ? tuple(y, fin, kept) : raise_status(s, "ssd_selective_scan");
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_selective_scan");
+    written_if(a[12], y, a[13], fin, a[14], kept);
+    return tuple(y, fin, kept);
     END_HANDLE_TH_ERRORS
 }
 
@@ -425,7 +451,11 @@ PyObject *selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     const ssd_status_t s = ssd_selective_scan_step(ptr(u), ptr(dt), ptr<float>(A), ptr(B), ptr(C), ptr<float>(D), ptr(z),
                                                    ptr<float>(bias), ptr<float>(state), ptr<float>(out), ptr(y), c.d,
                                                    c.r, truth(a[9]), c.code, on.stream);
-    return s == SSD_OK ? tuple(y, out) : raise_status(s, "ssd_selective_scan_step");
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_selective_scan_step");
+    written(out);
+    written_if(a[11], y);
+    return tuple(y, out);
     END_HANDLE_TH_ERRORS
 }
 
@@ -480,7 +510,10 @@ PyObject *block_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
     const ssd_status_t s = ssd_block_norm(ptr(y), ptr(res), ptr<float>(w), ptr<float>(pw), ptr<float>(gate), ptr(out),
                                           ptr(rout), c.tokens, c.dim, c.rows, (float)number(a[5]), (float)number(a[6]),
                                           c.code, c.residual(y, rout), on.stream);
-    return s == SSD_OK ? tuple(out, rout) : raise_status(s, "ssd_block_norm");
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_block_norm");
+    written_if(a[7], out, a[8], rout);
+    return tuple(out, rout);
     END_HANDLE_TH_ERRORS
 }
 

@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -164,7 +165,9 @@ template <typename... Ts> void written_if(PyObject *given, const Tensor &t, cons
 }
 
 // Workspace of n bytes: the caller's Workspace object grown to it, or a buffer
-// that the allocator takes back in stream order.
+// that the allocator takes back in stream order.  The caller's may come from
+// another stream's pool: the allocator is told of this one, so that a buffer
+// that the object grows out of is not given away while the call still uses it.
 struct Scratch {
     Tensor t;
     Scratch(PyObject *ws, size_t n, const Tensor &like, PyObject *like_obj)
@@ -185,6 +188,8 @@ struct Scratch {
         Py_DECREF(got);
         TORCH_CHECK_VALUE(t.defined() && t.device() == like.device(), "workspace.get must return a tensor on ",
                           like.device());
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
+                                                      c10::cuda::getCurrentCUDAStream(t.device().index()));
     }
     void *p() const { return t.defined() ? t.data_ptr() : nullptr; }
     size_t n() const { return t.defined() ? (size_t)t.nbytes() : 0; }

@@ -23,8 +23,10 @@ __all__ = ["ssd_causal_conv", "ssd_causal_conv_bwd", "ssd_causal_conv_step", "ss
 
 
 def _call(name, stream, *args):
-    """Calls the native binding on ``stream`` (None: the current one): outputs
-    and workspace come from that stream's pool, inputs are kept for it."""
+    """Calls the native binding on ``stream`` (None: the current one): outputs,
+    and a workspace that is not given, come from that stream's pool; inputs and
+    a given Workspace's buffer are kept for it.  One Workspace serves calls that
+    are ordered, on one stream or by events between several."""
     f = getattr(_lib.native(), name)
     if stream is None:
         return f(*args)

@@ -38,6 +38,14 @@ def _call(name, stream, *args):
     return out
 
 
+def _given(grad, like=None):
+    """An output's gradient, contiguous; where that output was not used, zeros
+    like ``like`` or None."""
+    if grad is not None:
+        return grad.contiguous()
+    return None if like is None else torch.zeros_like(like, memory_format=torch.contiguous_format)
+
+
 # ------------------------------------------------------------- convolution
 
 def _silu(activation):
@@ -86,14 +94,15 @@ class CausalConvFunction(torch.autograd.Function):
                                    return_final_state=True)
         ctx.save_for_backward(x, weight, bias, initial_state)
         ctx.activation = activation
+        ctx.set_materialize_grads(False)
         return y, final
 
     @staticmethod
     @first_order
     def backward(ctx, dy, dfinal):
         x, weight, bias, init = ctx.saved_tensors
-        g = ssd_causal_conv_bwd(x, weight, dy.contiguous(), bias, ctx.activation, init,
-                                dfinal.contiguous(), want_dinit=init is not None)
+        g = ssd_causal_conv_bwd(x, weight, _given(dy, x), bias, ctx.activation, init, _given(dfinal),
+                                want_dinit=init is not None and ctx.needs_input_grad[3])
         return g["dx"], g["dweight"], g["dbias"], g["dinit"], None
 
 
@@ -142,23 +151,36 @@ def ssd_selective_scan_step(u, dt, A, B, C, D, state, z=None, dt_bias=None, dt_s
 class SelectiveScanFunction(torch.autograd.Function):
     """torch.autograd binding of ssd_selective_scan: apply(u, dt, A, B, C, D,
     z, dt_bias, initial_state, dt_softplus) -> (y, final state).  The forward
-    keeps the chunk states its backward starts from."""
+    keeps the chunk states its backward starts from, in f32: dstate / 8 times
+    the bytes of a bf16 u.  Without a gradient to come it keeps none."""
+
+    @classmethod
+    def apply(cls, *args):
+        if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in args):
+            return super().apply(*args)
+        return cls._forward(*args)[:2]
+
+    @staticmethod
+    def _forward(u, dt, A, B, C, D=None, z=None, dt_bias=None, initial_state=None, dt_softplus=True, *,
+                 keep=False):
+        return ssd_selective_scan(u, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, return_chunk_states=keep)
 
     @staticmethod
     def forward(ctx, u, dt, A, B, C, D=None, z=None, dt_bias=None, initial_state=None,
                 dt_softplus=True):
-        y, final, kept = ssd_selective_scan(u, dt, A, B, C, D, z, dt_bias, dt_softplus,
-                                            initial_state, return_chunk_states=True)
+        y, final, kept = SelectiveScanFunction._forward(u, dt, A, B, C, D, z, dt_bias, initial_state, dt_softplus,
+                                                        keep=True)
         ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, initial_state, kept)
         ctx.dt_softplus = dt_softplus
+        ctx.set_materialize_grads(False)
         return y, final
 
     @staticmethod
     @first_order
     def backward(ctx, dy, dfinal):
         u, dt, A, B, C, D, z, dt_bias, init, kept = ctx.saved_tensors
-        g = ssd_selective_scan_bwd(u, dt, A, B, C, D, dy.contiguous(), z, dt_bias, ctx.dt_softplus,
-                                   init, dfinal.contiguous(), kept, want_dinit=init is not None)
+        g = ssd_selective_scan_bwd(u, dt, A, B, C, D, _given(dy, u), z, dt_bias, ctx.dt_softplus, init,
+                                   _given(dfinal), kept, want_dinit=init is not None and ctx.needs_input_grad[8])
         return (g["du"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddt_bias"],
                 g["dinit"], None)
 
@@ -201,13 +223,13 @@ class BlockNormFunction(torch.autograd.Function):
         ctx.save_for_backward(y, res, weight, post_weight, gate)
         ctx.scalars = (scale, eps)
         ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)
         return out, res
 
     @staticmethod
     @first_order
     def backward(ctx, dout, dres):
         y, res, weight, post_weight, gate = ctx.saved_tensors
-        g = ssd_block_norm_bwd(y, res, weight, dout.contiguous(), dres.contiguous(), post_weight,
-                               gate, *ctx.scalars)
+        g = ssd_block_norm_bwd(y, res, weight, _given(dout, y), _given(dres), post_weight, gate, *ctx.scalars)
         return (g["dy"], g["dresidual"] if ctx.has_residual else None, g["dweight"],
                 g["dpost_weight"], g["dgate"], None, None)

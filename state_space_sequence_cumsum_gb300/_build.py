@@ -39,22 +39,36 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
-            glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
-            [BINDING, os.path.abspath(__file__)])
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
+                  _headers())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(NATIVE, [BINDING] + _headers())
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(NATIVE)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and binding_up_to_date()
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
-        return LIB
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}{r.stderr}")
+    return r
+
+
+def build_library(verbose: bool = False, extra_flags=()) -> str:
+    """libssd.so, which needs the CUDA toolkit only."""
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     common = [nvcc, "-O3", "-std=c++17", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC",
@@ -62,46 +76,59 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = common + ["-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}{r.stderr}")
+        r = _run(common + ["-c", src, "-o", obj], f"nvcc failed for {os.path.basename(src)}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
         return obj
 
-    def compile_binding():
-        import torch
-        inc = os.path.join(os.path.dirname(torch.__file__), "include")
-        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
-        obj = os.path.join(BUILD, "binding.o")
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
-               os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-c", BINDING, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}{r.stderr}")
-        return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
-
     with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 2)) as ex:
-        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, _sources()))
-        binding_obj, torch_lib = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of libssd.so failed:\n{r.stdout}{r.stderr}")
+    _run([nvcc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"], "link of libssd.so failed")
     os.replace(tmp, LIB)
+    return LIB
+
+
+def _compile_binding() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    os.makedirs(BUILD, exist_ok=True)
+    obj = os.path.join(BUILD, "binding.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+          os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-c", BINDING, "-o", obj],
+         "g++ failed for binding.cpp")
+    return obj
+
+
+def _link_binding(obj) -> str:
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     # the binding finds libssd.so beside itself and PyTorch's libraries as loaded by torch
     tmp = NATIVE + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, binding_obj, "-L", PKG, "-l:libssd.so", "-L", torch_lib,
-                        "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
-                        f"-Wl,-rpath,{torch_lib}"], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of _native.so failed:\n{r.stdout}{r.stderr}")
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", os.path.dirname(LIB), "-l:libssd.so", "-L", torch_lib,
+          "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+          f"-Wl,-rpath,{torch_lib}"], "link of _native.so failed")
     os.replace(tmp, NATIVE)
+    return NATIVE
+
+
+def build_binding() -> str:
+    """_native.so, which needs g++, PyTorch's headers and libssd.so."""
+    return _link_binding(_compile_binding())
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Both.  What keeps the binding from compiling is raised once libssd.so,
+    which does not need it, is there."""
+    if not force and up_to_date():
+        return LIB
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding)
+        build_library(verbose, extra_flags)
+        _link_binding(binding.result())
     return LIB
 
 

@@ -82,8 +82,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     with _lock:
         if _lib is not None:
             return _lib
-        if build_if_missing and not _build.up_to_date():
-            _build.build()
+        if build_if_missing and not _build.library_up_to_date():
+            _build.build_library()
         if not os.path.exists(_build.LIB):
             raise RuntimeError(f"CUDA library {_build.LIB} is missing; run __graft_entry__.build()")
         lib = ctypes.CDLL(_build.LIB)
@@ -152,14 +152,19 @@ _native = None
 
 
 def native():
-    """The compiled binding of the layer operators (``_native.so``)."""
+    """The compiled binding of the layer operators (``_native.so``), built first
+    if needed."""
     global _native
     if _native is None:
         load()
-        import importlib
-        mod = importlib.import_module("." + os.path.splitext(os.path.basename(_build.NATIVE))[0], __package__)
-        mod.set_error(SsdError)
-        _native = mod
+        with _lock:
+            if _native is None:
+                if not _build.binding_up_to_date():
+                    _build.build_binding()
+                import importlib
+                mod = importlib.import_module("." + os.path.splitext(os.path.basename(_build.NATIVE))[0], __package__)
+                mod.set_error(SsdError)
+                _native = mod
     return _native
 
 

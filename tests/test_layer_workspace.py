@@ -38,9 +38,11 @@ def test_workspace_outgrown_while_another_stream_uses_it(name):
     got = call(workspace=ws, stream=side)
     ws.get(4 * size, ws.buf.device)           # grown: the buffer goes back to the allocator
     assert not side.query()
-    other = torch.empty(size, dtype=torch.uint8, device="cuda")
-    assert other.data_ptr() != old
-    other.fill_(255)
+    # enough of its size to take every free block of the pool that fits
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    assert not any(t.data_ptr() < old + size and old < t.data_ptr() + size for t in others)
+    for t in others:
+        t.fill_(255)
     side.synchronize()
     for k in want:
         if want[k] is not None:

@@ -432,14 +432,24 @@ scan_join_kernel(float *__restrict__ seg, const float *__restrict__ dsum, const 
             end[j] = there ? seg[s * DN + r] : 0.f;
             q[j] = there ? dsum[s * dim + d] : 0.f;
         }
+        float most = 0.f;
 #pragma unroll
-        for (int j = 0; j < kJoin; ++j) {
-            const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
-            if (k < n_seg) {
-                seg[s * DN + r] = h;
-                h = fmaf(ex2(A2 * q[j]), h, end[j]);
+        for (int j = 0; j < kJoin; ++j)
+            most = fmaxf(most, A2 * q[j]);
+        auto walk = [&](auto step) {
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+                const int64_t k = k0 + j, s = b * n_seg + (REV ? n_seg - 1 - k : k);
+                if (k < n_seg) {
+                    seg[s * DN + r] = h;
+                    h = step(A2 * q[j], h, end[j]);
+                }
             }
-        }
+        };
+        if (most <= kLargeExponent)  // decided once: a test at each step holds the loads above apart
+            walk([](float x, float v, float e) { return fmaf(ex2(x), v, e); });
+        else
+            walk(add_scaled);
     }
     if (REV && last)
         last[i] = h;

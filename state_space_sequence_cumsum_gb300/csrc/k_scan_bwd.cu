@@ -246,13 +246,35 @@ __global__ void __launch_bounds__(kGradThreads, grad_blocks<TI, LN>()) scan_grad
         __syncthreads();
 
         const f32x2 nudge = dup2(kDecayNudge);
-        if (a.enter.state)
+        if (a.enter.state) {
+            float x[2][4], most = 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const f32x2 q = dup2(after[j]);
-                e[j][0] = fma2(ex2_2(mul2(q, A[j][0])), in[j][0], e[j][0]);
-                e[j][1] = fma2(ex2_2(mul2(q, A[j][1])), in[j][1], e[j][1]);
+                un2(mul2(q, A[j][0]), x[j][0], x[j][1]);
+                un2(mul2(q, A[j][1]), x[j][2], x[j][3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    most = fmaxf(most, x[j][k]);
             }
+            if (most <= kLargeExponent) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    e[j][0] = fma2(pk2(ex2(x[j][0]), ex2(x[j][1])), in[j][0], e[j][0]);
+                    e[j][1] = fma2(pk2(ex2(x[j][2]), ex2(x[j][3])), in[j][1], e[j][1]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float v[2], o[2];
+                        un2(in[j][k], v[0], v[1]);
+                        un2(e[j][k], o[0], o[1]);
+                        e[j][k] = pk2(add_scaled(x[j][2 * k], v[0], o[0]), add_scaled(x[j][2 * k + 1], v[1], o[1]));
+                    }
+            }
+        }
         // a walk to each piece's start state
         constexpr int PIECES = T / kPiece;
         {

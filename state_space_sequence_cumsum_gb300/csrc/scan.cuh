@@ -103,4 +103,14 @@ __device__ __forceinline__ float decay_rate(float a)
     return r == -INFINITY ? -3.402823466e38f : r;
 }
 
+// e + 2^x v for a whole run's factor 2^x, which may be beyond f32 where the
+// states grow: one that is zero stays zero, a small one is scaled in two steps.
+constexpr float kLargeExponent = 120.f;
+__device__ __forceinline__ float add_scaled(float x, float v, float e)
+{
+    if (x > kLargeExponent)
+        return v == 0.f ? e : fmaf(v * ex2(x - kLargeExponent), ex2(kLargeExponent), e);
+    return fmaf(ex2(x), v, e);
+}
+
 }  // namespace ssd

@@ -195,9 +195,13 @@ def ssd_block_norm(y, residual, weight, post_weight=None, gate=None, scale=1.0, 
     zeros, and residual_dtype, y's or f32, is residual_out's), weights [dim]
     and gate [..., dim] f32 with one row for all tokens, for equal runs of
     them (one per sequence) or for each.  Returns (out, residual_out);
-    residual_out may be residual (in place)."""
+    residual_out may be residual (in place).  A residual_dtype other than that
+    of a given residual or residual_out is refused."""
     if residual_dtype not in (None, torch.float32, y.dtype):
         raise TypeError(f"the residual must be {y.dtype} or float32, got {residual_dtype}")
+    for name, t in (("residual", residual), ("residual_out", residual_out)):
+        if residual_dtype is not None and t is not None and t.dtype != residual_dtype:
+            raise TypeError(f"{name} is {t.dtype}, residual_dtype {residual_dtype}")
     return _call("block_norm", stream, y, residual, weight, post_weight, gate, scale, eps, out,
                  residual_out, residual_dtype == torch.float32)
 

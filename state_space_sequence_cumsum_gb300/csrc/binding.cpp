@@ -130,8 +130,10 @@ int64_t row_of(const Tensor &t, const char *name, int inner = 1)
     return row;
 }
 
-// A new tensor beside `like` (allocated directly: a backward returns nine, and
-// the dispatcher would cost as much as the allocation).
+// A new tensor beside `like`, allocated directly: a backward returns nine, and
+// the dispatcher would cost as much as the allocation.  The price: dispatch
+// modes do not see these allocations, and torch.utils.deterministic's fill of
+// uninitialised memory passes them by (the kernels write every element).
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor &like)
 {
     return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));

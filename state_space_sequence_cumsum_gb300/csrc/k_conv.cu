@@ -14,8 +14,11 @@
 // few threads to cover HBM's latency.  On a GB300, 4 x 4096 tokens of 5376
 // bf16 channels, W = 4 (DRAM traffic as computed, nothing read twice):
 //     forward   64 us, 5.5 TB/s (82% of the measured copy rate)
-//     backward 115 us, 4.6 TB/s (68%); 25 instructions an element at 12 warps
-//              an SM hold it back, not the copies
+//     backward 115 us, 4.6 TB/s (68%); 25 instructions an element by 2.8 warps
+//              a scheduler (154 registers), which is too few: half of the issue
+//              slots are empty, and of the 5.6 cycles a warp takes for an
+//              instruction 1.5 wait for the one before, 0.7 for memory and 0.7
+//              for the f32 pipe
 #include "ssd_internal.h"
 #include "vec.cuh"
 

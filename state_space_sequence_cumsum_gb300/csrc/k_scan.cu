@@ -11,9 +11,9 @@
 // which at 16 states outweigh the HBM traffic (u, dt, z in, out).  On a GB300,
 // bf16 with gate, 16 states, 5120 channels:
 //     4 x 4096 tokens  517 us; the exponentials alone (32 a clock an SM) take
-//                      180 us and the HBM traffic 100 us.  Half of the issue
-//                      slots and 71% of the shared memory pipe are busy.
-//     reverse pass of 2 x 4096 tokens, states kept: 209 us
+//                      180 us and the HBM traffic 100 us.  57% of the issue
+//                      slots and 72% of the shared memory pipe are busy.
+//     reverse pass of 2 x 4096 tokens, states kept: 205 us
 //     one token of 128 sequences 18.5 us, 4.8 TB/s (71% of the measured rate)
 #include "scan.cuh"
 
@@ -24,10 +24,9 @@ namespace {
 //   kOut      forward with the output: m = B, c = C, x = u, z gates the output
 //   kStates   forward, states only
 //   kReverse  m = C, x = dout gated by z, tokens from the last to the first
-// The block's threads first turn a tile of kScanChunk tokens into (delta,
-// delta u) pairs and f32 matrix rows in shared memory, then walk it with the
-// states in registers.  Tiles are double buffered: the next tile's loads are
-// issued before the walk and converted after it, one barrier a tile.
+// A tile is kScanChunk tokens as (delta, delta u) pairs and f32 matrix rows in
+// shared memory; there are two, one walked with the states in registers while
+// the next is made.
 enum PassMode { kOut, kStates, kReverse };
 
 template <typename TI> struct PassArgs {

@@ -15,7 +15,7 @@
 // parts of dB and dC are added over the block's threads in shared memory once
 // a piece and written as one partial per channel block; a last kernel adds
 // those in a fixed order (no atomics, so results do not depend on scheduling).
-// 2 x 4096 tokens of 5120 channels and 16 states take 821 us on a GB300; the
+// 2 x 4096 tokens of 5120 channels and 16 states take 825 us on a GB300; the
 // shared memory pipe (75 passes for a warp's 256 entries a token) is 76% busy,
 // issue slots (207) 53%.  With the start states, B, C and the piece's sums in
 // registers (255, two blocks an SM instead of three) it took 1010 us, and with
@@ -574,12 +574,13 @@ GradPlan grad_plan(const ScanGeom &g)
     const int64_t cb = 2 * kGradThreads / scan_lanes(g.N);
     p.nblk = (g.kpg + cb - 1) / cb;
     const int64_t nc = (g.seqlen + kScanChunk - 1) / kScanChunk;
-    // Many waves (the last one's idle slots then cost little; 2 x 4096 tokens of
-    // 5120 channels, two blocks an SM: 4 waves 1.86 ms a training step, 20 1.81,
-    // 40 1.83), each block over a run of chunks so that the sums over tokens
-    // leave few partials and a chunk's copies overlap the one before; but no
-    // run so long that an SM has less than twelve (1408 channels of 64 f32
-    // states, 256 tokens: 111 us a training step with three, 97 with twelve).
+    // Up to 40 blocks an SM (the last wave's idle slots then cost little; 2 x 4096
+    // tokens of 5120 channels, three blocks at a time: 12 blocks an SM 1453 us a
+    // training step, 20 1430, 40 1428, 80 1446), each block over a run of chunks so
+    // that the sums over tokens leave few partials and a chunk's copies overlap
+    // the one before; but no run so long that an SM has less than twelve (1408
+    // channels of 64 f32 states, 256 tokens: 117 us a training step with three,
+    // 106 with six, 105 with twelve and with 24).
     const int64_t cols = p.nblk * g.G * g.batch, sms = device_sm_count();
     int64_t n = min64(sms * 40 / cols, nc / 4);
     n = n < sms * 12 / cols ? sms * 12 / cols : n;

@@ -5,8 +5,9 @@
 
 namespace ssd {
 
-// A thread holds four of a channel's states; LN = 1, 2, 4, 8 or 16 lanes hold
-// the channel (up to 4 LN states; the ones past dstate stay zero).
+// A thread holds four states, of one channel (the single-token kernel) or of
+// each of two adjacent ones; LN = 1, 2, 4, 8 or 16 lanes hold all of a channel's
+// (up to 4 LN; the ones past dstate stay zero).
 // Tokens of one chunk: a state is kept at each chunk's start for the backward.
 constexpr int kScanChunk = 16;
 
@@ -77,14 +78,6 @@ __device__ __forceinline__ void store_states(float *p, int n, const float (&v)[4
     for (int i = 0; i < 4; ++i)
         if (i < n)
             p[i] = v[i];
-}
-
-template <int LN> __device__ __forceinline__ float lane_sum(float v)
-{
-#pragma unroll
-    for (int o = LN / 2; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 
 // ex2.approx is 2e-8 to 5e-8 low on average for exponents between -1e-2 and

@@ -121,14 +121,15 @@ def build_binding() -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Both.  What keeps the binding from compiling is raised once libssd.so,
-    which does not need it, is there."""
-    if not force and up_to_date():
-        return LIB
+    """What is not up to date of both.  What keeps the binding from compiling is
+    raised once libssd.so, which does not need it, is there."""
+    library, binding = force or not library_up_to_date(), force or not binding_up_to_date()
     with cf.ThreadPoolExecutor(max_workers=1) as ex:
-        binding = ex.submit(_compile_binding)
-        build_library(verbose, extra_flags)
-        _link_binding(binding.result())
+        obj = ex.submit(_compile_binding) if binding else None
+        if library:
+            build_library(verbose, extra_flags)
+        if obj:
+            _link_binding(obj.result())
     return LIB
 
 

@@ -541,6 +541,116 @@ ssd_status_t ssd_block_norm_bwd(const void *y, const void *residual_out, const f
                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 8-bit matrices with a scale for each block of 128 (conventions of the layer
+ * operators).  A matrix [rows, cols] of 8-bit floats stands for
+ *     values[r, c] * scales[r' * scale_row + (c / 128) * scale_block],
+ * r' = r, or with `tile` r / 128.  Its rows are `row` bytes apart and start on
+ * 16 bytes (row % 16 == 0; SSD_ERR_ALIGNMENT otherwise); scales are any f32
+ * values, their strides any that are not negative.
+ */
+typedef enum { SSD_E4M3 = 0, SSD_E5M2 = 1 } ssd_fp8_t;
+typedef struct {
+    const void *values;
+    const float *scales;
+    int64_t row, scale_row, scale_block;
+    int tile;
+    ssd_fp8_t type;
+} ssd_block_matrix_t;
+
+/*
+ * Quantises x [rows, cols] (`row` elements between rows) in blocks of one row
+ * x 128 columns, or with `tile` of 128 x 128:
+ *     s = 2^e, the least e >= -118 with max |x| <= F 2^e;  value = round(x / s)
+ * to nearest, ties to even; F = 448 (SSD_E4M3) or 57344 (SSD_E5M2).  A block
+ * that holds an infinity or a NaN has the scale NaN, and NaN for every value.
+ * Outputs: q [rows, cols] (row_q bytes between rows) with scale[j * scale_ld +
+ * r] of row r's block j; q_t [cols, rows] of the transpose, in blocks of one
+ * column x 128 rows, with scale_t alike.  Either q with its scale or q_t with
+ * its scale_t may be NULL (not wanted).  With `tile` there is one set of
+ * scales, scale[i * scale_ld + j] of row block i and column block j, for both;
+ * scale_t is NULL.  The bytes between rows of q and q_t are left alone.
+ */
+ssd_status_t ssd_block_quantize(const void *x, int64_t row, int64_t rows, int64_t cols,
+                                ssd_dtype_t dtype, int tile, ssd_fp8_t type, void *q,
+                                int64_t row_q, float *scale, int64_t scale_ld, void *q_t,
+                                int64_t row_qt, float *scale_t, int64_t scale_t_ld, void *stream);
+
+/*
+ * out [m, n] = A B^T of the values that A [m, k] and B [n, k] stand for: exact
+ * products, f32 sums (a block's on its own, then over the blocks in order, or
+ * in up to eight runs of them that are added in order), one rounding to
+ * out_dtype.  The two may differ in their 8-bit type.  k == 0 gives zeros.
+ */
+ssd_status_t ssd_block_matmul(ssd_block_matrix_t a, ssd_block_matrix_t b, void *out, int64_t m,
+                              int64_t n, int64_t k, ssd_dtype_t out_dtype, void *stream);
+
+/*
+ * A projection around the scan with an 8-bit weight [outputs, inputs]: y
+ * [tokens, outputs] = Q(x) weight^T, where Q quantises x [tokens, inputs] (rows
+ * `row` elements apart) in blocks of one token x 128 inputs (e4m3).  x_t
+ * [inputs, tokens] with x_t_scale (NULL: not wanted) receives x^T in blocks of
+ * one input x 128 tokens, as ssd_block_quantize's q_t: what the backward needs
+ * of x.
+ */
+size_t ssd_projection_workspace_size(int64_t tokens, int64_t inputs);
+ssd_status_t ssd_projection(const void *x, int64_t row, ssd_block_matrix_t weight, void *y,
+                            void *x_t, int64_t row_xt, float *x_t_scale, int64_t x_t_scale_ld,
+                            int64_t tokens, int64_t inputs, int64_t outputs, ssd_dtype_t dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of ssd_projection for dy [tokens, outputs] (rows row_dy apart):
+ *     dx [tokens, inputs] = Q(dy) weight_t^T,  weight_t [inputs, outputs]
+ *     dweight [outputs, inputs] f32 = Q(dy^T) x_t^T, blocks along the tokens
+ * Either output may be NULL (not wanted), and then what it is formed from too.
+ */
+size_t ssd_projection_bwd_workspace_size(int64_t tokens, int64_t outputs, int want_dx,
+                                         int want_dweight);
+ssd_status_t ssd_projection_bwd(const void *dy, int64_t row_dy, ssd_block_matrix_t weight_t,
+                                ssd_block_matrix_t x_t, void *dx, float *dweight, int64_t tokens,
+                                int64_t inputs, int64_t outputs, ssd_dtype_t dtype, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * One step of AdamW over many tensors, in place.  Per element, with g the
+ * gradient times grad_scale and t the step (1 for the first):
+ *     m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *     p <- (1 - lr weight_decay) p
+ *          - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in f32; p is SSD_F32 or SSD_BF16 (rounded to nearest), g either.
+ * state_bits 32: m and v are f32.  state_bits 8: m and r = sqrt(v) are kept as
+ * e4m3 values (one byte) times a scale for each 256 consecutive elements of a
+ * tensor (m_scale, v_scale, [ceil(n / 256)]): scale = max / 448, value =
+ * round(x * (448 / max)); blocks whose maximum is 2^-100 or less are kept as
+ * zeros, and a root above zero is never rounded to zero.  The update uses m
+ * and v before that rounding.  A block that meets an infinity or a NaN keeps
+ * NaN states.
+ * lr_device, step_device and grad_scale_device (each may be NULL) are read by
+ * the kernel and take the place of lr, step and grad_scale, for calls that are
+ * captured once and replayed.  Tensors are contiguous, with n >= 0 elements
+ * and element alignment; buffers that the call writes may overlap nothing
+ * else in it.
+ */
+typedef struct {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale; /* state_bits 8 only */
+    int64_t n;
+} ssd_adamw_tensor_t;
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    float grad_scale;
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *grad_scale_device;
+} ssd_adamw_t;
+ssd_status_t ssd_adamw_step(const ssd_adamw_tensor_t *tensors, int64_t count, ssd_adamw_t args,
+                            int state_bits, ssd_dtype_t p_dtype, ssd_dtype_t g_dtype, void *stream);
+
+/*
  * Number of kernel launches this library has issued in this process (all
  * devices, all threads).  Diagnostic: a call rejected by validation leaves it
  * unchanged; the benchmark reports launches per step from it.

@@ -1,0 +1,111 @@
+"""Float64 definitions of the 8-bit projections and of the optimiser's step
+(test infrastructure, numpy).
+
+8-bit values are held as the float64 values they stand for.  Everything follows
+the definitions directly: magnitudes by frexp, rounding on the type's own grid,
+sums in float64."""
+from __future__ import annotations
+
+import numpy as np
+
+BLOCK = 128
+STATES = 256
+#: largest value, least exponent of a normal value, bits of the fraction
+E4M3 = (448.0, -6, 3)
+E5M2 = (57344.0, -14, 2)
+LEAST_STATE = 2.0 ** -100
+
+
+def round8(t, kind=E4M3):
+    """To the nearest value of the type, ties to an even last bit, saturating."""
+    top, least, bits = kind
+    t = np.asarray(t, np.float64)
+    _, e = np.frexp(t)                                  # |t| = m 2^e, m in [0.5, 1)
+    step = np.ldexp(1.0, np.maximum(e - 1, least) - bits)
+    return np.clip(np.rint(t / step) * step, -top, top)
+
+
+def block_scale(amax, kind=E4M3):
+    """The least power of two, 2^-118 or more, that brings amax to the type's
+    largest value or less; NaN where amax is not finite."""
+    top = kind[0]
+    amax = np.asarray(amax, np.float64)
+    fine = np.where(np.isfinite(amax), amax, 1.0)
+    m, e = np.frexp(fine)
+    mt, et = np.frexp(top)
+    e = np.maximum(np.where(fine > 0, e - et + (m > mt), -118), -118)
+    return np.where(np.isfinite(amax), np.ldexp(1.0, e), np.nan)
+
+
+def _groups(n):
+    return [slice(i, min(i + BLOCK, n)) for i in range(0, n, BLOCK)]
+
+
+def quantise(x, tile=False, kind=E4M3):
+    """(values on the 8-bit grid, scales): by row and 128 columns, or by 128 x 128."""
+    x = np.asarray(x, np.float64)
+    rows = _groups(x.shape[0]) if tile else [slice(i, i + 1) for i in range(x.shape[0])]
+    cols = _groups(x.shape[1])
+    q, scale = np.zeros_like(x), np.zeros((len(rows), len(cols)))
+    with np.errstate(invalid="ignore"):
+        for j, c in enumerate(cols):
+            part = np.abs(x[:, c])
+            # NaN compares false with everything: a maximum that keeps it
+            amax = np.array([np.nan if np.isnan(part[r]).any() else part[r].max() for r in rows])
+            scale[:, j] = block_scale(amax, kind)
+            for i, r in enumerate(rows):
+                s = scale[i, j]
+                q[r, c] = np.full(x[r, c].shape, np.nan) if np.isnan(s) else round8(x[r, c] / s, kind)
+    return q, scale
+
+
+def values(q, scale):
+    """What an 8-bit matrix stands for; scales by row or by tile."""
+    q, scale = np.asarray(q, np.float64), np.asarray(scale, np.float64)
+    each = np.repeat(scale, BLOCK, axis=1)[:, :q.shape[1]]
+    if scale.shape[0] != q.shape[0]:
+        each = np.repeat(each, BLOCK, axis=0)[:q.shape[0]]
+    return q * each
+
+
+def projection(x, weight):
+    """y for weights given as what they stand for."""
+    return values(*quantise(x)) @ np.asarray(weight, np.float64).T
+
+
+def projection_bwd(x, weight, dy):
+    """(dx, dweight): the formula's, with dy quantised along the outputs for the
+    one, and x and dy along the tokens for the other."""
+    xt, dyt = (values(*quantise(np.asarray(t, np.float64).T)) for t in (x, dy))
+    return values(*quantise(dy)) @ np.asarray(weight, np.float64), dyt @ xt.T
+
+
+def quantise_state(x, root=False):
+    """An optimiser's state (flat) in 8 bits: (values on the grid, scales)."""
+    x = np.asarray(x, np.float64)
+    q, scales = np.zeros_like(x), []
+    for i in range(0, x.size, STATES):
+        part = x[i:i + STATES]
+        a = np.abs(part).max()
+        if not a > LEAST_STATE:
+            scales.append(0.0)
+            continue
+        scales.append(a / 448.0)
+        v = round8(part * (448.0 / a))
+        q[i:i + STATES] = np.where((part > 0) & (v == 0), 2.0 ** -9, v) if root else v
+    return q, np.array(scales)
+
+
+def state_values(q, scales):
+    return np.asarray(q, np.float64) * np.repeat(np.asarray(scales, np.float64), STATES)[:np.size(q)]
+
+
+def adamw(p, g, m, v, step, lr, betas, eps, weight_decay, grad_scale=1.0):
+    """(p, m, v) after one step, all float64."""
+    p, g, m, v = (np.asarray(t, np.float64) for t in (p, g, m, v))
+    b1, b2 = betas
+    g = g * grad_scale
+    m = b1 * m + (1 - b1) * g
+    v = b2 * v + (1 - b2) * g * g
+    hat_m, hat_v = m / (1 - b1 ** step), v / (1 - b2 ** step)
+    return p - lr * weight_decay * p - lr * hat_m / (np.sqrt(hat_v) + eps), m, v

@@ -15,4 +15,7 @@ from .layer import (BlockNormFunction, CausalConvFunction, SelectiveScanFunction
                     ssd_block_norm, ssd_block_norm_bwd, ssd_causal_conv, ssd_causal_conv_bwd,
                     ssd_causal_conv_step, ssd_selective_scan, ssd_selective_scan_bwd,
                     ssd_selective_scan_chunk, ssd_selective_scan_step)
+from .projection import (ProjectionFunction, ssd_block_matmul, ssd_block_quantize,  # noqa: F401
+                         ssd_projection, ssd_projection_bwd)
+from .optimizer import AdamW, ssd_adamw_step  # noqa: F401
 from ._build import build  # noqa: F401

@@ -21,6 +21,8 @@ SSD_ERR_TIMEOUT = 5
 SSD_ERR_WORKSPACE = 6
 SSD_BF16 = 0
 SSD_F32 = 1
+SSD_E4M3 = 0
+SSD_E5M2 = 1
 
 # Every entry point include/ssd.h declares (checked by the tests).
 EXPORTS = ("ssd_chunk_cumsum", "ssd_state_pass", "ssd_chunk_out", "ssd_state_out",
@@ -36,6 +38,8 @@ EXPORTS = ("ssd_chunk_cumsum", "ssd_state_pass", "ssd_chunk_out", "ssd_state_out
            "ssd_selective_scan_chunk", "ssd_selective_scan_bwd",
            "ssd_selective_scan_bwd_workspace_size", "ssd_selective_scan_step", "ssd_block_norm",
            "ssd_block_norm_bwd", "ssd_block_norm_bwd_workspace_size",
+           "ssd_block_quantize", "ssd_block_matmul", "ssd_projection", "ssd_projection_workspace_size",
+           "ssd_projection_bwd", "ssd_projection_bwd_workspace_size", "ssd_adamw_step",
            "ssd_launch_count", "ssd_status_string", "ssd_stream_status")
 PATH_NAMES = {0: "staged-cuda-cores", 1: "staged-tensor-cores", 2: "fused-tensor-cores",
               3: "fused-pair-tensor-cores"}
@@ -60,6 +64,24 @@ class ssd_scan_dims_t(ctypes.Structure):
 class ssd_scan_rows_t(ctypes.Structure):
     _fields_ = [("u", ctypes.c_int64), ("dt", ctypes.c_int64), ("z", ctypes.c_int64),
                 ("b", ctypes.c_int64), ("c", ctypes.c_int64), ("dy", ctypes.c_int64)]
+
+
+class ssd_block_matrix_t(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row", ctypes.c_int64),
+                ("scale_row", ctypes.c_int64), ("scale_block", ctypes.c_int64), ("tile", ctypes.c_int),
+                ("type", ctypes.c_int)]
+
+
+class ssd_adamw_tensor_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class ssd_adamw_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("grad_scale", ctypes.c_float), ("lr_device", ctypes.c_void_p), ("step_device", ctypes.c_void_p),
+                ("grad_scale_device", ctypes.c_void_p)]
 
 
 class SsdError(RuntimeError):
@@ -89,7 +111,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib = ctypes.CDLL(_build.LIB)
         vp, fp, i32, st = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int
         D, CD, SD, SR = ssd_dims_t, ssd_conv_dims_t, ssd_scan_dims_t, ssd_scan_rows_t
-        i64, f32 = ctypes.c_int64, ctypes.c_float
+        i64, f32, BM = ctypes.c_int64, ctypes.c_float, ssd_block_matrix_t
         sig = {
             "ssd_chunk_cumsum": ([fp, fp, fp, fp, D, i32, vp], st),
             "ssd_state_pass": ([vp, vp, fp, fp, fp, fp, fp, D, i32, i32, vp], st),
@@ -136,6 +158,13 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "ssd_block_norm_bwd_workspace_size": ([i64, i64, i64], ctypes.c_size_t),
             "ssd_block_norm_bwd": ([vp, vp, fp, fp, fp, vp, vp, vp, vp, fp, fp, fp, i64, i64, i64,
                                     f32, f32, i32, i32, vp, ctypes.c_size_t, vp], st),
+            "ssd_block_quantize": ([vp, i64, i64, i64, i32, i32, i32, vp, i64, fp, i64, vp, i64, fp, i64, vp], st),
+            "ssd_block_matmul": ([BM, BM, vp, i64, i64, i64, i32, vp], st),
+            "ssd_projection_workspace_size": ([i64, i64], ctypes.c_size_t),
+            "ssd_projection": ([vp, i64, BM, vp, vp, i64, fp, i64, i64, i64, i64, i32, vp, ctypes.c_size_t, vp], st),
+            "ssd_projection_bwd_workspace_size": ([i64, i64, i32, i32], ctypes.c_size_t),
+            "ssd_projection_bwd": ([vp, i64, BM, BM, vp, fp, i64, i64, i64, i32, vp, ctypes.c_size_t, vp], st),
+            "ssd_adamw_step": ([ctypes.POINTER(ssd_adamw_tensor_t), i64, ssd_adamw_t, i32, i32, i32, vp], st),
             "ssd_launch_count": ([], ctypes.c_uint64),
             "ssd_status_string": ([st], ctypes.c_char_p),
             "ssd_stream_status": ([vp], st),

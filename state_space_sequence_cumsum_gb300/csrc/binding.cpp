@@ -552,6 +552,296 @@ PyObject *block_norm_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------ 8-bit blocks
+
+// A new tensor of rows `row` elements apart (dimension 0 or, with `turned`, 1
+// is the one whose neighbours are next to each other).
+Tensor fresh_rows(int64_t rows, int64_t cols, int64_t row, bool turned, at::ScalarType type, const Tensor &like)
+{
+    const int64_t size[2] = {rows, cols}, stride[2] = {turned ? 1 : row, turned ? row : 1};
+    return Tensor(at::detail::empty_strided_cuda(size, stride, type, like.device()));
+}
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+ssd_fp8_t code8(at::ScalarType s, const char *name)
+{
+    TORCH_CHECK_TYPE(s == at::kFloat8_e4m3fn || s == at::kFloat8_e5m2, name, " must be float8_e4m3fn or float8_e5m2, got ",
+                     s);
+    return s == at::kFloat8_e4m3fn ? SSD_E4M3 : SSD_E5M2;
+}
+
+// An 8-bit matrix [rows, cols] and its scales, by row or by tile as their shape says.
+ssd_block_matrix_t matrix(const Tensor &q, const Tensor &scale, const char *name, const Tensor &like)
+{
+    TORCH_CHECK_VALUE(q.dim() == 2, name, " must be a matrix, got ", q.sizes());
+    const ssd_fp8_t type = code8(q.scalar_type(), name);
+    const int64_t rows = q.size(0), nb = blocks_of(q.size(1));
+    TORCH_CHECK_VALUE(scale.dim() == 2 && scale.size(1) == nb && (scale.size(0) == rows || scale.size(0) == blocks_of(rows)),
+                      "the scales of ", name, " must be [", rows, ", ", nb, "] or [", blocks_of(rows), ", ", nb, "], got ",
+                      scale.sizes());
+    TORCH_CHECK_TYPE(scale.scalar_type() == at::kFloat, "the scales of ", name, " must be Float, got ", scale.scalar_type());
+    TORCH_CHECK_VALUE(q.device() == like.device() && scale.device() == like.device(), name, " must be on ", like.device());
+    return {ptr(q), ptr<float>(scale), row_of(q, name), scale.stride(0), scale.stride(1), scale.size(0) != rows, type};
+}
+
+// New scales for each row's blocks, those of a block next to each other.
+Tensor row_scales(int64_t rows, int64_t cols, const Tensor &like)
+{
+    return fresh_rows(rows, blocks_of(cols), up(rows, 4), true, at::kFloat, like);
+}
+// The distance between two blocks' scales.
+int64_t scale_ld(const Tensor &s) { return s.defined() ? s.stride(1) : 0; }
+
+// x, tile, fp8 is e5m2, want_q, want_t
+PyObject *block_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 5);
+    const Tensor x = tensor(a[0], "x");
+    const ssd_dtype_t code = dtype_code(x, "x");
+    TORCH_CHECK_VALUE(x.dim() == 2, "x must be [rows, cols], got ", x.sizes());
+    const int64_t rows = x.size(0), cols = x.size(1), row = row_of(x, "x");
+    const bool tile = truth(a[1]), e5m2 = truth(a[2]), want_q = truth(a[3]), want_t = truth(a[4]);
+    on_gpu(x, "x");
+    const On on(x);
+    const at::ScalarType type = e5m2 ? at::kFloat8_e5m2 : at::kFloat8_e4m3fn;
+    Tensor q, s, qt, st;
+    if (want_q)
+        q = fresh_rows(rows, cols, up(cols, 16), false, type, x);
+    if (want_t)
+        qt = fresh_rows(cols, rows, up(rows, 16), false, type, x);
+    int64_t ld = 0;
+    if (tile && (want_q || want_t)) {
+        s = fresh({blocks_of(rows), blocks_of(cols)}, at::kFloat, x);
+        ld = blocks_of(cols);
+    } else if (!tile) {
+        if (want_q)
+            s = row_scales(rows, cols, x);
+        if (want_t)
+            st = row_scales(cols, rows, x);
+        ld = scale_ld(s);
+    }
+    const ssd_status_t e =
+        ssd_block_quantize(ptr(x), row, rows, cols, code, tile, e5m2 ? SSD_E5M2 : SSD_E4M3, ptr(q), up(cols, 16),
+                           ptr<float>(s), ld, ptr(qt), up(rows, 16), ptr<float>(st), scale_ld(st), on.stream);
+    if (e != SSD_OK)
+        return raise_status(e, "ssd_block_quantize");
+    if (tile && want_t)
+        st = s.t();
+    return tuple(q, want_q ? s : Tensor(), qt, st);
+    END_HANDLE_TH_ERRORS
+}
+
+// a, a_scale, b, b_scale, out is bf16, out
+PyObject *block_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    const Tensor A = tensor(a[0], "a"), as = tensor(a[1], "a_scale"), B = tensor(a[2], "b"), bs = tensor(a[3], "b_scale");
+    const ssd_block_matrix_t ma = matrix(A, as, "a", A), mb = matrix(B, bs, "b", A);
+    const int64_t M = A.size(0), N = B.size(0), K = A.size(1);
+    TORCH_CHECK_VALUE(B.size(1) == K, "a [m, k] and b [n, k] must have the same k, got ", A.sizes(), " and ", B.sizes());
+    const at::ScalarType type = truth(a[4]) ? at::kBFloat16 : at::kFloat;
+    on_gpu(A, "a");
+    const On on(A);
+    const Tensor out = output(a[5], "out", {M, N}, type, A);
+    const ssd_status_t s = ssd_block_matmul(ma, mb, ptr(out), M, N, K, type == at::kBFloat16 ? SSD_BF16 : SSD_F32, on.stream);
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_block_matmul");
+    written_if(a[5], out);
+    return wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// The tokens of x [..., dim]: what its other dimensions hold.
+int64_t tokens_of(const Tensor &x, const char *name)
+{
+    TORCH_CHECK_VALUE(x.dim() >= 1, name, " must be [..., dim]");
+    int64_t t = 1;
+    for (int64_t i = 0; i + 1 < x.dim(); ++i)
+        t *= x.size(i);
+    return t;
+}
+// x's shape with another last dimension.
+struct Shape {
+    c10::SmallVector<int64_t, 6> s;
+    Shape(const Tensor &x, int64_t last) : s(x.sizes().begin(), x.sizes().end()) { s.back() = last; }
+    operator at::IntArrayRef() const { return s; }
+};
+
+// x, weight, weight_scale, return_kept, y, workspace
+PyObject *projection(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    const Tensor x = tensor(a[0], "x"), w = tensor(a[1], "weight"), ws_ = tensor(a[2], "weight_scale");
+    const ssd_dtype_t code = dtype_code(x, "x");
+    const int64_t T = tokens_of(x, "x"), K = x.size(-1), row = row_of(x, "x");
+    const ssd_block_matrix_t m = matrix(w, ws_, "weight", x);
+    TORCH_CHECK_VALUE(w.size(1) == K, "weight must be [outputs, ", K, "], got ", w.sizes());
+    const int64_t N = w.size(0);
+    on_gpu(x, "x");
+    const On on(x);
+    const bool keep = truth(a[3]);
+    const Tensor y = output(a[4], "y", Shape(x, N), x.scalar_type(), x);
+    Tensor xt, xs;
+    if (keep) {
+        xt = fresh_rows(K, T, up(T, 16), false, at::kFloat8_e4m3fn, x);
+        xs = row_scales(K, T, x);
+    }
+    const Scratch ws(a[5], ssd_projection_workspace_size(T, K), x, a[0]);
+    const ssd_status_t s = ssd_projection(ptr(x), row, m, ptr(y), ptr(xt), up(T, 16), ptr<float>(xs), scale_ld(xs), T, K, N,
+                                          code, ws.p(), ws.n(), on.stream);
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_projection");
+    written_if(a[4], y);
+    return tuple(y, xt, xs);
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, weight_t, weight_t_scale, x_t, x_t_scale, workspace; without weight_t no dx, without x_t no dweight
+PyObject *projection_bwd(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    count(n, 6);
+    const Tensor dy = tensor(a[0], "dy"), w = optional(a[1], "weight_t"), xt = optional(a[3], "x_t");
+    const ssd_dtype_t code = dtype_code(dy, "dy");
+    const int64_t T = tokens_of(dy, "dy"), N = dy.size(-1), row = row_of(dy, "dy");
+    ssd_block_matrix_t mw = {}, mx = {};
+    int64_t K = 0;
+    if (w.defined()) {
+        mw = matrix(w, tensor(a[2], "weight_t_scale"), "weight_t", dy);
+        TORCH_CHECK_VALUE(w.size(1) == N, "weight_t must be [inputs, ", N, "], got ", w.sizes());
+        K = w.size(0);
+    }
+    if (xt.defined()) {
+        mx = matrix(xt, tensor(a[4], "x_t_scale"), "x_t", dy);
+        TORCH_CHECK_VALUE(xt.size(1) == T && (!w.defined() || xt.size(0) == K), "x_t must be [inputs, ", T, "], got ",
+                          xt.sizes());
+        K = xt.size(0);
+    }
+    on_gpu(dy, "dy");
+    const On on(dy);
+    Tensor dx, dw;
+    if (w.defined())
+        dx = fresh(Shape(dy, K), dy.scalar_type(), dy);
+    if (xt.defined())
+        dw = fresh({N, K}, at::kFloat, dy);
+    const Scratch ws(a[5], ssd_projection_bwd_workspace_size(T, N, w.defined(), xt.defined()), dy, a[0]);
+    const ssd_status_t s = ssd_projection_bwd(ptr(dy), row, mw, mx, ptr(dx), ptr<float>(dw), T, K, N, code, ws.p(), ws.n(),
+                                              on.stream);
+    return s == SSD_OK ? tuple(dx, dw) : raise_status(s, "ssd_projection_bwd");
+    END_HANDLE_TH_ERRORS
+}
+
+// -------------------------------------------------------------------- AdamW
+
+// A list or tuple of tensors.
+struct Tensors {
+    PyObject *seq;
+    Py_ssize_t n;
+    const char *name;
+    Tensors(PyObject *o, const char *name_, bool maybe = false) : seq(nullptr), n(0), name(name_)
+    {
+        if (maybe && o == Py_None)
+            return;
+        TORCH_CHECK_TYPE(PyList_Check(o) || PyTuple_Check(o), name, " must be a list or tuple of tensors");
+        seq = o;
+        n = PySequence_Fast_GET_SIZE(o);
+    }
+    const Tensor &operator[](Py_ssize_t i) const
+    {
+        PyObject *o = PySequence_Fast_GET_ITEM(seq, i);
+        TORCH_CHECK_TYPE(THPVariable_Check(o), name, "[", i, "] must be a tensor");
+        return THPVariable_Unpack(o);
+    }
+};
+
+// A scalar on the GPU, or a number.
+const void *device_scalar(PyObject *o, const char *name, at::ScalarType type, const Tensor &like)
+{
+    if (!THPVariable_Check(o))
+        return nullptr;
+    const Tensor &t = THPVariable_Unpack(o);
+    TORCH_CHECK_TYPE(t.scalar_type() == type, name, " must be ", type, ", got ", t.scalar_type());
+    TORCH_CHECK_VALUE(t.numel() == 1 && t.is_cuda() && t.device() == like.device(), name, " must be one value on ",
+                      like.device());
+    return t.data_ptr();
+}
+
+// params, grads, m, v, m_scales, v_scales, step, lr, beta1, beta2, eps, weight_decay, grad_scale
+PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
+{
+    HANDLE_TH_ERRORS
+    count(nargs, 13);
+    const Tensors P(a[0], "params"), G(a[1], "grads"), M(a[2], "m"), V(a[3], "v"), MS(a[4], "m_scales", true),
+        VS(a[5], "v_scales", true);
+    TORCH_CHECK_VALUE(G.n == P.n && M.n == P.n && V.n == P.n, "params, grads, m and v must be as many, got ", P.n, ", ", G.n,
+                      ", ", M.n, " and ", V.n);
+    const bool s8 = MS.seq != nullptr;
+    TORCH_CHECK_VALUE((VS.seq != nullptr) == s8 && (!s8 || (MS.n == P.n && VS.n == P.n)),
+                      "m_scales and v_scales are given together, one for each tensor");
+    if (P.n == 0)
+        Py_RETURN_NONE;
+    const Tensor &like = P[0];
+    const ssd_dtype_t pc = dtype_code(like, "params"), gc = dtype_code(G[0], "grads");
+    const at::ScalarType st = s8 ? at::kFloat8_e4m3fn : at::kFloat;
+    std::vector<ssd_adamw_tensor_t> t((size_t)P.n);
+    for (Py_ssize_t i = 0; i < P.n; ++i) {
+        const Tensor &p = P[i];
+        same(p, "params", p.sizes(), like.scalar_type(), like, true);
+        same(G[i], "grads", p.sizes(), G[0].scalar_type(), like, true);
+        same(M[i], "m", p.sizes(), st, like, true);
+        same(V[i], "v", p.sizes(), st, like, true);
+        float *ms = nullptr, *vs = nullptr;
+        if (s8) {
+            const int64_t blocks = (p.numel() + 255) / 256;
+            same_f32(MS[i], "m_scales", {blocks}, like);
+            same_f32(VS[i], "v_scales", {blocks}, like);
+            ms = ptr<float>(MS[i]);
+            vs = ptr<float>(VS[i]);
+        }
+        t[(size_t)i] = {ptr(p), ptr(G[i]), ptr(M[i]), ptr(V[i]), ms, vs, p.numel()};
+    }
+    on_gpu(like, "params");
+    const On on(like);
+    ssd_adamw_t args = {};
+    args.step_device = static_cast<const int64_t *>(device_scalar(a[6], "step", at::kLong, like));
+    if (!args.step_device) {
+        args.step = PyLong_AsLongLong(a[6]);
+        if (args.step == -1 && PyErr_Occurred())
+            throw python_error();
+    }
+    args.lr_device = static_cast<const float *>(device_scalar(a[7], "lr", at::kFloat, like));
+    if (!args.lr_device)
+        args.lr = number(a[7]);
+    args.beta1 = number(a[8]);
+    args.beta2 = number(a[9]);
+    args.eps = number(a[10]);
+    args.weight_decay = number(a[11]);
+    args.grad_scale = 1.f;
+    if (a[12] != Py_None) {
+        args.grad_scale_device = static_cast<const float *>(device_scalar(a[12], "grad_scale", at::kFloat, like));
+        if (!args.grad_scale_device)
+            args.grad_scale = (float)number(a[12]);
+    }
+    const ssd_status_t s = ssd_adamw_step(t.data(), P.n, args, s8 ? 8 : 32, pc, gc, on.stream);
+    if (s != SSD_OK)
+        return raise_status(s, "ssd_adamw_step");
+    for (Py_ssize_t i = 0; i < P.n; ++i) {
+        written(P[i]);
+        written(M[i]);
+        written(V[i]);
+        if (s8) {
+            written(MS[i]);
+            written(VS[i]);
+        }
+    }
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_error(PyObject *, PyObject *cls)
 {
     Py_INCREF(cls);
@@ -564,6 +854,8 @@ PyObject *set_error(PyObject *, PyObject *cls)
 PyMethodDef methods[] = {FAST(causal_conv),      FAST(causal_conv_bwd),     FAST(causal_conv_step),
                          FAST(selective_scan),   FAST(selective_scan_bwd),  FAST(selective_scan_step),
                          FAST(block_norm),       FAST(block_norm_bwd),
+                         FAST(block_quantize),   FAST(block_matmul),        FAST(projection),
+                         FAST(projection_bwd),   FAST(adamw_step),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "Native binding of the layer operators.", -1, methods,

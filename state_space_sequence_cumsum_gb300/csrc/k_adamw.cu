@@ -1,0 +1,328 @@
+// One AdamW step over many tensors in one launch, in place:
+//
+//     m <- b1 m + (1 - b1) g,   v <- b2 v + (1 - b2) g^2
+//     p <- (1 - lr wd) p - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// States in f32, or in 8 bits: m and r = sqrt(v) as e4m3 times a scale for each
+// 256 elements.  The root is kept because its range is half of v's in octaves
+// (e4m3 holds 18), and the update needs it anyway.  The scale is the block's
+// maximum over 448 and not a power of two: it carries the slow drift of the
+// averages, which a value's 3 bits of fraction would round away.
+//
+// A warp takes 256 elements, a thread 8 neighbours, so a block's maximum is one
+// warp reduction.  Bound by HBM: 28 bytes an element in f32, 14 with bf16
+// gradients and 8-bit states.  The tensors' addresses are a kernel parameter, in
+// constant memory; a thread block finds its own by bisection.
+#include <cmath>
+
+#include "common.cuh"
+#include "ssd_internal.h"
+#include "vec.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kUnit = 256;                  // elements of a warp: those that share a scale
+constexpr int64_t kPerBlock = kWarps * kUnit;
+
+struct Entry {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int64_t n;
+};
+template <int MOST> struct Table {
+    Entry e[MOST];
+    unsigned first[MOST];  // the tensor's first thread block
+    int count;
+};
+struct Step {
+    float b1, c1, b2, c2, eps, decay, rate, root;  // decay = 1 - lr wd, rate = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)
+    float grad_scale;
+    // of what is read on the device
+    float lr, wd, log_b1, log_b2;
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *grad_scale_device;
+    float step;
+};
+
+// decay, rate and root where the host does not know the learning rate or the
+// step: 1 - b^t = -expm1(t log b).
+__device__ __noinline__ float3 on_device(const float *lr_device, const int64_t *step_device, float lr, float step, float wd,
+                                         float log_b1, float log_b2)
+{
+    if (lr_device)
+        lr = *lr_device;
+    if (step_device)
+        step = (float)*step_device;
+    return make_float3(1.f - lr * wd, lr / -expm1f(step * log_b1), 1.f / sqrtf(-expm1f(step * log_b2)));
+}
+
+__device__ __forceinline__ void from_e4m3(uint2 q, float (&v)[8])
+{
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+            : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
+            : "r"(h));
+    }
+}
+
+// Eight values in 8 bits, and the scale of the warp's 256.  kRoot: values of
+// zero or more, of which none above zero becomes zero.
+template <bool kRoot> __device__ __forceinline__ uint2 to_e4m3(const float (&v)[8], float &scale)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const float a = __uint_as_float(top);
+    const bool none = top <= 0x0d800000u;  // 2^-100
+    scale = none ? 0.f : a >= INFINITY ? NAN : __fdiv_rn(a, 448.f);
+    if (top > 0x7f800000u)
+        scale = NAN;
+    const float inverse = none ? 0.f : top >= 0x7f800000u ? NAN : __fdiv_rn(448.f, a);
+    uint16_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float lo = __fmul_rn(v[2 * i], inverse), hi = __fmul_rn(v[2 * i + 1], inverse);
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(w[i]) : "f"(hi), "f"(lo));
+        if (kRoot && !none) {  // the least value, 2^-9
+            if (v[2 * i] > 0.f && (w[i] & 0x00ffu) == 0)
+                w[i] |= 0x0001u;
+            if (v[2 * i + 1] > 0.f && (w[i] & 0xff00u) == 0)
+                w[i] |= 0x0100u;
+        }
+    }
+    return make_uint2((uint32_t)w[0] | (uint32_t)w[1] << 16, (uint32_t)w[2] | (uint32_t)w[3] << 16);
+}
+
+// Eight neighbours from p on, `left` of them inside the tensor (zeros after).
+template <typename T> __device__ __forceinline__ void load8(const void *base, int64_t at, int left, bool vec, float (&v)[8])
+{
+    const T *p = static_cast<const T *>(base) + at;
+    if (vec && left >= 8) {
+        constexpr int per = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8; i += per) {
+            float w[per];
+            load_vec<T, per>(p + i, w);
+#pragma unroll
+            for (int j = 0; j < per; ++j)
+                v[i + j] = w[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = i < left ? to_f32(p[i]) : 0.f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *base, int64_t at, int left, bool vec, const float (&v)[8])
+{
+    T *p = static_cast<T *>(base) + at;
+    if (vec && left >= 8) {
+        constexpr int per = 16 / (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8; i += per) {
+            float w[per];
+#pragma unroll
+            for (int j = 0; j < per; ++j)
+                w[j] = v[i + j];
+            store_vec<T, per>(p + i, w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                p[i] = from_f32<T>(v[i]);
+    }
+}
+__device__ __forceinline__ uint2 load_bytes(const void *base, int64_t at, int left, bool vec)
+{
+    const uint8_t *p = static_cast<const uint8_t *>(base) + at;
+    if (vec && left >= 8)
+        return *reinterpret_cast<const uint2 *>(p);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left)
+            w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_bytes(void *base, int64_t at, int left, bool vec, uint2 q)
+{
+    uint8_t *p = static_cast<uint8_t *>(base) + at;
+    if (vec && left >= 8) {
+        *reinterpret_cast<uint2 *>(p) = q;
+        return;
+    }
+    const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left)
+            p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+}
+
+template <int MOST, typename TP, typename TG, bool k8>
+__global__ void __launch_bounds__(kWarps * 32)
+adamw_kernel(const __grid_constant__ Table<MOST> table, const __grid_constant__ Step s)
+{
+    float decay = s.decay, rate = s.rate, root = s.root;
+    if (s.lr_device || s.step_device) {
+        const float3 d = on_device(s.lr_device, s.step_device, s.lr, s.step, s.wd, s.log_b1, s.log_b2);
+        decay = d.x;
+        rate = d.y;
+        root = d.z;
+    }
+    const float grad_scale = s.grad_scale_device ? *s.grad_scale_device : s.grad_scale;
+    int lo = 0, hi = table.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (table.first[mid] <= blockIdx.x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Entry &t = table.e[lo];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)(blockIdx.x - table.first[lo]) * kWarps + warp;
+    const int64_t at = unit * kUnit + lane * 8;
+    if (unit * kUnit >= t.n)
+        return;
+    const int left = (int)min64(8, t.n - at);  // zero or less past the end
+    const bool vec = ((reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.g) |
+                       reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v)) & 15u) == 0;
+    float p[8], g[8], m[8], v[8];
+    load8<TP>(t.p, at, left, vec, p);
+    load8<TG>(t.g, at, left, vec, g);
+    if (k8) {
+        const uint2 qm = load_bytes(t.m, at, left, vec), qv = load_bytes(t.v, at, left, vec);
+        const float sm = t.m_scale[unit], sv = t.v_scale[unit];
+        from_e4m3(qm, m);
+        from_e4m3(qv, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = __fmul_rn(m[i], sm);
+            v[i] = __fmul_rn(v[i], sv);
+            v[i] = __fmul_rn(v[i], v[i]);
+        }
+    } else {
+        load8<float>(t.m, at, left, vec, m);
+        load8<float>(t.v, at, left, vec, v);
+    }
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float h = __fmul_rn(g[i], grad_scale);
+        m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(h, s.c1));
+        v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(h, h), s.c2));
+        r[i] = __fsqrt_rn(v[i]);
+        p[i] = p[i] * decay - __fdividef(m[i], r[i] * root + s.eps) * rate;
+    }
+    store8<TP>(t.p, at, left, vec, p);
+    if (k8) {
+        float sm, sv;
+        const uint2 qm = to_e4m3<false>(m, sm), qv = to_e4m3<true>(r, sv);
+        store_bytes(t.m, at, left, vec, qm);
+        store_bytes(t.v, at, left, vec, qv);
+        if (lane == 0) {
+            t.m_scale[unit] = sm;
+            t.v_scale[unit] = sv;
+        }
+    } else {
+        store8<float>(t.m, at, left, vec, m);
+        store8<float>(t.v, at, left, vec, v);
+    }
+}
+
+template <int MOST, typename TP, typename TG, bool k8>
+cudaError_t launch(const Table<MOST> &table, unsigned blocks, const Step &s, cudaStream_t st)
+{
+    adamw_kernel<MOST, TP, TG, k8><<<blocks, kWarps * 32, 0, st>>>(table, s);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+        note_launch(1);
+    return e;
+}
+
+template <int MOST>
+cudaError_t launch_types(const Table<MOST> &t, unsigned blocks, const Step &s, bool s8, bool p_bf16, bool g_bf16,
+                         cudaStream_t st)
+{
+    using bf = __nv_bfloat16;
+    if (p_bf16)
+        return g_bf16 ? (s8 ? launch<MOST, bf, bf, true>(t, blocks, s, st) : launch<MOST, bf, bf, false>(t, blocks, s, st))
+                      : (s8 ? launch<MOST, bf, float, true>(t, blocks, s, st) : launch<MOST, bf, float, false>(t, blocks, s, st));
+    return g_bf16 ? (s8 ? launch<MOST, float, bf, true>(t, blocks, s, st) : launch<MOST, float, bf, false>(t, blocks, s, st))
+                  : (s8 ? launch<MOST, float, float, true>(t, blocks, s, st) : launch<MOST, float, float, false>(t, blocks, s, st));
+}
+
+// As many tensors in one launch as a table and a grid hold.
+template <int MOST>
+cudaError_t launch_all(const ssd_adamw_tensor_t *tensors, int64_t count, const Step &s, bool s8, bool p_bf16, bool g_bf16,
+                       cudaStream_t st)
+{
+    Table<MOST> table;
+    table.count = 0;
+    int64_t blocks = 0;
+    auto go = [&] {
+        const cudaError_t e =
+            table.count ? launch_types(table, (unsigned)blocks, s, s8, p_bf16, g_bf16, st) : cudaSuccess;
+        table.count = 0;
+        blocks = 0;
+        return e;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const ssd_adamw_tensor_t &t = tensors[i];
+        if (t.n == 0)
+            continue;
+        const int64_t need = (t.n + kPerBlock - 1) / kPerBlock;
+        if (table.count == MOST || blocks + need > 2147483647LL)
+            if (cudaError_t e = go())
+                return e;
+        table.e[table.count] = {t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.n};
+        table.first[table.count++] = (unsigned)blocks;
+        blocks += need;
+    }
+    return go();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const ssd_adamw_tensor_t *tensors, int64_t count, const ssd_adamw_t &a, bool states8, bool p_bf16,
+                         bool g_bf16, cudaStream_t st)
+{
+    Step s = {};
+    s.b1 = (float)a.beta1;
+    s.c1 = (float)(1.0 - a.beta1);
+    s.b2 = (float)a.beta2;
+    s.c2 = (float)(1.0 - a.beta2);
+    s.eps = (float)a.eps;
+    s.grad_scale = a.grad_scale;
+    const double t = (double)(a.step_device ? 1 : a.step);
+    s.decay = (float)(1.0 - a.lr * a.weight_decay);
+    s.rate = (float)(a.lr / (1.0 - std::pow(a.beta1, t)));
+    s.root = (float)(1.0 / std::sqrt(1.0 - std::pow(a.beta2, t)));
+    s.lr = (float)a.lr;
+    s.wd = (float)a.weight_decay;
+    s.log_b1 = (float)std::log(a.beta1);  // -inf for 0: the correction is 1
+    s.log_b2 = (float)std::log(a.beta2);
+    s.step = (float)t;
+    s.lr_device = a.lr_device;
+    s.step_device = a.step_device;
+    s.grad_scale_device = a.grad_scale_device;
+    // a small table is a small kernel parameter
+    return count <= 32 ? launch_all<32>(tensors, count, s, states8, p_bf16, g_bf16, st)
+                       : launch_all<480>(tensors, count, s, states8, p_bf16, g_bf16, st);
+}
+
+}  // namespace ssd

@@ -1,0 +1,211 @@
+// Values in 8-bit floats with a scale for each block of 128:
+//
+//     q = round(x / s),   s = 2^e with the least e >= -118 such that max |x| <= F 2^e
+//
+// over a block of one row x 128 columns, or (tile) 128 x 128; F is the largest
+// 8-bit value, 448 = 1.75 2^8 (e4m3) or 57344 = 1.75 2^15 (e5m2).  Division by a
+// power of two is exact, so every value is rounded once, and the transpose of a
+// tile's values is the tile's of the transpose.  A block that holds an infinity
+// or a NaN has the scale NaN and nothing but NaN in it.
+//
+// One CTA takes 128 x 128 values, once from memory for both orientations: a
+// warp 16 rows, a thread 4 neighbouring columns of them, kept in registers.  A
+// row's maximum is one warp reduction, a column's the thread's own over its rows
+// and then over the warps.  The values of the transpose go through shared
+// memory, 16 of a column at a time, so that rows of 128 bytes are written.
+// Bound by HBM: e bytes in, 1 out per orientation.
+#include "common.cuh"
+#include "ssd_internal.h"
+#include "vec.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kB = 128;
+constexpr int kWarps = 8, kRowsOfWarp = kB / kWarps;
+
+// Bits of the scale and of its inverse for the largest magnitude's bits: with
+// amax = 1.f * 2^k, e = k - TOP + (f > 1.75), TOP = 8 or 15.
+template <bool kE5M2> __device__ __forceinline__ void scale_of(uint32_t amax, float &scale, float &inverse)
+{
+    constexpr int top = kE5M2 ? 15 : 8;
+    // the biased exponent of amax, one more where its fraction is over 0.75
+    const int k = (int)((amax + 0x1fffffu) >> 23);
+    const int e = max(k - top, 9);  // biased; 2^-118
+    const bool bad = amax >= 0x7f800000u;
+    scale = __uint_as_float(bad ? 0x7fffffffu : (uint32_t)e << 23);
+    inverse = __uint_as_float(bad ? 0x7fffffffu : (uint32_t)(254 - e) << 23);
+}
+
+// Four values to four bytes, the first in the low one.
+template <bool kE5M2> __device__ __forceinline__ uint32_t to_bytes(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    if (kE5M2) {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    }
+    return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// kVec: rows of x start on boundaries of four values.
+template <typename TI, bool kE5M2, bool kVec>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
+                      uint8_t *__restrict__ qt, float *__restrict__ scale_t, const QuantGeom g)
+{
+    __shared__ uint32_t col_max[kWarps][kB];
+    __shared__ __align__(16) uint4 turned[kB * kB / 16];  // [column][16-byte piece ^ (column / 4 % 8)]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned col_blocks = (unsigned)((g.cols + kB - 1) / kB);
+    const int64_t rb = blockIdx.x / col_blocks, r0 = rb * kB + warp * kRowsOfWarp;
+    const int64_t cb = blockIdx.x % col_blocks, c0 = cb * kB + lane * 4;
+
+    float v[kRowsOfWarp][4];
+#pragma unroll
+    for (int i = 0; i < kRowsOfWarp; ++i) {
+        const int64_t r = r0 + i;
+        const TI *p = x + r * g.row + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[i][j] = 0.f;
+        if (r < g.rows) {
+            if (kVec && c0 + 4 <= g.cols) {
+                load_vec<TI, 4>(p, v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < g.cols)
+                        v[i][j] = to_f32(p[j]);
+            }
+        }
+    }
+    uint32_t cm[4] = {0, 0, 0, 0};
+    if (qt || g.tile) {
+#pragma unroll
+        for (int i = 0; i < kRowsOfWarp; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                cm[j] = max(cm[j], magnitude(v[i][j]));
+        *reinterpret_cast<uint4 *>(&col_max[warp][lane * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const uint4 m = *reinterpret_cast<const uint4 *>(&col_max[w][lane * 4]);
+            cm[0] = max(cm[0], m.x);
+            cm[1] = max(cm[1], m.y);
+            cm[2] = max(cm[2], m.z);
+            cm[3] = max(cm[3], m.w);
+        }
+    }
+    float tile_scale = 0.f, tile_inverse = 0.f;
+    if (g.tile) {
+        scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, max(max(cm[0], cm[1]), max(cm[2], cm[3]))), tile_scale,
+                        tile_inverse);
+        if (threadIdx.x == 0)
+            scale[rb * g.scale_ld + cb] = tile_scale;
+    }
+    if (q) {
+        float mine = 0.f;  // lane i keeps row i's scale
+#pragma unroll
+        for (int i = 0; i < kRowsOfWarp; ++i) {
+            float s = tile_scale, inverse = tile_inverse;
+            if (!g.tile) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m = max(m, magnitude(v[i][j]));
+                scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, m), s, inverse);
+                mine = lane == i ? s : mine;
+            }
+            const int64_t r = r0 + i;
+            if (r < g.rows && c0 < g.cols) {
+                const uint32_t b = to_bytes<kE5M2>(v[i][0] * inverse, v[i][1] * inverse, v[i][2] * inverse,
+                                                   v[i][3] * inverse);
+                uint8_t *o = q + r * g.row_q + c0;
+                if (c0 + 4 <= g.cols) {
+                    *reinterpret_cast<uint32_t *>(o) = b;
+                } else {
+                    for (int j = 0; c0 + j < g.cols; ++j)
+                        o[j] = (uint8_t)(b >> (8 * j));
+                }
+            }
+        }
+        if (!g.tile && lane < kRowsOfWarp && r0 + lane < g.rows)
+            scale[cb * g.scale_ld + r0 + lane] = mine;
+    }
+    if (qt) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float s = tile_scale, inverse = tile_inverse;
+            if (!g.tile) {
+                scale_of<kE5M2>(cm[j], s, inverse);
+                if (warp == 0 && c0 + j < g.cols)
+                    scale_t[rb * g.scale_t_ld + c0 + j] = s;
+            }
+            uint32_t b[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                b[w] = to_bytes<kE5M2>(v[4 * w][j] * inverse, v[4 * w + 1][j] * inverse, v[4 * w + 2][j] * inverse,
+                                       v[4 * w + 3][j] * inverse);
+            turned[(lane * 4 + j) * (kB / 16) + (warp ^ (lane & 7))] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+        __syncthreads();
+        // a warp writes 16 columns, eight threads the 128 bytes of one
+        const int64_t first = rb * kB + (lane & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = warp * 16 + i * 4 + (lane >> 3);
+            const int64_t col = cb * kB + c;
+            if (col >= g.cols || first >= g.rows)
+                continue;
+            const uint4 b = turned[c * (kB / 16) + ((lane & 7) ^ ((c >> 2) & 7))];
+            uint8_t *o = qt + col * g.row_qt + first;
+            if (first + 16 <= g.rows) {
+                *reinterpret_cast<uint4 *>(o) = b;
+            } else {
+                const uint8_t *e = reinterpret_cast<const uint8_t *>(&b);
+                for (int j = 0; first + j < g.rows; ++j)
+                    o[j] = e[j];
+            }
+        }
+    }
+}
+
+template <typename TI, bool kE5M2>
+cudaError_t launch(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)(((g.cols + kB - 1) / kB) * ((g.rows + kB - 1) / kB));
+    const bool vec = g.row % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(TI)) == 0;
+    auto go = [&](auto kernel) {
+        kernel<<<grid, kWarps * 32, 0, st>>>(static_cast<const TI *>(x), static_cast<uint8_t *>(q), scale,
+                                             static_cast<uint8_t *>(qt), scale_t, g);
+    };
+    if (vec)
+        go(block_quantize_kernel<TI, kE5M2, true>);
+    else
+        go(block_quantize_kernel<TI, kE5M2, false>);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+        note_launch(1);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_block_quantize(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g,
+                                  bool bf16, cudaStream_t st)
+{
+    if (bf16)
+        return g.e5m2 ? launch<__nv_bfloat16, true>(x, q, scale, qt, scale_t, g, st)
+                      : launch<__nv_bfloat16, false>(x, q, scale, qt, scale_t, g, st);
+    return g.e5m2 ? launch<float, true>(x, q, scale, qt, scale_t, g, st)
+                  : launch<float, false>(x, q, scale, qt, scale_t, g, st);
+}
+
+}  // namespace ssd

@@ -1,0 +1,297 @@
+// C ABI of the 8-bit projections and of the optimiser's step: argument
+// validation and workspace layout.  See include/ssd.h for the contract of every
+// entry point.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "api_check.h"
+#include "common.cuh"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace {
+
+constexpr int64_t kMostRows = 2147483647LL - 512;  // TMA coordinates are 32-bit
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+bool known8(ssd_fp8_t t) { return t == SSD_E4M3 || t == SSD_E5M2; }
+
+// Sizes that the kernels' coordinates and grids hold.
+ssd_status_t check_sizes(int64_t rows, int64_t cols)
+{
+    if (rows < 0 || cols < 0)
+        return SSD_ERR_INVALID_ARG;
+    if (rows > kMostRows || cols > kMostRows || (double)(blocks_of(rows) + 1) * (double)(blocks_of(cols) + 1) * 8.0 > 2147483647.0)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// The memory of an 8-bit matrix [rows, cols].
+struct MatrixRanges {
+    Range values, scales;
+};
+ssd_status_t matrix_ranges(const ssd_block_matrix_t &a, int64_t rows, int64_t cols, MatrixRanges *r)
+{
+    if (!known8(a.type) || a.scale_row < 0 || a.scale_block < 0 || (rows > 1 && a.row < cols))
+        return SSD_ERR_INVALID_ARG;
+    if (a.row > (1LL << 39) || a.scale_row > (1LL << 39) || a.scale_block > (1LL << 39))
+        return SSD_ERR_UNSUPPORTED;
+    if (rows > 1 && a.row % 16 != 0)
+        return SSD_ERR_ALIGNMENT;
+    const int64_t srows = a.tile ? blocks_of(rows) : rows, nb = blocks_of(cols);
+    const bool any = rows > 0 && cols > 0;
+    r->values = {a.values, cols > 0 ? strided(rows, a.row, cols, 1) : 0, 16, true};
+    r->scales = {a.scales, any ? (size_t)((srows - 1) * a.scale_row + (nb - 1) * a.scale_block + 1) * 4 : 0, 4, true};
+    return SSD_OK;
+}
+
+BlockMatrix inner(const ssd_block_matrix_t &a, int64_t rows, int64_t cols)
+{
+    // one row has no distance to a next; the tensor map wants a multiple of 16
+    return {a.values, a.scales, rows > 1 ? a.row : up16(cols), a.scale_row, a.scale_block, a.tile != 0,
+            a.type == SSD_E5M2};
+}
+
+ssd_status_t zero(void *p, size_t bytes, cudaStream_t st)
+{
+    return bytes ? cuda_status(cudaMemsetAsync(p, 0, bytes, st)) : SSD_OK;
+}
+
+ssd_status_t product(const BlockMatrix &a, const BlockMatrix &b, void *out, int64_t m, int64_t n, int64_t k,
+                     ssd_dtype_t type, cudaStream_t st)
+{
+    if (m == 0 || n == 0)
+        return SSD_OK;
+    if (k == 0)
+        return zero(out, (size_t)m * n * elem(type), st);
+    return cuda_status(launch_block_matmul(a, b, out, m, n, k, type == SSD_BF16, st));
+}
+
+// A quantised matrix [rows, cols] in workspace: its values, then its scales by
+// column block.
+struct Quantised {
+    int64_t row, ld;
+    size_t values, bytes;
+    Quantised(int64_t rows, int64_t cols)
+        : row(up16(cols)), ld(rows), values(round256((size_t)rows * row)),
+          bytes(values + round256((size_t)rows * blocks_of(cols) * 4))
+    {
+    }
+    void *q(void *base) const { return base; }
+    float *scale(void *base) const { return reinterpret_cast<float *>(static_cast<char *>(base) + values); }
+    BlockMatrix matrix(void *base) const { return {base, scale(base), row, 1, ld, false, false}; }
+};
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+ssd_status_t ssd_block_quantize(const void *x, int64_t row, int64_t rows, int64_t cols, ssd_dtype_t dtype, int tile,
+                                ssd_fp8_t type, void *q, int64_t row_q, float *scale, int64_t scale_ld, void *q_t,
+                                int64_t row_qt, float *scale_t, int64_t scale_t_ld, void *stream)
+{
+    if (!known(dtype) || !known8(type) || (rows > 1 && row < cols) || (tile && scale_t))
+        return SSD_ERR_INVALID_ARG;
+    SSD_TRY(check_sizes(rows, cols));
+    if (row > (1LL << 39) || row_q > (1LL << 39) || row_qt > (1LL << 39) || scale_ld > (1LL << 39) ||
+        scale_t_ld > (1LL << 39))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t rb = blocks_of(rows), cb = blocks_of(cols);
+    const bool any = rows > 0 && cols > 0;
+    // the scales that are written: by column block of q, by row block of q_t, or the tiles'
+    const bool has_scale = tile ? q || q_t : q != nullptr, has_scale_t = !tile && q_t;
+    if ((q && rows > 1 && row_q < cols) || (q_t && cols > 1 && row_qt < rows) ||
+        (has_scale && (tile ? rb > 1 && scale_ld < cb : cb > 1 && scale_ld < rows)) ||
+        (has_scale_t && rb > 1 && scale_t_ld < cols) || (!has_scale && scale) || (!has_scale_t && scale_t))
+        return SSD_ERR_INVALID_ARG;
+    if ((q && rows > 1 && row_q % 16 != 0) || (q_t && cols > 1 && row_qt % 16 != 0))
+        return SSD_ERR_ALIGNMENT;
+    const size_t e = elem(dtype);
+    SSD_TRY(check_all({{x, cols > 0 ? strided(rows, row, cols, e) : 0, e, true}},
+                      {{q, any && q ? strided(rows, row_q, cols, 1) : 0, 16, false},
+                       {q_t, any && q_t ? strided(cols, row_qt, rows, 1) : 0, 16, false},
+                       {scale, !any || !has_scale ? 0 : tile ? strided(rb, scale_ld, cb, 4) : strided(cb, scale_ld, rows, 4),
+                        4, has_scale},
+                       {scale_t, any && has_scale_t ? strided(rb, scale_t_ld, cols, 4) : 0, 4, has_scale_t}}));
+    if (!any || (!q && !q_t))
+        return SSD_OK;
+    const QuantGeom g{rows, cols, row, row_q, row_qt, scale_ld, scale_t_ld, tile != 0, type == SSD_E5M2};
+    return cuda_status(launch_block_quantize(x, q, scale, q_t, scale_t, g, dtype == SSD_BF16, (cudaStream_t)stream));
+}
+
+ssd_status_t ssd_block_matmul(ssd_block_matrix_t a, ssd_block_matrix_t b, void *out, int64_t m, int64_t n, int64_t k,
+                              ssd_dtype_t out_dtype, void *stream)
+{
+    if (!known(out_dtype))
+        return SSD_ERR_INVALID_ARG;
+    SSD_TRY(check_sizes(m, k));
+    SSD_TRY(check_sizes(n, k));
+    SSD_TRY(check_sizes(m, n));
+    MatrixRanges ra, rb;
+    SSD_TRY(matrix_ranges(a, m, k, &ra));
+    SSD_TRY(matrix_ranges(b, n, k, &rb));
+    const size_t e = elem(out_dtype);
+    SSD_TRY(check_all({ra.values, ra.scales, rb.values, rb.scales}, {{out, (size_t)m * n * e, e, true}}));
+    return product(inner(a, m, k), inner(b, n, k), out, m, n, k, out_dtype, (cudaStream_t)stream);
+}
+
+size_t ssd_projection_workspace_size(int64_t tokens, int64_t inputs)
+{
+    return check_sizes(tokens, inputs) == SSD_OK ? Quantised(tokens, inputs).bytes : 0;
+}
+
+ssd_status_t ssd_projection(const void *x, int64_t row, ssd_block_matrix_t weight, void *y, void *x_t, int64_t row_xt,
+                            float *x_t_scale, int64_t x_t_scale_ld, int64_t tokens, int64_t inputs, int64_t outputs,
+                            ssd_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!known(dtype) || (tokens > 1 && row < inputs) || (!x_t && x_t_scale))
+        return SSD_ERR_INVALID_ARG;
+    SSD_TRY(check_sizes(tokens, inputs));
+    SSD_TRY(check_sizes(outputs, inputs));
+    SSD_TRY(check_sizes(tokens, outputs));
+    if (row > (1LL << 39) || row_xt > (1LL << 39) || x_t_scale_ld > (1LL << 39))
+        return SSD_ERR_UNSUPPORTED;
+    const int64_t tb = blocks_of(tokens);
+    if (x_t && ((inputs > 1 && row_xt < tokens) || (tb > 1 && x_t_scale_ld < inputs)))
+        return SSD_ERR_INVALID_ARG;
+    if (x_t && inputs > 1 && row_xt % 16 != 0)
+        return SSD_ERR_ALIGNMENT;
+    MatrixRanges w;
+    SSD_TRY(matrix_ranges(weight, outputs, inputs, &w));
+    const size_t e = elem(dtype), need = ssd_projection_workspace_size(tokens, inputs);
+    const bool any = tokens > 0 && inputs > 0;
+    SSD_TRY(check_all({{x, inputs > 0 ? strided(tokens, row, inputs, e) : 0, e, true}, w.values, w.scales},
+                      {{y, (size_t)tokens * outputs * e, e, true},
+                       {x_t, any && x_t ? strided(inputs, row_xt, tokens, 1) : 0, 16, false},
+                       {x_t_scale, any && x_t ? strided(tb, x_t_scale_ld, inputs, 4) : 0, 4, x_t != nullptr},
+                       {workspace, need, 1, false}}));
+    SSD_TRY(check_ws(workspace, workspace_bytes, need));
+    cudaStream_t st = (cudaStream_t)stream;
+    const Quantised xq(tokens, inputs);
+    if (any) {
+        const QuantGeom g{tokens, inputs, row, xq.row, row_xt, xq.ld, x_t_scale_ld, false, false};
+        SSD_TRY(cuda_status(launch_block_quantize(x, xq.q(workspace), xq.scale(workspace), x_t, x_t_scale, g,
+                                                  dtype == SSD_BF16, st)));
+    }
+    return product(xq.matrix(workspace), inner(weight, outputs, inputs), y, tokens, outputs, inputs, dtype, st);
+}
+
+size_t ssd_projection_bwd_workspace_size(int64_t tokens, int64_t outputs, int want_dx, int want_dweight)
+{
+    if (check_sizes(tokens, outputs) != SSD_OK)
+        return 0;
+    return (want_dx ? Quantised(tokens, outputs).bytes : 0) + (want_dweight ? Quantised(outputs, tokens).bytes : 0);
+}
+
+ssd_status_t ssd_projection_bwd(const void *dy, int64_t row_dy, ssd_block_matrix_t weight_t, ssd_block_matrix_t x_t,
+                                void *dx, float *dweight, int64_t tokens, int64_t inputs, int64_t outputs,
+                                ssd_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!known(dtype) || (tokens > 1 && row_dy < outputs))
+        return SSD_ERR_INVALID_ARG;
+    SSD_TRY(check_sizes(tokens, inputs));
+    SSD_TRY(check_sizes(inputs, outputs));
+    SSD_TRY(check_sizes(tokens, outputs));
+    if (row_dy > (1LL << 39))
+        return SSD_ERR_UNSUPPORTED;
+    const Range none{nullptr, 0, 1, false};
+    MatrixRanges w{none, none}, x{none, none};
+    if (dx)
+        SSD_TRY(matrix_ranges(weight_t, inputs, outputs, &w));
+    if (dweight)
+        SSD_TRY(matrix_ranges(x_t, inputs, tokens, &x));
+    const size_t e = elem(dtype), need = ssd_projection_bwd_workspace_size(tokens, outputs, dx != nullptr, dweight != nullptr);
+    SSD_TRY(check_all({{dy, outputs > 0 ? strided(tokens, row_dy, outputs, e) : 0, e, dx || dweight}, w.values, w.scales,
+                       x.values, x.scales},
+                      {{dx, (size_t)tokens * inputs * e, e, false},
+                       {dweight, (size_t)outputs * inputs * 4, 4, false},
+                       {workspace, need, 1, false}}));
+    SSD_TRY(check_ws(workspace, workspace_bytes, need));
+    cudaStream_t st = (cudaStream_t)stream;
+    const Quantised q(tokens, outputs), qt(outputs, tokens);
+    void *at = workspace, *at_t = dx ? static_cast<char *>(workspace) + q.bytes : workspace;
+    if (tokens > 0 && outputs > 0 && (dx || dweight)) {
+        const QuantGeom g{tokens, outputs, row_dy, q.row, qt.row, q.ld, qt.ld, false, false};
+        SSD_TRY(cuda_status(launch_block_quantize(dy, dx ? q.q(at) : nullptr, dx ? q.scale(at) : nullptr,
+                                                  dweight ? qt.q(at_t) : nullptr, dweight ? qt.scale(at_t) : nullptr, g,
+                                                  dtype == SSD_BF16, st)));
+    }
+    if (dx)
+        SSD_TRY(product(q.matrix(at), inner(weight_t, inputs, outputs), dx, tokens, inputs, outputs, dtype, st));
+    if (dweight)
+        SSD_TRY(product(qt.matrix(at_t), inner(x_t, inputs, tokens), dweight, outputs, inputs, tokens, SSD_F32, st));
+    return SSD_OK;
+}
+
+ssd_status_t ssd_adamw_step(const ssd_adamw_tensor_t *tensors, int64_t count, ssd_adamw_t args, int state_bits,
+                            ssd_dtype_t p_dtype, ssd_dtype_t g_dtype, void *stream)
+{
+    if (count < 0 || (count > 0 && !tensors) || !known(p_dtype) || !known(g_dtype) ||
+        (state_bits != 8 && state_bits != 32))
+        return SSD_ERR_INVALID_ARG;
+    if (!(args.beta1 >= 0 && args.beta1 < 1) || !(args.beta2 >= 0 && args.beta2 < 1) || !(args.eps >= 0) ||
+        !(args.weight_decay >= 0) || (!args.lr_device && !(args.lr >= 0)) || (!args.step_device && args.step < 1))
+        return SSD_ERR_INVALID_ARG;
+    const bool s8 = state_bits == 8;
+    const size_t ep = elem(p_dtype), eg = elem(g_dtype), es = s8 ? 1 : 4;
+    if (reinterpret_cast<uintptr_t>(args.lr_device) % 4 || reinterpret_cast<uintptr_t>(args.step_device) % 8 ||
+        reinterpret_cast<uintptr_t>(args.grad_scale_device) % 4)
+        return SSD_ERR_ALIGNMENT;
+    // every buffer present and aligned, and none that is written overlaps another
+    struct Span {
+        uintptr_t at, end;
+        bool written;
+    };
+    std::vector<Span> spans;
+    try {
+        spans.reserve((size_t)count * 6 + 3);
+    } catch (const std::bad_alloc &) {
+        return SSD_ERR_UNSUPPORTED;
+    }
+    auto add = [&](const void *p, size_t bytes, size_t align, bool written) {
+        SSD_TRY(check_range({p, bytes, align, true}));
+        if (bytes)
+            spans.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, written});
+        return SSD_OK;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const ssd_adamw_tensor_t &t = tensors[i];
+        if (t.n < 0)
+            return SSD_ERR_INVALID_ARG;
+        if (t.n > (1LL << 40))
+            return SSD_ERR_UNSUPPORTED;
+        const size_t n = (size_t)t.n, blocks = (n + 255) / 256;
+        SSD_TRY(add(t.p, n * ep, ep, true));
+        SSD_TRY(add(t.g, n * eg, eg, false));
+        SSD_TRY(add(t.m, n * es, es, true));
+        SSD_TRY(add(t.v, n * es, es, true));
+        if (s8) {
+            SSD_TRY(add(t.m_scale, blocks * 4, 4, true));
+            SSD_TRY(add(t.v_scale, blocks * 4, 4, true));
+        }
+    }
+    if (args.lr_device)
+        add(args.lr_device, 4, 4, false);
+    if (args.step_device)
+        add(args.step_device, 8, 8, false);
+    if (args.grad_scale_device)
+        add(args.grad_scale_device, 4, 4, false);
+    std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.at < b.at; });
+    uintptr_t any_end = 0, written_end = 0;  // of the spans before this one
+    for (const Span &s : spans) {
+        if (s.at < written_end || (s.written && s.at < any_end))
+            return SSD_ERR_INVALID_ARG;
+        any_end = std::max(any_end, s.end);
+        if (s.written)
+            written_end = std::max(written_end, s.end);
+    }
+    return cuda_status(launch_adamw(tensors, count, args, s8, p_dtype == SSD_BF16, g_dtype == SSD_BF16,
+                                    (cudaStream_t)stream));
+}
+
+}  // extern "C"

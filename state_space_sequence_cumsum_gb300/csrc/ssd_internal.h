@@ -43,6 +43,8 @@ cudaError_t launch_chunk_out_simt(const void *x, const void *Bm, const void *Cm,
 // TMA tensor maps (bf16, 128-byte swizzle, zero fill out of bounds).
 bool make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                     const uint64_t *strides_bytes, const uint32_t *box);
+bool make_tmap_bytes(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                     uint32_t box_rows);
 bool make_tmap_f32_rows(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                         uint32_t box_cols, uint32_t box_rows);
 bool make_tmap_tokens_heads(CUtensorMap *map, const void *base, const Geom &g);
@@ -221,5 +223,32 @@ cudaError_t launch_block_norm_bwd(const void *y, const void *r, const float *wei
                                   void *dresidual, float *dweight, float *dpost_weight, float *dgate,
                                   float *workspace, const NormGeom &g, bool bf16, bool res_bf16,
                                   cudaStream_t st);
+
+// 8-bit matrices with a scale for each block of 128 (k_block_quantize.cu,
+// k_block_matmul.cu): rows `row` bytes apart; the scale of row r (tile: of rows
+// 128 r..) and column block j at scale[r * scale_row + j * scale_block].
+struct BlockMatrix {
+    const void *q;
+    const float *scale;
+    int64_t row, scale_row, scale_block;
+    bool tile, e5m2;
+};
+cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void *out, int64_t m, int64_t n, int64_t k,
+                                bool bf16, cudaStream_t st);
+
+// What a quantising call writes: x [rows, cols] and / or its transpose (either
+// q null: not wanted).
+struct QuantGeom {
+    int64_t rows, cols, row;        // of x
+    int64_t row_q, row_qt;          // bytes
+    int64_t scale_ld, scale_t_ld;   // between the scales of two column blocks
+    bool tile, e5m2;
+};
+cudaError_t launch_block_quantize(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g,
+                                  bool bf16, cudaStream_t st);
+
+// An optimiser's step (k_adamw.cu).
+cudaError_t launch_adamw(const ssd_adamw_tensor_t *tensors, int64_t count, const ssd_adamw_t &args, bool states8,
+                         bool p_bf16, bool g_bf16, cudaStream_t st);
 
 }  // namespace ssd

@@ -64,6 +64,18 @@ bool make_tmap_f32_rows(CUtensorMap *map, const void *base, uint64_t cols, uint6
                   CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
+// 8-bit matrix [rows, cols], rows `pitch` bytes apart; box of 128 columns by
+// box_rows rows.
+bool make_tmap_bytes(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                     uint32_t box_rows)
+{
+    const uint64_t dims[2] = {cols, rows};
+    const uint64_t st[1] = {pitch};
+    const uint32_t box[2] = {128, box_rows};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, 2, dims, st, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 // x, y [B, L, H, P] viewed as 4-D {P, H, L, B}; box {64, 1, 128, 1}.
 bool make_tmap_tokens_heads(CUtensorMap *map, const void *base, const Geom &g)
 {

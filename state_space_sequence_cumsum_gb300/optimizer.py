@@ -1,0 +1,89 @@
+"""The optimiser's step (``ssd_adamw_step`` of ``include/ssd.h``) and an AdamW
+built on it."""
+from __future__ import annotations
+
+import torch
+
+from .layer import _call
+
+__all__ = ["ssd_adamw_step", "AdamW"]
+
+STATE_BLOCK = 256  # elements that share a scale of an 8-bit state
+
+
+def ssd_adamw_step(params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, m_scales=None,
+                   v_scales=None, grad_scale=None, stream=None):
+    """One AdamW step over lists of tensors in one launch, in place: params (f32
+    or bf16), grads (f32 or bf16), and the averages m of the gradients and v of
+    their squares, f32 and of the params' shapes.  With m_scales and v_scales
+    (f32, one for each 256 consecutive elements) the states are float8_e4m3fn
+    times those scales, and v holds the square's root.  step counts from 1.  The
+    gradients are multiplied by grad_scale first (None: 1), as for clipping.
+    step (int64), lr and grad_scale (f32) may be one-element CUDA tensors, read
+    when the kernel runs: for a call captured into a graph."""
+    args = (params, grads, m, v, m_scales, v_scales, step, lr, betas[0], betas[1], eps, weight_decay, grad_scale)
+    _call("adamw_step", stream, *args)
+    if stream is not None:
+        for tensors in args[:6]:
+            for t in tensors or ():
+                t.record_stream(stream)
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW whose step is one launch for each group and pair of types.
+    state_bits 8 keeps both averages in 8 bits (1/4 of their memory); parameters
+    and gradients are f32 or bf16 on the GPU, contiguous."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32):
+        if not (lr >= 0 and eps >= 0 and weight_decay >= 0 and all(0 <= b < 1 for b in betas)):
+            raise ValueError("lr, eps and weight_decay must not be negative, betas in [0, 1)")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
+
+    def _new_state(self, p, bits):
+        def zeros(dtype, shape=None):
+            return torch.zeros(p.shape if shape is None else shape, dtype=dtype, device=p.device)
+        if bits == 32:
+            return {"step": 0, "m": zeros(torch.float32), "v": zeros(torch.float32)}
+        blocks = (-(-p.numel() // STATE_BLOCK),)
+        return {"step": 0, "m": zeros(torch.uint8).view(torch.float8_e4m3fn),
+                "v": zeros(torch.uint8).view(torch.float8_e4m3fn), "m_scale": zeros(torch.float32, blocks),
+                "v_scale": zeros(torch.float32, blocks)}
+
+    def load_state_dict(self, state_dict):
+        """As torch's, but the states keep the types that they were saved with
+        (torch would give them their parameter's)."""
+        super().load_state_dict(state_dict)
+        saved = (i for group in state_dict["param_groups"] for i in group["params"])
+        for i, p in zip(saved, (p for group in self.param_groups for p in group["params"])):
+            for k, v in state_dict["state"].get(i, {}).items():
+                if isinstance(v, torch.Tensor):
+                    self.state[p][k] = v.to(p.device, copy=True)
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        """grad_scale: a factor of all gradients, a number or a CUDA scalar."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            calls = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                s = self.state[p]
+                if not s:
+                    s.update(self._new_state(p, group["state_bits"]))
+                s["step"] += 1
+                calls.setdefault((p.device, p.dtype, p.grad.dtype, s["step"]), []).append((p, p.grad, s))
+            for (_, _, _, step), items in calls.items():
+                states = [s for _, _, s in items]
+                scales = {}
+                if group["state_bits"] == 8:
+                    scales = {"m_scales": [s["m_scale"] for s in states], "v_scales": [s["v_scale"] for s in states]}
+                ssd_adamw_step([p for p, _, _ in items], [g for _, g, _ in items], [s["m"] for s in states],
+                               [s["v"] for s in states], step, group["lr"], group["betas"], group["eps"],
+                               group["weight_decay"], grad_scale=grad_scale, **scales)
+        return loss

@@ -13,11 +13,25 @@
 // 128 rows are rows of `a` or, with few tokens, of the weights (kSwap: the
 // output is then written transposed), its BN columns rows of the other matrix.
 //
-// One CTA: warps 0..4 WG-1 add (thread = MMA row, CW columns), one warp loads,
-// one issues MMAs.  BN 256 walks its tiles persistently, so the epilogue of one
-// tile runs under the MMAs of the next.  The others take one tile, or with few
-// tiles a part of its blocks: the CTAs of a cluster then add their partial
-// sums through distributed shared memory, in the order of the parts.
+// Warps of a CTA: 4 WG that add (thread = MMA row, CW columns), then one that
+// loads tiles, one (a pair: two) that issues MMAs, one that loads scales some
+// blocks ahead (without a pair: the tiles' loader).
+//   BN 256: two CTAs take a tile of 256 x 256 with cta_group::2 MMAs and walk
+// their tiles persistently; the output leaves by TMA while the next tile runs.
+// What bounds it: a block's MMAs take 512 clocks, and in the same time its 256
+// columns have to come out of TMEM and be added, 128 of them by each thread.
+// The threads that add are the slower side (some 750 clocks a block: two warps a
+// scheduler, the rest of the register file holds their sums), so their loop has
+// one load from TMEM in flight under the products of the one before and asks for
+// the next block's barriers early.  A block is two MMAs of 128 columns, each with
+// two TMEM buffers, barriers and an issuing warp of its own: one of 256 leaves
+// TMEM full for longer (measured 420 us against 345 at 16384 x 10576 x 2560).
+//   The others take one tile, or with few tiles a part of its blocks: the CTAs
+// of a cluster then add their partial sums through distributed shared memory, in
+// the order of the parts.
+//   16384 x 10576 x 2560, a scale for each 128 x 128 of b: 345 us, 2570 TFLOP/s
+// (1.34 of the measured bf16 rate); with a scale for each row's block on both
+// sides 535 us, bound by one more product per sum.
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,18 +45,26 @@ using namespace tc;
 constexpr int kRows = 128;                  // MMA rows of a tile
 constexpr uint32_t kABytes = kRows * 128;   // one block of them
 constexpr int kMostSplits = 8;              // CTAs of a cluster (portable limit)
+constexpr int kScales = 8;                  // blocks whose scales are in shared memory
 
 template <int BN> struct Tile {
+    static constexpr bool kPair = BN == 256;      // two CTAs on a tile of 256 x 256, persistent
     static constexpr int kWG = BN >= 64 ? 2 : 1;  // warpgroups that share the columns
-    static constexpr int kCW = BN / kWG;          // columns of a thread
+    // a pair's block is two MMAs of 128 columns with buffers and barriers of
+    // their own, so that TMEM is held for less time
+    static constexpr int kHalves = kPair ? 2 : 1;
+    static constexpr int kHN = BN / kHalves;      // columns of an MMA
+    static constexpr int kWGH = kWG / kHalves;    // warpgroups of a half
+    static constexpr int kCW = kHN / kWGH;        // columns of a thread
     static constexpr int kAddWarps = 4 * kWG;
-    static constexpr int kThreads = kAddWarps * 32 + 64;
-    static constexpr bool kPersistent = BN == 256;
-    static constexpr int kCtas = kPersistent ? 1 : 2;  // on an SM
-    static constexpr int kBuffers = BN >= 128 ? 2 : 4; // in TMEM
-    static constexpr uint32_t kStageBytes = kABytes + BN * 128;
-    static constexpr int kStages = BN == 256 ? 3 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
-    static constexpr uint32_t kStaging = kPersistent ? kAddWarps * 4096 : 0;  // of the output
+    static constexpr int kThreads = kAddWarps * 32 + (kPair ? 128 : 64);
+    static constexpr int kCtas = kPair ? 1 : 2;   // on an SM
+    static constexpr int kBuffers = BN >= 128 ? 2 : 4;  // in TMEM, of each half
+    static constexpr int kTileRows = kPair ? 2 * kRows : kRows;
+    static constexpr int kBRows = kPair ? BN / 2 : BN;  // of B in one CTA
+    static constexpr uint32_t kStageBytes = kABytes + kBRows * 128;
+    static constexpr int kStages = kPair ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr uint32_t kStaging = kPair ? kAddWarps * 8192 : 0;  // of the output
     static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024;
 };
 
@@ -59,20 +81,49 @@ struct Params {
     unsigned *status;
 };
 
-__device__ __forceinline__ void add_barrier(int threads)
+__device__ __forceinline__ bool ask(uint32_t bar, uint32_t parity)
 {
-    asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
-__device__ __forceinline__ void cluster_sync()
+// A bounded wait (2 s) whose clock starts only after 4096 polls: reading the
+// timer at every miss would cost the waiting roles more than the wait.  On
+// running out it records the timeout.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned *status)
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (ask(bar, parity))
+            return true;
+        if ((i & 4095u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 && now - t0 > 2000000000ull) {
+                atomicOr(status, 1u);
+                return false;
+            }
+            t0 = t0 ? t0 : now;
+        }
+    }
 }
-// A shared-memory address of this CTA as one of CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank)
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, unsigned *status)
 {
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
+    return wait_for(smem_u32(bar), parity, status);
+}
+// Asynchronous copy of one value (zero where there is none) ...
+__device__ __forceinline__ void copy_scale(float *dst, const float *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0)
+                 : "memory");
+}
+// ... and an arrival once this thread's copies have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ float4 load_cluster(uint32_t addr)
 {
@@ -139,45 +190,61 @@ __device__ __forceinline__ void copy_rows(const Params &p, const unsigned char *
 
 template <int BN, bool kSwap, bool kRowsB>
 __global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
-block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Params p)
+block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                    const __grid_constant__ CUtensorMap to, const Params p)
 {
     using T = Tile<BN>;
-    constexpr int ST = T::kStages, NB = T::kBuffers, CW = T::kCW;
+    constexpr int ST = T::kStages, NB = T::kBuffers, H = T::kHalves, HN = T::kHN, CW = T::kCW;
+    static_assert(HN <= 128, "a half's columns share a scale");
+    constexpr int LW = T::kPair ? 32 : 16;  // columns of a load from TMEM
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    unsigned char *staging = T::kPersistent ? smem + ST * T::kStageBytes : smem;
-    __shared__ uint64_t full[ST], empty[ST], done[NB], freed[NB];
+    unsigned char *staging = T::kPair ? smem + ST * T::kStageBytes : smem;
+    __shared__ uint64_t full[ST], empty[ST], done[H][NB], freed[H][NB];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float sb_smem[2][kRowsB ? BN : 4];
+    // scales of kScales blocks: of the rows, and of the columns (without kRowsB of each 128 columns)
+    __shared__ uint64_t scales_full[kScales], scales_empty[kScales];
+    __shared__ __align__(16) float sa_smem[kScales][kRows], sb_smem[kScales][kRowsB ? BN : 2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], H);
         }
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(&done[i], 1);
-            mbar_init(&freed[i], T::kAddWarps);
+        for (int i = 0; i < H * NB; ++i) {
+            mbar_init(&done[0][i], 1);
+            mbar_init(&freed[0][i], 4 * T::kWGH * (T::kPair ? 2 : 1));
+        }
+        for (int i = 0; i < kScales; ++i) {
+            mbar_init(&scales_full[i], 32);
+            mbar_init(&scales_empty[i], T::kAddWarps);
         }
         fence_barrier_init();
     }
     if (warp == T::kAddWarps + 1) {
-        tmem_alloc(&tmem_slot, NB * BN);
-        tmem_relinquish();
+        if (T::kPair) {
+            tmem_alloc_pair(&tmem_slot, NB * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&tmem_slot, NB * BN);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (T::kPair)
+        cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
     // this CTA's tiles and, in each, its blocks of the summed dimension
-    const int rank = T::kPersistent ? 0 : (int)(blockIdx.x % (unsigned)p.splits);
-    const int first = T::kPersistent ? (int)blockIdx.x : (int)(blockIdx.x / (unsigned)p.splits);
-    const int step = T::kPersistent ? (int)gridDim.x : p.m_tiles * p.n_tiles;
+    const int rank = (int)(blockIdx.x % (unsigned)(T::kPair ? 2 : p.splits));  // in the cluster
+    const int first = (int)(blockIdx.x / (unsigned)(T::kPair ? 2 : p.splits));
+    const int step = T::kPair ? (int)gridDim.x / 2 : p.m_tiles * p.n_tiles;
     const int tiles = p.m_tiles * p.n_tiles;
-    const int kb0 = T::kPersistent ? 0 : (int)((int64_t)p.blocks * rank / p.splits);
-    const int kb1 = T::kPersistent ? p.blocks : (int)((int64_t)p.blocks * (rank + 1) / p.splits);
+    const int kb0 = T::kPair ? 0 : (int)((int64_t)p.blocks * rank / p.splits);
+    const int kb1 = T::kPair ? p.blocks : (int)((int64_t)p.blocks * (rank + 1) / p.splits);
     // tiles in groups of kGroup rows of tiles, column after column: what a wave
     // of CTAs reads of both operands stays in L2
     constexpr int kGroup = 16;
@@ -188,137 +255,203 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         mt = g * kGroup + in % rows;
     };
 
-    if (warp == T::kAddWarps) {
-        // ---------------------------------------------------------- loads
-        if (lane == 0) {
-            prefetch_tmap(&ta);
-            prefetch_tmap(&tb);
+    if (T::kPair && warp >= T::kAddWarps)
+        // registers of these warps to those that add: 256 x 216 + 128 x 56 of the
+        // 384 x 168 that the CTA was launched with
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // one block's tiles into stage s
+    auto load_tiles = [&](int kb, uint32_t s, int mt, int nt) {
+        unsigned char *a = smem + s * T::kStageBytes;
+        if (T::kPair) {  // both CTAs' loads complete on the first one's barrier
+            if (rank == 0)
+                mbar_arrive_expect_tx(&full[s], 2 * T::kStageBytes);
+            const uint32_t bar = in_cta(smem_u32(&full[s]), 0);
+            tma_load_2d_pair(a, &ta, bar, kb * 128, mt * T::kTileRows + rank * kRows);
+#pragma unroll
+            for (int h = 0; h < H; ++h)  // this CTA's half of each MMA's columns
+                tma_load_2d_pair(a + kABytes + h * (HN / 2) * 128, &tb, bar, kb * 128, nt * BN + h * HN + rank * (HN / 2));
+        } else {
+            mbar_arrive_expect_tx(&full[s], T::kStageBytes);
+            tma_load_2d(a, &ta, &full[s], kb * 128, mt * kRows);
+            tma_load_2d(a + kABytes, &tb, &full[s], kb * 128, nt * BN);
+        }
+    };
+    if (T::kPair && warp == T::kAddWarps) {
+        // ------------------------------------------------------------- tiles
+        if (elect_one()) {
             uint32_t it = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 int mt, nt;
                 place(t, mt, nt);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const uint32_t s = it % ST;
-                    if (!mbar_wait(&empty[s], ((it / ST) & 1) ^ 1)) {
-                        atomicOr(p.status, 1u);
-                        ok = false;
-                        break;
-                    }
-                    unsigned char *a = smem + s * T::kStageBytes;
-                    mbar_arrive_expect_tx(&full[s], T::kStageBytes);
-                    tma_load_2d(a, &ta, &full[s], kb * 128, mt * kRows);
-                    tma_load_2d(a + kABytes, &tb, &full[s], kb * 128, nt * BN);
+                    ok = wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status);
+                    if (ok)
+                        load_tiles(kb, s, mt, nt);
                 }
             }
         }
-    } else if (warp == T::kAddWarps + 1) {
-        // ----------------------------------------------------------- MMAs
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += step) {
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % ST, b = it % NB;
-                    if (!mbar_wait(&freed[b], ((it / NB) & 1) ^ 1) || !mbar_wait(&full[s], (it / ST) & 1)) {
-                        atomicOr(p.status, 1u);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(smem + s * T::kStageBytes);
-                    const uint64_t da = desc_k0(a), db = desc_k0(a + kABytes);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f8_ss(tmem + b * BN, desc_k(da, 0, k), desc_k(db, 0, k), p.idesc, k > 0);
-                    mma_commit(&empty[s]);
-                    mma_commit(&done[b]);
-                }
-            }
-        }
-    } else {
-        // ----------------------------------------------- sums and output
-        const int wg = warp >> 2, quarter = warp & 3;
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + wg * CW;
+    } else if (warp == (T::kPair ? T::kAddWarps + 3 : T::kAddWarps)) {
+        // ---------------------------------- scales, and without a pair the tiles
+        const bool issues = !T::kPair && elect_one();
         uint32_t it = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
             int mt, nt;
             place(t, mt, nt);
-            const int64_t row0 = (int64_t)mt * kRows + quarter * 32, row = row0 + lane;
-            const int64_t col0 = (int64_t)nt * BN + wg * CW;
-            const float *sa = p.sa + (row < p.m ? row >> p.sa_shift : 0) * p.sa_row;
-            const float *sb;
-            bool mine = true;
-            if (kRowsB) {  // this thread brings one column's scale
-                const int64_t c = (int64_t)nt * BN + threadIdx.x;
-                mine = threadIdx.x < BN && c < p.n;
-                sb = p.sb + (mine ? c >> p.sb_shift : 0) * p.sb_row;
-            } else {       // its columns lie in one block of 128
-                sb = p.sb + (col0 < p.n ? col0 >> 7 : 0) * p.sb_row;
-            }
-            uint64_t acc[CW / 2];
+            const int64_t row0 = (int64_t)mt * T::kTileRows + (T::kPair ? rank * kRows : 0);
+            const float *sa[kRows / 32], *sb[kRowsB ? BN / 32 : 1];
+            uint32_t in_a = 0, in_b = 0;  // bit j: this lane's j-th scale exists
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i)
-                acc[i] = 0;
-            float fa = 0.f, fb = 0.f;
-            if (kb0 < kb1) {
-                fa = sa[kb0 * p.sa_block];
-                fb = mine ? sb[kb0 * p.sb_block] : 0.f;
+            for (int j = 0; j < kRows / 32; ++j) {
+                const int64_t r = row0 + j * 32 + lane;
+                in_a |= (uint32_t)(r < p.m) << j;
+                sa[j] = p.sa + (r < p.m ? r >> p.sa_shift : 0) * p.sa_row + kb0 * p.sa_block;
+            }
+#pragma unroll
+            for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
+                const int64_t c = (int64_t)nt * BN + (kRowsB ? j * 32 + lane : lane * 128);
+                const bool in = c < p.n && (kRowsB || lane < H);
+                in_b |= (uint32_t)in << j;
+                sb[j] = p.sb + (in ? c >> p.sb_shift : 0) * p.sb_row + kb0 * p.sb_block;
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t b = it % NB;
-                const float wa = fa, wb = fb;
-                if (kb + 1 < kb1) {
-                    fa = sa[(kb + 1) * p.sa_block];
-                    fb = mine ? sb[(kb + 1) * p.sb_block] : 0.f;
-                }
-                if (kRowsB) {
-                    if (threadIdx.x < BN)
-                        sb_smem[it & 1][threadIdx.x] = wb;
-                    add_barrier(T::kAddWarps * 32);
-                }
-                if (ok && !mbar_wait(&done[b], (it / NB) & 1)) {
-                    atomicOr(p.status, 1u);
-                    ok = false;
-                }
+                const uint32_t s = it % ST, z = it % kScales;
+                ok = (T::kPair || wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status)) &&
+                     wait_for(&scales_empty[z], ((it / kScales) & 1) ^ 1, p.status);
                 if (!ok)
-                    continue;
-                tc_fence_after();
-                const uint32_t f = __float_as_uint(kRowsB ? wa : wa * wb);
-                const uint64_t f2 = f2_pack(f, f);
-                uint32_t r[2][32];
-                tmem_ld32(at + b * BN, r[0]);
+                    break;
+                if (issues)
+                    load_tiles(kb, s, mt, nt);
+                __syncwarp();
 #pragma unroll
-                for (int c = 0; c < CW / 32; ++c) {
-                    tmem_ld_wait_on(r[c & 1]);
-                    if (c + 1 < CW / 32) {
-                        tmem_ld32(at + b * BN + (c + 1) * 32, r[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        warp_arrive(&freed[b]);
+                for (int j = 0; j < kRows / 32; ++j) {
+                    copy_scale(&sa_smem[z][j * 32 + lane], sa[j], in_a >> j & 1);
+                    sa[j] += p.sa_block;
+                }
+#pragma unroll
+                for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
+                    if (kRowsB || lane < H)
+                        copy_scale(&sb_smem[z][kRowsB ? j * 32 + lane : lane], sb[j], in_b >> j & 1);
+                    sb[j] += p.sb_block;
+                }
+                copies_arrive(&scales_full[z]);
+            }
+        }
+        cp_async_wait_all();
+    } else if (warp >= T::kAddWarps) {
+        // --------------------------------------------- MMAs: a warp for each half
+        const int h = warp - (T::kAddWarps + 1);
+        if (elect_one() && (!T::kPair || rank == 0)) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = first; ok && t < tiles; t += step) {
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % ST, b = it % NB;
+                    ok = wait_for(&full[s], (it / ST) & 1, p.status) &&
+                         wait_for(&freed[h][b], ((it / NB) & 1) ^ 1, p.status);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + s * T::kStageBytes), d = tmem + b * BN + h * HN;
+                    const uint64_t da = desc_k0(a), db = desc_k0(a + kABytes + h * (HN / 2) * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (T::kPair)
+                            mma_f8_ss_pair(d, desc_k(da, 0, k), desc_k(db, 0, k), p.idesc, k > 0);
+                        else
+                            mma_f8_ss(d, desc_k(da, 0, k), desc_k(db, 0, k), p.idesc, k > 0);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        uint64_t w0 = f2, w1 = f2;
-                        if (kRowsB) {
-                            const ulonglong2 s =
-                                *reinterpret_cast<const ulonglong2 *>(&sb_smem[it & 1][wg * CW + c * 32 + 2 * i]);
-                            w0 = f2_mul(s.x, f2);
-                            w1 = f2_mul(s.y, f2);
-                        }
-                        uint64_t &x = acc[c * 16 + i], &y = acc[c * 16 + i + 1];
-                        x = f2_fma(f2_pack(r[c & 1][2 * i], r[c & 1][2 * i + 1]), w0, x);
-                        y = f2_fma(f2_pack(r[c & 1][2 * i + 2], r[c & 1][2 * i + 3]), w1, y);
+                    if (T::kPair) {
+                        mma_commit_pair(&done[h][b]);
+                        mma_commit_pair(&empty[s]);
+                    } else {
+                        mma_commit(&done[h][b]);
+                        mma_commit(&empty[s]);
                     }
                 }
             }
-            auto value = [&](int c) {
-                uint32_t lo, hi;
-                f2_unpack(acc[c >> 1], lo, hi);
-                return __uint_as_float(c & 1 ? hi : lo);
-            };
-            if (!T::kPersistent && p.splits > 1) {
+        }
+    } else {
+        // ----------------------------------------------- sums and output
+        if (T::kPair)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int wg = warp >> 2, quarter = warp & 3;
+        const int h = wg / T::kWGH, in_tile = wg * CW;  // its half, and its first column in the tile
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + in_tile;
+        // the next block's TMEM buffer and scales, and the phases of their barriers
+        uint32_t b = 0, b_phase = 0, z = 0, z_phase = 0;
+        const uint32_t done_at = smem_u32(&done[h][0]), scales_at = smem_u32(&scales_full[0]);
+        const uint32_t freed_at = T::kPair ? in_cta(smem_u32(&freed[h][0]), 0) : 0;
+        const float *my_sa = &sa_smem[0][quarter * 32 + lane];
+        bool scales_ready = false, done_ready = false;  // as last asked
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+            int mt, nt;
+            place(t, mt, nt);
+            const int64_t row0 = (int64_t)mt * T::kTileRows + (T::kPair ? rank * kRows : 0) + quarter * 32, row = row0 + lane;
+            const int64_t col0 = (int64_t)nt * BN + in_tile;
+            float acc[CW];
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
+                acc[i] = 0.f;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = (scales_ready || wait_for(scales_at + z * 8, z_phase, p.status)) &&
+                     (done_ready || wait_for(done_at + b * 8, b_phase, p.status));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float r[2][LW];
+                tmem_ld_f32(at + b * BN, r[0]);
+                const float wa = my_sa[z * kRows];
+                const float f = kRowsB ? wa : wa * sb_smem[z][h];
+                const float *sbz = &sb_smem[z][kRowsB ? in_tile : 0];
+                const uint32_t z0 = z;
+#pragma unroll
+                for (int c = 0; c < CW / LW; ++c) {
+                    tmem_ld_wait_on(r[c & 1]);
+                    if (c + 1 < CW / LW) {
+                        tmem_ld_f32(at + b * BN + (c + 1) * LW, r[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        if (T::kPair)
+                            warp_arrive_cluster(freed_at + b * 8);
+                        else
+                            warp_arrive(&freed[h][b]);
+                        if (++z == kScales) {
+                            z = 0;
+                            z_phase ^= 1;
+                        }
+                        if (++b == NB) {
+                            b = 0;
+                            b_phase ^= 1;
+                        }
+                        // is the next block there already?  The answer comes under these products.
+                        scales_ready = ask(scales_at + z * 8, z_phase);
+                        done_ready = ask(done_at + b * 8, b_phase);
+                    }
+#pragma unroll
+                    for (int i = 0; i < LW; i += 4) {
+                        float w[4] = {f, f, f, f};
+                        if (kRowsB) {  // sa sb, two at a time
+                            const ulonglong2 sb = *reinterpret_cast<const ulonglong2 *>(sbz + c * LW + i);
+                            const uint64_t f2 = f2_pack(__float_as_uint(f), __float_as_uint(f));
+                            uint32_t v[4];
+                            f2_unpack(f2_mul(sb.x, f2), v[0], v[1]);
+                            f2_unpack(f2_mul(sb.y, f2), v[2], v[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = __uint_as_float(v[j]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[c * LW + i + j] = fmaf(r[c & 1][i + j], w[j], acc[c * LW + i + j]);
+                    }
+                }
+                warp_arrive(&scales_empty[z0]);
+            }
+            if (!T::kPair && p.splits > 1) {
                 // partial sums: rows of BN + 4 (out's rows), or columns of 128 (swapped)
                 float *part = reinterpret_cast<float *>(smem);
                 const int r = quarter * 32 + lane;
@@ -327,10 +460,10 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                     if (kSwap) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            part[(wg * CW + c + j) * kRows + r] = value(c + j);
+                            part[(in_tile + c + j) * kRows + r] = acc[c + j];
                     } else {
-                        *reinterpret_cast<float4 *>(part + r * (BN + 4) + wg * CW + c) =
-                            make_float4(value(c), value(c + 1), value(c + 2), value(c + 3));
+                        *reinterpret_cast<float4 *>(part + r * (BN + 4) + in_tile + c) =
+                            make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
                     }
                 }
             } else if (kSwap) {
@@ -340,46 +473,77 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                         if (col0 + c < p.n) {
                             const int64_t o = (col0 + c) * p.ld + row;
                             if (p.bf16)
-                                static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(value(c));
+                                static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc[c]);
                             else
-                                static_cast<float *>(p.out)[o] = value(c);
+                                static_cast<float *>(p.out)[o] = acc[c];
                         }
                 }
             } else {
-                unsigned char *stage = staging + warp * 4096;
-                if (p.bf16) {
-#pragma unroll
-                    for (int h = 0; h < CW; h += 64) {
-                        constexpr int chunks = (CW < 64 ? CW : 64) / 8;
-#pragma unroll
-                        for (int j = 0; j < chunks; ++j) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                v[q] = pack_bf16x2(value(h + j * 8 + 2 * q), value(h + j * 8 + 2 * q + 1));
-                            *reinterpret_cast<uint4 *>(stage + sw128_offset(lane, j)) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                // through shared memory in pieces of 32 rows x 128 bytes: by TMA from
+                // two of them in turn, or by the warp where out's rows are not aligned
+                unsigned char *stage = staging + warp * (T::kPair ? 8192 : 4096);
+                const bool bulk = T::kPair && p.vec;
+                auto piece = [&](int i, int c, auto fill, auto copy) {
+                    unsigned char *st = stage + (T::kPair ? (i & 1) * 4096 : 0);
+                    if (bulk) {
+                        if (lane == 0)
+                            bulk_wait_read_but_one();
                         __syncwarp();
-                        if (CW >= 64 || (lane & 7) < chunks)
-                            copy_rows<__nv_bfloat16>(p, stage, row0, col0 + h, lane);
+                        fill(st);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row0 < p.m && col0 + c < p.n)
+                                tma_store_2d(&to, st, (int)(col0 + c), (int)row0);
+                            bulk_commit();
+                        }
+                    } else {
+                        fill(st);
+                        __syncwarp();
+                        copy(st);
                         __syncwarp();
                     }
+                };
+                if (p.bf16) {
+                    constexpr int per = CW < 64 ? CW : 64;
+#pragma unroll
+                    for (int c = 0; c < CW; c += per)
+                        piece(
+                            c / per, c,
+                            [&](unsigned char *st) {
+#pragma unroll
+                                for (int j = 0; j < per / 8; ++j) {
+                                    const float *v = acc + c + j * 8;
+                                    *reinterpret_cast<uint4 *>(st + sw128_offset(lane, j)) =
+                                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                                   pack_bf16x2(v[6], v[7]));
+                                }
+                            },
+                            [&](unsigned char *st) {
+                                if ((lane & 7) < per / 8)
+                                    copy_rows<__nv_bfloat16>(p, st, row0, col0 + c, lane);
+                            });
                 } else {
 #pragma unroll
-                    for (int h = 0; h < CW; h += 32) {
+                    for (int c = 0; c < CW; c += 32)
+                        piece(
+                            c / 32, c,
+                            [&](unsigned char *st) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4 *>(stage + sw128_offset(lane, j)) =
-                                make_float4(value(h + j * 4), value(h + j * 4 + 1), value(h + j * 4 + 2), value(h + j * 4 + 3));
-                        __syncwarp();
-                        copy_rows<float>(p, stage, row0, col0 + h, lane);
-                        __syncwarp();
-                    }
+                                for (int j = 0; j < 8; ++j) {
+                                    const float *v = acc + c + j * 4;
+                                    *reinterpret_cast<float4 *>(st + sw128_offset(lane, j)) =
+                                        make_float4(v[0], v[1], v[2], v[3]);
+                                }
+                            },
+                            [&](unsigned char *st) { copy_rows<float>(p, st, row0, col0 + c, lane); });
                 }
             }
         }
+        if (lane == 0)
+            bulk_wait_all();
     }
-    if (!T::kPersistent && p.splits > 1) {
+    if (!T::kPair && p.splits > 1) {
         // the cluster's partial sums, each CTA every splits-th group of four
         __syncwarp();
         cluster_sync();
@@ -421,12 +585,19 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == T::kAddWarps + 1)
-        tmem_dealloc(tmem, NB * BN);
+    if (T::kPair)
+        cluster_sync();  // the pair's MMAs and arrivals reach into both CTAs
+    if (warp == T::kAddWarps + 1) {
+        if (T::kPair)
+            tmem_dealloc_pair(tmem, NB * BN);
+        else
+            tmem_dealloc(tmem, NB * BN);
+    }
 }
 
 template <int BN, bool kSwap, bool kRowsB>
-cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Params &p, int sms, cudaStream_t st)
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, const Params &p, int sms,
+                   cudaStream_t st)
 {
     using T = Tile<BN>;
     static SmemGrant granted;
@@ -435,17 +606,18 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Params &p
         return e;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(T::kPersistent ? std::min<int64_t>(tiles, sms) : tiles * p.splits));
+    const int cluster = T::kPair ? 2 : p.splits;
+    cfg.gridDim = dim3((unsigned)((T::kPair ? std::min<int64_t>(tiles, sms / 2) : tiles) * cluster));
     cfg.blockDim = dim3(T::kThreads);
     cfg.dynamicSmemBytes = T::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)p.splits;
+    attr.val.clusterDim.x = (unsigned)cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = p.splits > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, p);
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p);
     if (e == cudaSuccess)
         note_launch(1);
     return e;
@@ -465,10 +637,10 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
     const BlockMatrix &ra = swap ? b : a, &rb = swap ? a : b;
     const int64_t rm = swap ? n : m, rn = swap ? m : n;
     int bn = rn <= 32 ? 32 : rn <= 64 ? 64 : 128;
-    if (!swap && rn > 128 && up(rm, kRows) * up(rn, 256) * 4 >= 3 * sms)
+    if (!swap && rn > 128 && up(rm, 256) * up(rn, 256) * 8 >= 3 * sms)
         bn = 256;
     Params p = {};
-    p.m_tiles = (int)up(rm, kRows);
+    p.m_tiles = (int)up(rm, bn == 256 ? 2 * kRows : kRows);
     p.n_tiles = (int)up(rn, bn);
     p.blocks = blocks;
     p.splits = 1;
@@ -488,19 +660,21 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
     p.ld = n;
     p.m = rm;
     p.n = rn;
-    p.idesc = idesc_f8(kRows, bn, ra.e5m2 ? 1 : 0, rb.e5m2 ? 1 : 0);
+    p.idesc = idesc_f8(bn == 256 ? 2 * kRows : kRows, std::min(bn, 128), ra.e5m2 ? 1 : 0, rb.e5m2 ? 1 : 0);
     p.bf16 = bf16;
     const int64_t vec = bf16 ? 8 : 4;
     p.vec = n % vec == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
     p.status = device_status_word();
     if (!p.status)
         return cudaErrorUnknown;
-    CUtensorMap ta, tb;
-    if (!make_tmap_bytes(&ta, ra.q, (uint64_t)k, (uint64_t)rm, (uint64_t)ra.row, kRows) ||
-        !make_tmap_bytes(&tb, rb.q, (uint64_t)k, (uint64_t)rn, (uint64_t)rb.row, (uint32_t)bn))
+    CUtensorMap ta, tb, to = {};
+    if (bn == 256 && p.vec && !make_tmap_out(&to, out, (uint64_t)n, (uint64_t)m, bf16))
         return cudaErrorInvalidValue;
-#define SSD_BLOCK_MATMUL(BN, SWAP)                                                            \
-    return rb.tile ? launch<BN, SWAP, false>(ta, tb, p, sms, st) : launch<BN, SWAP, true>(ta, tb, p, sms, st)
+    if (!make_tmap_bytes(&ta, ra.q, (uint64_t)k, (uint64_t)rm, (uint64_t)ra.row, kRows) ||
+        !make_tmap_bytes(&tb, rb.q, (uint64_t)k, (uint64_t)rn, (uint64_t)rb.row, (uint32_t)(bn == 256 ? 64 : bn)))
+        return cudaErrorInvalidValue;
+#define SSD_BLOCK_MATMUL(BN, SWAP) \
+    return rb.tile ? launch<BN, SWAP, false>(ta, tb, to, p, sms, st) : launch<BN, SWAP, true>(ta, tb, to, p, sms, st)
     if (swap) {
         if (bn == 32)
             SSD_BLOCK_MATMUL(32, true);

@@ -45,6 +45,7 @@ bool make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const uint64_t
                     const uint64_t *strides_bytes, const uint32_t *box);
 bool make_tmap_bytes(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t pitch,
                      uint32_t box_rows);
+bool make_tmap_out(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, bool bf16);
 bool make_tmap_f32_rows(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows,
                         uint32_t box_cols, uint32_t box_rows);
 bool make_tmap_tokens_heads(CUtensorMap *map, const void *base, const Geom &g);

@@ -76,6 +76,15 @@ bool make_tmap_bytes(CUtensorMap *map, const void *base, uint64_t cols, uint64_t
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// A product's output [rows, cols], contiguous: boxes of 32 rows of 128 bytes.
+bool make_tmap_out(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, bool bf16)
+{
+    const uint64_t size = bf16 ? 2 : 4, dims[2] = {cols, rows}, st[1] = {cols * size};
+    const uint32_t box[2] = {(uint32_t)(128 / size), 32};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, 2, dims, st, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
 // x, y [B, L, H, P] viewed as 4-D {P, H, L, B}; box {64, 1, 128, 1}.
 bool make_tmap_tokens_heads(CUtensorMap *map, const void *base, const Geom &g)
 {

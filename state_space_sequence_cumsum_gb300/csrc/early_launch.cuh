@@ -1,0 +1,21 @@
+// Kernels that are set up under the end of the one before on their stream
+// (programmatic launch): what they do before wait_for_kernel_before touches no
+// memory but their own, and everything that they read or write follows it.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace ssd {
+
+inline cudaLaunchAttribute early_launch()
+{
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+// The kernel before has ended and its writes are visible to this thread.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel after may be set up from here on.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace ssd

@@ -28,15 +28,21 @@
 // TMEM full for longer (measured 420 us against 345 at 16384 x 10576 x 2560).
 //   The others take one tile, or with few tiles a part of its blocks: the CTAs
 // of a cluster then add their partial sums through distributed shared memory, in
-// the order of the parts.
+// the order of the parts.  A projection of few tokens (kFused) quantises them on
+// the way in: four warps read x and write the MMA's columns and their scales,
+// under the latency of the weights' loads, so it is one launch.
 //   16384 x 10576 x 2560, a scale for each 128 x 128 of b: 345 us, 2570 TFLOP/s
 // (1.34 of the measured bf16 rate); with a scale for each row's block on both
 // sides 535 us, bound by one more product per sum.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
+#include "early_launch.cuh"
+#include "quant.cuh"
 #include "ssd_internal.h"
 #include "tc05.cuh"
+#include "vec.cuh"
 
 namespace ssd {
 namespace {
@@ -47,7 +53,8 @@ constexpr uint32_t kABytes = kRows * 128;   // one block of them
 constexpr int kMostSplits = 8;              // CTAs of a cluster (portable limit)
 constexpr int kScales = 8;                  // blocks whose scales are in shared memory
 
-template <int BN> struct Tile {
+// kFused: the MMA's columns are tokens that are quantised here.
+template <int BN, bool kFused = false> struct Tile {
     static constexpr bool kPair = BN == 256;      // two CTAs on a tile of 256 x 256, persistent
     static constexpr int kWG = BN >= 64 ? 2 : 1;  // warpgroups that share the columns
     // a pair's block is two MMAs of 128 columns with buffers and barriers of
@@ -57,13 +64,16 @@ template <int BN> struct Tile {
     static constexpr int kWGH = kWG / kHalves;    // warpgroups of a half
     static constexpr int kCW = kHN / kWGH;        // columns of a thread
     static constexpr int kAddWarps = 4 * kWG;
-    static constexpr int kThreads = kAddWarps * 32 + (kPair ? 128 : 64);
-    static constexpr int kCtas = kPair ? 1 : 2;   // on an SM
+    static constexpr int kQuantWarps = kFused ? 4 : 0;
+    static constexpr int kThreads = (kAddWarps + (kPair ? 4 : 2) + kQuantWarps) * 32;
+    // on an SM; where a CTA has few blocks, as many stages as that hold them all
+    // early beat a second CTA
+    static constexpr int kCtas = BN >= 128 ? 1 : 2;
     static constexpr int kBuffers = BN >= 128 ? 2 : 4;  // in TMEM, of each half
     static constexpr int kTileRows = kPair ? 2 * kRows : kRows;
     static constexpr int kBRows = kPair ? BN / 2 : BN;  // of B in one CTA
     static constexpr uint32_t kStageBytes = kABytes + kBRows * 128;
-    static constexpr int kStages = kPair ? 4 : BN == 128 ? 3 : BN == 64 ? 4 : 5;
+    static constexpr int kStages = kPair ? 4 : BN == 128 ? 6 : BN == 64 ? 4 : 5;
     static constexpr uint32_t kStaging = kPair ? kAddWarps * 8192 : 0;  // of the output
     static constexpr uint32_t kSmem = kStages * kStageBytes + kStaging + 1024;
 };
@@ -79,26 +89,20 @@ struct Params {
     uint32_t idesc;
     bool bf16, vec;                              // vec: out takes 16-byte accesses
     unsigned *status;
+    // kFused: the tokens [n, k], rows x_row apart; x_vec: four values at a time
+    const void *x;
+    int64_t x_row, k;
+    bool x_vec;
 };
 
-__device__ __forceinline__ bool ask(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 // A bounded wait (2 s) whose clock starts only after 4096 polls: reading the
 // timer at every miss would cost the waiting roles more than the wait.  On
 // running out it records the timeout.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned *status)
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, unsigned *status)
 {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (ask(bar, parity))
+        if (mbar_try_wait(bar, parity))
             return true;
         if ((i & 4095u) == 0) {
             const uint64_t now = globaltimer_ns();
@@ -109,10 +113,6 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned
             t0 = t0 ? t0 : now;
         }
     }
-}
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, unsigned *status)
-{
-    return wait_for(smem_u32(bar), parity, status);
 }
 // Asynchronous copy of one value (zero where there is none) ...
 __device__ __forceinline__ void copy_scale(float *dst, const float *src, bool there)
@@ -188,12 +188,14 @@ __device__ __forceinline__ void copy_rows(const Params &p, const unsigned char *
     }
 }
 
-template <int BN, bool kSwap, bool kRowsB>
-__global__ void __launch_bounds__(Tile<BN>::kThreads, Tile<BN>::kCtas)
+// TX: void, or with kSwap and kRowsB the type of the tokens that are quantised.
+template <int BN, bool kSwap, bool kRowsB, typename TX = void>
+__global__ void __launch_bounds__(Tile<BN, !std::is_void_v<TX>>::kThreads, Tile<BN, !std::is_void_v<TX>>::kCtas)
 block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                     const __grid_constant__ CUtensorMap to, const Params p)
 {
-    using T = Tile<BN>;
+    constexpr bool kFused = !std::is_void_v<TX>;
+    using T = Tile<BN, kFused>;
     constexpr int ST = T::kStages, NB = T::kBuffers, H = T::kHalves, HN = T::kHN, CW = T::kCW;
     static_assert(HN <= 128, "a half's columns share a scale");
     constexpr int LW = T::kPair ? 32 : 16;  // columns of a load from TMEM
@@ -207,37 +209,6 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     __shared__ __align__(16) float sa_smem[kScales][kRows], sb_smem[kScales][kRowsB ? BN : 2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], H);
-        }
-        for (int i = 0; i < H * NB; ++i) {
-            mbar_init(&done[0][i], 1);
-            mbar_init(&freed[0][i], 4 * T::kWGH * (T::kPair ? 2 : 1));
-        }
-        for (int i = 0; i < kScales; ++i) {
-            mbar_init(&scales_full[i], 32);
-            mbar_init(&scales_empty[i], T::kAddWarps);
-        }
-        fence_barrier_init();
-    }
-    if (warp == T::kAddWarps + 1) {
-        if (T::kPair) {
-            tmem_alloc_pair(&tmem_slot, NB * BN);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(&tmem_slot, NB * BN);
-            tmem_relinquish();
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (T::kPair)
-        cluster_sync();  // the other CTA's barriers are there
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;
-
     // this CTA's tiles and, in each, its blocks of the summed dimension
     const int rank = (int)(blockIdx.x % (unsigned)(T::kPair ? 2 : p.splits));  // in the cluster
     const int first = (int)(blockIdx.x / (unsigned)(T::kPair ? 2 : p.splits));
@@ -254,11 +225,6 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         nt = in / rows;
         mt = g * kGroup + in % rows;
     };
-
-    if (T::kPair && warp >= T::kAddWarps)
-        // registers of these warps to those that add: 256 x 216 + 128 x 56 of the
-        // 384 x 168 that the CTA was launched with
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // one block's tiles into stage s
     auto load_tiles = [&](int kb, uint32_t s, int mt, int nt) {
         unsigned char *a = smem + s * T::kStageBytes;
@@ -271,14 +237,63 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             for (int h = 0; h < H; ++h)  // this CTA's half of each MMA's columns
                 tma_load_2d_pair(a + kABytes + h * (HN / 2) * 128, &tb, bar, kb * 128, nt * BN + h * HN + rank * (HN / 2));
         } else {
-            mbar_arrive_expect_tx(&full[s], T::kStageBytes);
+            mbar_arrive_expect_tx(&full[s], kFused ? kABytes : T::kStageBytes);
             tma_load_2d(a, &ta, &full[s], kb * 128, mt * kRows);
-            tma_load_2d(a + kABytes, &tb, &full[s], kb * 128, nt * BN);
+            if (!kFused)
+                tma_load_2d(a + kABytes, &tb, &full[s], kb * 128, nt * BN);
         }
     };
+
+    if (warp == T::kAddWarps && elect_one()) {
+        prefetch_tmap(&ta);
+        if (!kFused)
+            prefetch_tmap(&tb);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], kFused ? 2 : 1);
+            mbar_init(&empty[i], H);
+        }
+        for (int i = 0; i < H * NB; ++i) {
+            mbar_init(&done[0][i], 1);
+            mbar_init(&freed[0][i], 4 * T::kWGH * (T::kPair ? 2 : 1));
+        }
+        for (int i = 0; i < kScales; ++i) {
+            mbar_init(&scales_full[i], kFused ? 33 : 32);
+            mbar_init(&scales_empty[i], T::kAddWarps);
+        }
+        fence_barrier_init();
+        wait_for_kernel_before();
+        if (!T::kPair) {  // the first blocks are on their way during the rest of the setup
+            int mt, nt;
+            place(first, mt, nt);
+            for (int kb = kb0; kb < kb1 && kb - kb0 < ST; ++kb)
+                load_tiles(kb, kb - kb0, mt, nt);
+        }
+    }
+    if (warp == T::kAddWarps + 1) {
+        if (T::kPair) {
+            tmem_alloc_pair(&tmem_slot, NB * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&tmem_slot, NB * BN);
+            tmem_relinquish();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (T::kPair)
+        cluster_sync();  // the other CTA's barriers are there
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (T::kPair && warp >= T::kAddWarps)
+        // registers of these warps to those that add: 256 x 216 + 128 x 56 of the
+        // 384 x 168 that the CTA was launched with
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (T::kPair && warp == T::kAddWarps) {
         // ------------------------------------------------------------- tiles
         if (elect_one()) {
+            wait_for_kernel_before();
             uint32_t it = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
@@ -295,6 +310,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     } else if (warp == (T::kPair ? T::kAddWarps + 3 : T::kAddWarps)) {
         // ---------------------------------- scales, and without a pair the tiles
         const bool issues = !T::kPair && elect_one();
+        wait_for_kernel_before();
         uint32_t it = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
@@ -310,7 +326,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 sa[j] = p.sa + (r < p.m ? r >> p.sa_shift : 0) * p.sa_row + kb0 * p.sa_block;
             }
 #pragma unroll
-            for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
+            for (int j = 0; j < (kFused ? 0 : kRowsB ? BN / 32 : 1); ++j) {
                 const int64_t c = (int64_t)nt * BN + (kRowsB ? j * 32 + lane : lane * 128);
                 const bool in = c < p.n && (kRowsB || lane < H);
                 in_b |= (uint32_t)in << j;
@@ -318,11 +334,12 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const uint32_t s = it % ST, z = it % kScales;
-                ok = (T::kPair || wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status)) &&
+                const bool load = !T::kPair && it >= ST;  // the first ones were in the setup
+                ok = (!load || wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status)) &&
                      wait_for(&scales_empty[z], ((it / kScales) & 1) ^ 1, p.status);
                 if (!ok)
                     break;
-                if (issues)
+                if (load && issues)
                     load_tiles(kb, s, mt, nt);
                 __syncwarp();
 #pragma unroll
@@ -331,7 +348,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                     sa[j] += p.sa_block;
                 }
 #pragma unroll
-                for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
+                for (int j = 0; j < (kFused ? 0 : kRowsB ? BN / 32 : 1); ++j) {
                     if (kRowsB || lane < H)
                         copy_scale(&sb_smem[z][kRowsB ? j * 32 + lane : lane], sb[j], in_b >> j & 1);
                     sb[j] += p.sb_block;
@@ -340,6 +357,69 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             }
         }
         cp_async_wait_all();
+    } else if (kFused && warp >= T::kAddWarps + 2) {
+        if constexpr (kFused) {
+            // --------------- tokens, as k_block_quantize.cu: a warp every fourth block, so
+            // that four blocks' loads are on their way at once
+            const int own = warp - (T::kAddWarps + 2);
+            int mt, nt;
+            place(first, mt, nt);
+            const int rows = (int)p.n;
+            bool ok = true;
+            for (uint32_t it = own; ok && kb0 + (int)it < kb1; it += T::kQuantWarps) {
+                const uint32_t s = it % ST, z = it % kScales;
+                const int64_t c = (int64_t)(kb0 + it) * 128 + lane * 4;
+                const TX *x = static_cast<const TX *>(p.x) + c;
+                unsigned char *b = smem + s * T::kStageBytes + kABytes;
+                // rows past the last are the last once more: eight loads without a branch between
+                const bool whole = p.x_vec && (int64_t)(kb0 + it + 1) * 128 <= p.k;
+                for (int r0 = 0; ok && r0 < rows; r0 += 8) {
+                    float v[8][4];
+                    if (whole) {
+                        using V = typename Pack<TX, 4>::T;
+                        V raw[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            raw[i] = load_ahead_as<V>(x + min(r0 + i, rows - 1) * p.x_row);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            unpack<TX, 4>(raw[i], v[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[i][j] = r0 + i < rows && c + j < p.k ? to_f32(x[(r0 + i) * p.x_row + j]) : 0.f;
+                    }
+                    if (r0 == 0)
+                        ok = wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status) &&
+                             wait_for(&scales_empty[z], ((it / kScales) & 1) ^ 1, p.status);
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i;
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            top = max(top, magnitude(v[i][j]));
+                        float scale, inverse;
+                        scale_of<false>(__reduce_max_sync(0xffffffffu, top), scale, inverse);
+                        if (r < rows) {
+                            *reinterpret_cast<uint32_t *>(b + sw128_offset(r, lane >> 2) + (lane & 3) * 4) = to_bytes<false>(
+                                v[i][0] * inverse, v[i][1] * inverse, v[i][2] * inverse, v[i][3] * inverse);
+                            if (lane == 0)
+                                sb_smem[z][r] = scale;
+                        }
+                    }
+                }
+                if (!ok)
+                    break;
+                fence_proxy_async_smem();
+                warp_arrive(&full[s]);
+                warp_arrive(&scales_full[z]);
+            }
+        }
     } else if (warp >= T::kAddWarps) {
         // --------------------------------------------- MMAs: a warp for each half
         const int h = warp - (T::kAddWarps + 1);
@@ -382,7 +462,6 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + in_tile;
         // the next block's TMEM buffer and scales, and the phases of their barriers
         uint32_t b = 0, b_phase = 0, z = 0, z_phase = 0;
-        const uint32_t done_at = smem_u32(&done[h][0]), scales_at = smem_u32(&scales_full[0]);
         const uint32_t freed_at = T::kPair ? in_cta(smem_u32(&freed[h][0]), 0) : 0;
         const float *my_sa = &sa_smem[0][quarter * 32 + lane];
         bool scales_ready = false, done_ready = false;  // as last asked
@@ -397,8 +476,8 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             for (int i = 0; i < CW; ++i)
                 acc[i] = 0.f;
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = (scales_ready || wait_for(scales_at + z * 8, z_phase, p.status)) &&
-                     (done_ready || wait_for(done_at + b * 8, b_phase, p.status));
+                ok = (scales_ready || wait_for(&scales_full[z], z_phase, p.status)) &&
+                     (done_ready || wait_for(&done[h][b], b_phase, p.status));
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -427,9 +506,10 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                             b = 0;
                             b_phase ^= 1;
                         }
-                        // is the next block there already?  The answer comes under these products.
-                        scales_ready = ask(scales_at + z * 8, z_phase);
-                        done_ready = ask(done_at + b * 8, b_phase);
+                        // is the next block there already?  The answer comes under
+                        // these products (a test: try_wait would park the warp)
+                        scales_ready = mbar_test(&scales_full[z], z_phase);
+                        done_ready = mbar_test(&done[h][b], b_phase);
                     }
 #pragma unroll
                     for (int i = 0; i < LW; i += 4) {
@@ -551,35 +631,51 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         place(first, mt, nt);
         const uint32_t part = smem_u32(smem);
         constexpr int kGroups = kRows * BN / 4;
-        for (int i = rank * T::kThreads + (int)threadIdx.x; i < kGroups; i += p.splits * T::kThreads) {
-            int64_t outer, inner, n_outer, n_inner;
-            uint32_t off;
+        // a group's place in a CTA's partial sums and in the output
+        auto group = [&](int i, uint32_t &off, int64_t &outer, int64_t &inner) {
             if (kSwap) {
                 const int c = i / (kRows / 4), r = i % (kRows / 4) * 4;
                 outer = (int64_t)nt * BN + c;
                 inner = (int64_t)mt * kRows + r;
-                n_outer = p.n;
-                n_inner = p.m;
                 off = (uint32_t)(c * kRows + r) * 4;
             } else {
                 const int r = i / (BN / 4), c = i % (BN / 4) * 4;
                 outer = (int64_t)mt * kRows + r;
                 inner = (int64_t)nt * BN + c;
-                n_outer = p.m;
-                n_inner = p.n;
                 off = (uint32_t)(r * (BN + 4) + c) * 4;
             }
-            if (outer >= n_outer || inner >= n_inner)
-                continue;
-            float4 v = load_cluster(in_cta(part + off, 0));
-            for (int k = 1; k < p.splits; ++k) {
-                const float4 w = load_cluster(in_cta(part + off, k));
-                v.x += w.x;
-                v.y += w.y;
-                v.z += w.z;
-                v.w += w.w;
+            return i < kGroups && outer < (kSwap ? p.n : p.m) && inner < (kSwap ? p.m : p.n);
+        };
+        const int stride = p.splits * T::kThreads;
+        for (int i = rank * T::kThreads + (int)threadIdx.x; i < kGroups; i += 2 * stride) {
+            // two groups' parts on their way before the first is added
+            float4 of[2][kMostSplits];
+            uint32_t off[2];
+            int64_t outer[2], inner[2];
+            bool in[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                in[g] = group(i + g * stride, off[g], outer[g], inner[g]);
+#pragma unroll
+                for (int k = 0; k < kMostSplits; ++k)
+                    if (in[g] && k < p.splits)
+                        of[g][k] = load_cluster(in_cta(part + off[g], k));
             }
-            store4(p, outer * p.ld + inner, v, (int)min64(4, n_inner - inner));
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                if (!in[g])
+                    continue;
+                float4 v = of[g][0];
+#pragma unroll
+                for (int k = 1; k < kMostSplits; ++k)
+                    if (k < p.splits) {
+                        v.x += of[g][k].x;
+                        v.y += of[g][k].y;
+                        v.z += of[g][k].z;
+                        v.w += of[g][k].w;
+                    }
+                store4(p, outer[g] * p.ld + inner[g], v, (int)min64(4, (kSwap ? p.m : p.n) - inner[g]));
+            }
         }
         cluster_sync();  // nobody leaves while its sums are read
     }
@@ -595,13 +691,13 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     }
 }
 
-template <int BN, bool kSwap, bool kRowsB>
+template <int BN, bool kSwap, bool kRowsB, typename TX = void>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, const Params &p, int sms,
                    cudaStream_t st)
 {
-    using T = Tile<BN>;
+    using T = Tile<BN, !std::is_void_v<TX>>;
     static SmemGrant granted;
-    const auto kernel = block_matmul_kernel<BN, kSwap, kRowsB>;
+    const auto kernel = block_matmul_kernel<BN, kSwap, kRowsB, TX>;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), T::kSmem, &granted))
         return e;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
@@ -611,43 +707,46 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorM
     cfg.blockDim = dim3(T::kThreads);
     cfg.dynamicSmemBytes = T::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    attr[cfg.numAttrs++] = early_launch();
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p);
     if (e == cudaSuccess)
         note_launch(1);
     return e;
 }
 
-}  // namespace
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to; }
 
-cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void *out, int64_t m, int64_t n, int64_t k,
-                                bool bf16, cudaStream_t st)
+// Few tokens: the weights take the MMA's rows, the tokens its columns, so no
+// row of the MMA is idle.
+bool few(int64_t m, int64_t n) { return m <= 128 && n > m; }
+constexpr int kFewest = 32;
+int columns_for(int64_t rn) { return rn <= kFewest ? kFewest : rn <= 64 ? 64 : 128; }
+
+// Clusters of 1..8 CTAs that GB300's 152 SMs run at once, with one and with two
+// CTAs on an SM (cudaOccupancyMaxActiveClusters: they stay within a GPC).
+constexpr int kAtOnce[2][kMostSplits] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
+
+// The product of ra's rows (the MMA's) with rb's (its columns, bn a tile).
+Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int64_t rm, int64_t rn, int64_t n, int64_t k,
+            bool bf16)
 {
-    const int sms = device_sm_count();
-    const int blocks = (int)((k + 127) / 128);
-    auto up = [](int64_t v, int64_t to) { return (v + to - 1) / to; };
-    // Few tokens: the weights take the MMA's rows, the tokens its columns, so no
-    // row of the MMA is idle.
-    const bool swap = m <= 128 && n > m;
-    const BlockMatrix &ra = swap ? b : a, &rb = swap ? a : b;
-    const int64_t rm = swap ? n : m, rn = swap ? m : n;
-    int bn = rn <= 32 ? 32 : rn <= 64 ? 64 : 128;
-    if (!swap && rn > 128 && up(rm, 256) * up(rn, 256) * 8 >= 3 * sms)
-        bn = 256;
     Params p = {};
     p.m_tiles = (int)up(rm, bn == 256 ? 2 * kRows : kRows);
     p.n_tiles = (int)up(rn, bn);
-    p.blocks = blocks;
+    p.blocks = (int)up(k, 128);
     p.splits = 1;
-    if (bn < 256) {
-        const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({2 * sms / tiles, (int64_t)kMostSplits, blocks / 2}));
-    }
+    if (bn < 256)  // as many parts of two blocks or more as run at once
+        while (p.splits < kMostSplits && 2 * (p.splits + 1) <= p.blocks &&
+               (int64_t)p.m_tiles * p.n_tiles <= kAtOnce[bn == 128 ? 0 : 1][p.splits])
+            ++p.splits;
     p.sa = ra.scale;
     p.sa_row = ra.scale_row;
     p.sa_block = ra.scale_block;
@@ -662,9 +761,24 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
     p.n = rn;
     p.idesc = idesc_f8(bn == 256 ? 2 * kRows : kRows, std::min(bn, 128), ra.e5m2 ? 1 : 0, rb.e5m2 ? 1 : 0);
     p.bf16 = bf16;
-    const int64_t vec = bf16 ? 8 : 4;
-    p.vec = n % vec == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    p.vec = n % (bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
     p.status = device_status_word();
+    return p;
+}
+
+}  // namespace
+
+cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void *out, int64_t m, int64_t n, int64_t k,
+                                bool bf16, cudaStream_t st)
+{
+    const int sms = device_sm_count();
+    const bool swap = few(m, n);
+    const BlockMatrix &ra = swap ? b : a, &rb = swap ? a : b;
+    const int64_t rm = swap ? n : m, rn = swap ? m : n;
+    int bn = columns_for(rn);
+    if (!swap && rn > 128 && up(rm, 256) * up(rn, 256) * 8 >= 3 * sms)
+        bn = 256;
+    const Params p = plan(ra, rb, bn, out, rm, rn, n, k, bf16);
     if (!p.status)
         return cudaErrorUnknown;
     CUtensorMap ta, tb, to = {};
@@ -690,6 +804,28 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
         SSD_BLOCK_MATMUL(128, false);
     SSD_BLOCK_MATMUL(256, false);
 #undef SSD_BLOCK_MATMUL
+}
+
+// With more tokens a CTA would read and round the same ones as many times as there
+// are rows of tiles, and be bound by that (128 tokens: measured 77 us against 21).
+bool projects_few_tokens(int64_t tokens, int64_t outputs) { return tokens <= kFewest && few(tokens, outputs); }
+
+cudaError_t launch_few_tokens(const void *x, int64_t row, const BlockMatrix &w, void *y, int64_t tokens, int64_t outputs,
+                              int64_t inputs, bool bf16, cudaStream_t st)
+{
+    const int sms = device_sm_count();
+    Params p = plan(w, BlockMatrix{}, kFewest, y, outputs, tokens, outputs, inputs, bf16);
+    if (!p.status)
+        return cudaErrorUnknown;
+    p.x = x;
+    p.x_row = row;
+    p.k = inputs;
+    p.x_vec = row % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (bf16 ? 8 : 16) == 0;
+    CUtensorMap ta, none = {};
+    if (!make_tmap_bytes(&ta, w.q, (uint64_t)inputs, (uint64_t)outputs, (uint64_t)w.row, kRows))
+        return cudaErrorInvalidValue;
+    return bf16 ? launch<kFewest, true, true, __nv_bfloat16>(ta, none, none, p, sms, st)
+                : launch<kFewest, true, true, float>(ta, none, none, p, sms, st);
 }
 
 }  // namespace ssd

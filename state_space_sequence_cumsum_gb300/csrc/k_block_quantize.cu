@@ -15,6 +15,8 @@
 // memory, 16 of a column at a time, so that rows of 128 bytes are written.
 // Bound by HBM: e bytes in, 1 out per orientation.
 #include "common.cuh"
+#include "early_launch.cuh"
+#include "quant.cuh"
 #include "ssd_internal.h"
 #include "vec.cuh"
 
@@ -24,35 +26,6 @@ namespace {
 constexpr int kB = 128;
 constexpr int kWarps = 8, kRowsOfWarp = kB / kWarps;
 
-// Bits of the scale and of its inverse for the largest magnitude's bits: with
-// amax = 1.f * 2^k, e = k - TOP + (f > 1.75), TOP = 8 or 15.
-template <bool kE5M2> __device__ __forceinline__ void scale_of(uint32_t amax, float &scale, float &inverse)
-{
-    constexpr int top = kE5M2 ? 15 : 8;
-    // the biased exponent of amax, one more where its fraction is over 0.75
-    const int k = (int)((amax + 0x1fffffu) >> 23);
-    const int e = max(k - top, 9);  // biased; 2^-118
-    const bool bad = amax >= 0x7f800000u;
-    scale = __uint_as_float(bad ? 0x7fffffffu : (uint32_t)e << 23);
-    inverse = __uint_as_float(bad ? 0x7fffffffu : (uint32_t)(254 - e) << 23);
-}
-
-// Four values to four bytes, the first in the low one.
-template <bool kE5M2> __device__ __forceinline__ uint32_t to_bytes(float a, float b, float c, float d)
-{
-    uint16_t lo, hi;
-    if (kE5M2) {
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    } else {
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    }
-    return (uint32_t)lo | (uint32_t)hi << 16;
-}
-
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // kVec: rows of x start on boundaries of four values.
 template <typename TI, bool kE5M2, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32, 2)
@@ -61,29 +34,31 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
 {
     __shared__ uint32_t col_max[kWarps][kB];
     __shared__ __align__(16) uint4 turned[kB * kB / 16];  // [column][16-byte piece ^ (column / 4 % 8)]
+    let_next_kernel_start();
+    wait_for_kernel_before();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned col_blocks = (unsigned)((g.cols + kB - 1) / kB);
     const int64_t rb = blockIdx.x / col_blocks, r0 = rb * kB + warp * kRowsOfWarp;
     const int64_t cb = blockIdx.x % col_blocks, c0 = cb * kB + lane * 4;
 
     float v[kRowsOfWarp][4];
+    if (kVec && r0 + kRowsOfWarp <= g.rows && cb * kB + kB <= g.cols) {
+        // all of them in flight before the first is used
+        using V = typename Pack<TI, 4>::T;
+        V raw[kRowsOfWarp];
+        const TI *p = x + r0 * g.row + c0;
 #pragma unroll
-    for (int i = 0; i < kRowsOfWarp; ++i) {
-        const int64_t r = r0 + i;
-        const TI *p = x + r * g.row + c0;
+        for (int i = 0; i < kRowsOfWarp; ++i)
+            raw[i] = load_ahead_as<V>(p + i * g.row);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[i][j] = 0.f;
-        if (r < g.rows) {
-            if (kVec && c0 + 4 <= g.cols) {
-                load_vec<TI, 4>(p, v[i]);
-            } else {
+        for (int i = 0; i < kRowsOfWarp; ++i)
+            unpack<TI, 4>(raw[i], v[i]);
+    } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (c0 + j < g.cols)
-                        v[i][j] = to_f32(p[j]);
-            }
-        }
+        for (int i = 0; i < kRowsOfWarp; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[i][j] = r0 + i < g.rows && c0 + j < g.cols ? to_f32(x[(r0 + i) * g.row + c0 + j]) : 0.f;
     }
     uint32_t cm[4] = {0, 0, 0, 0};
     if (qt || g.tile) {
@@ -182,15 +157,16 @@ cudaError_t launch(const void *x, void *q, float *scale, void *qt, float *scale_
 {
     const unsigned grid = (unsigned)(((g.cols + kB - 1) / kB) * ((g.rows + kB - 1) / kB));
     const bool vec = g.row % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(TI)) == 0;
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kWarps * 32, 0, st>>>(static_cast<const TI *>(x), static_cast<uint8_t *>(q), scale,
-                                             static_cast<uint8_t *>(qt), scale_t, g);
-    };
-    if (vec)
-        go(block_quantize_kernel<TI, kE5M2, true>);
-    else
-        go(block_quantize_kernel<TI, kE5M2, false>);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchAttribute attr = early_launch();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, vec ? block_quantize_kernel<TI, kE5M2, true> : block_quantize_kernel<TI, kE5M2, false>,
+                           static_cast<const TI *>(x), static_cast<uint8_t *>(q), scale, static_cast<uint8_t *>(qt), scale_t, g);
     if (e == cudaSuccess)
         note_launch(1);
     return e;

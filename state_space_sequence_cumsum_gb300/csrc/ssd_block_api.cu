@@ -172,6 +172,9 @@ ssd_status_t ssd_projection(const void *x, int64_t row, ssd_block_matrix_t weigh
                        {workspace, need, 1, false}}));
     SSD_TRY(check_ws(workspace, workspace_bytes, need));
     cudaStream_t st = (cudaStream_t)stream;
+    if (any && outputs > 0 && !x_t && projects_few_tokens(tokens, outputs))
+        return cuda_status(launch_few_tokens(x, tokens > 1 ? row : up16(inputs), inner(weight, outputs, inputs), y, tokens,
+                                             outputs, inputs, dtype == SSD_BF16, st));
     const Quantised xq(tokens, inputs);
     if (any) {
         const QuantGeom g{tokens, inputs, row, xq.row, row_xt, xq.ld, x_t_scale_ld, false, false};

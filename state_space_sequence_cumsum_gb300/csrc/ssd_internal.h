@@ -237,6 +237,12 @@ struct BlockMatrix {
 cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void *out, int64_t m, int64_t n, int64_t k,
                                 bool bf16, cudaStream_t st);
 
+// A projection of few tokens (rows `row` elements apart), quantised on the way in:
+// one launch, where projects_few_tokens says so.
+bool projects_few_tokens(int64_t tokens, int64_t outputs);
+cudaError_t launch_few_tokens(const void *x, int64_t row, const BlockMatrix &weight, void *y, int64_t tokens,
+                              int64_t outputs, int64_t inputs, bool bf16, cudaStream_t st);
+
 // What a quantising call writes: x [rows, cols] and / or its transpose (either
 // q null: not wanted).
 struct QuantGeom {

@@ -26,9 +26,49 @@ namespace {
 constexpr int kB = 128;
 constexpr int kWarps = 8, kRowsOfWarp = kB / kWarps;
 
+// Four neighbouring values as they are in memory: bf16 stays packed, in half the
+// registers, and its largest magnitudes are found two at a time.
+template <typename TI> struct Four;
+template <> struct Four<float> {
+    float4 v;
+    using Peak = uint4;
+    __device__ __forceinline__ float operator[](int j) const { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+    __device__ __forceinline__ Peak peak() const
+    {
+        return make_uint4(magnitude(v.x), magnitude(v.y), magnitude(v.z), magnitude(v.w));
+    }
+    static __device__ __forceinline__ Peak larger(Peak a, Peak b)
+    {
+        return make_uint4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), max(a.w, b.w));
+    }
+    // the magnitudes' bits as f32, of the four and of all of them
+    static __device__ __forceinline__ uint4 bits(Peak p) { return p; }
+    static __device__ __forceinline__ uint32_t top(Peak p) { return max(max(p.x, p.y), max(p.z, p.w)); }
+};
+template <> struct Four<__nv_bfloat16> {
+    uint2 v;
+    using Peak = uint2;
+    __device__ __forceinline__ float operator[](int j) const
+    {
+        const uint32_t w = j < 2 ? v.x : v.y;
+        return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    }
+    __device__ __forceinline__ Peak peak() const { return make_uint2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu); }
+    static __device__ __forceinline__ Peak larger(Peak a, Peak b) { return make_uint2(__vmaxu2(a.x, b.x), __vmaxu2(a.y, b.y)); }
+    static __device__ __forceinline__ uint4 bits(Peak p)
+    {
+        return make_uint4(p.x << 16, p.x & 0xffff0000u, p.y << 16, p.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t top(Peak p)
+    {
+        const uint32_t m = __vmaxu2(p.x, p.y);
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
+
 // kVec: rows of x start on boundaries of four values.
 template <typename TI, bool kE5M2, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+__global__ void __launch_bounds__(kWarps * 32, sizeof(TI) == 2 ? 3 : 2)
 block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
                       uint8_t *__restrict__ qt, float *__restrict__ scale_t, const QuantGeom g)
 {
@@ -41,46 +81,41 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
     const int64_t rb = blockIdx.x / col_blocks, r0 = rb * kB + warp * kRowsOfWarp;
     const int64_t cb = blockIdx.x % col_blocks, c0 = cb * kB + lane * 4;
 
-    float v[kRowsOfWarp][4];
+    using F = Four<TI>;
+    F v[kRowsOfWarp];
     if (kVec && r0 + kRowsOfWarp <= g.rows && cb * kB + kB <= g.cols) {
         // all of them in flight before the first is used
-        using V = typename Pack<TI, 4>::T;
-        V raw[kRowsOfWarp];
         const TI *p = x + r0 * g.row + c0;
 #pragma unroll
         for (int i = 0; i < kRowsOfWarp; ++i)
-            raw[i] = load_ahead_as<V>(p + i * g.row);
-#pragma unroll
-        for (int i = 0; i < kRowsOfWarp; ++i)
-            unpack<TI, 4>(raw[i], v[i]);
+            v[i].v = load_ahead_as<decltype(v[i].v)>(p + i * g.row);
     } else {
 #pragma unroll
-        for (int i = 0; i < kRowsOfWarp; ++i)
+        for (int i = 0; i < kRowsOfWarp; ++i) {
+            TI e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[i][j] = r0 + i < g.rows && c0 + j < g.cols ? to_f32(x[(r0 + i) * g.row + c0 + j]) : 0.f;
+                e[j] = r0 + i < g.rows && c0 + j < g.cols ? x[(r0 + i) * g.row + c0 + j] : from_f32<TI>(0.f);
+            memcpy(&v[i].v, e, sizeof(e));
+        }
     }
-    uint32_t cm[4] = {0, 0, 0, 0};
+    uint4 cm = make_uint4(0, 0, 0, 0);
     if (qt || g.tile) {
+        typename F::Peak m = v[0].peak();
 #pragma unroll
-        for (int i = 0; i < kRowsOfWarp; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                cm[j] = max(cm[j], magnitude(v[i][j]));
-        *reinterpret_cast<uint4 *>(&col_max[warp][lane * 4]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+        for (int i = 1; i < kRowsOfWarp; ++i)
+            m = F::larger(m, v[i].peak());
+        *reinterpret_cast<uint4 *>(&col_max[warp][lane * 4]) = F::bits(m);
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const uint4 m = *reinterpret_cast<const uint4 *>(&col_max[w][lane * 4]);
-            cm[0] = max(cm[0], m.x);
-            cm[1] = max(cm[1], m.y);
-            cm[2] = max(cm[2], m.z);
-            cm[3] = max(cm[3], m.w);
+            const uint4 o = *reinterpret_cast<const uint4 *>(&col_max[w][lane * 4]);
+            cm = make_uint4(max(cm.x, o.x), max(cm.y, o.y), max(cm.z, o.z), max(cm.w, o.w));
         }
     }
     float tile_scale = 0.f, tile_inverse = 0.f;
     if (g.tile) {
-        scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, max(max(cm[0], cm[1]), max(cm[2], cm[3]))), tile_scale,
+        scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, max(max(cm.x, cm.y), max(cm.z, cm.w))), tile_scale,
                         tile_inverse);
         if (threadIdx.x == 0)
             scale[rb * g.scale_ld + cb] = tile_scale;
@@ -91,11 +126,7 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
         for (int i = 0; i < kRowsOfWarp; ++i) {
             float s = tile_scale, inverse = tile_inverse;
             if (!g.tile) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    m = max(m, magnitude(v[i][j]));
-                scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, m), s, inverse);
+                scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, F::top(v[i].peak())), s, inverse);
                 mine = lane == i ? s : mine;
             }
             const int64_t r = r0 + i;
@@ -119,7 +150,7 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
         for (int j = 0; j < 4; ++j) {
             float s = tile_scale, inverse = tile_inverse;
             if (!g.tile) {
-                scale_of<kE5M2>(cm[j], s, inverse);
+                scale_of<kE5M2>(j == 0 ? cm.x : j == 1 ? cm.y : j == 2 ? cm.z : cm.w, s, inverse);
                 if (warp == 0 && c0 + j < g.cols)
                     scale_t[rb * g.scale_t_ld + c0 + j] = s;
             }

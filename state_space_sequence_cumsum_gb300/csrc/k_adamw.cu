@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kUnit = 256;                  // elements of a warp: those that share a scale
-constexpr int units(bool states8) { return states8 ? 4 : 1; }  // that a warp walks
+__host__ __device__ constexpr int units(bool states8) { return states8 ? 4 : 1; }  // that a warp walks
 
 struct Entry {
     void *p;

@@ -13,8 +13,7 @@
 // is one warp reduction.  The tensors' addresses are a kernel parameter, in
 // constant memory; a thread block finds its own by bisection and stays in it for
 // 2048 elements or, with 8-bit states, up to 8192 (there the instructions count
-// too: 749 -> 581 us for 241M elements with bf16 gradients, with the roundings
-// that need no exact root; with f32 states 982 -> 947 us the other way round).
+// too; with f32 states one stretch is faster: 947 against 982 us for 241M).
 #include <cmath>
 
 #include "common.cuh"
@@ -106,7 +105,7 @@ template <bool kRoot> __device__ __forceinline__ uint2 to_e4m3(const float (&v)[
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float x = v[2 * i + j];
-            q[j] = x * inverse;
+            q[j] = __fmul_rn(x, inverse);
             if (kRoot)  // a NaN stays one
                 q[j] = x > 0.f && q[j] < least ? least : q[j];
         }
@@ -220,14 +219,18 @@ adamw_kernel(const __grid_constant__ Table<MOST> table, const __grid_constant__ 
         load8<TG>(t.g, at, left, vec, g);
         if (k8) {
             const uint2 qm = load_bytes(t.m, at, left, vec), qv = load_bytes(t.v, at, left, vec);
-            const float b1 = s.b1 * t.m_scale[unit], sv = t.v_scale[unit];
+            const float sm = t.m_scale[unit], sv = t.v_scale[unit];
             from_e4m3(qm, m);
             from_e4m3(qv, v);
+            // what is rounded to 8 bits is rounded step by step as the formula is
+            // written: next to a border one rounding more or less is a step of 6 to
+            // 12 %, and from then on another state
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                m[i] = fmaf(m[i], b1, g[i] * c1);
-                v[i] *= sv;
-                v[i] = fmaf(v[i] * s.b2, v[i], g[i] * c2 * g[i]);
+                const float h = __fmul_rn(g[i], grad_scale);
+                m[i] = __fadd_rn(__fmul_rn(__fmul_rn(m[i], sm), s.b1), __fmul_rn(h, s.c1));
+                v[i] = __fmul_rn(v[i], sv);
+                v[i] = __fadd_rn(__fmul_rn(__fmul_rn(v[i], v[i]), s.b2), __fmul_rn(__fmul_rn(h, h), s.c2));
             }
         } else {
             load8<float>(t.m, at, left, vec, m);
@@ -241,7 +244,7 @@ adamw_kernel(const __grid_constant__ Table<MOST> table, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             // the denominator is no subnormal: a root is 2^-75 or more, or zero
-            r[i] = root_of(v[i]);
+            r[i] = k8 ? __fsqrt_rn(v[i]) : root_of(v[i]);
             p[i] = fmaf(m[i] * -rate, rcp(fmaf(r[i], root, s.eps)), p[i] * decay);
         }
         store8<TP>(t.p, at, left, vec, p);

@@ -87,7 +87,7 @@ struct Params {
     int64_t m, n;                                // rows of the MMA's A and B
     int m_tiles, n_tiles, blocks, splits;
     uint32_t idesc;
-    bool bf16, vec;                              // vec: out takes 16-byte accesses
+    bool bf16, vec, pairs;                       // out takes 16-byte accesses, those of two bf16
     unsigned *status;
     // kFused: the tokens [n, k], rows x_row apart; x_vec: four values at a time
     const void *x;
@@ -161,29 +161,45 @@ __device__ __forceinline__ void store4(const Params &p, int64_t at, const float4
     }
 }
 
-// A warp's 32 rows of 128 bytes, staged with the swizzle, to the output: rows
-// row0.., `cols` values each from column col on.
+// A warp's 32 rows of `bytes` (64 or 128), staged with the swizzle, to the output:
+// rows row0.., from column col on.  Where out's rows start on no 16 bytes, row by
+// row with neighbouring lanes on neighbouring values.
 template <typename T>
-__device__ __forceinline__ void copy_rows(const Params &p, const unsigned char *stage, int64_t row0, int64_t col, int lane)
+__device__ __forceinline__ void copy_rows(const Params &p, const unsigned char *stage, int bytes, int64_t row0, int64_t col,
+                                          int lane)
 {
     constexpr int per = 16 / (int)sizeof(T);  // values of a 16-byte chunk
-    const int chunk = lane & 7;
-    const int64_t c = col + chunk * per;
+    if (p.vec) {
+        const int chunk = lane & 7;
+        const int64_t c = col + chunk * per;
+        if (chunk * 16 >= bytes || c >= p.n)
+            return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3);
-        if (row0 + r >= p.m || c >= p.n)
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (row0 + r < p.m)  // rows are a multiple of a chunk long
+                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (row0 + r) * p.ld + c) =
+                    *reinterpret_cast<const uint4 *>(stage + sw128_offset(r, chunk));
+        }
+        return;
+    }
+    const int rows = (int)min64(32, p.m - row0);
+    const bool pairs = sizeof(T) == 2 && p.pairs;
+    const int step = pairs ? 64 : 32;  // values of a warp's store
+    const int own = pairs ? 2 * lane : lane;
+    for (int k = 0; k * step * (int)sizeof(T) < bytes; ++k) {
+        const int v = k * step + own;
+        const unsigned char *from = stage + (v % per) * sizeof(T);
+        T *o = static_cast<T *>(p.out) + row0 * p.ld + col + v;
+        if (col + v >= p.n)
             continue;
-        const uint4 v = *reinterpret_cast<const uint4 *>(stage + sw128_offset(r, chunk));
-        T *o = static_cast<T *>(p.out) + (row0 + r) * p.ld + c;
-        if (p.vec && c + per <= p.n) {
-            *reinterpret_cast<uint4 *>(o) = v;
-        } else {
-            const T *e = reinterpret_cast<const T *>(&v);
-#pragma unroll
-            for (int j = 0; j < per; ++j)
-                if (c + j < p.n)
-                    o[j] = e[j];
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r, o += p.ld) {
+            const unsigned char *e = from + sw128_offset(r, v / per);
+            if (pairs)
+                *reinterpret_cast<uint32_t *>(o) = *reinterpret_cast<const uint32_t *>(e);
+            else
+                *o = *reinterpret_cast<const T *>(e);
         }
     }
 }
@@ -600,8 +616,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                                 }
                             },
                             [&](unsigned char *st) {
-                                if ((lane & 7) < per / 8)
-                                    copy_rows<__nv_bfloat16>(p, st, row0, col0 + c, lane);
+                                copy_rows<__nv_bfloat16>(p, st, per * 2, row0, col0 + c, lane);
                             });
                 } else {
 #pragma unroll
@@ -616,7 +631,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                                         make_float4(v[0], v[1], v[2], v[3]);
                                 }
                             },
-                            [&](unsigned char *st) { copy_rows<float>(p, st, row0, col0 + c, lane); });
+                            [&](unsigned char *st) { copy_rows<float>(p, st, 128, row0, col0 + c, lane); });
                 }
             }
         }
@@ -734,6 +749,43 @@ int columns_for(int64_t rn) { return rn <= kFewest ? kFewest : rn <= 64 ? 64 : 1
 // CTAs on an SM (cudaOccupancyMaxActiveClusters: they stay within a GPC).
 constexpr int kAtOnce[2][kMostSplits] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
 
+// As many parts of two blocks or more as run at once.
+int splits_for(int64_t tiles, int blocks, int bn)
+{
+    int s = 1;
+    if (bn < 256)
+        while (s < kMostSplits && 2 * (s + 1) <= blocks && tiles <= kAtOnce[bn == 128 ? 0 : 1][s])
+            ++s;
+    return s;
+}
+
+// Columns of a tile: those with the least estimated time.  Waves of tiles (of
+// parts), each with a start and a time for each block, in us as fitted to
+// measurements from 200 x 200 x 10000 to 2299 x 1984 x 4160: a pair of CTAs is the
+// fastest by far where its tiles fill the SMs, and smaller tiles where they do
+// not (12010 x 192 x 1152: 8.8, 13.6 and 9.3 us with 64, 128 and 256 columns;
+// 1602 x 1728 x 2853: 28, 28 and 17; 256 x 2560 x 5120: 14, 12 and 23).
+int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
+{
+    if (rn <= 64)
+        return columns_for(rn);
+    int best = 0;
+    double least = 0;
+    for (int bn : {64, 128, 256}) {
+        const int64_t tiles = up(rm, bn == 256 ? 2 * kRows : kRows) * up(rn, bn);
+        const int splits = splits_for(tiles, blocks, bn), parts = (blocks + splits - 1) / splits;
+        const int64_t waves = up(tiles * splits, bn == 256 ? 76 : bn == 128 ? 152 : 304);
+        const double start = bn == 256 ? 5.0 : 3.5;
+        const double block = bn == 256 ? (rows_b ? 0.68 : 0.43) : bn == 128 ? (rows_b ? 0.50 : 0.39) : (rows_b ? 0.62 : 0.52);
+        const double t = (double)waves * (start + block * parts) + (splits > 1 ? 1.5 : 0);
+        if (!best || t < least) {
+            best = bn;
+            least = t;
+        }
+    }
+    return best;
+}
+
 // The product of ra's rows (the MMA's) with rb's (its columns, bn a tile).
 Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int64_t rm, int64_t rn, int64_t n, int64_t k,
             bool bf16)
@@ -742,11 +794,7 @@ Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int
     p.m_tiles = (int)up(rm, bn == 256 ? 2 * kRows : kRows);
     p.n_tiles = (int)up(rn, bn);
     p.blocks = (int)up(k, 128);
-    p.splits = 1;
-    if (bn < 256)  // as many parts of two blocks or more as run at once
-        while (p.splits < kMostSplits && 2 * (p.splits + 1) <= p.blocks &&
-               (int64_t)p.m_tiles * p.n_tiles <= kAtOnce[bn == 128 ? 0 : 1][p.splits])
-            ++p.splits;
+    p.splits = splits_for((int64_t)p.m_tiles * p.n_tiles, p.blocks, bn);
     p.sa = ra.scale;
     p.sa_row = ra.scale_row;
     p.sa_block = ra.scale_block;
@@ -762,6 +810,7 @@ Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int
     p.idesc = idesc_f8(bn == 256 ? 2 * kRows : kRows, std::min(bn, 128), ra.e5m2 ? 1 : 0, rb.e5m2 ? 1 : 0);
     p.bf16 = bf16;
     p.vec = n % (bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    p.pairs = bf16 && n % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3u) == 0;
     p.status = device_status_word();
     return p;
 }
@@ -775,9 +824,7 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
     const bool swap = few(m, n);
     const BlockMatrix &ra = swap ? b : a, &rb = swap ? a : b;
     const int64_t rm = swap ? n : m, rn = swap ? m : n;
-    int bn = columns_for(rn);
-    if (!swap && rn > 128 && up(rm, 256) * up(rn, 256) * 8 >= 3 * sms)
-        bn = 256;
+    const int bn = swap ? columns_for(rn) : columns_of_tile(rm, rn, (int)up(k, 128), !rb.tile);
     const Params p = plan(ra, rb, bn, out, rm, rn, n, k, bf16);
     if (!p.status)
         return cudaErrorUnknown;

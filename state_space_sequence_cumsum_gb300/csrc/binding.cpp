@@ -787,22 +787,36 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     const Tensor &like = P[0];
     const ssd_dtype_t pc = dtype_code(like, "params"), gc = dtype_code(G[0], "grads");
     const at::ScalarType st = s8 ? at::kFloat8_e4m3fn : at::kFloat;
+    const at::ScalarType pt = like.scalar_type(), gt = G[0].scalar_type();
+    const c10::Device dev = like.device();
+    // a list is mostly right: the messages are put together for what is not
+    auto alike = [&](const Tensor &x, const char *name, at::IntArrayRef shape, at::ScalarType type) {
+        if (!(x.sizes() == shape && x.scalar_type() == type && x.device() == dev && x.is_contiguous()))
+            same(x, name, shape, type, like, true);
+    };
     std::vector<ssd_adamw_tensor_t> t((size_t)P.n);
+    c10::SmallVector<at::TensorImpl *, 256> outs;  // the caller keeps them
     for (Py_ssize_t i = 0; i < P.n; ++i) {
-        const Tensor &p = P[i];
-        same(p, "params", p.sizes(), like.scalar_type(), like, true);
-        same(G[i], "grads", p.sizes(), G[0].scalar_type(), like, true);
-        same(M[i], "m", p.sizes(), st, like, true);
-        same(V[i], "v", p.sizes(), st, like, true);
-        float *ms = nullptr, *vs = nullptr;
+        const Tensor &p = P[i], &g = G[i], &m = M[i], &v = V[i];
+        const at::IntArrayRef shape = p.sizes();
+        alike(p, "params", shape, pt);
+        alike(g, "grads", shape, gt);
+        alike(m, "m", shape, st);
+        alike(v, "v", shape, st);
+        ssd_adamw_tensor_t &e = t[(size_t)i];
+        e = {ptr(p), ptr(g), ptr(m), ptr(v), nullptr, nullptr, p.numel()};
+        for (const Tensor *w : {&p, &m, &v})
+            outs.push_back(w->unsafeGetTensorImpl());
         if (s8) {
-            const int64_t blocks = (p.numel() + 255) / 256;
-            same_f32(MS[i], "m_scales", {blocks}, like);
-            same_f32(VS[i], "v_scales", {blocks}, like);
-            ms = ptr<float>(MS[i]);
-            vs = ptr<float>(VS[i]);
+            const Tensor &ms = MS[i], &vs = VS[i];
+            const int64_t blocks[1] = {(e.n + 255) / 256};
+            alike(ms, "m_scales", blocks, at::kFloat);
+            alike(vs, "v_scales", blocks, at::kFloat);
+            e.m_scale = ptr<float>(ms);
+            e.v_scale = ptr<float>(vs);
+            outs.push_back(ms.unsafeGetTensorImpl());
+            outs.push_back(vs.unsafeGetTensorImpl());
         }
-        t[(size_t)i] = {ptr(p), ptr(G[i]), ptr(M[i]), ptr(V[i]), ms, vs, p.numel()};
     }
     on_gpu(like, "params");
     const On on(like);
@@ -829,15 +843,9 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t nargs)
     const ssd_status_t s = ssd_adamw_step(t.data(), P.n, args, s8 ? 8 : 32, pc, gc, on.stream);
     if (s != SSD_OK)
         return raise_status(s, "ssd_adamw_step");
-    for (Py_ssize_t i = 0; i < P.n; ++i) {
-        written(P[i]);
-        written(M[i]);
-        written(V[i]);
-        if (s8) {
-            written(MS[i]);
-            written(VS[i]);
-        }
-    }
+    for (at::TensorImpl *w : outs)
+        if (!w->is_inference())
+            w->bump_version();
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }

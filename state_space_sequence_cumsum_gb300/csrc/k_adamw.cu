@@ -341,9 +341,10 @@ cudaError_t launch_adamw(const ssd_adamw_tensor_t *tensors, int64_t count, const
     s.lr_device = a.lr_device;
     s.step_device = a.step_device;
     s.grad_scale_device = a.grad_scale_device;
-    // a small table is a small kernel parameter
-    return count <= 32 ? launch_all<32>(tensors, count, s, states8, p_bf16, g_bf16, st)
-                       : launch_all<480>(tensors, count, s, states8, p_bf16, g_bf16, st);
+    // a small table is a small kernel parameter; 480 are near the 32 KB limit
+    return count <= 32    ? launch_all<32>(tensors, count, s, states8, p_bf16, g_bf16, st)
+           : count <= 128 ? launch_all<128>(tensors, count, s, states8, p_bf16, g_bf16, st)
+                          : launch_all<480>(tensors, count, s, states8, p_bf16, g_bf16, st);
 }
 
 }  // namespace ssd

@@ -69,6 +69,37 @@ ssd_status_t product(const BlockMatrix &a, const BlockMatrix &b, void *out, int6
     return cuda_status(launch_block_matmul(a, b, out, m, n, k, type == SSD_BF16, st));
 }
 
+// A buffer of an optimiser's step.
+struct Span {
+    uintptr_t at, end;
+    bool written;
+};
+
+// By address, merging the runs that are there: the buffers of one kind mostly
+// come in the allocator's order, and sorting from scratch took half of a call on
+// a hundred small tensors.
+void sort_runs(std::vector<Span> &v)
+{
+    const auto before = [](const Span &a, const Span &b) { return a.at < b.at; };
+    std::vector<size_t> ends;  // of the runs
+    for (size_t i = 1; i <= v.size(); ++i)
+        if (i == v.size() || before(v[i], v[i - 1]))
+            ends.push_back(i);
+    std::vector<Span> other(v.size());
+    while (ends.size() > 1) {
+        std::vector<size_t> merged;
+        size_t from = 0;
+        for (size_t k = 0; k < ends.size(); k += 2) {
+            const size_t mid = ends[k], to = k + 1 < ends.size() ? ends[k + 1] : mid;
+            std::merge(v.begin() + from, v.begin() + mid, v.begin() + mid, v.begin() + to, other.begin() + from, before);
+            merged.push_back(to);
+            from = to;
+        }
+        v.swap(other);
+        ends.swap(merged);
+    }
+}
+
 // A quantised matrix [rows, cols] in workspace: its values, then its scales by
 // column block.
 struct Quantised {
@@ -242,20 +273,8 @@ ssd_status_t ssd_adamw_step(const ssd_adamw_tensor_t *tensors, int64_t count, ss
         return SSD_ERR_INVALID_ARG;
     const bool s8 = state_bits == 8;
     const size_t ep = elem(p_dtype), eg = elem(g_dtype), es = s8 ? 1 : 4;
-    if (reinterpret_cast<uintptr_t>(args.lr_device) % 4 || reinterpret_cast<uintptr_t>(args.step_device) % 8 ||
-        reinterpret_cast<uintptr_t>(args.grad_scale_device) % 4)
-        return SSD_ERR_ALIGNMENT;
     // every buffer present and aligned, and none that is written overlaps another
-    struct Span {
-        uintptr_t at, end;
-        bool written;
-    };
     std::vector<Span> spans;
-    try {
-        spans.reserve((size_t)count * 6 + 3);
-    } catch (const std::bad_alloc &) {
-        return SSD_ERR_UNSUPPORTED;
-    }
     auto add = [&](const void *p, size_t bytes, size_t align, bool written) {
         SSD_TRY(check_range({p, bytes, align, true}));
         if (bytes)
@@ -263,28 +282,36 @@ ssd_status_t ssd_adamw_step(const ssd_adamw_tensor_t *tensors, int64_t count, ss
         return SSD_OK;
     };
     for (int64_t i = 0; i < count; ++i) {
-        const ssd_adamw_tensor_t &t = tensors[i];
-        if (t.n < 0)
+        if (tensors[i].n < 0)
             return SSD_ERR_INVALID_ARG;
-        if (t.n > (1LL << 40))
+        if (tensors[i].n > (1LL << 40))
             return SSD_ERR_UNSUPPORTED;
-        const size_t n = (size_t)t.n, blocks = (n + 255) / 256;
-        SSD_TRY(add(t.p, n * ep, ep, true));
-        SSD_TRY(add(t.g, n * eg, eg, false));
-        SSD_TRY(add(t.m, n * es, es, true));
-        SSD_TRY(add(t.v, n * es, es, true));
-        if (s8) {
-            SSD_TRY(add(t.m_scale, blocks * 4, 4, true));
-            SSD_TRY(add(t.v_scale, blocks * 4, 4, true));
-        }
     }
-    if (args.lr_device)
-        add(args.lr_device, 4, 4, false);
-    if (args.step_device)
-        add(args.step_device, 8, 8, false);
-    if (args.grad_scale_device)
-        add(args.grad_scale_device, 4, 4, false);
-    std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.at < b.at; });
+    const auto each = [&](auto buffer) {
+        for (int64_t i = 0; i < count; ++i)
+            SSD_TRY(buffer(tensors[i], (size_t)tensors[i].n));
+        return SSD_OK;
+    };
+    try {
+        spans.reserve((size_t)count * (s8 ? 6 : 4) + 3);
+        SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.p, n * ep, ep, true); }));
+        SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.g, n * eg, eg, false); }));
+        SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.m, n * es, es, true); }));
+        SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.v, n * es, es, true); }));
+        if (s8) {
+            SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.m_scale, (n + 255) / 256 * 4, 4, true); }));
+            SSD_TRY(each([&](const ssd_adamw_tensor_t &t, size_t n) { return add(t.v_scale, (n + 255) / 256 * 4, 4, true); }));
+        }
+        if (args.lr_device)
+            SSD_TRY(add(args.lr_device, 4, 4, false));
+        if (args.step_device)
+            SSD_TRY(add(args.step_device, 8, 8, false));
+        if (args.grad_scale_device)
+            SSD_TRY(add(args.grad_scale_device, 4, 4, false));
+        sort_runs(spans);
+    } catch (const std::bad_alloc &) {
+        return SSD_ERR_UNSUPPORTED;
+    }
     uintptr_t any_end = 0, written_end = 0;  // of the spans before this one
     for (const Span &s : spans) {
         if (s.at < written_end || (s.written && s.at < any_end))

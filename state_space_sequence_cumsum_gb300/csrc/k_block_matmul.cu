@@ -377,10 +377,8 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         if constexpr (kFused) {
             // --------------- tokens, as k_block_quantize.cu: a warp every fourth block, so
             // that four blocks' loads are on their way at once
-            const int own = warp - (T::kAddWarps + 2);
-            int mt, nt;
-            place(first, mt, nt);
-            const int rows = (int)p.n;
+            wait_for_kernel_before();
+            const int own = warp - (T::kAddWarps + 2), rows = (int)p.n;
             bool ok = true;
             for (uint32_t it = own; ok && kb0 + (int)it < kb1; it += T::kQuantWarps) {
                 const uint32_t s = it % ST, z = it % kScales;

@@ -386,3 +386,69 @@ def test_captured_and_replayed(t):
     assert torch.equal(y, y1) and all(torch.equal(g[k], g1[k]) for k in g)
     assert not torch.equal(eager.detach(), y1)
     assert ssd.ssd_stream_status() == 0
+
+
+@pytest.mark.parametrize("t", [8, 100, 2000])
+def test_inputs_written_just_before(t):
+    """Each call reads what the kernel before it on the stream has written:
+    inputs, weights and workspace change from call to call without a pause."""
+    w = [tokens(300, 512, F32, i) for i in range(2)]
+    x = [tokens(t, 512, BF, 7 + i) for i in range(2)]
+    want = [ssd.ssd_projection(x[i], *ssd.ssd_block_quantize(w[i], tile=True)[:2])[0] for i in range(2)]
+    torch.cuda.synchronize()
+    ws, xb, wb = ssd.Workspace(), torch.empty_like(x[0]), torch.empty_like(w[0])
+    got = []
+    for i in range(60):
+        wb.copy_(w[i % 2])
+        q, s, _, _ = ssd.ssd_block_quantize(wb, tile=True)
+        xb.copy_(x[i % 2])
+        got.append(ssd.ssd_projection(xb, q, s, workspace=ws)[0])
+        if i % 3 == 0:  # the weights' kernel last
+            q, s, _, _ = ssd.ssd_block_quantize(wb, tile=True)
+            got[-1] = ssd.ssd_projection(xb, q, s, workspace=ws)[0]
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))
+
+
+def test_two_streams_at_once():
+    """Calls of all kinds of tiles beside one another on two streams."""
+    cases = []
+    for t, k, n in ((5, 700, 900), (60, 300, 1000), (120, 900, 640), (400, 384, 300), (3000, 256, 2100)):
+        x, (q, s, _, _) = tokens(t, k, BF, t), ssd.ssd_block_quantize(tokens(n, k, F32, n), tile=True)
+        cases.append((x, q, s, ssd.ssd_projection(x, q, s)[0]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            for x, q, s, _ in cases[::-1] if i else cases:
+                got[i].append(ssd.ssd_projection(x, q, s, stream=st)[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        order = cases[::-1] if i else cases
+        for j, y in enumerate(got[i]):
+            assert torch.equal(y, order[j % len(order)][3])
+    assert ssd.ssd_stream_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 bytes and outputs of more than 2^31 elements: the
+    last rows are those of a small call on them alone."""
+    m, k, n = (1 << 20) + 77, 4112, 2056
+    x = torch.empty(m, k, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(0))
+    q, s, qt, st = ssd.ssd_block_quantize(x, want_t=True)
+    last = ssd.ssd_block_quantize(x[-300:])
+    assert torch.equal(q[-300:].float(), last[0].float()) and torch.equal(s[-300:], last[1])
+    # the transpose's last row, block by block of 128 tokens
+    col = x[:, -1].float()
+    pad = torch.nn.functional.pad(col, (0, -m % 128)).view(-1, 128)
+    values = (qt[-1].float() * st[-1].repeat_interleave(128)[:m])
+    assert bool(((values - col).abs() <= 2.0 ** -4 * pad.abs().amax(1).repeat_interleave(128)[:m]).all())
+    assert torch.equal(values[:128], qt[-1, :128].float() * st[-1, 0]) and bool((values != 0).any())
+    b, sb, _, _ = ssd.ssd_block_quantize(tokens(n, k, F32, 3), tile=True)
+    y = ssd.ssd_block_matmul(q, s, b, sb)
+    assert y.numel() > 1 << 31
+    for rows in (slice(-300, None), slice(0, 300), slice(m // 2, m // 2 + 300)):
+        part = ssd.ssd_block_matmul(q[rows], s[rows], b, sb, out_dtype=F32)
+        assert bool(((y[rows].float() - part).abs() <= 2.0 ** -8 * part.abs() + 2.0 ** -14 * float(part.abs().max())).all())
+    assert ssd.ssd_stream_status() == 0

@@ -4,9 +4,11 @@ selective scan -> output projection -> block norm.
 
 Training runs the prompt forms and their gradients (the autograd functions);
 generation carries the convolution's and the scan's states from the prompt
-into the single-token forms.  The projections are plain matrix products.
+into the single-token forms.  The projections are plain matrix products or,
+with --eight-bit, the package's in 8 bits, and then the optimiser keeps its
+states in 8 bits too; its step is the package's either way.
 
-    python examples/selective_model.py [--steps 150]
+    python examples/selective_model.py [--steps 150] [--eight-bit]
 """
 import argparse
 import math
@@ -22,9 +24,9 @@ import state_space_sequence_cumsum_gb300 as ssd  # noqa: E402
 class Layer(torch.nn.Module):
     """Projections, convolution and scan of one block; dim -> dim."""
 
-    def __init__(self, dim, inner, dstate, rank, width):
+    def __init__(self, dim, inner, dstate, rank, width, eight_bit=False):
         super().__init__()
-        self.inner, self.dstate, self.rank = inner, dstate, rank
+        self.inner, self.dstate, self.rank, self.eight_bit = inner, dstate, rank, eight_bit
 
         def weight(*shape):
             return torch.nn.Parameter(torch.randn(shape) / math.sqrt(shape[0]))
@@ -38,9 +40,15 @@ class Layer(torch.nn.Module):
         self.dt_bias = torch.nn.Parameter(torch.log(torch.expm1(torch.exp(
             torch.empty(inner).uniform_(math.log(1e-3), math.log(1e-1))))))
 
+    def project(self, x, w):
+        """x times w [inputs, outputs]."""
+        if self.eight_bit:
+            return ssd.ProjectionFunction.apply(x, w.t().contiguous())
+        return x @ w.to(x.dtype)
+
     def inputs(self, x):
         """u and z, two slices of one projection."""
-        return (x @ self.w_in.to(x.dtype)).split(self.inner, -1)
+        return self.project(x, self.w_in).split(self.inner, -1)
 
     def steps(self, u):
         """dt, B and C of each token."""
@@ -53,7 +61,7 @@ class Layer(torch.nn.Module):
         u, conv_state = ssd.CausalConvFunction.apply(u, self.conv, self.conv_bias)
         dt, B, C = self.steps(u)
         y, state = ssd.SelectiveScanFunction.apply(u, dt, -torch.exp(self.log_a), B, C, self.skip, z, self.dt_bias)
-        return y @ self.w_out.to(x.dtype), (conv_state, state)
+        return self.project(y, self.w_out), (conv_state, state)
 
     def token(self, x, states):
         """One token [batch, dim]; updates the states in place."""
@@ -61,14 +69,14 @@ class Layer(torch.nn.Module):
         u, _ = ssd.ssd_causal_conv_step(u, self.conv, states[0], self.conv_bias)
         dt, B, C = self.steps(u)
         y, _ = ssd.ssd_selective_scan_step(u, dt, -torch.exp(self.log_a), B, C, self.skip, states[1], z, self.dt_bias)
-        return y @ self.w_out.to(x.dtype)
+        return self.project(y, self.w_out)
 
 
 class Model(torch.nn.Module):
-    def __init__(self, vocab=64, dim=128, inner=256, dstate=16, rank=8, width=4, layers=2):
+    def __init__(self, vocab=64, dim=128, inner=256, dstate=16, rank=8, width=4, layers=2, eight_bit=False):
         super().__init__()
         self.embed = torch.nn.Parameter(torch.randn(vocab, dim) / math.sqrt(dim))
-        self.layers = torch.nn.ModuleList(Layer(dim, inner, dstate, rank, width) for _ in range(layers))
+        self.layers = torch.nn.ModuleList(Layer(dim, inner, dstate, rank, width, eight_bit) for _ in range(layers))
         # norm before each block (and the last one's output), after it, and its gate
         self.norm = torch.nn.ParameterList(torch.ones(dim) for _ in range(layers + 1))
         self.post = torch.nn.ParameterList(torch.ones(dim) for _ in range(layers))
@@ -111,11 +119,11 @@ def batch(g, n, length, table):
     return torch.stack(seq, 1)
 
 
-def main(steps=150, seqlen=96, sequences=16, generate=24, quiet=False):
+def main(steps=150, seqlen=96, sequences=16, generate=24, quiet=False, eight_bit=False):
     torch.manual_seed(0)
-    model = Model().cuda()
+    model = Model(eight_bit=eight_bit).cuda()
     vocab = model.embed.shape[0]
-    opt = torch.optim.AdamW(model.parameters(), lr=3e-3)
+    opt = ssd.AdamW(model.parameters(), lr=3e-3, state_bits=8 if eight_bit else 32)
     g = torch.Generator(device="cuda").manual_seed(1)
     table = torch.randperm(vocab, generator=g, device="cuda")
     losses = []
@@ -151,4 +159,6 @@ def main(steps=150, seqlen=96, sequences=16, generate=24, quiet=False):
 if __name__ == "__main__":
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--steps", type=int, default=150)
-    main(p.parse_args().steps)
+    p.add_argument("--eight-bit", action="store_true")
+    a = p.parse_args()
+    main(a.steps, eight_bit=a.eight_bit)

@@ -740,28 +740,38 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to; }
 // Few tokens: the weights take the MMA's rows, the tokens its columns, so no
 // row of the MMA is idle.
 bool few(int64_t m, int64_t n) { return m <= 128 && n > m; }
-constexpr int kFewest = 32;
-int columns_for(int64_t rn) { return rn <= kFewest ? kFewest : rn <= 64 ? 64 : 128; }
+int columns_for(int64_t rn) { return rn <= 32 ? 32 : rn <= 64 ? 64 : 128; }
 
 // Clusters of 1..8 CTAs that GB300's 152 SMs run at once, with one and with two
 // CTAs on an SM (cudaOccupancyMaxActiveClusters: they stay within a GPC).
 constexpr int kAtOnce[2][kMostSplits] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
 
-// As many parts of two blocks or more as run at once.
-int splits_for(int64_t tiles, int blocks, int bn)
+// us for a block of the summed dimension, as fitted to measurements from
+// 200 x 200 x 10000 to 2299 x 1984 x 4160.
+double block_time(int bn, bool rows_b)
 {
-    int s = 1;
-    if (bn < 256)
-        while (s < kMostSplits && 2 * (s + 1) <= blocks && tiles <= kAtOnce[bn == 128 ? 0 : 1][s])
-            ++s;
-    return s;
+    return bn == 256 ? (rows_b ? 0.68 : 0.43) : bn == 128 ? (rows_b ? 0.50 : 0.39) : (rows_b ? 0.62 : 0.52);
+}
+
+// Parts of the blocks, no more than run at once and two blocks at least: what they
+// save against the 1.5 us that joining them takes.
+int splits_for(int64_t tiles, int blocks, int bn, double block)
+{
+    int best = 1;
+    double least = block * blocks;
+    for (int s = 2; bn < 256 && s <= kMostSplits && 2 * s <= blocks && tiles <= kAtOnce[bn == 128 ? 0 : 1][s - 1]; ++s) {
+        const double t = block * ((blocks + s - 1) / s) + 1.5;
+        if (t < least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
 }
 
 // Columns of a tile: those with the least estimated time.  Waves of tiles (of
-// parts), each with a start and a time for each block, in us as fitted to
-// measurements from 200 x 200 x 10000 to 2299 x 1984 x 4160: a pair of CTAs is the
-// fastest by far where its tiles fill the SMs, and smaller tiles where they do
-// not (12010 x 192 x 1152: 8.8, 13.6 and 9.3 us with 64, 128 and 256 columns;
+// parts), each with a start and its blocks: a pair of CTAs is the fastest by far
+// where its tiles fill the SMs, and smaller tiles where they do not (12010 x 192 x 1152: 8.8, 13.6 and 9.3 us with 64, 128 and 256 columns;
 // 1602 x 1728 x 2853: 28, 28 and 17; 256 x 2560 x 5120: 14, 12 and 23).
 int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
 {
@@ -771,11 +781,11 @@ int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
     double least = 0;
     for (int bn : {64, 128, 256}) {
         const int64_t tiles = up(rm, bn == 256 ? 2 * kRows : kRows) * up(rn, bn);
-        const int splits = splits_for(tiles, blocks, bn), parts = (blocks + splits - 1) / splits;
+        const double block = block_time(bn, rows_b);
+        const int splits = splits_for(tiles, blocks, bn, block), part = (blocks + splits - 1) / splits;
         const int64_t waves = up(tiles * splits, bn == 256 ? 76 : bn == 128 ? 152 : 304);
         const double start = bn == 256 ? 5.0 : 3.5;
-        const double block = bn == 256 ? (rows_b ? 0.68 : 0.43) : bn == 128 ? (rows_b ? 0.50 : 0.39) : (rows_b ? 0.62 : 0.52);
-        const double t = (double)waves * (start + block * parts) + (splits > 1 ? 1.5 : 0);
+        const double t = (double)waves * (start + block * part) + (splits > 1 ? 1.5 : 0);
         if (!best || t < least) {
             best = bn;
             least = t;
@@ -783,6 +793,8 @@ int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
     }
     return best;
 }
+
+constexpr int kFewColumns = 32;  // of a tile of few tokens
 
 // The product of ra's rows (the MMA's) with rb's (its columns, bn a tile).
 Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int64_t rm, int64_t rn, int64_t n, int64_t k,
@@ -792,7 +804,7 @@ Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int
     p.m_tiles = (int)up(rm, bn == 256 ? 2 * kRows : kRows);
     p.n_tiles = (int)up(rn, bn);
     p.blocks = (int)up(k, 128);
-    p.splits = splits_for((int64_t)p.m_tiles * p.n_tiles, p.blocks, bn);
+    p.splits = splits_for((int64_t)p.m_tiles * p.n_tiles, p.blocks, bn, block_time(bn, !rb.tile));
     p.sa = ra.scale;
     p.sa_row = ra.scale_row;
     p.sa_block = ra.scale_block;
@@ -851,15 +863,16 @@ cudaError_t launch_block_matmul(const BlockMatrix &a, const BlockMatrix &b, void
 #undef SSD_BLOCK_MATMUL
 }
 
-// With more tokens a CTA would read and round the same ones as many times as there
-// are rows of tiles, and be bound by that (128 tokens: measured 77 us against 21).
-bool projects_few_tokens(int64_t tokens, int64_t outputs) { return tokens <= kFewest && few(tokens, outputs); }
+// With more tokens their rounding, four warps a CTA, takes longer than a launch of
+// the quantiser (2560 outputs of 5120 inputs: 1 token 7.5 us against 9.7, 32 tokens
+// 13.7 against 10.6).
+bool projects_few_tokens(int64_t tokens, int64_t outputs) { return tokens <= 16 && few(tokens, outputs); }
 
 cudaError_t launch_few_tokens(const void *x, int64_t row, const BlockMatrix &w, void *y, int64_t tokens, int64_t outputs,
                               int64_t inputs, bool bf16, cudaStream_t st)
 {
     const int sms = device_sm_count();
-    Params p = plan(w, BlockMatrix{}, kFewest, y, outputs, tokens, outputs, inputs, bf16);
+    Params p = plan(w, BlockMatrix{}, kFewColumns, y, outputs, tokens, outputs, inputs, bf16);
     if (!p.status)
         return cudaErrorUnknown;
     p.x = x;
@@ -869,8 +882,8 @@ cudaError_t launch_few_tokens(const void *x, int64_t row, const BlockMatrix &w, 
     CUtensorMap ta, none = {};
     if (!make_tmap_bytes(&ta, w.q, (uint64_t)inputs, (uint64_t)outputs, (uint64_t)w.row, kRows))
         return cudaErrorInvalidValue;
-    return bf16 ? launch<kFewest, true, true, __nv_bfloat16>(ta, none, none, p, sms, st)
-                : launch<kFewest, true, true, float>(ta, none, none, p, sms, st);
+    return bf16 ? launch<kFewColumns, true, true, __nv_bfloat16>(ta, none, none, p, sms, st)
+                : launch<kFewColumns, true, true, float>(ta, none, none, p, sms, st);
 }
 
 }  // namespace ssd

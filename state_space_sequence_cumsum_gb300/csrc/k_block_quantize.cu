@@ -83,12 +83,18 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
 
     using F = Four<TI>;
     F v[kRowsOfWarp];
-    if (kVec && r0 + kRowsOfWarp <= g.rows && cb * kB + kB <= g.cols) {
-        // all of them in flight before the first is used
-        const TI *p = x + r0 * g.row + c0;
+    if (kVec && c0 + 4 <= g.cols) {
+        // all of them in flight before the first is used; rows past the last are
+        // the last, and then zeros
 #pragma unroll
         for (int i = 0; i < kRowsOfWarp; ++i)
-            v[i].v = load_ahead_as<decltype(v[i].v)>(p + i * g.row);
+            v[i].v = load_ahead_as<decltype(v[i].v)>(x + min64(r0 + i, g.rows - 1) * g.row + c0);
+        if (r0 + kRowsOfWarp > g.rows) {
+#pragma unroll
+            for (int i = 0; i < kRowsOfWarp; ++i)
+                if (r0 + i >= g.rows)
+                    v[i] = F{};
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kRowsOfWarp; ++i) {
@@ -137,8 +143,10 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
                 if (c0 + 4 <= g.cols) {
                     *reinterpret_cast<uint32_t *>(o) = b;
                 } else {
-                    for (int j = 0; c0 + j < g.cols; ++j)
-                        o[j] = (uint8_t)(b >> (8 * j));
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (c0 + j < g.cols)
+                            o[j] = (uint8_t)(b >> (8 * j));
                 }
             }
         }
@@ -175,9 +183,11 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
             if (first + 16 <= g.rows) {
                 *reinterpret_cast<uint4 *>(o) = b;
             } else {
-                const uint8_t *e = reinterpret_cast<const uint8_t *>(&b);
-                for (int j = 0; first + j < g.rows; ++j)
-                    o[j] = e[j];
+                const uint32_t e[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (first + j < g.rows)
+                        o[j] = (uint8_t)(e[j >> 2] >> (8 * (j & 3)));
             }
         }
     }

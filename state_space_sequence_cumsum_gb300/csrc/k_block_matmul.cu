@@ -51,7 +51,6 @@ using namespace tc;
 constexpr int kRows = 128;                  // MMA rows of a tile
 constexpr uint32_t kABytes = kRows * 128;   // one block of them
 constexpr int kMostSplits = 8;              // CTAs of a cluster (portable limit)
-constexpr int kScales = 8;                  // blocks whose scales are in shared memory
 
 // kFused: the MMA's columns are tokens that are quantised here.
 template <int BN, bool kFused = false> struct Tile {
@@ -215,14 +214,17 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     constexpr int ST = T::kStages, NB = T::kBuffers, H = T::kHalves, HN = T::kHN, CW = T::kCW;
     static_assert(HN <= 128, "a half's columns share a scale");
     constexpr int LW = T::kPair ? 32 : 16;  // columns of a load from TMEM
+    // blocks whose scales are in shared memory, and how many of a tile come under one
+    // barrier: a pair's adding threads have no time for one each (382 -> 344 us)
+    constexpr int BATCH = T::kPair && !kRowsB ? 8 : 1, SCALES = 8 + BATCH / 8 * 8;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     unsigned char *staging = T::kPair ? smem + ST * T::kStageBytes : smem;
     __shared__ uint64_t full[ST], empty[ST], done[H][NB], freed[H][NB];
     __shared__ uint32_t tmem_slot;
-    // scales of kScales blocks: of the rows, and of the columns (without kRowsB of each 128 columns)
-    __shared__ uint64_t scales_full[kScales], scales_empty[kScales];
-    __shared__ __align__(16) float sa_smem[kScales][kRows], sb_smem[kScales][kRowsB ? BN : 2];
+    // scales: of the rows, and of the columns (without kRowsB of each 128 columns)
+    __shared__ uint64_t scales_full[SCALES / BATCH], scales_empty[SCALES / BATCH];
+    __shared__ __align__(16) float sa_smem[SCALES][kRows], sb_smem[SCALES][kRowsB ? BN : 2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's tiles and, in each, its blocks of the summed dimension
@@ -272,7 +274,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             mbar_init(&done[0][i], 1);
             mbar_init(&freed[0][i], 4 * T::kWGH * (T::kPair ? 2 : 1));
         }
-        for (int i = 0; i < kScales; ++i) {
+        for (int i = 0; i < SCALES / BATCH; ++i) {
             mbar_init(&scales_full[i], kFused ? 33 : 32);
             mbar_init(&scales_empty[i], T::kAddWarps);
         }
@@ -327,7 +329,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         // ---------------------------------- scales, and without a pair the tiles
         const bool issues = !T::kPair && elect_one();
         wait_for_kernel_before();
-        uint32_t it = 0;
+        uint32_t it = 0, g = 0, g_phase = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
             int mt, nt;
@@ -349,12 +351,13 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 sb[j] = p.sb + (in ? c >> p.sb_shift : 0) * p.sb_row + kb0 * p.sb_block;
             }
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = it % ST, z = it % kScales;
+                const uint32_t s = it % ST, in_batch = (uint32_t)(kb - kb0) % BATCH;
                 const bool load = !T::kPair && it >= ST;  // the first ones were in the setup
                 ok = (!load || wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status)) &&
-                     wait_for(&scales_empty[z], ((it / kScales) & 1) ^ 1, p.status);
+                     (in_batch || wait_for(&scales_empty[g], g_phase ^ 1, p.status));
                 if (!ok)
                     break;
+                const uint32_t z = g * BATCH + in_batch;
                 if (load && issues)
                     load_tiles(kb, s, mt, nt);
                 __syncwarp();
@@ -369,7 +372,11 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                         copy_scale(&sb_smem[z][kRowsB ? j * 32 + lane : lane], sb[j], in_b >> j & 1);
                     sb[j] += p.sb_block;
                 }
-                copies_arrive(&scales_full[z]);
+                if (in_batch == BATCH - 1 || kb + 1 == kb1) {
+                    copies_arrive(&scales_full[g]);
+                    g_phase ^= ++g == SCALES / BATCH;
+                    g %= SCALES / BATCH;
+                }
             }
         }
         cp_async_wait_all();
@@ -381,7 +388,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             const int own = warp - (T::kAddWarps + 2), rows = (int)p.n;
             bool ok = true;
             for (uint32_t it = own; ok && kb0 + (int)it < kb1; it += T::kQuantWarps) {
-                const uint32_t s = it % ST, z = it % kScales;
+                const uint32_t s = it % ST, z = it % SCALES;
                 const int64_t c = (int64_t)(kb0 + it) * 128 + lane * 4;
                 const TX *x = static_cast<const TX *>(p.x) + c;
                 unsigned char *b = smem + s * T::kStageBytes + kABytes;
@@ -407,7 +414,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                     }
                     if (r0 == 0)
                         ok = wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status) &&
-                             wait_for(&scales_empty[z], ((it / kScales) & 1) ^ 1, p.status);
+                             wait_for(&scales_empty[z], ((it / SCALES) & 1) ^ 1, p.status);
                     if (!ok)
                         break;
 #pragma unroll
@@ -474,11 +481,11 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         const int wg = warp >> 2, quarter = warp & 3;
         const int h = wg / T::kWGH, in_tile = wg * CW;  // its half, and its first column in the tile
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + in_tile;
-        // the next block's TMEM buffer and scales, and the phases of their barriers
-        uint32_t b = 0, b_phase = 0, z = 0, z_phase = 0;
+        // the next block's TMEM buffer, its batch of scales, and their barriers' phases
+        uint32_t b = 0, b_phase = 0, g = 0, g_phase = 0;
         const uint32_t freed_at = T::kPair ? in_cta(smem_u32(&freed[h][0]), 0) : 0;
         const float *my_sa = &sa_smem[0][quarter * 32 + lane];
-        bool scales_ready = false, done_ready = false;  // as last asked
+        bool done_ready = false;  // as last asked
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
             int mt, nt;
@@ -490,7 +497,8 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             for (int i = 0; i < CW; ++i)
                 acc[i] = 0.f;
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = (scales_ready || wait_for(&scales_full[z], z_phase, p.status)) &&
+                const uint32_t in_batch = (uint32_t)(kb - kb0) % BATCH, z = g * BATCH + in_batch;
+                ok = (in_batch || wait_for(&scales_full[g], g_phase, p.status)) &&
                      (done_ready || wait_for(&done[h][b], b_phase, p.status));
                 if (!ok)
                     break;
@@ -500,7 +508,6 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 const float wa = my_sa[z * kRows];
                 const float f = kRowsB ? wa : wa * sb_smem[z][h];
                 const float *sbz = &sb_smem[z][kRowsB ? in_tile : 0];
-                const uint32_t z0 = z;
 #pragma unroll
                 for (int c = 0; c < CW / LW; ++c) {
                     tmem_ld_wait_on(r[c & 1]);
@@ -512,17 +519,12 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                             warp_arrive_cluster(freed_at + b * 8);
                         else
                             warp_arrive(&freed[h][b]);
-                        if (++z == kScales) {
-                            z = 0;
-                            z_phase ^= 1;
-                        }
                         if (++b == NB) {
                             b = 0;
                             b_phase ^= 1;
                         }
                         // is the next block there already?  The answer comes under
                         // these products (a test: try_wait would park the warp)
-                        scales_ready = mbar_test(&scales_full[z], z_phase);
                         done_ready = mbar_test(&done[h][b], b_phase);
                     }
 #pragma unroll
@@ -543,7 +545,11 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                             acc[c * LW + i + j] = fmaf(r[c & 1][i + j], w[j], acc[c * LW + i + j]);
                     }
                 }
-                warp_arrive(&scales_empty[z0]);
+                if (in_batch == BATCH - 1 || kb + 1 == kb1) {
+                    warp_arrive(&scales_empty[g]);
+                    g_phase ^= ++g == SCALES / BATCH;
+                    g %= SCALES / BATCH;
+                }
             }
             if (!T::kPair && p.splits > 1) {
                 // partial sums: rows of BN + 4 (out's rows), or columns of 128 (swapped)

@@ -76,23 +76,28 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
     __shared__ __align__(16) uint4 turned[kB * kB / 16];  // [column][16-byte piece ^ (column / 4 % 8)]
     let_next_kernel_start();
     wait_for_kernel_before();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const unsigned col_blocks = (unsigned)((g.cols + kB - 1) / kB);
     const int64_t rb = blockIdx.x / col_blocks, r0 = rb * kB + warp * kRowsOfWarp;
     const int64_t cb = blockIdx.x % col_blocks, c0 = cb * kB + lane * 4;
 
+    const int rows = (int)max(min64(kRowsOfWarp, g.rows - r0), (int64_t)0);  // of this warp's that exist
     using F = Four<TI>;
     F v[kRowsOfWarp];
-    if (kVec && c0 + 4 <= g.cols) {
+    if (kVec && c0 + 4 <= g.cols && rows > 0) {
         // all of them in flight before the first is used; rows past the last are
         // the last, and then zeros
+        const TI *p = x + r0 * g.row + c0;
 #pragma unroll
-        for (int i = 0; i < kRowsOfWarp; ++i)
-            v[i].v = load_ahead_as<decltype(v[i].v)>(x + min64(r0 + i, g.rows - 1) * g.row + c0);
-        if (r0 + kRowsOfWarp > g.rows) {
+        for (int i = 0; i < kRowsOfWarp; ++i) {
+            v[i].v = load_ahead_as<decltype(v[i].v)>(p);
+            if (i + 1 < rows)
+                p += g.row;
+        }
+        if (rows < kRowsOfWarp) {
 #pragma unroll
             for (int i = 0; i < kRowsOfWarp; ++i)
-                if (r0 + i >= g.rows)
+                if (i >= rows)
                     v[i] = F{};
         }
     } else {
@@ -101,7 +106,7 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
             TI e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                e[j] = r0 + i < g.rows && c0 + j < g.cols ? x[(r0 + i) * g.row + c0 + j] : from_f32<TI>(0.f);
+                e[j] = i < rows && c0 + j < g.cols ? x[(r0 + i) * g.row + c0 + j] : from_f32<TI>(0.f);
             memcpy(&v[i].v, e, sizeof(e));
         }
     }
@@ -127,31 +132,36 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
             scale[rb * g.scale_ld + cb] = tile_scale;
     }
     if (q) {
-        float mine = 0.f;  // lane i keeps row i's scale
+        float inverse = tile_inverse;
+        if (!g.tile) {  // lane i has row i's
+            uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < kRowsOfWarp; ++i) {
-            float s = tile_scale, inverse = tile_inverse;
-            if (!g.tile) {
-                scale_of<kE5M2>(__reduce_max_sync(0xffffffffu, F::top(v[i].peak())), s, inverse);
-                mine = lane == i ? s : mine;
+            for (int i = 0; i < kRowsOfWarp; ++i) {
+                const uint32_t t = __reduce_max_sync(0xffffffffu, F::top(v[i].peak()));
+                top = lane == i ? t : top;
             }
-            const int64_t r = r0 + i;
-            if (r < g.rows && c0 < g.cols) {
-                const uint32_t b = to_bytes<kE5M2>(v[i][0] * inverse, v[i][1] * inverse, v[i][2] * inverse,
-                                                   v[i][3] * inverse);
-                uint8_t *o = q + r * g.row_q + c0;
-                if (c0 + 4 <= g.cols) {
-                    *reinterpret_cast<uint32_t *>(o) = b;
-                } else {
+            float s;
+            scale_of<kE5M2>(top, s, inverse);
+            if (lane < rows)
+                scale[cb * g.scale_ld + r0 + lane] = s;
+        }
+        uint8_t *o = q + r0 * g.row_q + c0;
+        const int left = (int)min64(4, g.cols - c0);  // of this thread's columns, or none
 #pragma unroll
-                    for (int j = 0; j < 3; ++j)
-                        if (c0 + j < g.cols)
-                            o[j] = (uint8_t)(b >> (8 * j));
-                }
+        for (int i = 0; i < kRowsOfWarp; ++i, o += g.row_q) {
+            const float w = g.tile ? inverse : __shfl_sync(0xffffffffu, inverse, i);
+            const uint32_t b = to_bytes<kE5M2>(v[i][0] * w, v[i][1] * w, v[i][2] * w, v[i][3] * w);
+            if (i >= rows)
+                continue;
+            if (left == 4) {
+                *reinterpret_cast<uint32_t *>(o) = b;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (j < left)
+                        o[j] = (uint8_t)(b >> (8 * j));
             }
         }
-        if (!g.tile && lane < kRowsOfWarp && r0 + lane < g.rows)
-            scale[cb * g.scale_ld + r0 + lane] = mine;
     }
     if (qt) {
 #pragma unroll

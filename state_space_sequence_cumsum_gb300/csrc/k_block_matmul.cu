@@ -22,18 +22,19 @@
 // columns have to come out of TMEM and be added, 128 of them by each thread.
 // The threads that add are the slower side (some 750 clocks a block: two warps a
 // scheduler, the rest of the register file holds their sums), so their loop has
-// one load from TMEM in flight under the products of the one before and asks for
-// the next block's barriers early.  A block is two MMAs of 128 columns, each with
-// two TMEM buffers, barriers and an issuing warp of its own: one of 256 leaves
-// TMEM full for longer (measured 420 us against 345 at 16384 x 10576 x 2560).
+// one load from TMEM in flight under the products of the one before, asks for the
+// next block's barrier early and waits for scales once in eight blocks.  A block
+// is two MMAs of 128 columns, each with two TMEM buffers, barriers and an issuing
+// warp of its own: one of 256 leaves TMEM full for longer (420 us against 378).
 //   The others take one tile, or with few tiles a part of its blocks: the CTAs
 // of a cluster then add their partial sums through distributed shared memory, in
 // the order of the parts.  A projection of few tokens (kFused) quantises them on
 // the way in: four warps read x and write the MMA's columns and their scales,
 // under the latency of the weights' loads, so it is one launch.
-//   16384 x 10576 x 2560, a scale for each 128 x 128 of b: 345 us, 2570 TFLOP/s
-// (1.34 of the measured bf16 rate); with a scale for each row's block on both
-// sides 535 us, bound by one more product per sum.
+//   16384 x 10576 x 2560, a scale for each 128 x 128 of b: 381 us, 2330 TFLOP/s
+// (1.22 of the measured bf16 rate; 347 us with scales of zero, which take less
+// power).  With a scale for each row's block on both sides 545 us, bound by one
+// more product per sum.  8 x 10576 x 2560 with its tokens rounded here 9.0 us.
 #include <algorithm>
 #include <type_traits>
 

@@ -280,6 +280,9 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             mbar_init(&scales_empty[i], T::kAddWarps);
         }
         fence_barrier_init();
+        fence_proxy_async_smem();
+        // also keeps the other warps' bounded waits from starting before: they are
+        // at the barrier below
         wait_for_kernel_before();
         if (!T::kPair) {  // the first blocks are on their way during the rest of the setup
             int mt, nt;

@@ -63,7 +63,11 @@ class AdamW(torch.optim.Optimizer):
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
-        """grad_scale: a factor of all gradients, a number or a CUDA scalar."""
+        """grad_scale: a factor of all gradients, a number or a CUDA scalar.  Not
+        for capture into a graph, whose replays would repeat one step's number:
+        ssd_adamw_step takes it from the device."""
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("AdamW.step counts its steps on the host: capture ssd_adamw_step with step on the device")
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -76,8 +80,7 @@ class AdamW(torch.optim.Optimizer):
                 s = self.state[p]
                 if not s:
                     s.update(self._new_state(p, group["state_bits"]))
-                s["step"] += 1
-                calls.setdefault((p.device, p.dtype, p.grad.dtype, s["step"]), []).append((p, p.grad, s))
+                calls.setdefault((p.device, p.dtype, p.grad.dtype, s["step"] + 1), []).append((p, p.grad, s))
             for (_, _, _, step), items in calls.items():
                 states = [s for _, _, s in items]
                 scales = {}
@@ -86,4 +89,6 @@ class AdamW(torch.optim.Optimizer):
                 ssd_adamw_step([p for p, _, _ in items], [g for _, g, _ in items], [s["m"] for s in states],
                                [s["v"] for s in states], step, group["lr"], group["betas"], group["eps"],
                                group["weight_decay"], grad_scale=grad_scale, **scales)
+                for s in states:
+                    s["step"] = step
         return loss

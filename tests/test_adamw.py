@@ -309,3 +309,33 @@ def test_optimiser_state_is_saved_and_loaded(bits):
     for k, v in a.state[p].items():
         w = fresh.state[q][k]
         assert v == w if k == "step" else (v.dtype == w.dtype and torch.equal(v.float(), w.float()))
+
+
+def test_the_optimisers_step_is_not_captured():
+    """A replay would repeat the step's number: refused, with nothing changed."""
+    p = torch.ones(300, device="cuda", requires_grad=True)
+    p.grad = torch.ones_like(p)
+    opt = ssd.AdamW([p])
+    opt.step()
+    torch.cuda.synchronize()
+    before, step = p.detach().clone(), opt.state[p]["step"]
+    graph, other = torch.cuda.CUDAGraph(), torch.zeros(1, device="cuda")
+    with torch.cuda.graph(graph):
+        other += 1
+        with pytest.raises(RuntimeError, match="step on the device"):
+            opt.step()
+    graph.replay()
+    assert torch.equal(p, before) and opt.state[p]["step"] == step == 1 and float(other) == 1
+
+
+def test_a_refused_step_is_not_counted():
+    p = torch.ones(300, device="cuda", requires_grad=True)
+    opt = ssd.AdamW([p])
+    p.grad = torch.ones_like(p)
+    opt.param_groups[0]["lr"] = -1.0
+    with pytest.raises(ssd.SsdError):
+        opt.step()
+    assert opt.state[p]["step"] == 0 and torch.equal(p, torch.ones_like(p))
+    opt.param_groups[0]["lr"] = 0.5
+    opt.step()
+    assert opt.state[p]["step"] == 1

@@ -191,7 +191,7 @@ __device__ __forceinline__ void copy_rows(const Params &p, const unsigned char *
         const int v = k * step + own;
         const unsigned char *from = stage + (v % per) * sizeof(T);
         T *o = static_cast<T *>(p.out) + row0 * p.ld + col + v;
-        if (col + v >= p.n)
+        if (v * (int)sizeof(T) >= bytes || col + v >= p.n)
             continue;
 #pragma unroll 4
         for (int r = 0; r < rows; ++r, o += p.ld) {

@@ -166,6 +166,18 @@ def test_matmul_many_tiles(m, n, k, out, tile):
     check_product(ssd.ssd_block_matmul(a, sa, b, sb, out_dtype=out), va, vb)
 
 
+@pytest.mark.parametrize("n", [29, 30, 33, 34, 36, 40, 50, 62, 63, 64, 90, 94, 100, 126, 127, 130, 186, 250, 333, 500])
+@pytest.mark.parametrize("m,k", [(150, 200), (700, 1500), (8071, 300)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_matmul_widths(m, n, k, out):
+    """Rows of the output on every kind of boundary, and tiles of every width."""
+    a, sa, va = operand(m, k, False, 1)
+    b, sb, vb = operand(n, k, True, 2)
+    y = torch.full((m, n), float("nan"), dtype=out, device="cuda")
+    ssd.ssd_block_matmul(a, sa, b, sb, out_dtype=out, out=y)
+    check_product(y, va, vb)
+
+
 @pytest.mark.parametrize("m,n,k", [(40, 300, 900), (300, 300, 900), (2000, 2056, 300)])
 @pytest.mark.parametrize("ta,tb", [(E4, E5), (E5, E4), (E5, E5)])
 def test_matmul_types(m, n, k, ta, tb):

@@ -14,8 +14,8 @@
 // output is then written transposed), its BN columns rows of the other matrix.
 //
 // Warps of a CTA: 4 WG that add (thread = MMA row, CW columns), then one that
-// loads tiles, one (a pair: two) that issues MMAs, one that loads scales some
-// blocks ahead (without a pair: the tiles' loader).
+// loads tiles, one (a pair: two) that issues MMAs, and in a pair one that loads
+// scales some blocks ahead.
 //   BN 256: two CTAs take a tile of 256 x 256 with cta_group::2 MMAs and walk
 // their tiles persistently; the output leaves by TMA while the next tile runs.
 // What bounds it: a block's MMAs take 512 clocks, and in the same time its 256
@@ -28,13 +28,17 @@
 // warp of its own: one of 256 leaves TMEM full for longer (420 us against 378).
 //   The others take one tile, or with few tiles a part of its blocks: the CTAs
 // of a cluster then add their partial sums through distributed shared memory, in
-// the order of the parts.  A projection of few tokens (kFused) quantises them on
+// the order of the parts.  The threads that add load their scales themselves: no
+// barrier, and no warp with more to do than a block takes (1536 x 1536 x 2560 12.2
+// -> 8.9 us, 1531 x 507 x 2561 11.6 -> 8.9).  Scales of each column, broadcast to
+// the warp from shared memory, cost as much of its bandwidth as tiles and MMAs do
+// (12.7 and 11.3 us).  A projection of few tokens (kFused) quantises them on
 // the way in: four warps read x and write the MMA's columns and their scales,
 // under the latency of the weights' loads, so it is one launch.
 //   16384 x 10576 x 2560, a scale for each 128 x 128 of b: 381 us, 2330 TFLOP/s
 // (1.22 of the measured bf16 rate; 347 us with scales of zero, which take less
 // power).  With a scale for each row's block on both sides 545 us, bound by one
-// more product per sum.  8 x 10576 x 2560 with its tokens rounded here 9.0 us.
+// more product per sum.  8 x 10576 x 2560 with its tokens rounded here 8.8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -215,8 +219,10 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     constexpr int ST = T::kStages, NB = T::kBuffers, H = T::kHalves, HN = T::kHN, CW = T::kCW;
     static_assert(HN <= 128, "a half's columns share a scale");
     constexpr int LW = T::kPair ? 32 : 16;  // columns of a load from TMEM
-    // blocks whose scales are in shared memory, and how many of a tile come under one
-    // barrier: a pair's adding threads have no time for one each (382 -> 344 us)
+    // A pair's scales, and those of tokens that are quantised here, come through shared
+    // memory: so many blocks of them, and so many of a tile under one barrier (a pair's
+    // adding threads have no time for one each: 382 -> 344 us).
+    constexpr bool kShared = T::kPair || kFused;
     constexpr int BATCH = T::kPair && !kRowsB ? 8 : 1, SCALES = 8 + BATCH / 8 * 8;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -225,7 +231,10 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
     __shared__ uint32_t tmem_slot;
     // scales: of the rows, and of the columns (without kRowsB of each 128 columns)
     __shared__ uint64_t scales_full[SCALES / BATCH], scales_empty[SCALES / BATCH];
-    __shared__ __align__(16) float sa_smem[SCALES][kRows], sb_smem[SCALES][kRowsB ? BN : 2];
+    __shared__ float sa_smem[T::kPair ? SCALES : 1][kRows];
+    __shared__ __align__(16) float sb_smem[kShared ? SCALES : 1][kRowsB ? BN : 2];
+    // without kShared: an adding warp's columns' scales of two blocks
+    __shared__ __align__(16) float own_sb[!kShared && kRowsB ? T::kAddWarps : 1][2][CW];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this CTA's tiles and, in each, its blocks of the summed dimension
@@ -276,7 +285,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
             mbar_init(&freed[0][i], 4 * T::kWGH * (T::kPair ? 2 : 1));
         }
         for (int i = 0; i < SCALES / BATCH; ++i) {
-            mbar_init(&scales_full[i], kFused ? 33 : 32);
+            mbar_init(&scales_full[i], kFused ? 1 : 32);
             mbar_init(&scales_empty[i], T::kAddWarps);
         }
         fence_barrier_init();
@@ -312,7 +321,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         // registers of these warps to those that add: 256 x 216 + 128 x 56 of the
         // 384 x 168 that the CTA was launched with
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (T::kPair && warp == T::kAddWarps) {
+    if (warp == T::kAddWarps) {
         // ------------------------------------------------------------- tiles
         if (elect_one()) {
             wait_for_kernel_before();
@@ -323,22 +332,23 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 place(t, mt, nt);
                 for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
                     const uint32_t s = it % ST;
+                    if (!T::kPair && it < ST)  // on its way since the setup
+                        continue;
                     ok = wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status);
                     if (ok)
                         load_tiles(kb, s, mt, nt);
                 }
             }
         }
-    } else if (warp == (T::kPair ? T::kAddWarps + 3 : T::kAddWarps)) {
-        // ---------------------------------- scales, and without a pair the tiles
-        const bool issues = !T::kPair && elect_one();
+    } else if (T::kPair && warp == T::kAddWarps + 3) {
+        // ----------------------------------------------------- a pair's scales
         wait_for_kernel_before();
-        uint32_t it = 0, g = 0, g_phase = 0;
+        uint32_t g = 0, g_phase = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
             int mt, nt;
             place(t, mt, nt);
-            const int64_t row0 = (int64_t)mt * T::kTileRows + (T::kPair ? rank * kRows : 0);
+            const int64_t row0 = (int64_t)mt * T::kTileRows + rank * kRows;
             const float *sa[kRows / 32], *sb[kRowsB ? BN / 32 : 1];
             uint32_t in_a = 0, in_b = 0;  // bit j: this lane's j-th scale exists
 #pragma unroll
@@ -348,22 +358,17 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 sa[j] = p.sa + (r < p.m ? r >> p.sa_shift : 0) * p.sa_row + kb0 * p.sa_block;
             }
 #pragma unroll
-            for (int j = 0; j < (kFused ? 0 : kRowsB ? BN / 32 : 1); ++j) {
+            for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
                 const int64_t c = (int64_t)nt * BN + (kRowsB ? j * 32 + lane : lane * 128);
                 const bool in = c < p.n && (kRowsB || lane < H);
                 in_b |= (uint32_t)in << j;
                 sb[j] = p.sb + (in ? c >> p.sb_shift : 0) * p.sb_row + kb0 * p.sb_block;
             }
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = it % ST, in_batch = (uint32_t)(kb - kb0) % BATCH;
-                const bool load = !T::kPair && it >= ST;  // the first ones were in the setup
-                ok = (!load || wait_for(&empty[s], ((it / ST) & 1) ^ 1, p.status)) &&
-                     (in_batch || wait_for(&scales_empty[g], g_phase ^ 1, p.status));
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const uint32_t in_batch = (uint32_t)(kb - kb0) % BATCH, z = g * BATCH + in_batch;
+                ok = in_batch || wait_for(&scales_empty[g], g_phase ^ 1, p.status);
                 if (!ok)
                     break;
-                const uint32_t z = g * BATCH + in_batch;
-                if (load && issues)
-                    load_tiles(kb, s, mt, nt);
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < kRows / 32; ++j) {
@@ -371,7 +376,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                     sa[j] += p.sa_block;
                 }
 #pragma unroll
-                for (int j = 0; j < (kFused ? 0 : kRowsB ? BN / 32 : 1); ++j) {
+                for (int j = 0; j < (kRowsB ? BN / 32 : 1); ++j) {
                     if (kRowsB || lane < H)
                         copy_scale(&sb_smem[z][kRowsB ? j * 32 + lane : lane], sb[j], in_b >> j & 1);
                     sb[j] += p.sb_block;
@@ -488,7 +493,39 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
         // the next block's TMEM buffer, its batch of scales, and their barriers' phases
         uint32_t b = 0, b_phase = 0, g = 0, g_phase = 0;
         const uint32_t freed_at = T::kPair ? in_cta(smem_u32(&freed[h][0]), 0) : 0;
-        const float *my_sa = &sa_smem[0][quarter * 32 + lane];
+        // Without a pair the scales come straight from global memory, two blocks at a
+        // time and two ahead: no barrier, and no warp that brings them, in a block's
+        // way (1024 x 1024 x 12800 by tiles of 64 columns 40 -> 25 us).
+        const float *sa = nullptr, *sb[kRowsB ? CW / 32 : 1];
+        float next_a[2], next_b[2][kRowsB ? CW / 32 : 1], now[2];
+        auto load_scales = [&](int kb) {  // of blocks kb and kb + 1
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (kb + j >= kb1)
+                    break;
+                next_a[j] = load_ahead_as<float>(sa);
+                sa += p.sa_block;
+#pragma unroll
+                for (int i = 0; i < (kFused ? 0 : kRowsB ? CW / 32 : 1); ++i) {
+                    next_b[j][i] = load_ahead_as<float>(sb[i]);
+                    sb[i] += p.sb_block;
+                }
+            }
+        };
+        if (!T::kPair) {
+            int mt, nt;
+            place(first, mt, nt);
+            // scales of rows and columns that do not exist: the first one's
+            const int64_t r = (int64_t)mt * kRows + quarter * 32 + lane;
+            sa = p.sa + (r < p.m ? r >> p.sa_shift : 0) * p.sa_row + kb0 * p.sa_block;
+#pragma unroll
+            for (int i = 0; i < (kFused ? 0 : kRowsB ? CW / 32 : 1); ++i) {
+                const int64_t c = (int64_t)nt * BN + in_tile + (kRowsB ? i * 32 + lane : 0);
+                sb[i] = p.sb + (c < p.n ? c >> p.sb_shift : 0) * p.sb_row + kb0 * p.sb_block;
+            }
+            wait_for_kernel_before();
+            load_scales(kb0);
+        }
         bool done_ready = false;  // as last asked
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
@@ -502,16 +539,36 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                 acc[i] = 0.f;
             for (int kb = kb0; kb < kb1; ++kb) {
                 const uint32_t in_batch = (uint32_t)(kb - kb0) % BATCH, z = g * BATCH + in_batch;
-                ok = (in_batch || wait_for(&scales_full[g], g_phase, p.status)) &&
+                const uint32_t of_two = (uint32_t)(kb - kb0) & 1;
+                if (!T::kPair && !of_two) {
+                    if (!kShared && kRowsB)
+                        __syncwarp();  // the two before have been read
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        now[j] = kRowsB ? next_a[j] : next_a[j] * next_b[j][0];
+#pragma unroll
+                        for (int i = 0; i < (!kShared && kRowsB ? CW / 32 : 0); ++i)
+                            own_sb[warp][j][i * 32 + lane] = next_b[j][i];
+                    }
+                    if (!kShared && kRowsB)
+                        __syncwarp();
+                    load_scales(kb + 2);
+                }
+                ok = (!kShared || in_batch || wait_for(&scales_full[g], g_phase, p.status)) &&
                      (done_ready || wait_for(&done[h][b], b_phase, p.status));
                 if (!ok)
                     break;
                 tc_fence_after();
                 float r[2][LW];
                 tmem_ld_f32(at + b * BN, r[0]);
-                const float wa = my_sa[z * kRows];
-                const float f = kRowsB ? wa : wa * sb_smem[z][h];
-                const float *sbz = &sb_smem[z][kRowsB ? in_tile : 0];
+                float f;
+                if (T::kPair) {
+                    f = sa_smem[z][quarter * 32 + lane];
+                    f = kRowsB ? f : f * sb_smem[z][h];
+                } else {
+                    f = of_two ? now[1] : now[0];
+                }
+                const float *sbz = kShared ? &sb_smem[z][kRowsB ? in_tile : 0] : own_sb[kRowsB ? warp : 0][of_two];
 #pragma unroll
                 for (int c = 0; c < CW / LW; ++c) {
                     tmem_ld_wait_on(r[c & 1]);
@@ -549,7 +606,7 @@ block_matmul_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constan
                             acc[c * LW + i + j] = fmaf(r[c & 1][i + j], w[j], acc[c * LW + i + j]);
                     }
                 }
-                if (in_batch == BATCH - 1 || kb + 1 == kb1) {
+                if (kShared && (in_batch == BATCH - 1 || kb + 1 == kb1)) {
                     warp_arrive(&scales_empty[g]);
                     g_phase ^= ++g == SCALES / BATCH;
                     g %= SCALES / BATCH;
@@ -756,21 +813,36 @@ int columns_for(int64_t rn) { return rn <= 32 ? 32 : rn <= 64 ? 64 : 128; }
 // CTAs on an SM (cudaOccupancyMaxActiveClusters: they stay within a GPC).
 constexpr int kAtOnce[2][kMostSplits] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
 
-// us for a block of the summed dimension, as fitted to measurements from
-// 200 x 200 x 10000 to 2299 x 1984 x 4160.
-double block_time(int bn, bool rows_b)
+// Estimated us of a product in tiles of bn columns, its blocks in `splits` parts:
+// waves of CTAs, each with a start and its blocks, and the parts' joining.  Fitted to
+// measurements from 40 x 2560 x 5120 to 2299 x 1984 x 4160; two CTAs on an SM slow one
+// another down.
+double estimate(int64_t tiles, int blocks, int bn, bool rows_b, bool fused, int splits)
 {
-    return bn == 256 ? (rows_b ? 0.68 : 0.43) : bn == 128 ? (rows_b ? 0.50 : 0.39) : (rows_b ? 0.62 : 0.52);
+    const bool alone = bn >= 128 || tiles <= kAtOnce[0][splits - 1];
+    double block = alone ? 0.22 : 0.30, join = alone ? 2.0 : 3.5;
+    if (bn == 256) {
+        block = rows_b ? 0.69 : 0.41;
+    } else if (bn == 128) {
+        block = rows_b ? 0.47 : 0.27;
+        join = 3.0;
+    } else if (bn == 64) {
+        block = alone ? (rows_b ? 0.38 : 0.24) : (rows_b ? 0.56 : 0.34);
+    } else if (fused) {
+        block = alone ? 0.35 : 0.40;
+        join = alone ? 1.5 : 2.5;
+    }
+    const int64_t waves = up(tiles * splits, bn == 256 ? 76 : bn == 128 ? 152 : 304);
+    return (double)waves * ((bn == 256 ? 5.0 : 3.5) + block * ((blocks + splits - 1) / splits)) + (splits > 1 ? join : 0);
 }
 
-// Parts of the blocks, no more than run at once and two blocks at least: what they
-// save against the 1.5 us that joining them takes.
-int splits_for(int64_t tiles, int blocks, int bn, double block)
+// Parts of the blocks: no more than run at once, and two blocks at least in each.
+int splits_for(int64_t tiles, int blocks, int bn, bool rows_b, bool fused = false)
 {
     int best = 1;
-    double least = block * blocks;
+    double least = estimate(tiles, blocks, bn, rows_b, fused, 1);
     for (int s = 2; bn < 256 && s <= kMostSplits && 2 * s <= blocks && tiles <= kAtOnce[bn == 128 ? 0 : 1][s - 1]; ++s) {
-        const double t = block * ((blocks + s - 1) / s) + 1.5;
+        const double t = estimate(tiles, blocks, bn, rows_b, fused, s);
         if (t < least) {
             best = s;
             least = t;
@@ -779,10 +851,10 @@ int splits_for(int64_t tiles, int blocks, int bn, double block)
     return best;
 }
 
-// Columns of a tile: those with the least estimated time.  Waves of tiles (of
-// parts), each with a start and its blocks: a pair of CTAs is the fastest by far
-// where its tiles fill the SMs, and smaller tiles where they do not (12010 x 192 x 1152: 8.8, 13.6 and 9.3 us with 64, 128 and 256 columns;
-// 1602 x 1728 x 2853: 28, 28 and 17; 256 x 2560 x 5120: 14, 12 and 23).
+// Columns of a tile: those with the least estimated time.  A pair of CTAs is the
+// fastest by far where its tiles fill the SMs, and smaller tiles where they do not
+// (12010 x 192 x 1152: 7.0, 10.8 and 9.5 us with 64, 128 and 256 columns; 1602 x 1728
+// x 2853: 29, 22 and 15; 256 x 2560 x 5120: 11, 10 and 22).
 int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
 {
     if (rn <= 64)
@@ -791,11 +863,7 @@ int columns_of_tile(int64_t rm, int64_t rn, int blocks, bool rows_b)
     double least = 0;
     for (int bn : {64, 128, 256}) {
         const int64_t tiles = up(rm, bn == 256 ? 2 * kRows : kRows) * up(rn, bn);
-        const double block = block_time(bn, rows_b);
-        const int splits = splits_for(tiles, blocks, bn, block), part = (blocks + splits - 1) / splits;
-        const int64_t waves = up(tiles * splits, bn == 256 ? 76 : bn == 128 ? 152 : 304);
-        const double start = bn == 256 ? 5.0 : 3.5;
-        const double t = (double)waves * (start + block * part) + (splits > 1 ? 1.5 : 0);
+        const double t = estimate(tiles, blocks, bn, rows_b, false, splits_for(tiles, blocks, bn, rows_b));
         if (!best || t < least) {
             best = bn;
             least = t;
@@ -808,13 +876,13 @@ constexpr int kFewColumns = 32;  // of a tile of few tokens
 
 // The product of ra's rows (the MMA's) with rb's (its columns, bn a tile).
 Params plan(const BlockMatrix &ra, const BlockMatrix &rb, int bn, void *out, int64_t rm, int64_t rn, int64_t n, int64_t k,
-            bool bf16)
+            bool bf16, bool fused = false)
 {
     Params p = {};
     p.m_tiles = (int)up(rm, bn == 256 ? 2 * kRows : kRows);
     p.n_tiles = (int)up(rn, bn);
     p.blocks = (int)up(k, 128);
-    p.splits = splits_for((int64_t)p.m_tiles * p.n_tiles, p.blocks, bn, block_time(bn, !rb.tile));
+    p.splits = splits_for((int64_t)p.m_tiles * p.n_tiles, p.blocks, bn, !rb.tile, fused);
     p.sa = ra.scale;
     p.sa_row = ra.scale_row;
     p.sa_block = ra.scale_block;
@@ -882,7 +950,7 @@ cudaError_t launch_few_tokens(const void *x, int64_t row, const BlockMatrix &w, 
                               int64_t inputs, bool bf16, cudaStream_t st)
 {
     const int sms = device_sm_count();
-    Params p = plan(w, BlockMatrix{}, kFewColumns, y, outputs, tokens, outputs, inputs, bf16);
+    Params p = plan(w, BlockMatrix{}, kFewColumns, y, outputs, tokens, outputs, inputs, bf16, true);
     if (!p.status)
         return cudaErrorUnknown;
     p.x = x;

@@ -464,3 +464,16 @@ def test_offsets_past_32_bits():
         part = ssd.ssd_block_matmul(q[rows], s[rows], b, sb, out_dtype=F32)
         assert bool(((y[rows].float() - part).abs() <= 2.0 ** -8 * part.abs() + 2.0 ** -14 * float(part.abs().max())).all())
     assert ssd.ssd_stream_status() == 0
+
+
+@pytest.mark.parametrize("inference", [False, True])
+def test_the_transposes_scales_of_tiles_are_the_tiles(inference):
+    """One memory and one version for both, in inference mode too."""
+    with torch.inference_mode(inference):
+        _, s, _, st = ssd.ssd_block_quantize(tokens(300, 200, F32), tile=True, want_t=True)
+        assert st.shape == (2, 3) and torch.equal(st, s.t()) and st.data_ptr() == s.data_ptr()
+        assert s.is_inference() == st.is_inference() == inference
+        s[2, 1] = 7.0
+        assert float(st[1, 2]) == 7.0
+        if not inference:
+            assert st._version == s._version == 1

@@ -9,7 +9,8 @@
 // or a NaN has the scale NaN and nothing but NaN in it.
 //
 // One CTA takes 128 x 128 values, once from memory for both orientations: a
-// warp 16 rows, a thread 4 neighbouring columns of them, kept in registers.  A
+// warp 16 rows (8 where few CTAs run: 1024 x 1024 2.7 -> 2.2 us one way), a thread
+// 4 neighbouring columns of them, kept in registers.  A
 // row's maximum is one warp reduction, a column's the thread's own over its rows
 // and then over the warps.  The values of the transpose go through shared
 // memory, 16 of a column at a time, so that rows of 128 bytes are written.
@@ -24,7 +25,7 @@ namespace ssd {
 namespace {
 
 constexpr int kB = 128;
-constexpr int kWarps = 8, kRowsOfWarp = kB / kWarps;
+constexpr unsigned kFewBlocks = 152;  // GB300's SMs
 
 // Four neighbouring values as they are in memory: bf16 stays packed, in half the
 // registers, and its largest magnitudes are found two at a time.
@@ -67,11 +68,12 @@ template <> struct Four<__nv_bfloat16> {
 };
 
 // kVec: rows of x start on boundaries of four values.
-template <typename TI, bool kE5M2, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(TI) == 2 ? 3 : 2)
+template <typename TI, bool kE5M2, bool kVec, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 16 ? 1 : sizeof(TI) == 2 ? 3 : 2)
 block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *__restrict__ scale,
                       uint8_t *__restrict__ qt, float *__restrict__ scale_t, const QuantGeom g)
 {
+    constexpr int kRowsOfWarp = kB / kWarps;
     __shared__ uint32_t col_max[kWarps][kB];
     __shared__ __align__(16) uint4 turned[kB * kB / 16];  // [column][16-byte piece ^ (column / 4 % 8)]
     let_next_kernel_start();
@@ -100,6 +102,10 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
                 if (i >= rows)
                     v[i] = F{};
         }
+    } else if (kVec && (c0 >= g.cols || rows == 0)) {
+#pragma unroll
+        for (int i = 0; i < kRowsOfWarp; ++i)
+            v[i] = F{};
     } else {
 #pragma unroll
         for (int i = 0; i < kRowsOfWarp; ++i) {
@@ -172,41 +178,56 @@ block_quantize_kernel(const TI *__restrict__ x, uint8_t *__restrict__ q, float *
                 if (warp == 0 && c0 + j < g.cols)
                     scale_t[rb * g.scale_t_ld + c0 + j] = s;
             }
-            uint32_t b[4];
+            uint32_t b[kRowsOfWarp / 4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int w = 0; w < kRowsOfWarp / 4; ++w)
                 b[w] = to_bytes<kE5M2>(v[4 * w][j] * inverse, v[4 * w + 1][j] * inverse, v[4 * w + 2][j] * inverse,
                                        v[4 * w + 3][j] * inverse);
-            turned[(lane * 4 + j) * (kB / 16) + (warp ^ (lane & 7))] = make_uint4(b[0], b[1], b[2], b[3]);
+            const int at = (lane * 4 + j) * (kB / 16) + (warp * kRowsOfWarp / 16 ^ (lane & 7));
+            if constexpr (kRowsOfWarp == 16)
+                turned[at] = make_uint4(b[0], b[1], b[2], b[3]);
+            else
+                reinterpret_cast<uint2 *>(&turned[at])[warp & 1] = make_uint2(b[0], b[1]);
         }
         __syncthreads();
-        // a warp writes 16 columns, eight threads the 128 bytes of one
+        // a warp writes 16 (8) columns, eight threads the 128 bytes of one
         const int64_t first = rb * kB + (lane & 7) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = warp * 16 + i * 4 + (lane >> 3);
+        for (int i = 0; i < kRowsOfWarp / 4; ++i) {
+            const int c = warp * kRowsOfWarp + i * 4 + (lane >> 3);
             const int64_t col = cb * kB + c;
             if (col >= g.cols || first >= g.rows)
                 continue;
-            const uint4 b = turned[c * (kB / 16) + ((lane & 7) ^ ((c >> 2) & 7))];
+            uint4 b = turned[c * (kB / 16) + ((lane & 7) ^ ((c >> 2) & 7))];
             uint8_t *o = qt + col * g.row_qt + first;
             if (first + 16 <= g.rows) {
                 *reinterpret_cast<uint4 *>(o) = b;
-            } else {
-                const uint32_t e[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (first + j < g.rows)
-                        o[j] = (uint8_t)(e[j >> 2] >> (8 * (j & 3)));
+            } else {  // 8, 4, 2 and 1 of the last ones
+                const int left = (int)(g.rows - first);
+                if (left & 8) {
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(b.x, b.y);
+                    b.x = b.z;
+                    b.y = b.w;
+                }
+                if (left & 4) {
+                    *reinterpret_cast<uint32_t *>(o + (left & 8)) = b.x;
+                    b.x = b.y;
+                }
+                if (left & 2) {
+                    *reinterpret_cast<uint16_t *>(o + (left & 12)) = (uint16_t)b.x;
+                    b.x >>= 16;
+                }
+                if (left & 1)
+                    o[left & 14] = (uint8_t)b.x;
             }
         }
     }
 }
 
-template <typename TI, bool kE5M2>
-cudaError_t launch(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g, cudaStream_t st)
+template <typename TI, bool kE5M2, int kWarps>
+cudaError_t launch_warps(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g, unsigned grid,
+                         cudaStream_t st)
 {
-    const unsigned grid = (unsigned)(((g.cols + kB - 1) / kB) * ((g.rows + kB - 1) / kB));
     const bool vec = g.row % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * sizeof(TI)) == 0;
     cudaLaunchAttribute attr = early_launch();
     cudaLaunchConfig_t cfg = {};
@@ -215,12 +236,23 @@ cudaError_t launch(const void *x, void *q, float *scale, void *qt, float *scale_
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, vec ? block_quantize_kernel<TI, kE5M2, true> : block_quantize_kernel<TI, kE5M2, false>,
-                           static_cast<const TI *>(x), static_cast<uint8_t *>(q), scale, static_cast<uint8_t *>(qt), scale_t, g);
+    const auto kernel =
+        vec ? block_quantize_kernel<TI, kE5M2, true, kWarps> : block_quantize_kernel<TI, kE5M2, false, kWarps>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const TI *>(x), static_cast<uint8_t *>(q), scale,
+                                             static_cast<uint8_t *>(qt), scale_t, g);
     if (e == cudaSuccess)
         note_launch(1);
     return e;
+}
+
+template <typename TI, bool kE5M2>
+cudaError_t launch(const void *x, void *q, float *scale, void *qt, float *scale_t, const QuantGeom &g, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)(((g.cols + kB - 1) / kB) * ((g.rows + kB - 1) / kB));
+    // at most one CTA an SM: twice the warps shorten each (with 320 of them they cost
+    // more than they save, 6.7 -> 9.8 us for 2000 x 2560)
+    return grid <= kFewBlocks ? launch_warps<TI, kE5M2, 16>(x, q, scale, qt, scale_t, g, grid, st)
+                              : launch_warps<TI, kE5M2, 8>(x, q, scale, qt, scale_t, g, grid, st);
 }
 
 }  // namespace

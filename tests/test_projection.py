@@ -477,3 +477,11 @@ def test_the_transposes_scales_of_tiles_are_the_tiles(inference):
         assert float(st[1, 2]) == 7.0
         if not inference:
             assert st._version == s._version == 1
+
+
+@pytest.mark.parametrize("rows", list(range(241, 258)))
+@pytest.mark.parametrize("wide", [False, True])
+def test_quantise_tails(rows, wide):
+    """Every number of last rows and columns, with 16 warps a block and with 8."""
+    check_quantised(tokens(rows, 13000 if wide else 300 - rows % 17, BF, rows), False)
+    check_quantised(tokens(rows, 12996 if wide else rows, F32, rows), True)
